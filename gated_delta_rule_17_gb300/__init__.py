@@ -1,6 +1,8 @@
-"""GB300-native chunked gated-delta-rule (GDN) prefill forward.
+"""GB300-native chunked gated-delta-rule (GDN) prefill forward, and the softmax-attention
+operators that stand next to it in a hybrid model.
 
-A thin ctypes binding over the C ABI in ``include/gdn_prefill.h``; every step
+A thin ctypes binding over the C ABI in ``include/gdn_prefill.h`` and
+``include/gdn_attention.h``; every step
 of the computation runs in the library's CUDA kernels. PyTorch only supplies
 device memory and the current stream. There is no fallback: if the compiled
 library is missing, importing works but every call raises ``GdnError``.
@@ -13,8 +15,10 @@ import threading
 
 __all__ = ["prefill", "prefill_noalloc", "prefill_host", "host_scratch_bytes", "NOALLOC_MAX_SEQS", "workspace_bytes", "check", "last_launch_count",
            "backward", "backward_workspace_bytes",
+           "head_norm_rope", "head_norm_rope_backward", "head_norm_rope_backward_workspace_bytes", "paged_append",
+           "tree_attention", "tree_attention_workspace_bytes",
            "set_timing_events", "set_test_hooks", "decode", "lib_path", "load", "GdnError",
-           "Strides", "GDN_OK", "GDN_ERR_ARG", "GDN_ERR_UNSUPPORTED", "GDN_ERR_CUDA",
+           "Strides", "Rope", "NormStrides", "Paged", "GDN_OK", "GDN_ERR_ARG", "GDN_ERR_UNSUPPORTED", "GDN_ERR_CUDA",
            "GDN_ERR_DEVICE_STATUS", "GDN_ERR_TIMEOUT", "GDN_ERR_RANGE"]
 
 (GDN_OK, GDN_ERR_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_DEVICE_STATUS, GDN_ERR_TIMEOUT,
@@ -37,6 +41,25 @@ class Strides(ctypes.Structure):
     _fields_ = [("q", ctypes.c_int64), ("k", ctypes.c_int64), ("v", ctypes.c_int64),
                 ("g", ctypes.c_int64), ("beta", ctypes.c_int64), ("out", ctypes.c_int64),
                 ("state_is_table", ctypes.c_int32), ("qk_l2norm", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("positions", ctypes.c_int32), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class NormStrides(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_int64), ("k", ctypes.c_int64), ("q_out", ctypes.c_int64), ("k_out", ctypes.c_int64),
+                ("q_grad", ctypes.c_int64), ("k_grad", ctypes.c_int64)]
+
+
+class Paged(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_page", ctypes.c_int64), ("k_token", ctypes.c_int64),
+                ("k_head", ctypes.c_int64), ("v_page", ctypes.c_int64), ("v_token", ctypes.c_int64),
+                ("v_head", ctypes.c_int64), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int32),
+                ("B", ctypes.c_int32), ("rows", ctypes.c_int32), ("ctx_lens", ctypes.c_void_p),
+                ("cu_rows", ctypes.c_void_p)]
 
 
 def lib_path() -> str:
@@ -78,6 +101,21 @@ def load():
             lib.gdn_prefill_backward_workspace_bytes.restype = sz
             lib.gdn_prefill_backward.argtypes = [vp] * 14 + [i] * 6 + [ctypes.POINTER(Strides), vp, vp, sz, vp]
             lib.gdn_prefill_backward.restype = i
+            f32 = ctypes.c_float
+            rope, norm_st, paged = (ctypes.POINTER(x) for x in (Rope, NormStrides, Paged))
+            lib.gdn_head_norm_rope.argtypes = [vp, vp, vp, rope, vp, vp, f32, vp, vp] + [i] * 5 + [norm_st, vp]
+            lib.gdn_head_norm_rope.restype = i
+            lib.gdn_head_norm_rope_backward_workspace_bytes.argtypes = [i] * 4
+            lib.gdn_head_norm_rope_backward_workspace_bytes.restype = sz
+            lib.gdn_head_norm_rope_backward.argtypes = ([vp, vp, vp, rope, vp, vp, f32] + [vp] * 6 + [i] * 5
+                                                        + [norm_st, vp, sz, vp])
+            lib.gdn_head_norm_rope_backward.restype = i
+            lib.gdn_paged_append.argtypes = [vp, vp, paged, vp, rope, i, vp, f32, i, i, i, i64, i64, vp]
+            lib.gdn_paged_append.restype = i
+            lib.gdn_tree_attention_workspace_bytes.argtypes = [i] * 3
+            lib.gdn_tree_attention_workspace_bytes.restype = sz
+            lib.gdn_tree_attention.argtypes = [vp, paged, vp, i, f32, vp, i, i, i, i, i64, i64, i, vp, sz, vp]
+            lib.gdn_tree_attention.restype = i
             lib.gdn_set_timing_events.argtypes = [vp, vp, vp]
             lib.gdn_set_timing_events.restype = None
             lib.gdn_set_test_hooks.argtypes = [i64, i64, i]
@@ -339,6 +377,220 @@ def backward(q, k, v, g, beta, h0, dout, dq, dk, dv, dg, dbeta, *, nk: int, nv: 
                                   dout.data_ptr(), ptr(dST), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
                                   dbeta.data_ptr(), ptr(dh0), B, T, nk, nv, dk_dim, dv_dim, ctypes.byref(st),
                                   ptr(cu_seqlens), ws_ptr, ws_size, stream)
+    if rc != GDN_OK:
+        _raise(rc)
+
+
+# ---- the softmax-attention operators (include/gdn_attention.h) ----------------------------
+
+def _stream(torch, stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dtype(torch, t, name, allowed):
+    """The ABI's number of an activation type."""
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(t.dtype)
+    if code is None or code not in allowed:
+        raise GdnError(GDN_ERR_ARG, f"{name} must be {' or '.join(('bfloat16', 'float16', 'float32')[a] for a in allowed)}, "
+                                    f"got {t.dtype}")
+    return code
+
+
+def _check_like(torch, dt, named):
+    """Rows of one element type on the GPU."""
+    for name, t in named:
+        if t is not None and t.dtype != dt:
+            raise GdnError(GDN_ERR_ARG, f"{name} must be {dt}, got {t.dtype}")
+        if t is not None and not t.is_cuda:
+            raise GdnError(GDN_ERR_ARG, f"{name} must be a CUDA tensor")
+
+
+def _check_vector(t, name, dt, n):
+    """A contiguous CUDA vector of n elements, or None."""
+    if t is not None and (not t.is_cuda or t.dtype != dt or not t.is_contiguous() or t.numel() != n):
+        raise GdnError(GDN_ERR_ARG, f"{name} must be a contiguous {dt} CUDA tensor of {n} elements")
+
+
+def _rows_of(t, name, rows, inner):
+    if t.shape[0] != rows:
+        raise GdnError(GDN_ERR_ARG, f"{name} has {t.shape[0]} rows, need {rows}")
+    return _row_stride(t, name, inner)
+
+
+def _rope(torch, cos, sin, interleaved):
+    if (cos is None) != (sin is None):
+        raise GdnError(GDN_ERR_ARG, "cos and sin must be given together")
+    if cos is None:
+        return None
+    for name, t in (("cos", cos), ("sin", sin)):
+        if not t.is_cuda or t.dtype != torch.float32 or t.dim() != 2 or t.shape != cos.shape or (
+                t.shape[1] > 1 and t.stride(1) != 1) or t.stride(0) != cos.stride(0):
+            raise GdnError(GDN_ERR_ARG, f"{name} must be an fp32 CUDA tensor [positions, rot/2], contiguous in a row, "
+                                        "cos and sin alike")
+    n, half = cos.shape
+    return Rope(cos.data_ptr(), sin.data_ptr(), cos.stride(0) if n > 1 else max(cos.stride(0), half), n, 2 * half,
+                1 if interleaved else 0)
+
+
+def _check_workspace(workspace):
+    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
+        raise GdnError(GDN_ERR_ARG, "workspace must be a contiguous CUDA tensor")
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def _norm_args(torch, q, k, positions, cos, sin, outs, grads, nq, nkv, d, q_weight, k_weight, interleaved):
+    """Shared checks of head_norm_rope and its backward: (rows, dtype, rope, strides)."""
+    x = q if q is not None else k
+    if x is None:
+        raise GdnError(GDN_ERR_ARG, "q or k must be given")
+    if (q is None) != (nq == 0) or (k is None) != (nkv == 0):
+        raise GdnError(GDN_ERR_ARG, "q (k) is None just where nq (nkv) is 0")
+    code = _dtype(torch, x, "q" if q is not None else "k", (0, 1, 2))
+    rows, st = x.shape[0], []
+    for names, ts in ((("q", "k"), (q, k)), (("q_out", "k_out"), outs), (("q_grad", "k_grad"), grads)):
+        for name, t, heads in zip(names, ts, (nq, nkv)):
+            if heads and t is None:
+                raise GdnError(GDN_ERR_ARG, f"{name} is missing")
+            _check_like(torch, x.dtype, ((name, t),))
+            st.append(_rows_of(t, name, rows, heads * d) if heads else 0)
+    _check_vector(q_weight, "q_weight", torch.float32, d)
+    _check_vector(k_weight, "k_weight", torch.float32, d)
+    _check_vector(positions, "positions", torch.int32, rows)
+    return rows, code, _rope(torch, cos, sin, interleaved), NormStrides(*st)
+
+
+def head_norm_rope(q, k, positions, cos, sin, q_out, k_out, *, nq: int, nkv: int, head_dim: int = 128, q_weight=None,
+                   k_weight=None, eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """RMS norm of every query and key head row, then the position rotation, in one pass
+    (``gdn_head_norm_rope``): y = rotate(x / sqrt(mean(x^2) + eps) * weight).
+
+    q, q_out: [rows, nq*head_dim] (or [rows, nq, head_dim]); k, k_out likewise with nkv heads; bf16, fp16 or
+    fp32, all alike. Either may be None with a head count of 0; q_out may be q itself, k_out k. ``q_weight``,
+    ``k_weight``: fp32 [head_dim], shared by the heads (None: ones). ``positions``: int32 [rows] into the fp32
+    tables ``cos``, ``sin`` [positions, rot/2] (both None: no rotation); the first ``rot`` values of a head are
+    turned, in pairs (i, i + rot/2), or (2i, 2i + 1) if ``interleaved``. head_dim is 64 or 128."""
+    import torch
+
+    lib = load()
+    rows, code, rope, st = _norm_args(torch, q, k, positions, cos, sin, (q_out, k_out), (q, k), nq, nkv, head_dim,
+                                      q_weight, k_weight, interleaved)
+    rc = lib.gdn_head_norm_rope(_ptr(q), _ptr(k), _ptr(positions), rope, _ptr(q_weight), _ptr(k_weight), eps,
+                                _ptr(q_out), _ptr(k_out), rows, nq, nkv, head_dim, code, st,
+                                _stream(torch, stream, (q if q is not None else k).device))
+    if rc != GDN_OK:
+        _raise(rc)
+
+
+def head_norm_rope_backward_workspace_bytes(rows, nq, nkv, head_dim=128) -> int:
+    return int(load().gdn_head_norm_rope_backward_workspace_bytes(rows, nq, nkv, head_dim))
+
+
+def head_norm_rope_backward(q, k, positions, cos, sin, q_grad, k_grad, dq, dk, dq_weight=None, dk_weight=None, *,
+                            nq: int, nkv: int, head_dim: int = 128, q_weight=None, k_weight=None, eps: float = 1e-6,
+                            interleaved: bool = False, workspace=None, stream=None) -> None:
+    """The backward of ``head_norm_rope`` (``gdn_head_norm_rope_backward``). q, k and the rest as given to the
+    forward; ``q_grad``, ``k_grad``: dL/dq_out, dL/dk_out; outputs ``dq``, ``dk`` of the same type (may be
+    q_grad, k_grad themselves) and, where given, ``dq_weight``, ``dk_weight``: fp32 [head_dim], overwritten with
+    the sums over all rows and heads."""
+    import torch
+
+    lib = load()
+    rows, code, rope, st = _norm_args(torch, q, k, positions, cos, sin, (dq, dk), (q_grad, k_grad), nq, nkv, head_dim,
+                                      q_weight, k_weight, interleaved)
+    _check_vector(dq_weight, "dq_weight", torch.float32, head_dim)
+    _check_vector(dk_weight, "dk_weight", torch.float32, head_dim)
+    ws, size = _check_workspace(workspace)
+    rc = lib.gdn_head_norm_rope_backward(_ptr(q), _ptr(k), _ptr(positions), rope, _ptr(q_weight), _ptr(k_weight), eps,
+                                         _ptr(q_grad), _ptr(k_grad), _ptr(dq), _ptr(dk), _ptr(dq_weight),
+                                         _ptr(dk_weight), rows, nq, nkv, head_dim, code, st, ws, size,
+                                         _stream(torch, stream, (q if q is not None else k).device))
+    if rc != GDN_OK:
+        _raise(rc)
+
+
+def _paged(torch, x, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, d):
+    """The cache and the batch of rows x as the ABI's struct."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not t.is_cuda or t.dtype != x.dtype:
+            raise GdnError(GDN_ERR_ARG, f"{name} must be a {x.dtype} CUDA tensor")
+        if t.dim() != 4 or t.shape[2] != nkv or t.shape[3] != d or t.stride(3) != 1 or t.shape != k_cache.shape:
+            raise GdnError(GDN_ERR_ARG, f"{name} must be [pages, page_size, {nkv}, {d}], the last dimension contiguous")
+    if not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or (
+            block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise GdnError(GDN_ERR_ARG, "block_table must be an int32 CUDA tensor [B, max_pages], contiguous in a row")
+    B, most = block_table.shape
+    _check_vector(ctx_lens, "ctx_lens", torch.int32, B)
+    _check_vector(cu_rows, "cu_rows", torch.int32, B + 1)
+    ks, vs = k_cache.stride(), v_cache.stride()
+    return Paged(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], k_cache.shape[0],
+                 k_cache.shape[1], block_table.data_ptr(), max(block_table.stride(0), most), most, B, x.shape[0],
+                 ctx_lens.data_ptr(), _ptr(cu_rows))
+
+
+def paged_append(k, v, k_cache, v_cache, block_table, ctx_lens, *, nkv: int, head_dim: int = 128, cu_rows=None,
+                 positions=None, cos=None, sin=None, norm: bool = False, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, stream=None) -> None:
+    """Write new keys and values into a paged cache (``gdn_paged_append``), the keys normed (``norm``) and rotated
+    on the way.
+
+    k, v: bf16 or fp16 [rows, nkv*head_dim]; k_cache, v_cache: [pages, page_size, nkv, head_dim] of the same type,
+    any strides with a contiguous last dimension; block_table: int32 [B, max_pages]; ctx_lens: int32 [B], each
+    sequence's tokens before this call; cu_rows: int32 [B + 1], the rows of each sequence (None: row b belongs to
+    sequence b). Row i of sequence b becomes its token ctx_lens[b] + i. ``positions``: int32 [rows] for the
+    rotation (None: the token's index); ``cos``, ``sin``, ``interleaved``, ``k_weight``: as ``head_norm_rope``."""
+    import torch
+
+    lib = load()
+    code = _dtype(torch, k, "k", (0, 1))
+    _check_like(torch, k.dtype, (("k", k), ("v", v)))
+    rows = k.shape[0]
+    cache = _paged(torch, k, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, head_dim)
+    _check_vector(positions, "positions", torch.int32, rows)
+    _check_vector(k_weight, "k_weight", torch.float32, head_dim)
+    rc = lib.gdn_paged_append(_ptr(k), _ptr(v), cache, _ptr(positions), _rope(torch, cos, sin, interleaved),
+                              1 if norm else 0, _ptr(k_weight), eps, nkv, head_dim, code,
+                              _rows_of(k, "k", rows, nkv * head_dim), _rows_of(v, "v", rows, nkv * head_dim),
+                              _stream(torch, stream, k.device))
+    if rc != GDN_OK:
+        _raise(rc)
+
+
+def tree_attention_workspace_bytes(nq, nkv, head_dim=128) -> int:
+    return int(load().gdn_tree_attention_workspace_bytes(nq, nkv, head_dim))
+
+
+def tree_attention(q, k_cache, v_cache, block_table, ctx_lens, out, *, nq: int, nkv: int, head_dim: int = 128,
+                   cu_rows=None, mask=None, max_rows: int | None = None, scale: float | None = None, workspace=None,
+                   stream=None) -> None:
+    """Attention of decode tokens or drafted trees over a paged cache (``gdn_tree_attention``); the new tokens' keys
+    and values are in the cache already (``paged_append``), whose arguments these share.
+
+    q, out: [rows, nq*head_dim] of the cache's type, nq a multiple of nkv. Every row sees the ctx_lens[b] tokens of
+    its sequence's context; of its sequence's new rows it sees those whose bit is set in ``mask`` (int64 [rows,
+    words], bit j % 64 of word j // 64 for new row j), or without a mask those up to itself. A row that sees
+    nothing gives zeros. ``max_rows``: the most rows of a sequence, by which the kernel is chosen; ``scale``:
+    1/sqrt(head_dim) by default; ``workspace``: uint8 CUDA tensor of ``tree_attention_workspace_bytes(...)``."""
+    import torch
+
+    lib = load()
+    code = _dtype(torch, q, "q", (0, 1))
+    _check_like(torch, q.dtype, (("q", q), ("out", out)))
+    rows = q.shape[0]
+    cache = _paged(torch, q, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, head_dim)
+    if mask is not None and (not mask.is_cuda or mask.dtype != torch.int64 or mask.dim() != 2
+                             or mask.shape[0] != rows or not mask.is_contiguous()):
+        raise GdnError(GDN_ERR_ARG, f"mask must be a contiguous int64 CUDA tensor [{rows}, words]")
+    ws, size = _check_workspace(workspace)
+    rc = lib.gdn_tree_attention(_ptr(q), cache, _ptr(mask), 0 if mask is None else mask.shape[1],
+                                head_dim ** -0.5 if scale is None else scale, _ptr(out), nq, nkv, head_dim, code,
+                                _rows_of(q, "q", rows, nq * head_dim), _rows_of(out, "out", rows, nq * head_dim),
+                                max_rows or 0, ws, size, _stream(torch, stream, q.device))
     if rc != GDN_OK:
         _raise(rc)
 

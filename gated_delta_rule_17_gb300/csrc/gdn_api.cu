@@ -15,14 +15,17 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
+#include "gdn_attention.h"
 #include "gdn_prefill.h"
 #include "gdn_prefill_kernel.cuh"
 #include "gdn_wy_kernel.cuh"
 #include "gdn_decode_kernel.cuh"
 #include "gdn_bwd_dstates_tc.cuh"
 #include "gdn_bwd_grads_tc.cuh"
+#include "gdn_attn_kernel.cuh"
 
 namespace {
 
@@ -100,7 +103,15 @@ int device_info(DeviceInfo** out) {
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     const std::pair<const void*, int> bwd[] = {
         {reinterpret_cast<const void*>(gdn::gdn_bwd_dstates_tc_kernel), gdn::DsPlan::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_bwd_grads_tc_kernel), gdn::GtPlan::DYN_SMEM}};
+        {reinterpret_cast<const void*>(gdn::gdn_bwd_grads_tc_kernel), gdn::GtPlan::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__nv_bfloat16, 64, 1>), gdn::AttnPlan<64, 1>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__nv_bfloat16, 64, 2>), gdn::AttnPlan<64, 2>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__nv_bfloat16, 128, 1>), gdn::AttnPlan<128, 1>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__nv_bfloat16, 128, 2>), gdn::AttnPlan<128, 2>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 64, 1>), gdn::AttnPlan<64, 1>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 64, 2>), gdn::AttnPlan<64, 2>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 128, 1>), gdn::AttnPlan<128, 1>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 128, 2>), gdn::AttnPlan<128, 2>::DYN_SMEM}};
     for (const auto& f : bwd) {
       e = cudaFuncSetAttribute(f.first, cudaFuncAttributeMaxDynamicSharedMemorySize, f.second);
       if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -920,6 +931,10 @@ int gdn_prefill_check(void* stream) {
   if (st & gdn::kStatusTimeout) return fail(GDN_ERR_TIMEOUT, "a bounded on-device wait expired (status 0x%x)", st);
   if (st & gdn::kStatusBadSeqlens)
     return fail(GDN_ERR_DEVICE_STATUS, "cu_seqlens is malformed: not non-decreasing from 0 to T (status 0x%x)", st);
+  if (st & gdn::kStatusBadPage)
+    return fail(GDN_ERR_DEVICE_STATUS, "a token's page number, or the token itself, is outside the cache or its block table (status 0x%x)", st);
+  if (st & gdn::kStatusBadPosition)
+    return fail(GDN_ERR_DEVICE_STATUS, "a rotation position is outside the table (status 0x%x)", st);
   if (st & gdn::kStatusRange)
     return fail(GDN_ERR_RANGE,
                 "an output or final state is not finite: v, the state or an intermediate left the fp16 operand "
@@ -1157,3 +1172,5 @@ void gdn_set_timing_events(void* before_wy, void* before_spine, void* after_spin
 }
 
 }  // extern "C"
+
+#include "gdn_attn_api.cuh"

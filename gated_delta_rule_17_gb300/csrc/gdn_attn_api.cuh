@@ -1,0 +1,419 @@
+// Host side of the entry points in include/gdn_attention.h: argument checks (each rejection
+// names the guard) and launches. Included by gdn_api.cu, whose error message, launch count,
+// device table and status word it shares.
+#pragma once
+
+namespace {
+
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+int launched(int launches) {
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+  g_launches = launches;
+  return GDN_OK;
+}
+
+int check_head_dim(int d) {
+  if (d != 64 && d != 128) return fail(GDN_ERR_UNSUPPORTED, "head_dim = %d is neither 64 nor 128", d);
+  return GDN_OK;
+}
+
+int check_rope(const gdn_rope_t* r, int d, gdn::RopeParams* out, int* interleaved) {
+  *out = gdn::RopeParams{};
+  *interleaved = 0;
+  if (!r || r->rot == 0) return GDN_OK;
+  if (r->rot < 0 || r->rot > d || r->rot % 8)
+    return fail(GDN_ERR_ARG, "rot = %d must be a multiple of 8 in 0..head_dim", r->rot);
+  if (r->interleaved != 0 && r->interleaved != 1) return fail(GDN_ERR_ARG, "interleaved must be 0 or 1");
+  if (!r->cos || !r->sin) return fail(GDN_ERR_ARG, "a rotation table pointer is NULL");
+  if (!aligned16(r->cos) || !aligned16(r->sin)) return fail(GDN_ERR_ARG, "cos and sin must be 16-byte aligned");
+  if (r->positions < 0) return fail(GDN_ERR_ARG, "the rotation table's positions = %d is negative", r->positions);
+  if (r->stride < r->rot / 2 || r->stride % 4)
+    return fail(GDN_ERR_ARG, "rotation table stride %lld must be >= rot / 2 and a multiple of 4", (long long)r->stride);
+  out->cos = r->cos;
+  out->sin = r->sin;
+  out->stride = r->stride;
+  out->positions = r->positions;
+  out->rot = r->rot;
+  *interleaved = r->interleaved;
+  return GDN_OK;
+}
+
+int check_stride(int64_t stride, int64_t least, const char* name) {
+  if (stride < least || stride % 8)
+    return fail(GDN_ERR_ARG, "%s row stride %lld must be >= %lld and a multiple of 8", name, (long long)stride,
+                (long long)least);
+  return GDN_OK;
+}
+
+constexpr int kNormBwdCtasPerSm = 4;
+
+int norm_chunks(int heads, int d, int unroll) {
+  const int per = unroll * (32 / (d / 8));
+  return (heads + per - 1) / per;
+}
+
+// The checks that the forward and the backward share; fills all but the gradients' fields.
+int norm_setup(const void* q, const void* k, const int32_t* positions, const gdn_rope_t* rope, const float* q_weight,
+               const float* k_weight, float eps, void* q_out, void* k_out, int rows, int nq, int nkv, int d, int dtype,
+               const gdn_norm_strides_t* st, int unroll, gdn::NormRopeParams* p, int* interleaved) {
+  *p = gdn::NormRopeParams{};
+  if (rows < 0) return fail(GDN_ERR_ARG, "rows = %d is negative", rows);
+  if (nq < 0 || nkv < 0 || nq + static_cast<int64_t>(nkv) < 1)
+    return fail(GDN_ERR_ARG, "head counts nq = %d, nkv = %d: neither negative, one at least positive", nq, nkv);
+  if (int rc = check_head_dim(d)) return rc;
+  if (dtype != GDN_BF16 && dtype != GDN_F16 && dtype != GDN_F32) return fail(GDN_ERR_UNSUPPORTED, "dtype %d is unknown", dtype);
+  if (!(eps >= 0.f)) return fail(GDN_ERR_ARG, "eps must not be negative");
+  if (int rc = check_rope(rope, d, &p->rope, interleaved)) return rc;
+  const int64_t wq = static_cast<int64_t>(nq) * d, wk = static_cast<int64_t>(nkv) * d;
+  p->q_stride = st ? st->q : wq;
+  p->k_stride = st ? st->k : wk;
+  p->q_out_stride = st ? st->q_out : wq;
+  p->k_out_stride = st ? st->k_out : wk;
+  p->q_grad_stride = st ? st->q_grad : wq;
+  p->k_grad_stride = st ? st->k_grad : wk;
+  if (nq) {
+    if (int rc = check_stride(p->q_stride, wq, "q")) return rc;
+    if (int rc = check_stride(p->q_out_stride, wq, "q_out")) return rc;
+  }
+  if (nkv) {
+    if (int rc = check_stride(p->k_stride, wk, "k")) return rc;
+    if (int rc = check_stride(p->k_out_stride, wk, "k_out")) return rc;
+  }
+  p->q_chunks = norm_chunks(nq, d, unroll);
+  p->chunks = p->q_chunks + norm_chunks(nkv, d, unroll);
+  if (static_cast<int64_t>(rows) * p->chunks > INT32_MAX - (1 << 20))
+    return fail(GDN_ERR_UNSUPPORTED, "%d rows of %d + %d heads exceed the item range", rows, nq, nkv);
+  if (rows == 0) return GDN_OK;
+  if ((nq && (!q || !q_out)) || (nkv && (!k || !k_out))) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out))
+    return fail(GDN_ERR_ARG, "q, k and their outputs must be 16-byte aligned");
+  if (!aligned16(q_weight) || !aligned16(k_weight)) return fail(GDN_ERR_ARG, "weights must be 16-byte aligned");
+  if (p->rope.rot && !positions) return fail(GDN_ERR_ARG, "a rotation needs positions");
+  p->q = q;
+  p->k = k;
+  p->q_out = q_out;
+  p->k_out = k_out;
+  p->positions = positions;
+  p->q_weight = q_weight;
+  p->k_weight = k_weight;
+  p->rows = rows;
+  p->nq = nq;
+  p->nkv = nkv;
+  p->eps = eps;
+  return GDN_OK;
+}
+
+// Calls f(T{}, D, interleaved) with compile-time element type, head size and pairing.
+template <int N>
+using IntC = std::integral_constant<int, N>;
+template <typename F>
+void by_head(int d, int interleaved, F&& f) {
+  if (d == 64) interleaved ? f(IntC<64>{}, std::true_type{}) : f(IntC<64>{}, std::false_type{});
+  else interleaved ? f(IntC<128>{}, std::true_type{}) : f(IntC<128>{}, std::false_type{});
+}
+template <typename F>
+void by_type16(int dtype, F&& f) {
+  dtype == GDN_BF16 ? f(__nv_bfloat16{}) : f(__half{});
+}
+template <typename F>
+void by_type(int dtype, F&& f) {
+  if (dtype == GDN_F32) f(float{});
+  else by_type16(dtype, f);
+}
+
+int check_paged(const gdn_paged_t* c, int nkv, int d, gdn::PagedParams* p) {
+  *p = gdn::PagedParams{};
+  if (!c) return fail(GDN_ERR_ARG, "the cache is NULL");
+  if (c->B < 0 || c->rows < 0) return fail(GDN_ERR_ARG, "B = %d or rows = %d is negative", c->B, c->rows);
+  if (c->page_size < 1 || c->num_pages < 0 || c->max_pages < 0)
+    return fail(GDN_ERR_ARG, "page_size = %d, num_pages = %d or max_pages = %d is out of range", c->page_size, c->num_pages,
+                c->max_pages);
+  if (static_cast<int64_t>(c->max_pages) * c->page_size > INT32_MAX - 256)
+    return fail(GDN_ERR_UNSUPPORTED, "max_pages * page_size exceeds the 2^31 token range");
+  if (c->table_stride < c->max_pages)
+    return fail(GDN_ERR_ARG, "block_table row stride %lld is below max_pages = %d", (long long)c->table_stride, c->max_pages);
+  for (const int64_t s : {c->k_page, c->k_token, c->k_head, c->v_page, c->v_token, c->v_head})
+    if (s < 0 || s % 8) return fail(GDN_ERR_ARG, "cache stride %lld must be a multiple of 8", (long long)s);
+  if (nkv > 1 && (c->k_head < d || c->v_head < d)) return fail(GDN_ERR_ARG, "cache head strides are below head_dim = %d", d);
+  if (!c->cu_rows && c->rows != c->B)
+    return fail(GDN_ERR_ARG, "without cu_rows there is one row a sequence: rows = %d, B = %d", c->rows, c->B);
+  if (c->rows > 0 && c->B == 0) return fail(GDN_ERR_ARG, "%d rows of no sequence", c->rows);
+  if (c->rows == 0) return GDN_OK;
+  if (!c->k || !c->v || !c->block_table || !c->ctx_lens) return fail(GDN_ERR_ARG, "a required cache pointer is NULL");
+  if (!aligned16(c->k) || !aligned16(c->v)) return fail(GDN_ERR_ARG, "the caches must be 16-byte aligned");
+  p->k = c->k;
+  p->v = c->v;
+  p->k_page = c->k_page;
+  p->k_token = c->k_token;
+  p->k_head = c->k_head;
+  p->v_page = c->v_page;
+  p->v_token = c->v_token;
+  p->v_head = c->v_head;
+  p->num_pages = c->num_pages;
+  p->page_size = c->page_size;
+  p->block_table = c->block_table;
+  p->table_stride = c->table_stride;
+  p->max_pages = c->max_pages;
+  p->B = c->B;
+  p->rows = c->rows;
+  p->ctx_lens = c->ctx_lens;
+  p->cu_rows = c->cu_rows;
+  return GDN_OK;
+}
+
+// ---- attention -----------------------------------------------------------------------
+constexpr int kAttnCtasPerSm = 2;
+constexpr int kAttnMaxRows = 32;  // query rows of the largest tile
+
+struct AttnLayout {
+  size_t ml, o, cut, total;
+};
+AttnLayout attn_layout(int runs, int d) {
+  AttnLayout l;
+  l.cut = 0;
+  l.ml = align256(static_cast<size_t>(runs) * sizeof(int4));
+  l.o = l.ml + align256(static_cast<size_t>(runs) * 2 * kAttnMaxRows * 2 * sizeof(float));
+  l.total = l.o + align256(static_cast<size_t>(runs) * 2 * kAttnMaxRows * d * sizeof(float));
+  return l;
+}
+
+template <typename T, int D, int MB>
+cudaError_t launch_attn(gdn::AttnParams& p, cudaStream_t s) {
+  gdn::gdn_attn_kernel<T, D, MB><<<p.runs, gdn::kAttnThreads, gdn::AttnPlan<D, MB>::DYN_SMEM, s>>>(p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.runs), 16 * MB);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gdn::gdn_attn_join_kernel<T, D, 16 * MB>, const_cast<const gdn::AttnParams&>(p));
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_head_norm_rope(const void* q, const void* k, const int32_t* positions, const gdn_rope_t* rope,
+                       const float* q_weight, const float* k_weight, float eps, void* q_out, void* k_out, int rows,
+                       int nq, int nkv, int d, int dtype, const gdn_norm_strides_t* strides, void* stream) {
+  g_err[0] = 0;
+  g_launches = 0;
+  gdn::NormRopeParams p;
+  int next = 0;
+  if (int rc = norm_setup(q, k, positions, rope, q_weight, k_weight, eps, q_out, k_out, rows, nq, nkv, d, dtype, strides,
+                          gdn::kNormUnroll, &p, &next))
+    return rc;
+  if (rows == 0) return GDN_OK;
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  p.status = dev->status;
+  const int warps = gdn::kNormThreads / 32;
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(rows) * p.chunks + warps - 1) / warps);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  by_type(dtype, [&](auto t) {
+    by_head(d, next, [&](auto dim, auto pairs) {
+      gdn::gdn_head_norm_rope_kernel<decltype(t), dim.value, pairs.value><<<grid, gdn::kNormThreads, 0, s>>>(p);
+    });
+  });
+  return launched(1);
+}
+
+size_t gdn_head_norm_rope_backward_workspace_bytes(int rows, int nq, int nkv, int d) {
+  (void)nq;
+  (void)nkv;
+  if (rows <= 0 || (d != 64 && d != 128)) return 0;
+  return static_cast<size_t>(plan_sms()) * kNormBwdCtasPerSm * 2 * d * sizeof(float);
+}
+
+int gdn_head_norm_rope_backward(const void* q, const void* k, const int32_t* positions, const gdn_rope_t* rope,
+                                const float* q_weight, const float* k_weight, float eps, const void* q_grad,
+                                const void* k_grad, void* dq, void* dk, float* dq_weight, float* dk_weight, int rows,
+                                int nq, int nkv, int d, int dtype, const gdn_norm_strides_t* strides, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  g_launches = 0;
+  gdn::NormRopeParams p;
+  int next = 0;
+  if (int rc = norm_setup(q, k, positions, rope, q_weight, k_weight, eps, dq, dk, rows, nq, nkv, d, dtype, strides,
+                          gdn::kNormBwdUnroll, &p, &next))
+    return rc;
+  if (nq)
+    if (int rc = check_stride(p.q_grad_stride, static_cast<int64_t>(nq) * d, "q_grad")) return rc;
+  if (nkv)
+    if (int rc = check_stride(p.k_grad_stride, static_cast<int64_t>(nkv) * d, "k_grad")) return rc;
+  const bool sums = dq_weight || dk_weight;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {  // sums over no rows
+    for (float* w : {dq_weight, dk_weight})
+      if (w) {
+        cudaError_t e = cudaMemsetAsync(w, 0, static_cast<size_t>(d) * sizeof(float), s);
+        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(e));
+      }
+    return GDN_OK;
+  }
+  if ((nq && !q_grad) || (nkv && !k_grad)) return fail(GDN_ERR_ARG, "an incoming gradient pointer is NULL");
+  if (!aligned16(q_grad) || !aligned16(k_grad)) return fail(GDN_ERR_ARG, "q_grad and k_grad must be 16-byte aligned");
+  const size_t need = gdn_head_norm_rope_backward_workspace_bytes(rows, nq, nkv, d);
+  if (workspace && sums) {
+    if (workspace_bytes < need)
+      return fail(GDN_ERR_ARG, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, need);
+    if (!aligned256(workspace)) return fail(GDN_ERR_ARG, "workspace must be 256-byte aligned");
+  }
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  p.status = dev->status;
+  p.q_grad = q_grad;
+  p.k_grad = k_grad;
+  void* ws = sums ? workspace : nullptr;
+  if (sums && !ws) {
+    cudaError_t e = cudaMallocAsync(&ws, need, s);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaMallocAsync(%zu): %s", need, cudaGetErrorString(e));
+  }
+  p.partials = static_cast<float*>(ws);
+  const int64_t warps = gdn::kNormThreads / 32, ctas = (static_cast<int64_t>(rows) * p.chunks + warps - 1) / warps;
+  const int64_t slots = static_cast<int64_t>(dev->sms) * kNormBwdCtasPerSm;
+  const int grid = static_cast<int>(ctas < slots ? ctas : slots);
+  by_type(dtype, [&](auto t) {
+    by_head(d, next, [&](auto dim, auto pairs) {
+      gdn::gdn_head_norm_rope_bwd_kernel<decltype(t), dim.value, pairs.value><<<grid, gdn::kNormThreads, 0, s>>>(p);
+    });
+  });
+  if (sums) {
+    if (d == 64) gdn::gdn_norm_weight_sum_kernel<64><<<2, 1024, 0, s>>>(p.partials, grid, dq_weight, dk_weight);
+    else gdn::gdn_norm_weight_sum_kernel<128><<<2, 1024, 0, s>>>(p.partials, grid, dq_weight, dk_weight);
+  }
+  int rc = launched(sums ? 2 : 1);
+  if (sums && !workspace) {
+    cudaError_t e = cudaFreeAsync(ws, s);
+    if (e != cudaSuccess && rc == GDN_OK) rc = fail(GDN_ERR_CUDA, "cudaFreeAsync: %s", cudaGetErrorString(e));
+  }
+  return rc;
+}
+
+int gdn_paged_append(const void* k, const void* v, const gdn_paged_t* cache, const int32_t* positions,
+                     const gdn_rope_t* rope, int norm, const float* k_weight, float eps, int nkv, int d, int dtype,
+                     int64_t k_stride, int64_t v_stride, void* stream) {
+  g_err[0] = 0;
+  g_launches = 0;
+  gdn::AppendParams p{};
+  int next = 0;
+  if (nkv < 1) return fail(GDN_ERR_ARG, "nkv = %d must be positive", nkv);
+  if (int rc = check_head_dim(d)) return rc;
+  if (dtype != GDN_BF16 && dtype != GDN_F16) return fail(GDN_ERR_UNSUPPORTED, "dtype %d is neither bf16 nor fp16", dtype);
+  if (norm != 0 && norm != 1) return fail(GDN_ERR_ARG, "norm must be 0 or 1");
+  if (!norm && k_weight) return fail(GDN_ERR_ARG, "k_weight is given without norm");
+  if (!(eps >= 0.f)) return fail(GDN_ERR_ARG, "eps must not be negative");
+  if (int rc = check_rope(rope, d, &p.rope, &next)) return rc;
+  if (int rc = check_paged(cache, nkv, d, &p.cache)) return rc;
+  const int64_t w = static_cast<int64_t>(nkv) * d;
+  p.k_stride = k_stride ? k_stride : w;
+  p.v_stride = v_stride ? v_stride : w;
+  if (int rc = check_stride(p.k_stride, w, "k")) return rc;
+  if (int rc = check_stride(p.v_stride, w, "v")) return rc;
+  p.chunks = norm_chunks(nkv, d, gdn::kNormUnroll);
+  const int64_t items = static_cast<int64_t>(cache->rows) * p.chunks * 2;
+  if (items > INT32_MAX - (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "%d rows of %d heads exceed the item range", cache->rows, nkv);
+  if (cache->rows == 0) return GDN_OK;
+  if (!k || !v) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_weight)) return fail(GDN_ERR_ARG, "k, v and k_weight must be 16-byte aligned");
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  p.k = k;
+  p.v = v;
+  p.positions = positions;
+  p.k_weight = k_weight;
+  p.nkv = nkv;
+  p.norm = norm;
+  p.eps = eps;
+  p.status = dev->status;
+  const int warps = gdn::kNormThreads / 32;
+  const unsigned grid = static_cast<unsigned>((items + warps - 1) / warps);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  by_type16(dtype, [&](auto t) {
+    by_head(d, next, [&](auto dim, auto pairs) {
+      gdn::gdn_paged_append_kernel<decltype(t), dim.value, pairs.value><<<grid, gdn::kNormThreads, 0, s>>>(p);
+    });
+  });
+  return launched(1);
+}
+
+size_t gdn_tree_attention_workspace_bytes(int nq, int nkv, int d) {
+  if (nq <= 0 || nkv <= 0 || (d != 64 && d != 128)) return 0;
+  return attn_layout(plan_sms() * kAttnCtasPerSm, d).total;
+}
+
+int gdn_tree_attention(const void* q, const gdn_paged_t* cache, const uint64_t* mask, int mask_words, float scale,
+                       void* out, int nq, int nkv, int d, int dtype, int64_t q_stride, int64_t out_stride,
+                       int max_rows, void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  g_launches = 0;
+  gdn::AttnParams p{};
+  if (nq < 1 || nkv < 1) return fail(GDN_ERR_ARG, "head counts nq = %d, nkv = %d must be positive", nq, nkv);
+  if (nq % nkv) return fail(GDN_ERR_UNSUPPORTED, "nq = %d is not a multiple of nkv = %d", nq, nkv);
+  if (int rc = check_head_dim(d)) return rc;
+  if (dtype != GDN_BF16 && dtype != GDN_F16) return fail(GDN_ERR_UNSUPPORTED, "dtype %d is neither bf16 nor fp16", dtype);
+  if (!(scale - scale == 0.f)) return fail(GDN_ERR_ARG, "scale must be finite");
+  if (mask && mask_words < 1) return fail(GDN_ERR_ARG, "mask_words = %d must be positive", mask_words);
+  if (max_rows < 0) return fail(GDN_ERR_ARG, "max_rows = %d is negative", max_rows);
+  if (int rc = check_paged(cache, nkv, d, &p.cache)) return rc;
+  const int64_t w = static_cast<int64_t>(nq) * d;
+  p.q_stride = q_stride ? q_stride : w;
+  p.out_stride = out_stride ? out_stride : w;
+  if (int rc = check_stride(p.q_stride, w, "q")) return rc;
+  if (int rc = check_stride(p.out_stride, w, "out")) return rc;
+  if (static_cast<int64_t>(cache->rows) * nq > INT32_MAX - 4096)
+    return fail(GDN_ERR_UNSUPPORTED, "%d rows of %d heads exceed the 2^31 row range", cache->rows, nq);
+  if (cache->rows == 0) return GDN_OK;
+  if (!q || !out) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(GDN_ERR_ARG, "q and out must be 16-byte aligned");
+  const size_t need = gdn_tree_attention_workspace_bytes(nq, nkv, d);
+  if (workspace) {
+    if (workspace_bytes < need)
+      return fail(GDN_ERR_ARG, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, need);
+    if (!aligned256(workspace)) return fail(GDN_ERR_ARG, "workspace must be 256-byte aligned");
+  }
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* ws = workspace;
+  if (!ws) {
+    cudaError_t e = cudaMallocAsync(&ws, need, s);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaMallocAsync(%zu): %s", need, cudaGetErrorString(e));
+  }
+  p.q = q;
+  p.out = out;
+  p.mask = mask;
+  p.mask_words = mask_words;
+  p.nq = nq;
+  p.nkv = nkv;
+  p.group = nq / nkv;
+  p.scale_log2 = scale * 1.4426950408889634f;  // log2 e
+  p.status = dev->status;
+  p.runs = dev->sms * kAttnCtasPerSm;
+  const AttnLayout l = attn_layout(p.runs, d);
+  p.cut = reinterpret_cast<int4*>(static_cast<char*>(ws) + l.cut);
+  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + l.ml);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + l.o);
+  // rows of a kv head, by the caller's bound: one block of 16 where they fit, else two
+  const int most = !cache->cu_rows ? 1 : (max_rows && max_rows < cache->rows ? max_rows : cache->rows);
+  const bool small = static_cast<int64_t>(most) * p.group <= 16;
+  cudaError_t e = cudaSuccess;
+  by_type16(dtype, [&](auto t) {
+    using T = decltype(t);
+    if (d == 64) e = small ? launch_attn<T, 64, 1>(p, s) : launch_attn<T, 64, 2>(p, s);
+    else e = small ? launch_attn<T, 128, 1>(p, s) : launch_attn<T, 128, 2>(p, s);
+  });
+  int rc = e != cudaSuccess ? fail(GDN_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e)) : launched(2);
+  if (!workspace) {
+    e = cudaFreeAsync(ws, s);
+    if (e != cudaSuccess && rc == GDN_OK) rc = fail(GDN_ERR_CUDA, "cudaFreeAsync: %s", cudaGetErrorString(e));
+  }
+  return rc;
+}
+
+}  // extern "C"

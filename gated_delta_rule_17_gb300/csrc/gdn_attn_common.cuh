@@ -1,0 +1,169 @@
+// Shared parts of the attention kernels over a paged cache: the split of the work over the
+// CTAs and the join of its parts.
+//
+// A unit is one tile of query rows of one (sequence, kv head). The rows of a kv head are
+// r = i (nq / nkv) + g for new token i and head g of its group, so that all heads that read
+// a key share its load. A unit walks its sequence's tokens in tiles of KT. The tiles of all
+// units in a row, (sequence, kv head, row tile, token tile), are cut into as many equal runs
+// as there are CTAs: the load is even whatever the lengths, one long sequence fills the
+// card, and no length is needed on the host. A unit that lies in one run is written by it. A
+// unit that is cut leaves a partial (m, l, o) of every piece in the workspace,
+//
+//     m = max_t x_t,   l = sum_t 2^(x_t - m),   o = sum_t 2^(x_t - m) v_t
+//
+// (x in units of log2 e), and gdn_attn_join_kernel adds the pieces up in their order,
+// with weights 2^(m_piece - max m). A run has at most two cut units, its first (slot 0)
+// and its last (slot 1), so the workspace does not grow with the batch.
+#pragma once
+#include "gdn_norm_rope_kernel.cuh"
+
+namespace gdn {
+
+struct AttnParams {
+  const void* q;
+  void* out;
+  PagedParams cache;
+  const uint64_t* mask;  // [rows][mask_words] or null
+  int mask_words;
+  int nq, nkv, group;
+  float scale_log2;  // scale * log2 e
+  int64_t q_stride, out_stride;
+  int runs;        // CTAs of the attention kernel
+  float* part_ml;  // [runs][2][MT][2]: m and l
+  float* part_o;   // [runs][2][MT][D]
+  int4* cut;       // [runs]: the unit that begins in the run and is cut: first row, rows, kv head and row tile, last run (-1: none)
+  unsigned* status;
+};
+
+struct AttnSeq {
+  int first, n;  // its new rows
+  int ctx, len;  // tokens before them, and with them (as many as the table holds)
+  int tiles;     // token tiles, at least 1
+  int qtiles;    // row tiles of a kv head
+};
+
+template <int MT, int KT>
+__device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b, bool report) {
+  const PagedParams& c = p.cache;
+  AttnSeq s;
+  s.first = c.cu_rows ? c.cu_rows[b] : b;
+  const int end = c.cu_rows ? c.cu_rows[b + 1] : b + 1;
+  s.ctx = c.ctx_lens[b];
+  s.n = end - s.first;
+  const bool ends = !c.cu_rows || ((b != 0 || s.first == 0) && (b != c.B - 1 || end == c.rows));
+  if (s.first < 0 || end < s.first || end > c.rows || s.ctx < 0 || !ends) {
+    if (report) atomicOr(p.status, kStatusBadSeqlens);
+    if (s.first < 0 || end < s.first || end > c.rows || s.ctx < 0) s.n = s.ctx = 0;
+  }
+  const int64_t cap = static_cast<int64_t>(c.max_pages) * c.page_size;  // < 2^31
+  int64_t len = static_cast<int64_t>(s.ctx) + s.n;
+  if (len > cap) {
+    if (report && s.n > 0) atomicOr(p.status, kStatusBadPage);
+    len = cap;
+  }
+  s.len = static_cast<int>(len);
+  s.tiles = s.len > 0 ? (s.len + KT - 1) / KT : 1;
+  s.qtiles = (s.n * p.group + MT - 1) / MT;
+  return s;
+}
+
+__device__ __forceinline__ int64_t attn_cost(const AttnParams& p, const AttnSeq& s) {
+  return static_cast<int64_t>(s.tiles) * s.qtiles * p.nkv;
+}
+
+// Inclusive prefix of `x` over the block's threads; *total is the sum. s_scan: a word a warp.
+template <int THREADS>
+__device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t* s_scan, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // the last use of s_scan is over
+  if (lane == 31) s_scan[warp] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += s_scan[w];
+    all += s_scan[w];
+  }
+  *total = all;
+  return x + before;
+}
+
+// Where a run starts: sequence, unit and tile of it, and how many tiles it has.
+struct AttnStart {
+  int b;
+  int64_t within;      // tiles of sequence b before the run
+  int64_t end, total;  // tiles up to the run's end, and of all runs
+  int64_t count;       // tiles of the run
+  int runs;            // runs that have tiles
+};
+
+// Run i of `runs` has the tiles [total i / runs, total (i + 1) / runs).
+__device__ __forceinline__ int64_t run_begin(int64_t i, int64_t total, int runs) { return total * i / runs; }
+
+// The run that holds tile `at`.
+__device__ __forceinline__ int run_of(int64_t at, int64_t total, int runs) {
+  int64_t i = at * runs / total;
+  while (run_begin(i + 1, total, runs) <= at) ++i;
+  while (run_begin(i, total, runs) > at) --i;
+  return static_cast<int>(i);
+}
+
+// All threads of the block take part. s_scan: THREADS / 32 words; s_start: shared.
+template <int MT, int KT, int THREADS>
+__device__ __forceinline__ AttnStart attn_start(const AttnParams& p, int run, int64_t* s_scan, AttnStart* s_start) {
+  const int B = p.cache.B, tid = threadIdx.x;
+  int64_t total = 0;
+  for (int b0 = 0; b0 < B; b0 += THREADS) {
+    int64_t sum;
+    block_prefix<THREADS>(b0 + tid < B ? attn_cost(p, attn_seq<MT, KT>(p, b0 + tid, run == 0)) : 0, s_scan, &sum);
+    total += sum;
+  }
+  const int runs = total < p.runs ? static_cast<int>(total) : p.runs;  // no run is empty
+  const bool works = run < runs;
+  const int64_t begin = works ? run_begin(run, total, runs) : 0, end = works ? run_begin(run + 1, total, runs) : 0;
+  if (tid == 0) *s_start = AttnStart{0, 0, end, total, 0, runs};
+  __syncthreads();
+  if (works) {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < B && before <= begin; b0 += THREADS) {
+      int64_t sum;
+      const int64_t cost = b0 + tid < B ? attn_cost(p, attn_seq<MT, KT>(p, b0 + tid, false)) : 0;
+      const int64_t upto = before + block_prefix<THREADS>(cost, s_scan, &sum);
+      if (upto > begin && upto - cost <= begin) {  // one thread's, at most
+        s_start->b = b0 + tid;
+        s_start->within = begin - (upto - cost);
+        s_start->count = end - begin;
+      }
+      before += sum;
+    }
+  }
+  __syncthreads();
+  return *s_start;
+}
+
+// ---- 16-bit element types ---------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  return pack_half2(a, b);
+}
+
+// 2^x on the special function unit (relative error about 2^-22; 0 for -inf).
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+}  // namespace gdn

@@ -1,0 +1,392 @@
+// Attention of decode tokens and small drafted trees over a paged cache, for sm_103a.
+//
+// For few query rows a kv head (R = rows x heads of a group) the operator does R flops a
+// byte of the cache, far below the 289 flops a byte at which the card's tensor rate meets
+// its bandwidth, so it is bound by reading K and V once. Every warp is on its own: it
+// streams 16-token slabs of K and V through its private ring in shared memory (16-byte
+// cp.async from the tokens' places in the pages, any page size), and has all MB x 16 query
+// rows against them with register tensor products: scores S = Q K^T, running maximum and sum, O += P V.
+// No barrier is needed in the loop; the warps' (m, l, O) are added up at a unit's end.
+#pragma once
+#include "gdn_attn_common.cuh"
+
+namespace gdn {
+
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kAttnSlab = 16;                      // tokens of a warp's step
+constexpr int kAttnTile = kAttnWarps * kAttnSlab;  // tokens of a CTA's step
+
+template <int D, int MB>
+struct AttnPlan {
+  static constexpr int MT = 16 * MB;
+  static constexpr int ROW = D * 2;                        // bytes of a key or value
+  static constexpr int SLAB = kAttnSlab * ROW;             // bytes of a slab of K or V
+  static constexpr int STAGES = 3 * 128 / D;
+  static constexpr int RING = STAGES * 2 * SLAB;           // bytes of a warp's ring
+  static constexpr int JOIN = kAttnWarps * MT * (D + 2) * 4;  // the warps' O, m and l at a unit's end
+  static constexpr int BYTES = kAttnWarps * RING > JOIN ? kAttnWarps * RING : JOIN;
+  static constexpr int DYN_SMEM = BYTES + 128;
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t saddr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t saddr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+// d += a (16 x 16) b (16 x 8)
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void cp_async_16(uint32_t dst_saddr, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_saddr), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+
+// Byte offset of 16-byte piece c of row r: pieces are exchanged within a row by the row's number,
+// so that eight rows' pieces c lie in different banks.
+template <int D>
+__device__ __forceinline__ uint32_t attn_sw(int r, int c) {
+  return static_cast<uint32_t>(r * (D * 2) + ((c ^ (r & 7)) << 4));
+}
+
+// The place of a token: its page (-1 for none) and place in it.
+struct TokenPlace {
+  int page, place;
+};
+__device__ __forceinline__ TokenPlace token_place(const AttnParams& p, const int32_t* table, int t, int len) {
+  TokenPlace r{-1, 0};
+  if (t < len) {
+    const int at = t / p.cache.page_size;
+    r.place = t - at * p.cache.page_size;
+    r.page = table[at];
+    if (r.page < 0 || r.page >= p.cache.num_pages) {
+      r.page = -1;
+      atomicOr(p.status, kStatusBadPage);
+    }
+  }
+  return r;
+}
+
+template <typename T, int D, int MB>
+__global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnParams p) {
+  using Plan = AttnPlan<D, MB>;
+  constexpr int MT = Plan::MT, KS = D / 16, NT = D / 8, CH = D / 8, STAGES = Plan::STAGES;
+  extern __shared__ uint8_t dyn[];
+  __shared__ int64_t s_scan[kAttnWarps];
+  __shared__ AttnStart s_start;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 127) & ~static_cast<uintptr_t>(127));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gr = lane >> 2, tc = lane & 3;  // fragment row and column pair
+  const uint32_t ring = tc::smem_u32(smem) + warp * Plan::RING;
+  const PagedParams& c = p.cache;
+  const int run = blockIdx.x;
+
+  AttnStart st = attn_start<MT, kAttnTile, kAttnThreads>(p, run, s_scan, &s_start);
+  if (threadIdx.x == 0) p.cut[run] = make_int4(0, 0, 0, -1);
+  int64_t left = st.count;
+  int b = st.b;
+  int64_t within = st.within;
+  while (left > 0) {
+    const AttnSeq s = attn_seq<MT, kAttnTile>(p, b, false);
+    const int64_t cost = attn_cost(p, s);
+    if (within >= cost) {
+      within -= cost;
+      ++b;
+      continue;
+    }
+    const int unit = static_cast<int>(within / s.tiles), t0 = static_cast<int>(within - static_cast<int64_t>(unit) * s.tiles);
+    const int kvh = unit / s.qtiles, qt = unit - kvh * s.qtiles;
+    const int t1 = left < s.tiles - t0 ? t0 + static_cast<int>(left) : s.tiles;
+    const int R = s.n * p.group;
+    const int32_t* table = c.block_table + b * c.table_stride;
+
+    // Q fragments: row gr (+8) of each block of 16
+    uint32_t qf[MB][KS][4];
+    int node[MB][2];  // the new token of each of this thread's rows, -1 for none
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = qt * MT + mb * 16 + hf * 8 + gr;
+        node[mb][hf] = r < R ? r / p.group : -1;
+        const int i = r < R ? r / p.group : 0, g = r < R ? r - i * p.group : 0;
+        const T* src = static_cast<const T*>(p.q) + (static_cast<int64_t>(s.first) + i) * p.q_stride +
+                       static_cast<int64_t>(kvh * p.group + g) * D + 2 * tc;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          qf[mb][ks][hf] = r < R ? *reinterpret_cast<const uint32_t*>(src + 16 * ks) : 0u;
+          qf[mb][ks][2 + hf] = r < R ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 8) : 0u;
+        }
+      }
+    float o[MB][NT][4], m[MB][2], l[MB][2];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      m[mb][0] = m[mb][1] = -INFINITY;
+      l[mb][0] = l[mb][1] = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[mb][nt][j] = 0.f;
+    }
+
+    const T* kbase = static_cast<const T*>(c.k) + kvh * c.k_head;
+    const T* vbase = static_cast<const T*>(c.v) + kvh * c.v_head;
+    // the copies of slab `t` of this warp: lane i & 15 knows token i's place
+    auto find = [&](int t) { return token_place(p, table, t * kAttnTile + warp * kAttnSlab + (lane & 15), t < t1 ? s.len : 0); };
+    auto issue = [&](int t, const TokenPlace& place) {
+      const uint32_t dst = ring + (t % STAGES) * (2 * Plan::SLAB);
+      constexpr int ROWS = 32 / CH;  // tokens of one copy instruction
+#pragma unroll
+      for (int i = 0; i < kAttnSlab / ROWS; ++i) {
+        const int r = i * ROWS + lane / CH, ch = lane % CH;
+        const int page = __shfl_sync(0xffffffffu, place.page, r), at = __shfl_sync(0xffffffffu, place.place, r);
+        const bool real = page >= 0;
+        const int64_t pg = real ? page : 0;
+        cp_async_16(dst + attn_sw<D>(r, ch), kbase + pg * c.k_page + at * c.k_token + 8 * ch, real);
+        cp_async_16(dst + Plan::SLAB + attn_sw<D>(r, ch), vbase + pg * c.v_page + at * c.v_token + 8 * ch, real);
+      }
+    };
+    TokenPlace next = find(t0);
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) {
+      const TokenPlace place = next;
+      next = find(t0 + i + 1);
+      if (t0 + i < t1) issue(t0 + i, place);
+      tc::cp_async_commit();
+    }
+    for (int t = t0; t < t1; ++t) {
+      const TokenPlace place = next;
+      next = find(t + STAGES);
+      __syncwarp();  // all lanes have read the slab that is overwritten now
+      if (t + STAGES - 1 < t1) issue(t + STAGES - 1, place);
+      tc::cp_async_commit();
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+      __syncwarp();
+      const uint32_t ks_addr = ring + (t % STAGES) * (2 * Plan::SLAB), vs_addr = ks_addr + Plan::SLAB;
+      const int tok = t * kAttnTile + warp * kAttnSlab;
+      if (tok >= s.len) continue;  // the whole warp: nothing of its slab is there
+
+      float sc[MB][2][4];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sc[mb][nt][j] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t kf[4];
+        ldmatrix4(ks_addr + attn_sw<D>((lane >> 4) * 8 + (lane & 7), 2 * ks + ((lane >> 3) & 1)), kf);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          mma16816<T>(sc[mb][0], qf[mb][ks], kf[0], kf[1]);
+          mma16816<T>(sc[mb][1], qf[mb][ks], kf[2], kf[3]);
+        }
+      }
+      // tokens that a row does not see; before the new tokens every row sees all
+      if (tok + kAttnSlab > s.ctx) {
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int at = tok + nt * 8 + 2 * tc + (j & 1), i = node[mb][j >> 1], x = at - s.ctx;
+              bool sees = at < s.len;
+              if (sees && x >= 0) {
+                if (!p.mask)
+                  sees = x <= i;
+                else
+                  sees = i >= 0 && (x >> 6) < p.mask_words &&
+                         ((p.mask[(static_cast<int64_t>(s.first) + i) * p.mask_words + (x >> 6)] >> (x & 63)) & 1);
+              }
+              if (!sees) sc[mb][nt][j] = -INFINITY;
+            }
+      }
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        uint32_t pf[4];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          float x0 = sc[mb][0][2 * hf] * p.scale_log2, x1 = sc[mb][0][2 * hf + 1] * p.scale_log2;
+          float x2 = sc[mb][1][2 * hf] * p.scale_log2, x3 = sc[mb][1][2 * hf + 1] * p.scale_log2;
+          float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[mb][hf], mx), base = mn == -INFINITY ? 0.f : mn;
+          if (__any_sync(0xffffffffu, mn > m[mb][hf])) {
+            const float f = exp2_approx(m[mb][hf] - base);
+            l[mb][hf] *= f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              o[mb][nt][2 * hf] *= f;
+              o[mb][nt][2 * hf + 1] *= f;
+            }
+            m[mb][hf] = mn;
+          }
+          x0 = exp2_approx(x0 - base);
+          x1 = exp2_approx(x1 - base);
+          x2 = exp2_approx(x2 - base);
+          x3 = exp2_approx(x3 - base);
+          l[mb][hf] += (x0 + x1) + (x2 + x3);  // this thread's tokens; over the row at the end
+          pf[hf] = pack2<T>(x0, x1);
+          pf[2 + hf] = pack2<T>(x2, x3);
+        }
+#pragma unroll
+        for (int cp = 0; cp < NT / 2; ++cp) {
+          uint32_t vf[4];
+          ldmatrix4_trans(vs_addr + attn_sw<D>(((lane >> 3) & 1) * 8 + (lane & 7), 2 * cp + (lane >> 4)), vf);
+          mma16816<T>(o[mb][2 * cp], pf, vf[0], vf[1]);
+          mma16816<T>(o[mb][2 * cp + 1], pf, vf[2], vf[3]);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+    // add up the warps' parts
+    float* jo = reinterpret_cast<float*>(smem);       // [warp][MT][D]
+    float* jml = jo + kAttnWarps * MT * D;            // [warp][MT][2]
+    __syncthreads();                                  // the rings are done with
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = mb * 16 + hf * 8 + gr;
+        float ll = l[mb][hf];
+        ll += __shfl_xor_sync(0xffffffffu, ll, 1);
+        ll += __shfl_xor_sync(0xffffffffu, ll, 2);
+        if (tc == 0) {
+          jml[(warp * MT + r) * 2] = m[mb][hf];
+          jml[(warp * MT + r) * 2 + 1] = ll;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          *reinterpret_cast<float2*>(jo + (warp * MT + r) * D + nt * 8 + 2 * tc) =
+              make_float2(o[mb][nt][2 * hf], o[mb][nt][2 * hf + 1]);
+      }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == s.tiles;
+    const int slot = t0 == 0 ? 1 : 0;
+    constexpr int LPR = D / 4;  // threads of a row
+    for (int r = threadIdx.x / LPR; r < MT; r += kAttnThreads / LPR) {
+      const int row = qt * MT + r;
+      if (row >= R) continue;
+      const int d4 = (threadIdx.x % LPR) * 4;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) mm = fmaxf(mm, jml[(w * MT + r) * 2]);
+      const float base = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f, a[4] = {};
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) {
+        const float f = exp2_approx(jml[(w * MT + r) * 2] - base);
+        const float4 v = *reinterpret_cast<const float4*>(jo + (w * MT + r) * D + d4);
+        ll = fmaf(f, jml[(w * MT + r) * 2 + 1], ll);
+        a[0] = fmaf(f, v.x, a[0]);
+        a[1] = fmaf(f, v.y, a[1]);
+        a[2] = fmaf(f, v.z, a[2]);
+        a[3] = fmaf(f, v.w, a[3]);
+      }
+      if (whole) {
+        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        const int i = row / p.group, g = row - i * p.group;
+        T* dst = static_cast<T*>(p.out) + (static_cast<int64_t>(s.first) + i) * p.out_stride +
+                 static_cast<int64_t>(kvh * p.group + g) * D + d4;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(a[0] * inv, a[1] * inv), pack2<T>(a[2] * inv, a[3] * inv));
+      } else {
+        const int64_t at = (static_cast<int64_t>(run) * 2 + slot) * MT + r;
+        *reinterpret_cast<float4*>(p.part_o + at * D + d4) = make_float4(a[0], a[1], a[2], a[3]);
+        if (d4 == 0) {
+          p.part_ml[at * 2] = mm;
+          p.part_ml[at * 2 + 1] = ll;
+        }
+      }
+    }
+    __syncthreads();  // the join buffer is done with
+    within += t1 - t0;
+    left -= t1 - t0;
+    if (t0 == 0 && t1 < s.tiles && threadIdx.x == 0) 
+      p.cut[run] = make_int4(s.first, s.n, unit, run_of(st.end + (s.tiles - t1) - 1, st.total, st.runs));
+  }
+}
+
+// Joins the pieces of the unit that begins in run blockIdx.x and goes on in the next runs: one
+// CTA a row, every warp a fourth of the pieces.
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(128) gdn_attn_join_kernel(const AttnParams p) {
+  constexpr int WARPS = 4;
+  __shared__ float s_m[WARPS], s_l[WARPS];
+  __shared__ __align__(16) float s_o[WARPS][D];
+  tc::grid_dependency_wait();
+  const int run = blockIdx.x, r = blockIdx.y;
+  const int4 cut = p.cut[run];
+  if (cut.w < 0) return;
+  const int unit_qtiles = (cut.y * p.group + MT - 1) / MT;
+  const int kvh = cut.z / unit_qtiles, qt = cut.z - kvh * unit_qtiles, row = qt * MT + r;
+  if (row >= cut.y * p.group) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int last = cut.w;  // the run with the unit's last tile
+  constexpr int V = D / 32;
+  float m = -INFINITY, l = 0.f, o[V] = {};
+  for (int i = run + warp; i <= last; i += WARPS) {
+    const int64_t at = (static_cast<int64_t>(i) * 2 + (i == run ? 1 : 0)) * MT + r;
+    const float pm = p.part_ml[at * 2], pl = p.part_ml[at * 2 + 1];
+    float v[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = p.part_o[at * D + j * 32 + lane];
+    const float mn = fmaxf(m, pm), base = mn == -INFINITY ? 0.f : mn;
+    const float f = exp2_approx(m - base), g = exp2_approx(pm - base);
+    m = mn;
+    l = l * f + pl * g;
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = o[j] * f + v[j] * g;
+  }
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) s_o[warp][j * 32 + lane] = o[j];
+  __syncthreads();
+  if (threadIdx.x < D / 2) {
+    float mm = -INFINITY, ll = 0.f, a = 0.f, c = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, s_m[w]);
+    const float base = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = exp2_approx(s_m[w] - base);
+      ll = fmaf(f, s_l[w], ll);
+      a = fmaf(f, s_o[w][2 * threadIdx.x], a);
+      c = fmaf(f, s_o[w][2 * threadIdx.x + 1], c);
+    }
+    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    const int i = row / p.group, g = row - i * p.group;
+    T* dst = static_cast<T*>(p.out) + (static_cast<int64_t>(cut.x) + i) * p.out_stride +
+             static_cast<int64_t>(kvh * p.group + g) * D;
+    reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = pack2<T>(a * inv, c * inv);
+  }
+}
+
+}  // namespace gdn

@@ -1,0 +1,480 @@
+// RMS norm and rotation of query and key heads, its backward, and the append of
+// keys and values to a paged cache, for sm_103a.
+//
+// For a head row x of d values, with r = 1 / sqrt(mean(x^2) + eps) and weights w,
+//
+//     z = x r w;   y = R z      (R turns the value pairs of the first `rot` values)
+//
+// and backward, given dy:
+//
+//     dz = R^T dy;  dw = sum dz x r;  t = dz w;  dx = r (t - x r^2 mean(t x))
+//
+// All of it is bound by HBM: ~10 (20) flops a value against 4 (6) bytes in 16-bit
+// types. So each head row is read once and stays in registers: d / 8 lanes hold it,
+// eight values each, and the two values of a pair sit in the same lane, so the
+// rotation needs no exchange; only the row sums go over the lanes. A lane's eight
+// values are two runs of four: values 4l and 4l + rot/2 for pairs half a rotation
+// apart, 8l and 8l + 4 for neighbouring pairs and for values past `rot`. A warp takes
+// kUnroll x (32 lanes / lanes a row) heads of one token, all loads first, with the
+// products of weight and cosine or sine in registers for all of them.
+#pragma once
+#include "gdn_common.cuh"
+
+namespace gdn {
+
+constexpr unsigned kStatusBadPosition = 8u;  // a rotation position outside the table
+constexpr unsigned kStatusBadPage = 16u;     // a page number or token index outside the cache or table
+
+constexpr int kNormThreads = 256;
+constexpr int kNormUnroll = 4;
+
+// ---- four consecutive values of a row -----------------------------------------------
+__device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&f)[4]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  f[0] = __uint_as_float(v.x << 16);
+  f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+  f[2] = __uint_as_float(v.y << 16);
+  f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void load4(const __half* p, float (&f)[4]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+  f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+}
+__device__ __forceinline__ void store4(float* p, const float (&f)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&f)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void store4(__half* p, const float (&f)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]));
+}
+
+struct RopeParams {
+  const float* cos;
+  const float* sin;
+  int64_t stride;
+  int positions;
+  int rot;  // 0: no rotation
+};
+
+// A lane's part of a head row: its two runs of four values and its four pairs' angles.
+template <int D, bool kNext>
+struct HeadLane {
+  int a, b;  // first value of each run
+  int pair;  // index of the first of its four pairs
+  bool turned;
+  __device__ __forceinline__ HeadLane(int l, int rot) {
+    turned = 8 * l < rot;
+    pair = 4 * l;
+    a = (!kNext && turned) ? 4 * l : 8 * l;
+    b = (!kNext && turned) ? 4 * l + rot / 2 : 8 * l + 4;
+  }
+  // The angles of the lane's pairs at position `pos` (cos 1, sin 0 where not turned).
+  __device__ __forceinline__ void angles(const RopeParams& r, int64_t pos, float (&c)[4], float (&s)[4]) const {
+    if (turned) {
+      load4(r.cos + pos * r.stride + pair, c);
+      load4(r.sin + pos * r.stride + pair, s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = 1.f;
+        s[i] = 0.f;
+      }
+    }
+  }
+  // Regroups the two runs as pairs (u, v), and back.
+  __device__ __forceinline__ static void to_pairs(const float (&xa)[4], const float (&xb)[4], float (&u)[4],
+                                                  float (&v)[4]) {
+    if (kNext) {
+      u[0] = xa[0]; v[0] = xa[1]; u[1] = xa[2]; v[1] = xa[3];
+      u[2] = xb[0]; v[2] = xb[1]; u[3] = xb[2]; v[3] = xb[3];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        u[i] = xa[i];
+        v[i] = xb[i];
+      }
+    }
+  }
+  __device__ __forceinline__ static void from_pairs(const float (&u)[4], const float (&v)[4], float (&xa)[4],
+                                                    float (&xb)[4]) {
+    if (kNext) {
+      xa[0] = u[0]; xa[1] = v[0]; xa[2] = u[1]; xa[3] = v[1];
+      xb[0] = u[2]; xb[1] = v[2]; xb[2] = u[3]; xb[3] = v[3];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        xa[i] = u[i];
+        xb[i] = v[i];
+      }
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void load(const T* row, float (&u)[4], float (&v)[4]) const {
+    float xa[4], xb[4];
+    load4(row + a, xa);
+    load4(row + b, xb);
+    to_pairs(xa, xb, u, v);
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, const float (&u)[4], const float (&v)[4]) const {
+    float xa[4], xb[4];
+    from_pairs(u, v, xa, xb);
+    store4(row + a, xa);
+    store4(row + b, xb);
+  }
+  __device__ __forceinline__ void weights(const float* w, float (&u)[4], float (&v)[4]) const {
+    if (w) {
+      load(w, u, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = v[i] = 1.f;
+    }
+  }
+};
+
+// Sum over the LPH lanes that hold one head row.
+template <int LPH>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = LPH / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Norms (unless kNormed is off at run time) and rotates up to kNormUnroll x SLOTS heads of one
+// token row, from `src` to `dst` (head h at h * src_head, h * dst_head).
+template <typename T, int D, bool kNext>
+__device__ __forceinline__ void norm_rope_heads(const T* src, T* dst, int64_t src_head, int64_t dst_head, int h0,
+                                                int heads, const float* weight, bool normed, float eps,
+                                                const RopeParams& rope, int64_t pos) {
+  constexpr int LPH = D / 8, SLOTS = 32 / LPH;
+  const int lane = threadIdx.x & 31, l = lane % LPH, slot = lane / LPH;
+  const HeadLane<D, kNext> hl(l, rope.rot);
+  float u[kNormUnroll][4], v[kNormUnroll][4];
+#pragma unroll
+  for (int i = 0; i < kNormUnroll; ++i) {
+    const int h = h0 + i * SLOTS + slot;
+    if (h < heads) {
+      hl.load(src + h * src_head, u[i], v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[i][j] = v[i][j] = 0.f;
+    }
+  }
+  float c[4], s[4], wu[4], wv[4];
+  hl.angles(rope, pos, c, s);
+  hl.weights(weight, wu, wv);
+  float uc[4], us[4], vc[4], vs[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uc[j] = wu[j] * c[j];
+    us[j] = wu[j] * s[j];
+    vc[j] = wv[j] * c[j];
+    vs[j] = wv[j] * s[j];
+  }
+#pragma unroll
+  for (int i = 0; i < kNormUnroll; ++i) {
+    const int h = h0 + i * SLOTS + slot;
+    float r = 1.f;
+    if (normed) {  // the same for the whole warp
+      float q = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q = fmaf(u[i][j], u[i][j], fmaf(v[i][j], v[i][j], q));
+      r = rsqrtf(row_sum<LPH>(q) * (1.f / D) + eps);
+    }
+    float yu[4], yv[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      yu[j] = r * (u[i][j] * uc[j] - v[i][j] * vs[j]);
+      yv[j] = r * (v[i][j] * vc[j] + u[i][j] * us[j]);
+    }
+    if (h < heads) hl.store(dst + h * dst_head, yu, yv);
+  }
+}
+
+struct NormRopeParams {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  const void* q_grad;  // backward
+  const void* k_grad;
+  const int32_t* positions;
+  RopeParams rope;
+  const float* q_weight;
+  const float* k_weight;
+  float* partials;  // backward: [grid][2][D] sums of the weight gradients, or null
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride, q_grad_stride, k_grad_stride;
+  int rows, nq, nkv;
+  int q_chunks, chunks;  // warp items of a token: q_chunks for q's heads, the rest for k's
+  float eps;
+  unsigned* status;
+};
+
+// The position of a row, or -1 (and the status bit) where the table does not hold it.
+__device__ __forceinline__ int64_t row_position(const int32_t* positions, int row, const RopeParams& rope,
+                                                unsigned* status) {
+  if (rope.rot == 0) return 0;
+  const int pos = positions[row];
+  if (pos < 0 || pos >= rope.positions) {
+    if ((threadIdx.x & 31) == 0) atomicOr(status, kStatusBadPosition);
+    return -1;
+  }
+  return pos;
+}
+
+template <typename T, int D, bool kNext>
+__global__ void __launch_bounds__(kNormThreads) gdn_head_norm_rope_kernel(const NormRopeParams p) {
+  constexpr int PER = kNormUnroll * (32 / (D / 8));  // heads of an item
+  const unsigned item = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
+  const unsigned row = item / static_cast<unsigned>(p.chunks);
+  if (row >= static_cast<unsigned>(p.rows)) return;
+  const int ch = static_cast<int>(item - row * p.chunks);
+  const int64_t pos = row_position(p.positions, static_cast<int>(row), p.rope, p.status);
+  if (pos < 0) return;
+  if (ch < p.q_chunks)
+    norm_rope_heads<T, D, kNext>(static_cast<const T*>(p.q) + row * p.q_stride, static_cast<T*>(p.q_out) + row * p.q_out_stride,
+                                 D, D, ch * PER, p.nq, p.q_weight, true, p.eps, p.rope, pos);
+  else
+    norm_rope_heads<T, D, kNext>(static_cast<const T*>(p.k) + row * p.k_stride, static_cast<T*>(p.k_out) + row * p.k_out_stride,
+                                 D, D, (ch - p.q_chunks) * PER, p.nkv, p.k_weight, true, p.eps, p.rope, pos);
+}
+
+// ---- backward ------------------------------------------------------------------------
+constexpr int kNormBwdUnroll = 2;
+
+// dx of up to kNormBwdUnroll x SLOTS heads of one token row; adds dz x r to the lane's sums.
+template <typename T, int D, bool kNext>
+__device__ __forceinline__ void norm_rope_heads_bwd(const T* x, const T* dy, T* dx, int h0, int heads,
+                                                    const float* weight, float eps, const RopeParams& rope,
+                                                    int64_t pos, float (&du)[4], float (&dv)[4]) {
+  constexpr int LPH = D / 8, SLOTS = 32 / LPH;
+  const int lane = threadIdx.x & 31, l = lane % LPH, slot = lane / LPH;
+  const HeadLane<D, kNext> hl(l, rope.rot);
+  float u[kNormBwdUnroll][4], v[kNormBwdUnroll][4], gu[kNormBwdUnroll][4], gv[kNormBwdUnroll][4];
+#pragma unroll
+  for (int i = 0; i < kNormBwdUnroll; ++i) {
+    const int h = h0 + i * SLOTS + slot;
+    if (h < heads) {
+      hl.load(x + h * D, u[i], v[i]);
+      hl.load(dy + h * D, gu[i], gv[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[i][j] = v[i][j] = gu[i][j] = gv[i][j] = 0.f;
+    }
+  }
+  float c[4], s[4], wu[4], wv[4];
+  hl.angles(rope, pos, c, s);
+  hl.weights(weight, wu, wv);
+#pragma unroll
+  for (int i = 0; i < kNormBwdUnroll; ++i) {
+    const int h = h0 + i * SLOTS + slot;
+    float zu[4], zv[4], q = 0.f, m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      zu[j] = gu[i][j] * c[j] + gv[i][j] * s[j];
+      zv[j] = gv[i][j] * c[j] - gu[i][j] * s[j];
+      q = fmaf(u[i][j], u[i][j], fmaf(v[i][j], v[i][j], q));
+      m = fmaf(zu[j] * wu[j], u[i][j], fmaf(zv[j] * wv[j], v[i][j], m));
+    }
+    const float r = rsqrtf(row_sum<LPH>(q) * (1.f / D) + eps);
+    const float f = r * r * (row_sum<LPH>(m) * (1.f / D));
+    float xu[4], xv[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      du[j] = fmaf(zu[j], u[i][j] * r, du[j]);
+      dv[j] = fmaf(zv[j], v[i][j] * r, dv[j]);
+      xu[j] = r * (zu[j] * wu[j] - u[i][j] * f);
+      xv[j] = r * (zv[j] * wv[j] - v[i][j] * f);
+    }
+    if (h < heads) hl.store(dx + h * D, xu, xv);
+  }
+}
+
+// A fixed grid walks the items, so that the weight gradients' sums stay in registers; each
+// CTA adds its warps' sums in a fixed order and writes one row of partials for q and for k.
+template <typename T, int D, bool kNext>
+__global__ void __launch_bounds__(kNormThreads) gdn_head_norm_rope_bwd_kernel(const NormRopeParams p) {
+  constexpr int LPH = D / 8, SLOTS = 32 / LPH, PER = kNormBwdUnroll * SLOTS, WARPS = kNormThreads / 32;
+  __shared__ __align__(16) float s_sum[WARPS][2][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned items = static_cast<unsigned>(p.rows) * static_cast<unsigned>(p.chunks);
+  float qu[4] = {}, qv[4] = {}, ku[4] = {}, kv[4] = {};
+  for (unsigned item = blockIdx.x * WARPS + warp; item < items; item += gridDim.x * WARPS) {
+    const unsigned row = item / static_cast<unsigned>(p.chunks);
+    const int ch = static_cast<int>(item - row * p.chunks);
+    const int64_t pos = row_position(p.positions, static_cast<int>(row), p.rope, p.status);
+    if (pos < 0) continue;
+    if (ch < p.q_chunks)
+      norm_rope_heads_bwd<T, D, kNext>(static_cast<const T*>(p.q) + row * p.q_stride,
+                                       static_cast<const T*>(p.q_grad) + row * p.q_grad_stride,
+                                       static_cast<T*>(p.q_out) + row * p.q_out_stride, ch * PER, p.nq, p.q_weight,
+                                       p.eps, p.rope, pos, qu, qv);
+    else
+      norm_rope_heads_bwd<T, D, kNext>(static_cast<const T*>(p.k) + row * p.k_stride,
+                                       static_cast<const T*>(p.k_grad) + row * p.k_grad_stride,
+                                       static_cast<T*>(p.k_out) + row * p.k_out_stride, (ch - p.q_chunks) * PER, p.nkv,
+                                       p.k_weight, p.eps, p.rope, pos, ku, kv);
+  }
+  if (!p.partials) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // over the head rows that a warp holds side by side
+#pragma unroll
+    for (int o = LPH; o < 32; o <<= 1) {
+      qu[j] += __shfl_xor_sync(0xffffffffu, qu[j], o);
+      qv[j] += __shfl_xor_sync(0xffffffffu, qv[j], o);
+      ku[j] += __shfl_xor_sync(0xffffffffu, ku[j], o);
+      kv[j] += __shfl_xor_sync(0xffffffffu, kv[j], o);
+    }
+  }
+  if (lane < LPH) {
+    const HeadLane<D, kNext> hl(lane, p.rope.rot);
+    hl.store(&s_sum[warp][0][0], qu, qv);
+    hl.store(&s_sum[warp][1][0], ku, kv);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * D; i += kNormThreads) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) t += (&s_sum[w][0][0])[i];
+    p.partials[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = t;
+  }
+}
+
+// dw[i] = sum over the grid's partials, in a fixed order: one CTA for q's and one for k's
+// weights, D threads wide and 1024 / D partials at a time.
+template <int D>
+__global__ void __launch_bounds__(1024) gdn_norm_weight_sum_kernel(const float* partials, int n, float* dq_weight,
+                                                                  float* dk_weight) {
+  constexpr int LANES = 1024 / D;
+  __shared__ float s_part[LANES][D];
+  const int i = threadIdx.x % D, g = threadIdx.x / D;
+  float* dst = blockIdx.x == 0 ? dq_weight : dk_weight;
+  float t = 0.f;
+  if (dst)
+    for (int j = g; j < n; j += LANES) t += partials[static_cast<int64_t>(j) * 2 * D + blockIdx.x * D + i];
+  s_part[g][i] = t;
+  __syncthreads();
+  if (g == 0 && dst) {
+#pragma unroll
+    for (int j = 1; j < LANES; ++j) t += s_part[j][i];
+    dst[i] = t;
+  }
+}
+
+// ---- paged cache -----------------------------------------------------------------------
+struct PagedParams {
+  void* k;
+  void* v;
+  int64_t k_page, k_token, k_head;
+  int64_t v_page, v_token, v_head;
+  int num_pages, page_size;
+  const int32_t* block_table;
+  int64_t table_stride;
+  int max_pages;
+  int B, rows;
+  const int32_t* ctx_lens;
+  const int32_t* cu_rows;
+};
+
+// The sequence that owns a row: the last b with cu[b] <= row, by a 32-way search of the whole
+// warp (two steps for 1024 sequences). Any cu gives some b in [0, B).
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int row) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, at < n && cu[lo + (at < n ? at : 0)] <= row);
+    const int w = m ? 31 - __clz(m) : 0;
+    lo += w * step;
+    n = n - w * step < step ? n - w * step : step;
+  }
+  return lo;
+}
+
+struct AppendParams {
+  const void* k;
+  const void* v;
+  PagedParams cache;
+  const int32_t* positions;
+  RopeParams rope;
+  const float* k_weight;
+  int64_t k_stride, v_stride;
+  int nkv, chunks;  // warp items of a token: `chunks` for k's heads, as many for v's
+  int norm;
+  float eps;
+  unsigned* status;
+};
+
+template <typename T, int D, bool kNext>
+__global__ void __launch_bounds__(kNormThreads) gdn_paged_append_kernel(const AppendParams p) {
+  constexpr int LPH = D / 8, SLOTS = 32 / LPH, PER = kNormUnroll * SLOTS;
+  const unsigned per_row = 2u * static_cast<unsigned>(p.chunks);
+  const unsigned item = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
+  const unsigned row = item / per_row;
+  const PagedParams& c = p.cache;
+  if (row >= static_cast<unsigned>(c.rows)) return;
+  int ch = static_cast<int>(item - row * per_row);
+  const int lane = threadIdx.x & 31;
+  // the token's place in the cache
+  const int b = c.cu_rows ? find_sequence(c.cu_rows, c.B, static_cast<int>(row)) : static_cast<int>(row);
+  const int first = c.cu_rows ? c.cu_rows[b] : static_cast<int>(row);
+  const int end = c.cu_rows ? c.cu_rows[b + 1] : static_cast<int>(row) + 1;
+  const int ctx = c.ctx_lens[b];
+  if (first < 0 || first > static_cast<int>(row) || end <= static_cast<int>(row) || end > c.rows || ctx < 0) {
+    if (lane == 0) atomicOr(p.status, kStatusBadSeqlens);
+    return;
+  }
+  const int64_t token = static_cast<int64_t>(ctx) + (static_cast<int>(row) - first);
+  const int64_t at = token / c.page_size;
+  const int page = at < c.max_pages ? c.block_table[b * c.table_stride + at] : -1;
+  if (page < 0 || page >= c.num_pages) {
+    if (lane == 0) atomicOr(p.status, kStatusBadPage);
+    return;
+  }
+  const int64_t place = token - at * c.page_size;
+  if (ch < p.chunks) {
+    int64_t pos = 0;
+    if (p.rope.rot) {
+      pos = p.positions ? p.positions[row] : token;
+      if (pos < 0 || pos >= p.rope.positions) {
+        if (lane == 0) atomicOr(p.status, kStatusBadPosition);
+        return;
+      }
+    }
+    norm_rope_heads<T, D, kNext>(static_cast<const T*>(p.k) + row * p.k_stride,
+                                 static_cast<T*>(c.k) + page * c.k_page + place * c.k_token, D, c.k_head, ch * PER, p.nkv,
+                                 p.k_weight, p.norm != 0, p.eps, p.rope, pos);
+    return;
+  }
+  ch -= p.chunks;
+  if (p.rope.rot) {  // a token with a bad position is left out whole
+    const int64_t pos = p.positions ? p.positions[row] : token;
+    if (pos < 0 || pos >= p.rope.positions) return;
+  }
+  const int l = lane % LPH, slot = lane / LPH;
+  const T* src = static_cast<const T*>(p.v) + row * p.v_stride + 8 * l;
+  T* dst = static_cast<T*>(c.v) + page * c.v_page + place * c.v_token + 8 * l;
+  uint4 x[kNormUnroll];
+#pragma unroll
+  for (int i = 0; i < kNormUnroll; ++i) {
+    const int h = ch * PER + i * SLOTS + slot;
+    if (h < p.nkv) x[i] = *reinterpret_cast<const uint4*>(src + h * D);
+  }
+#pragma unroll
+  for (int i = 0; i < kNormUnroll; ++i) {
+    const int h = ch * PER + i * SLOTS + slot;
+    if (h < p.nkv) *reinterpret_cast<uint4*>(dst + h * c.v_head) = x[i];
+  }
+}
+
+}  // namespace gdn
