@@ -14,7 +14,7 @@ SRC = os.path.join(HERE, "csrc", "gdn_api.cu")
 DEPS = [os.path.join(HERE, "csrc", f) for f in ("gdn_api.cu", "gdn_common.cuh", "gdn_prefill_kernel.cuh", "gdn_decode_kernel.cuh",
                                                            "gdn_wy_kernel.cuh", "gdn_bwd_common.cuh", "gdn_bwd_dstates_tc.cuh", "gdn_bwd_grads_tc.cuh",
                                                            "tc.cuh", "gdn_norm_rope_kernel.cuh", "gdn_attn_common.cuh",
-                                                           "gdn_attn_kernel.cuh", "gdn_attn_api.cuh")] + [
+                                                           "gdn_attn_kernel.cuh", "gdn_attn_tc_kernel.cuh", "gdn_attn_api.cuh")] + [
     os.path.join(os.path.dirname(HERE), "include", f) for f in ("gdn_prefill.h", "gdn_attention.h")]
 OUT_DIR = os.path.join(HERE, "_lib")
 OUT = os.path.join(OUT_DIR, "libgdn_gb300.so")

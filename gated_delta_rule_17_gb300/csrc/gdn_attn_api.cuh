@@ -164,26 +164,36 @@ int check_paged(const gdn_paged_t* c, int nkv, int d, gdn::PagedParams* p) {
 }
 
 // ---- attention -----------------------------------------------------------------------
-constexpr int kAttnCtasPerSm = 2;
-constexpr int kAttnMaxRows = 32;  // query rows of the largest tile
+constexpr int kAttnCtasPerSm = 2;  // of gdn_attn_kernel; gdn_attn_tc_kernel has an SM to itself
+
+// The kernel for the rows that a kv head may have (new rows of a sequence x heads of a group).
+enum AttnKind { kAttn16, kAttn32, kAttnTc128, kAttnTc256 };
+constexpr int kAttnKindRows[] = {16, 32, gdn::kTcTile, 2 * gdn::kTcTile};
+AttnKind attn_kind(int64_t rows, float scale) {
+  if (rows <= 16) return kAttn16;
+  // the tensor-core kernel keeps its maxima in unscaled scores, which a scale <= 0 would turn round
+  if (rows <= 32 || !(scale > 0.f)) return kAttn32;
+  return rows <= gdn::kTcTile ? kAttnTc128 : kAttnTc256;
+}
+int attn_runs(AttnKind kind, int sms) { return kind < kAttnTc128 ? sms * kAttnCtasPerSm : sms; }
 
 struct AttnLayout {
-  size_t ml, o, cut, total;
+  size_t cut, ml, o, total;
 };
-AttnLayout attn_layout(int runs, int d) {
+AttnLayout attn_layout(AttnKind kind, int sms, int d) {
+  const size_t runs = attn_runs(kind, sms), rows = runs * 2 * kAttnKindRows[kind];
   AttnLayout l;
   l.cut = 0;
-  l.ml = align256(static_cast<size_t>(runs) * sizeof(int4));
-  l.o = l.ml + align256(static_cast<size_t>(runs) * 2 * kAttnMaxRows * 2 * sizeof(float));
-  l.total = l.o + align256(static_cast<size_t>(runs) * 2 * kAttnMaxRows * d * sizeof(float));
+  l.ml = align256(runs * sizeof(int4));
+  l.o = l.ml + align256(rows * 2 * sizeof(float));
+  l.total = l.o + align256(rows * d * sizeof(float));
   return l;
 }
 
-template <typename T, int D, int MB>
-cudaError_t launch_attn(gdn::AttnParams& p, cudaStream_t s) {
-  gdn::gdn_attn_kernel<T, D, MB><<<p.runs, gdn::kAttnThreads, gdn::AttnPlan<D, MB>::DYN_SMEM, s>>>(p);
+template <typename T, int D, int MT>
+cudaError_t launch_join(const gdn::AttnParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.runs), 16 * MB);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.runs), MT);
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute a[1];
@@ -191,7 +201,25 @@ cudaError_t launch_attn(gdn::AttnParams& p, cudaStream_t s) {
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gdn::gdn_attn_join_kernel<T, D, 16 * MB>, const_cast<const gdn::AttnParams&>(p));
+  return cudaLaunchKernelEx(&cfg, gdn::gdn_attn_join_kernel<T, D, MT>, p);
+}
+
+template <typename T, int D>
+cudaError_t launch_attn(AttnKind kind, const gdn::AttnParams& p, cudaStream_t s) {
+  if (kind == kAttn16) {
+    gdn::gdn_attn_kernel<T, D, 1><<<p.runs, gdn::kAttnThreads, gdn::AttnPlan<D, 1>::DYN_SMEM, s>>>(p);
+    return launch_join<T, D, 16>(p, s);
+  }
+  if (kind == kAttn32) {
+    gdn::gdn_attn_kernel<T, D, 2><<<p.runs, gdn::kAttnThreads, gdn::AttnPlan<D, 2>::DYN_SMEM, s>>>(p);
+    return launch_join<T, D, 32>(p, s);
+  }
+  if (kind == kAttnTc128) {
+    gdn::gdn_attn_tc_kernel<T, D, true><<<p.runs, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s>>>(p);
+    return launch_join<T, D, gdn::kTcTile>(p, s);
+  }
+  gdn::gdn_attn_tc_kernel<T, D, false><<<p.runs, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s>>>(p);
+  return launch_join<T, D, 2 * gdn::kTcTile>(p, s);
 }
 
 }  // namespace
@@ -344,7 +372,12 @@ int gdn_paged_append(const void* k, const void* v, const gdn_paged_t* cache, con
 
 size_t gdn_tree_attention_workspace_bytes(int nq, int nkv, int d) {
   if (nq <= 0 || nkv <= 0 || (d != 64 && d != 128)) return 0;
-  return attn_layout(plan_sms() * kAttnCtasPerSm, d).total;
+  size_t most = 0;
+  for (AttnKind kind : {kAttn16, kAttn32, kAttnTc128, kAttnTc256}) {
+    const size_t n = attn_layout(kind, plan_sms(), d).total;
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 int gdn_tree_attention(const void* q, const gdn_paged_t* cache, const uint64_t* mask, int mask_words, float scale,
@@ -394,19 +427,16 @@ int gdn_tree_attention(const void* q, const gdn_paged_t* cache, const uint64_t* 
   p.group = nq / nkv;
   p.scale_log2 = scale * 1.4426950408889634f;  // log2 e
   p.status = dev->status;
-  p.runs = dev->sms * kAttnCtasPerSm;
-  const AttnLayout l = attn_layout(p.runs, d);
+  const int most = !cache->cu_rows ? 1 : (max_rows && max_rows < cache->rows ? max_rows : cache->rows);
+  const AttnKind kind = attn_kind(static_cast<int64_t>(most) * p.group, scale);
+  p.runs = attn_runs(kind, dev->sms);
+  const AttnLayout l = attn_layout(kind, dev->sms, d);
   p.cut = reinterpret_cast<int4*>(static_cast<char*>(ws) + l.cut);
   p.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + l.ml);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + l.o);
-  // rows of a kv head, by the caller's bound: one block of 16 where they fit, else two
-  const int most = !cache->cu_rows ? 1 : (max_rows && max_rows < cache->rows ? max_rows : cache->rows);
-  const bool small = static_cast<int64_t>(most) * p.group <= 16;
   cudaError_t e = cudaSuccess;
   by_type16(dtype, [&](auto t) {
-    using T = decltype(t);
-    if (d == 64) e = small ? launch_attn<T, 64, 1>(p, s) : launch_attn<T, 64, 2>(p, s);
-    else e = small ? launch_attn<T, 128, 1>(p, s) : launch_attn<T, 128, 2>(p, s);
+    e = d == 64 ? launch_attn<decltype(t), 64>(kind, p, s) : launch_attn<decltype(t), 128>(kind, p, s);
   });
   int rc = e != cudaSuccess ? fail(GDN_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e)) : launched(2);
   if (!workspace) {

@@ -146,6 +146,38 @@ __device__ __forceinline__ AttnStart attn_start(const AttnParams& p, int run, in
   return *s_start;
 }
 
+// Walks a run: the unit pieces in their order. Every thread of a role walks by itself.
+template <int MT, int KT>
+struct AttnWalk {
+  int b;
+  int64_t within, left;
+  AttnSeq s;      // the sequence
+  int unit;       // kv head and row tile
+  int kvh, qt;
+  int t0, t1;     // token tiles of the piece
+  __device__ __forceinline__ explicit AttnWalk(const AttnStart& st) : b(st.b), within(st.within), left(st.count) {}
+  __device__ __forceinline__ bool next(const AttnParams& p) {
+    while (left > 0) {
+      s = attn_seq<MT, KT>(p, b, false);
+      const int64_t cost = attn_cost(p, s);
+      if (within >= cost) {
+        within -= cost;
+        ++b;
+        continue;
+      }
+      unit = static_cast<int>(within / s.tiles);
+      t0 = static_cast<int>(within - static_cast<int64_t>(unit) * s.tiles);
+      t1 = left < s.tiles - t0 ? t0 + static_cast<int>(left) : s.tiles;
+      kvh = unit / s.qtiles;
+      qt = unit - kvh * s.qtiles;
+      within += t1 - t0;
+      left -= t1 - t0;
+      return true;
+    }
+    return false;
+  }
+};
+
 // ---- 16-bit element types ---------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);

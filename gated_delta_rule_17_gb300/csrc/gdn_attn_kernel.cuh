@@ -102,22 +102,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
   const PagedParams& c = p.cache;
   const int run = blockIdx.x;
 
-  AttnStart st = attn_start<MT, kAttnTile, kAttnThreads>(p, run, s_scan, &s_start);
+  const AttnStart st = attn_start<MT, kAttnTile, kAttnThreads>(p, run, s_scan, &s_start);
   if (threadIdx.x == 0) p.cut[run] = make_int4(0, 0, 0, -1);
-  int64_t left = st.count;
-  int b = st.b;
-  int64_t within = st.within;
-  while (left > 0) {
-    const AttnSeq s = attn_seq<MT, kAttnTile>(p, b, false);
-    const int64_t cost = attn_cost(p, s);
-    if (within >= cost) {
-      within -= cost;
-      ++b;
-      continue;
-    }
-    const int unit = static_cast<int>(within / s.tiles), t0 = static_cast<int>(within - static_cast<int64_t>(unit) * s.tiles);
-    const int kvh = unit / s.qtiles, qt = unit - kvh * s.qtiles;
-    const int t1 = left < s.tiles - t0 ? t0 + static_cast<int>(left) : s.tiles;
+  AttnWalk<MT, kAttnTile> w(st);
+  while (w.next(p)) {
+    const AttnSeq& s = w.s;
+    const int b = w.b, unit = w.unit, kvh = w.kvh, qt = w.qt, t0 = w.t0, t1 = w.t1;
     const int R = s.n * p.group;
     const int32_t* table = c.block_table + b * c.table_stride;
 
@@ -324,8 +314,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
       }
     }
     __syncthreads();  // the join buffer is done with
-    within += t1 - t0;
-    left -= t1 - t0;
     if (t0 == 0 && t1 < s.tiles && threadIdx.x == 0) 
       p.cut[run] = make_int4(s.first, s.n, unit, run_of(st.end + (s.tiles - t1) - 1, st.total, st.runs));
   }
