@@ -175,6 +175,9 @@ AttnKind attn_kind(int64_t rows, float scale) {
   if (rows <= 32 || !(scale > 0.f)) return kAttn32;
   return rows <= gdn::kTcTile ? kAttnTc128 : kAttnTc256;
 }
+// A block table with room for at most this many tokens a sequence is not split over the CTAs: a
+// unit of them costs less than the join that a split needs.
+constexpr int64_t kAttnWholeTokens = 512;
 int attn_runs(AttnKind kind, int sms) { return kind < kAttnTc128 ? sms * kAttnCtasPerSm : sms; }
 
 struct AttnLayout {
@@ -190,11 +193,37 @@ AttnLayout attn_layout(AttnKind kind, int sms, int d) {
   return l;
 }
 
+// Tokens of a TMA box: the largest power of two that divides the page size, from 8 (the rows of a
+// swizzle atom) to the 32 of a copying warp; 0 where there is none.
+int attn_box(int page_size) {
+  int box = page_size & -page_size;
+  if (box > 32) box = 32;
+  return box >= 8 ? box : 0;
+}
+
+// A cache as [pages][page_size][heads][d] with boxes of 64 values, one head, `box` tokens.
+bool cache_map(CUtensorMap* m, const void* base, int64_t page, int64_t token, int64_t head, const gdn::PagedParams& c,
+               int nkv, int d, int box, int dtype) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  // a dimension of one takes any stride; the encoder wants one that is not zero
+  auto bytes = [&](int64_t stride, int64_t n) { return static_cast<cuuint64_t>(n > 1 ? stride : d) * 2; };
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(nkv), static_cast<cuuint64_t>(c.page_size),
+                        static_cast<cuuint64_t>(c.num_pages)};
+  cuuint64_t strides[3] = {bytes(head, nkv), bytes(token, c.page_size), bytes(page, c.num_pages)};
+  cuuint32_t boxes[4] = {64, 1, static_cast<cuuint32_t>(box), 1}, estr[4] = {1, 1, 1, 1};
+  return fn(m, dtype == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+            const_cast<void*>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int D, int MT>
 cudaError_t launch_join(const gdn::AttnParams& p, cudaStream_t s) {
+  if (p.whole) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.runs), MT);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.runs), MT / gdn::kJoinWarps);
+  cfg.blockDim = dim3(32 * gdn::kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -205,7 +234,7 @@ cudaError_t launch_join(const gdn::AttnParams& p, cudaStream_t s) {
 }
 
 template <typename T, int D>
-cudaError_t launch_attn(AttnKind kind, const gdn::AttnParams& p, cudaStream_t s) {
+cudaError_t launch_attn(AttnKind kind, const gdn::AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
   if (kind == kAttn16) {
     gdn::gdn_attn_kernel<T, D, 1><<<p.runs, gdn::kAttnThreads, gdn::AttnPlan<D, 1>::DYN_SMEM, s>>>(p);
     return launch_join<T, D, 16>(p, s);
@@ -215,10 +244,10 @@ cudaError_t launch_attn(AttnKind kind, const gdn::AttnParams& p, cudaStream_t s)
     return launch_join<T, D, 32>(p, s);
   }
   if (kind == kAttnTc128) {
-    gdn::gdn_attn_tc_kernel<T, D, true><<<p.runs, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s>>>(p);
+    gdn::gdn_attn_tc_kernel<T, D, true><<<p.runs, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s>>>(k, v, p);
     return launch_join<T, D, gdn::kTcTile>(p, s);
   }
-  gdn::gdn_attn_tc_kernel<T, D, false><<<p.runs, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s>>>(p);
+  gdn::gdn_attn_tc_kernel<T, D, false><<<p.runs, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s>>>(k, v, p);
   return launch_join<T, D, 2 * gdn::kTcTile>(p, s);
 }
 
@@ -430,15 +459,25 @@ int gdn_tree_attention(const void* q, const gdn_paged_t* cache, const uint64_t* 
   const int most = !cache->cu_rows ? 1 : (max_rows && max_rows < cache->rows ? max_rows : cache->rows);
   const AttnKind kind = attn_kind(static_cast<int64_t>(most) * p.group, scale);
   p.runs = attn_runs(kind, dev->sms);
+  p.whole = static_cast<int64_t>(cache->max_pages) * cache->page_size <= kAttnWholeTokens;
+  CUtensorMap maps[2] = {};
+  if (kind >= kAttnTc128) {
+    // strides that TMA cannot take (or no pages at all) leave the copies to the threads
+    p.box = cache->num_pages > 0 ? attn_box(cache->page_size) : 0;
+    if (p.box && (!cache_map(&maps[0], cache->k, cache->k_page, cache->k_token, cache->k_head, p.cache, nkv, d, p.box, dtype) ||
+                  !cache_map(&maps[1], cache->v, cache->v_page, cache->v_token, cache->v_head, p.cache, nkv, d, p.box, dtype)))
+      p.box = 0;
+  }
   const AttnLayout l = attn_layout(kind, dev->sms, d);
   p.cut = reinterpret_cast<int4*>(static_cast<char*>(ws) + l.cut);
   p.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + l.ml);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + l.o);
   cudaError_t e = cudaSuccess;
   by_type16(dtype, [&](auto t) {
-    e = d == 64 ? launch_attn<decltype(t), 64>(kind, p, s) : launch_attn<decltype(t), 128>(kind, p, s);
+    e = d == 64 ? launch_attn<decltype(t), 64>(kind, p, maps[0], maps[1], s)
+                : launch_attn<decltype(t), 128>(kind, p, maps[0], maps[1], s);
   });
-  int rc = e != cudaSuccess ? fail(GDN_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e)) : launched(2);
+  int rc = e != cudaSuccess ? fail(GDN_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e)) : launched(p.whole ? 1 : 2);
   if (!workspace) {
     e = cudaFreeAsync(ws, s);
     if (e != cudaSuccess && rc == GDN_OK) rc = fail(GDN_ERR_CUDA, "cudaFreeAsync: %s", cudaGetErrorString(e));

@@ -13,7 +13,8 @@
 //
 // (x in units of log2 e), and gdn_attn_join_kernel adds the pieces up in their order,
 // with weights 2^(m_piece - max m). A run has at most two cut units, its first (slot 0)
-// and its last (slot 1), so the workspace does not grow with the batch.
+// and its last (slot 1), so the workspace does not grow with the batch. Where the block table
+// has room for few tokens only, the runs are cut at units and the join falls away.
 #pragma once
 #include "gdn_norm_rope_kernel.cuh"
 
@@ -29,6 +30,8 @@ struct AttnParams {
   float scale_log2;  // scale * log2 e
   int64_t q_stride, out_stride;
   int runs;        // CTAs of the attention kernel
+  int box;         // tokens of a TMA box inside a page, 0: pages do not hold whole boxes
+  int whole;       // runs are cut at units only: nothing to join
   float* part_ml;  // [runs][2][MT][2]: m and l
   float* part_o;   // [runs][2][MT][D]
   int4* cut;       // [runs]: the unit that begins in the run and is cut: first row, rows, kv head and row tile, last run (-1: none)
@@ -67,8 +70,9 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b, bool rep
   return s;
 }
 
+// What the runs count: token tiles, or units.
 __device__ __forceinline__ int64_t attn_cost(const AttnParams& p, const AttnSeq& s) {
-  return static_cast<int64_t>(s.tiles) * s.qtiles * p.nkv;
+  return static_cast<int64_t>(p.whole ? 1 : s.tiles) * s.qtiles * p.nkv;
 }
 
 // Inclusive prefix of `x` over the block's threads; *total is the sum. s_scan: a word a warp.
@@ -165,13 +169,21 @@ struct AttnWalk {
         ++b;
         continue;
       }
-      unit = static_cast<int>(within / s.tiles);
-      t0 = static_cast<int>(within - static_cast<int64_t>(unit) * s.tiles);
-      t1 = left < s.tiles - t0 ? t0 + static_cast<int>(left) : s.tiles;
+      if (p.whole) {
+        unit = static_cast<int>(within);
+        t0 = 0;
+        t1 = s.tiles;
+        ++within;
+        --left;
+      } else {
+        unit = static_cast<int>(within / s.tiles);
+        t0 = static_cast<int>(within - static_cast<int64_t>(unit) * s.tiles);
+        t1 = left < s.tiles - t0 ? t0 + static_cast<int>(left) : s.tiles;
+        within += t1 - t0;
+        left -= t1 - t0;
+      }
       kvh = unit / s.qtiles;
       qt = unit - kvh * s.qtiles;
-      within += t1 - t0;
-      left -= t1 - t0;
       return true;
     }
     return false;

@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
   const int run = blockIdx.x;
 
   const AttnStart st = attn_start<MT, kAttnTile, kAttnThreads>(p, run, s_scan, &s_start);
-  if (threadIdx.x == 0) p.cut[run] = make_int4(0, 0, 0, -1);
+  tc::allow_dependent_launch();  // the join waits for this grid's end before it reads anything
+  if (threadIdx.x == 0 && !p.whole) p.cut[run] = make_int4(0, 0, 0, -1);
   AttnWalk<MT, kAttnTile> w(st);
   while (w.next(p)) {
     const AttnSeq& s = w.s;
@@ -319,62 +320,63 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
   }
 }
 
-// Joins the pieces of the unit that begins in run blockIdx.x and goes on in the next runs: one
-// CTA a row, every warp a fourth of the pieces.
+// Joins the pieces of the unit that begins in run blockIdx.x and goes on in the next runs: a warp a
+// row, kJoinWarps rows a CTA, several pieces' loads in flight.
+constexpr int kJoinWarps = 8;
 template <typename T, int D, int MT>
-__global__ void __launch_bounds__(128) gdn_attn_join_kernel(const AttnParams p) {
-  constexpr int WARPS = 4;
-  __shared__ float s_m[WARPS], s_l[WARPS];
-  __shared__ __align__(16) float s_o[WARPS][D];
+__global__ void __launch_bounds__(32 * kJoinWarps) gdn_attn_join_kernel(const AttnParams p) {
   tc::grid_dependency_wait();
-  const int run = blockIdx.x, r = blockIdx.y;
+  const int run = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + warp;
   const int4 cut = p.cut[run];
   if (cut.w < 0) return;
   const int unit_qtiles = (cut.y * p.group + MT - 1) / MT;
   const int kvh = cut.z / unit_qtiles, qt = cut.z - kvh * unit_qtiles, row = qt * MT + r;
   if (row >= cut.y * p.group) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int last = cut.w;  // the run with the unit's last tile
-  constexpr int V = D / 32;
+  constexpr int V = D / 32, U = 8;  // values of a lane, pieces in flight
   float m = -INFINITY, l = 0.f, o[V] = {};
-  for (int i = run + warp; i <= last; i += WARPS) {
-    const int64_t at = (static_cast<int64_t>(i) * 2 + (i == run ? 1 : 0)) * MT + r;
-    const float pm = p.part_ml[at * 2], pl = p.part_ml[at * 2 + 1];
-    float v[V];
+  for (int i0 = run; i0 <= cut.w; i0 += U) {
+    float pm[U], pl[U], v[U][V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = p.part_o[at * D + j * 32 + lane];
-    const float mn = fmaxf(m, pm), base = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2_approx(m - base), g = exp2_approx(pm - base);
-    m = mn;
-    l = l * f + pl * g;
+    for (int u = 0; u < U; ++u) {
+      pm[u] = -INFINITY;
+      pl[u] = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = o[j] * f + v[j] * g;
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
+      for (int j = 0; j < V; ++j) v[u][j] = 0.f;
+      if (i0 + u <= cut.w) {
+        const int64_t at = (static_cast<int64_t>(i0 + u) * 2 + (i0 + u == run ? 1 : 0)) * MT + r;
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+        pm[u] = ml.x;
+        pl[u] = ml.y;
 #pragma unroll
-  for (int j = 0; j < V; ++j) s_o[warp][j * 32 + lane] = o[j];
-  __syncthreads();
-  if (threadIdx.x < D / 2) {
-    float mm = -INFINITY, ll = 0.f, a = 0.f, c = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, s_m[w]);
-    const float base = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float f = exp2_approx(s_m[w] - base);
-      ll = fmaf(f, s_l[w], ll);
-      a = fmaf(f, s_o[w][2 * threadIdx.x], a);
-      c = fmaf(f, s_o[w][2 * threadIdx.x + 1], c);
+        for (int j = 0; j < V; j += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(p.part_o + at * D + V * lane + j);
+          v[u][j] = x.x;
+          v[u][j + 1] = x.y;
+        }
+      }
     }
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
-    const int i = row / p.group, g = row - i * p.group;
-    T* dst = static_cast<T*>(p.out) + (static_cast<int64_t>(cut.x) + i) * p.out_stride +
-             static_cast<int64_t>(kvh * p.group + g) * D;
-    reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = pack2<T>(a * inv, c * inv);
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = fmaxf(mn, pm[u]);
+    const float base = mn == -INFINITY ? 0.f : mn, f = exp2_approx(m - base);
+    m = mn;
+    l *= f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] *= f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float g = exp2_approx(pm[u] - base);
+      l = fmaf(pl[u], g, l);
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] = fmaf(v[u][j], g, o[j]);
+    }
   }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int i = row / p.group, g = row - i * p.group;
+  T* dst = static_cast<T*>(p.out) + (static_cast<int64_t>(cut.x) + i) * p.out_stride +
+           static_cast<int64_t>(kvh * p.group + g) * D + V * lane;
+#pragma unroll
+  for (int j = 0; j < V; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack2<T>(o[j] * inv, o[j + 1] * inv);
 }
 
 }  // namespace gdn

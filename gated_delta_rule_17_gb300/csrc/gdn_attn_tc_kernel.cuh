@@ -19,8 +19,9 @@
 // costs no precision in fp32 and 16-bit floats (their relative error does not depend on the size;
 // 2^8 is far inside fp16's range), and most tiles skip the round trip through the registers.
 //
-// Roles: warps 0-3 and 4-7 one stream each; warps 8-11 copy K and V tiles (16-byte cp.async, any
-// page size, 128-byte-swizzled rows) through a ring of STAGES tiles; a thread of warp 12 issues the
+// Roles: warps 0-3 and 4-7 one stream each; warps 8-11 copy K and V tiles (TMA boxes
+// inside the pages, or 16-byte cp.async for any page size; 128-byte-swizzled rows) through a ring of
+// STAGES tiles; a thread of warp 12 issues the
 // products. The hand-offs are mbarriers; every wait is bounded, and when one expires the status
 // word says so and all roles run out.
 #pragma once
@@ -100,7 +101,9 @@ struct TcShared {
 };
 
 template <typename T, int D, bool kSplit>
-__global__ void __launch_bounds__(kTcThreads, 1) gdn_attn_tc_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kTcThreads, 1)
+gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                   const AttnParams p) {
   using Plan = AttnTcPlan<D>;
   constexpr int MT = kSplit ? kTcTile : 2 * kTcTile, TILE = Plan::TILE, NS = Plan::STAGES, LAG = Plan::LAG;
   extern __shared__ uint8_t dyn[];
@@ -131,12 +134,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdn_attn_tc_kernel(const AttnPa
     tc::mbar_init(sh.bar(Plan::X_FULL), 128);
     tc::mbar_init(sh.bar(Plan::X_FREE), 128);
     tc::mbar_fence_init();
-    p.cut[run] = make_int4(0, 0, 0, -1);
+    if (!p.whole) p.cut[run] = make_int4(0, 0, 0, -1);
   }
   if (warp == 12) tc::tmem_alloc(tc::smem_u32(&s_tmem), Plan::TMEM_COLS);
   tc::fence_before_sync();
   const AttnStart st = attn_start<MT, kTcTile, kTcThreads>(p, run, s_scan, &s_start);
   tc::fence_after_sync();
+  tc::allow_dependent_launch();  // the join waits for this grid's end before it reads anything
   const uint32_t tmem = s_tmem;
   AttnWalk<MT, kTcTile> w(st);
 
@@ -338,18 +342,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdn_attn_tc_kernel(const AttnPa
   } else if (warp < 12) {
     // ---- copies of K and V -----------------------------------------------------------------
     constexpr int CH = D / 8, ROWS = 32 / CH;
+    // A warp copies 32 tokens of every tile. Where a page holds whole boxes of p.box tokens and all
+    // 32 tokens are there, a lane a box starts a TMA copy; else the warp copies by 16 bytes, with
+    // zeros for the tokens that are not there.
     const int lw = warp - 8;
-    int n = 0;  // tiles issued
+    int n = 0;       // tiles issued
+    int landed = 0;  // tiles whose arrival is made; those of TMA copies are made at once
     bool ok = true;
+    auto land = [&](int upto) {
+      tc::fence_proxy_async();
+      for (; landed < upto; ++landed) tc::mbar_arrive(sh.bar(Plan::FULL + landed % NS));
+    };
     while (ok && w.next(p)) {
       const int32_t* table = c.block_table + w.b * c.table_stride;
       const T* kbase = static_cast<const T*>(c.k) + w.kvh * c.k_head;
       const T* vbase = static_cast<const T*>(c.v) + w.kvh * c.v_head;
-      auto load = [&](const T* base, int64_t page_stride, int64_t token_stride, const TokenPlace& place) {
+      auto load = [&](const CUtensorMap* map, const T* base, int64_t page_stride, int64_t token_stride, const TokenPlace& place) {
         const int slot = n % NS;
         if (n >= NS) ok = sh.wait_warp(Plan::FREE + slot, ((n / NS) - 1) & 1);
         if (!ok) return;
         const uint32_t dst = sbase + Plan::RING + slot * TILE;
+        if (p.box && __all_sync(0xffffffffu, place.page >= 0)) {
+          if (landed < n) {
+            tc::cp_async_wait_all();
+            land(n);
+          }
+          const uint32_t bar = sh.bar(Plan::FULL + slot);
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar, 32 * D * 2);
+          else tc::mbar_arrive(bar);
+          __syncwarp();
+          constexpr int HALVES = D / 64;
+          const int box = lane / HALVES, half = lane % HALVES, first = box * p.box & 31;
+          const int page = __shfl_sync(0xffffffffu, place.page, first), at = __shfl_sync(0xffffffffu, place.place, first);
+          if (box * p.box < 32)
+            tc::tma_load_4d(dst + half * (kTcTile * 128) + (lw * 32 + first) * 128, map, 64 * half, w.kvh, at, page, bar);
+          ++n;
+          ++landed;
+          return;
+        }
 #pragma unroll 4
         for (int j = 0; j < 32 / ROWS; ++j) {
           const int r = j * ROWS + lane / CH, ch = lane % CH;
@@ -359,25 +389,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdn_attn_tc_kernel(const AttnPa
                       base + (real ? page : 0) * page_stride + at * token_stride + 8 * ch, real);
         }
         tc::cp_async_commit();
-        if (n >= LAG) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
-          tc::fence_proxy_async();
-          tc::mbar_arrive(sh.bar(Plan::FULL + (n - LAG) % NS));
-        }
         ++n;
+        if (n - landed > LAG) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
+          land(n - LAG);
+        }
       };
       TokenPlace next = token_place(p, table, w.t0 * kTcTile + lw * 32 + lane, w.s.len), prev = next;
       for (int t = w.t0; t <= w.t1 && ok; ++t) {
         const TokenPlace cur = next;
         next = token_place(p, table, (t + 1) * kTcTile + lw * 32 + lane, t + 1 < w.t1 ? w.s.len : 0);
-        if (t < w.t1) load(kbase, c.k_page, c.k_token, cur);
-        if (t > w.t0 && ok) load(vbase, c.v_page, c.v_token, prev);
+        if (t < w.t1) load(&k_map, kbase, c.k_page, c.k_token, cur);
+        if (t > w.t0 && ok) load(&v_map, vbase, c.v_page, c.v_token, prev);
         prev = cur;
       }
     }
     tc::cp_async_wait_all();
-    tc::fence_proxy_async();
-    for (int i = n > LAG ? n - LAG : 0; ok && i < n; ++i) tc::mbar_arrive(sh.bar(Plan::FULL + i % NS));
+    if (ok) land(n);
   } else if (lane == 0) {
     // ---- products --------------------------------------------------------------------------
     constexpr uint32_t fmt = std::is_same<T, __half>::value ? tc::kF16 : tc::kBF16;
