@@ -406,8 +406,11 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     }
     tc::cp_async_wait_all();
     if (ok) land(n);
-  } else if (lane == 0) {
+  } else {
     // ---- products --------------------------------------------------------------------------
+    // The whole warp walks and waits, and one elected thread issues: the descriptors then stay in
+    // uniform registers. (With a lane-0 branch around it all, an MMA took 160 cycles to issue,
+    // 2.5 times its own 64.)
     constexpr uint32_t fmt = std::is_same<T, __half>::value ? tc::kF16 : tc::kBF16;
     constexpr uint32_t id_s = tc::idesc_f16(128, kTcTile, fmt, false, false), id_o = tc::idesc_f16(128, D, fmt, false, true);
     int base = 0;
@@ -416,41 +419,48 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     while (ok && w.next(p)) {
       const int n = w.t1 - w.t0;
       const int streams = kSplit ? 2 : (w.qt * MT + kTcTile < w.s.n * p.group ? 2 : 1);
-      ok = sh.wait(Plan::Q_FULL, q_ph);
+      ok = sh.wait_warp(Plan::Q_FULL, q_ph);
       q_ph ^= 1;
       // tiles are loaded in the order K0, K1, V0, K2, V1, ..., V(n-1)
       auto scores = [&](int x, int j) {
         if (!ok) return;
         const int at = base + (j == 0 ? 0 : 2 * j - 1), slot = at % NS;
-        ok = sh.wait(Plan::FULL + slot, (at / NS) & 1);
+        ok = sh.wait_warp(Plan::FULL + slot, (at / NS) & 1);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t a = sbase + Plan::Q + (kSplit ? 0 : x * TILE), b = sbase + Plan::RING + slot * TILE;
+        const uint64_t a = tc::desc_sw128(sbase + Plan::Q + (kSplit ? 0 : x * TILE), 16, 1024);
+        const uint64_t b = tc::desc_sw128(sbase + Plan::RING + slot * TILE, 16, 1024);
+        const uint32_t d = tmem + Plan::COL_S + x * kTcTile;
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * (kTcTile * 128) + (k & 3) * 32;
-          tc::mma_f16(tmem + Plan::COL_S + x * kTcTile, tc::desc_sw128(a + off, 16, 1024), tc::desc_sw128(b + off, 16, 1024), id_s, k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * (kTcTile * 128) + (k & 3) * 32) >> 4;
+            tc::mma_f16(d, a + off, b + off, id_s, k > 0);
+          }
+          tc::mma_commit(sh.bar(Plan::S_FULL + x));
+          if (kSplit || x == streams - 1) tc::mma_commit(sh.bar(Plan::FREE + slot));
         }
-        tc::mma_commit(sh.bar(Plan::S_FULL + x));
-        if (kSplit || x == streams - 1) tc::mma_commit(sh.bar(Plan::FREE + slot));
+        __syncwarp();
       };
       auto values = [&](int x, int j) {
         if (!ok) return;
         const int at = base + (j == n - 1 ? 2 * n - 1 : 2 * j + 2), slot = at % NS;
-        ok = sh.wait(Plan::P_FULL + x, (p_ph >> x) & 1) && sh.wait(Plan::FULL + slot, (at / NS) & 1);
+        ok = sh.wait_warp(Plan::FULL + slot, (at / NS) & 1) && sh.wait_warp(Plan::P_FULL + x, (p_ph >> x) & 1);
         p_ph ^= 1u << x;
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t b = sbase + Plan::RING + slot * TILE;
+        const uint64_t b = tc::desc_sw128(sbase + Plan::RING + slot * TILE, kTcTile * 128, 1024);
+        const uint32_t d = tmem + Plan::COL_O + x * D, a = tmem + Plan::COL_S + x * kTcTile;
         const bool first = kSplit ? j < 2 : j == 0;
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kTcTile / 16; ++k)
-          tc::mma_f16_ts(tmem + Plan::COL_O + x * D, tmem + Plan::COL_S + x * kTcTile + 8 * k,
-                         tc::desc_sw128(b + k * 2048, kTcTile * 128, 1024), id_o, !first || k > 0);
-        if (kSplit || x == streams - 1) tc::mma_commit(sh.bar(Plan::FREE + slot));
-        if (kSplit ? j + 2 >= n : j == n - 1) tc::mma_commit(sh.bar(Plan::O_FULL + x));
-        // a stream without tiles is told too: it must not run ahead into the next unit's Q
-        if (kSplit ? n == 1 : streams == 1 && j == n - 1) tc::mma_commit(sh.bar(Plan::O_FULL + 1));
+          for (int k = 0; k < kTcTile / 16; ++k) tc::mma_f16_ts(d, a + 8 * k, b + ((k * 2048) >> 4), id_o, !first || k > 0);
+          if (kSplit || x == streams - 1) tc::mma_commit(sh.bar(Plan::FREE + slot));
+          if (kSplit ? j + 2 >= n : j == n - 1) tc::mma_commit(sh.bar(Plan::O_FULL + x));
+          // a stream without tiles is told too: it must not run ahead into the next unit's Q
+          if (kSplit ? n == 1 : streams == 1 && j == n - 1) tc::mma_commit(sh.bar(Plan::O_FULL + 1));
+        }
+        __syncwarp();
       };
       if (kSplit) {
         scores(0, 0);
