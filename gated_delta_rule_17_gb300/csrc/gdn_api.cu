@@ -112,14 +112,10 @@ int device_info(DeviceInfo** out) {
         {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 64, 2>), gdn::AttnPlan<64, 2>::DYN_SMEM},
         {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 128, 1>), gdn::AttnPlan<128, 1>::DYN_SMEM},
         {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 128, 2>), gdn::AttnPlan<128, 2>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__nv_bfloat16, 64, true>), gdn::AttnTcPlan<64>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__nv_bfloat16, 64, false>), gdn::AttnTcPlan<64>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__nv_bfloat16, 128, true>), gdn::AttnTcPlan<128>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__nv_bfloat16, 128, false>), gdn::AttnTcPlan<128>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__half, 64, true>), gdn::AttnTcPlan<64>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__half, 64, false>), gdn::AttnTcPlan<64>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__half, 128, true>), gdn::AttnTcPlan<128>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__half, 128, false>), gdn::AttnTcPlan<128>::DYN_SMEM}};
+        {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__nv_bfloat16, 64>), gdn::AttnTcPlan<64>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__nv_bfloat16, 128>), gdn::AttnTcPlan<128>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__half, 64>), gdn::AttnTcPlan<64>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__half, 128>), gdn::AttnTcPlan<128>::DYN_SMEM}};
     for (const auto& f : bwd) {
       e = cudaFuncSetAttribute(f.first, cudaFuncAttributeMaxDynamicSharedMemorySize, f.second);
       if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));

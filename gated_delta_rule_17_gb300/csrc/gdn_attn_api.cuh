@@ -167,18 +167,17 @@ int check_paged(const gdn_paged_t* c, int nkv, int d, gdn::PagedParams* p) {
 constexpr int kAttnCtasPerSm = 2;  // of gdn_attn_kernel; gdn_attn_tc_kernel has an SM to itself
 
 // The kernel for the rows that a kv head may have (new rows of a sequence x heads of a group).
-enum AttnKind { kAttn16, kAttn32, kAttnTc128, kAttnTc256 };
-constexpr int kAttnKindRows[] = {16, 32, gdn::kTcTile, 2 * gdn::kTcTile};
+enum AttnKind { kAttn16, kAttn32, kAttnTc };
+constexpr int kAttnKindRows[] = {16, 32, gdn::kTcRows};
 AttnKind attn_kind(int64_t rows, float scale) {
   if (rows <= 16) return kAttn16;
   // the tensor-core kernel keeps its maxima in unscaled scores, which a scale <= 0 would turn round
-  if (rows <= 32 || !(scale > 0.f)) return kAttn32;
-  return rows <= gdn::kTcTile ? kAttnTc128 : kAttnTc256;
+  return rows <= 32 || !(scale > 0.f) ? kAttn32 : kAttnTc;
 }
 // A block table with room for at most this many tokens a sequence is not split over the CTAs: a
 // unit of them costs less than the join that a split needs.
 constexpr int64_t kAttnWholeTokens = 512;
-int attn_runs(AttnKind kind, int sms) { return kind < kAttnTc128 ? sms * kAttnCtasPerSm : sms; }
+int attn_runs(AttnKind kind, int sms) { return kind != kAttnTc ? sms * kAttnCtasPerSm : sms; }
 
 struct AttnLayout {
   size_t cut, ml, o, total;
@@ -243,12 +242,8 @@ cudaError_t launch_attn(AttnKind kind, const gdn::AttnParams& p, const CUtensorM
     gdn::gdn_attn_kernel<T, D, 2><<<p.runs, gdn::kAttnThreads, gdn::AttnPlan<D, 2>::DYN_SMEM, s>>>(p);
     return launch_join<T, D, 32>(p, s);
   }
-  if (kind == kAttnTc128) {
-    gdn::gdn_attn_tc_kernel<T, D, true><<<p.runs, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s>>>(k, v, p);
-    return launch_join<T, D, gdn::kTcTile>(p, s);
-  }
-  gdn::gdn_attn_tc_kernel<T, D, false><<<p.runs, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s>>>(k, v, p);
-  return launch_join<T, D, 2 * gdn::kTcTile>(p, s);
+  gdn::gdn_attn_tc_kernel<T, D><<<p.runs, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s>>>(k, v, p);
+  return launch_join<T, D, gdn::kTcRows>(p, s);
 }
 
 }  // namespace
@@ -402,7 +397,7 @@ int gdn_paged_append(const void* k, const void* v, const gdn_paged_t* cache, con
 size_t gdn_tree_attention_workspace_bytes(int nq, int nkv, int d) {
   if (nq <= 0 || nkv <= 0 || (d != 64 && d != 128)) return 0;
   size_t most = 0;
-  for (AttnKind kind : {kAttn16, kAttn32, kAttnTc128, kAttnTc256}) {
+  for (AttnKind kind : {kAttn16, kAttn32, kAttnTc}) {
     const size_t n = attn_layout(kind, plan_sms(), d).total;
     if (n > most) most = n;
   }
@@ -461,7 +456,7 @@ int gdn_tree_attention(const void* q, const gdn_paged_t* cache, const uint64_t* 
   p.runs = attn_runs(kind, dev->sms);
   p.whole = static_cast<int64_t>(cache->max_pages) * cache->page_size <= kAttnWholeTokens;
   CUtensorMap maps[2] = {};
-  if (kind >= kAttnTc128) {
+  if (kind == kAttnTc) {
     // strides that TMA cannot take (or no pages at all) leave the copies to the threads
     p.box = cache->num_pages > 0 ? attn_box(cache->page_size) : 0;
     if (p.box && (!cache_map(&maps[0], cache->k, cache->k_page, cache->k_token, cache->k_head, p.cache, nkv, d, p.box, dtype) ||

@@ -107,11 +107,17 @@ struct AttnStart {
 };
 
 // Run i of `runs` has the tiles [total i / runs, total (i + 1) / runs).
-__device__ __forceinline__ int64_t run_begin(int64_t i, int64_t total, int runs) { return total * i / runs; }
+__device__ __forceinline__ int64_t run_begin(int64_t i, int64_t total, int runs) {
+  const uint64_t x = static_cast<uint64_t>(total) * static_cast<uint64_t>(i);
+  return x >> 32 ? static_cast<int64_t>(x / static_cast<uint64_t>(runs))
+                 : static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(runs));
+}
 
 // The run that holds tile `at`.
 __device__ __forceinline__ int run_of(int64_t at, int64_t total, int runs) {
-  int64_t i = at * runs / total;
+  const uint64_t x = static_cast<uint64_t>(at) * static_cast<uint64_t>(runs);
+  int64_t i = (x | static_cast<uint64_t>(total)) >> 32 ? static_cast<int64_t>(x / static_cast<uint64_t>(total))
+                                                       : static_cast<uint32_t>(x) / static_cast<uint32_t>(total);
   while (run_begin(i + 1, total, runs) <= at) ++i;
   while (run_begin(i, total, runs) > at) --i;
   return static_cast<int>(i);
@@ -121,10 +127,11 @@ __device__ __forceinline__ int run_of(int64_t at, int64_t total, int runs) {
 template <int MT, int KT, int THREADS>
 __device__ __forceinline__ AttnStart attn_start(const AttnParams& p, int run, int64_t* s_scan, AttnStart* s_start) {
   const int B = p.cache.B, tid = threadIdx.x;
-  int64_t total = 0;
+  int64_t total = 0, cost = 0, upto = 0;
   for (int b0 = 0; b0 < B; b0 += THREADS) {
     int64_t sum;
-    block_prefix<THREADS>(b0 + tid < B ? attn_cost(p, attn_seq<MT, KT>(p, b0 + tid, run == 0)) : 0, s_scan, &sum);
+    cost = b0 + tid < B ? attn_cost(p, attn_seq<MT, KT>(p, b0 + tid, run == 0)) : 0;
+    upto = block_prefix<THREADS>(cost, s_scan, &sum);
     total += sum;
   }
   const int runs = total < p.runs ? static_cast<int>(total) : p.runs;  // no run is empty
@@ -135,15 +142,17 @@ __device__ __forceinline__ AttnStart attn_start(const AttnParams& p, int run, in
   if (works) {
     int64_t before = 0;
     for (int b0 = 0; b0 < B && before <= begin; b0 += THREADS) {
-      int64_t sum;
-      const int64_t cost = b0 + tid < B ? attn_cost(p, attn_seq<MT, KT>(p, b0 + tid, false)) : 0;
-      const int64_t upto = before + block_prefix<THREADS>(cost, s_scan, &sum);
+      if (B > THREADS) {  // else the first pass has left this thread's sequence
+        int64_t sum;
+        cost = b0 + tid < B ? attn_cost(p, attn_seq<MT, KT>(p, b0 + tid, false)) : 0;
+        upto = before + block_prefix<THREADS>(cost, s_scan, &sum);
+        before += sum;
+      }
       if (upto > begin && upto - cost <= begin) {  // one thread's, at most
         s_start->b = b0 + tid;
         s_start->within = begin - (upto - cost);
         s_start->count = end - begin;
       }
-      before += sum;
     }
   }
   __syncthreads();
@@ -176,7 +185,7 @@ struct AttnWalk {
         ++within;
         --left;
       } else {
-        unit = static_cast<int>(within / s.tiles);
+        unit = within >> 32 ? static_cast<int>(within / s.tiles) : static_cast<int>(static_cast<uint32_t>(within) / static_cast<uint32_t>(s.tiles));
         t0 = static_cast<int>(within - static_cast<int64_t>(unit) * s.tiles);
         t1 = left < s.tiles - t0 ? t0 + static_cast<int>(left) : s.tiles;
         within += t1 - t0;

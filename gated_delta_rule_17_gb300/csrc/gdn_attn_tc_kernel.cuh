@@ -3,51 +3,53 @@
 //
 // With R query rows a kv head the operator does R flops a byte of the cache, so from some tens of
 // rows on the register products of gdn_attn_kernel bound it, and from about 256 rows the tensor
-// cores' rate does. A CTA works on two score streams x = 0, 1, each with 128 query rows and its own
-// accumulators in tensor memory, and takes tiles of 128 tokens:
+// cores' rate does. A CTA works on two score streams x = 0, 1 of 128 query rows, each with its own
+// scores and accumulators in tensor memory, and takes tiles of 128 tokens:
 //
 //     S_x = Q_x K^T (tcgen05)  ->  four warps: running maximum m, P = 2^(S c - m c), sum l
 //     O_x += P V  (tcgen05, P from tensor memory, where it takes the place of S_x)
 //
-// so that the products of one stream run while the warps of the other take exponentials.
-// Two ways to feed the streams:
-//   kSplit = false: 256 rows, both streams on every token tile; one load of K and V for 256 rows.
-//   kSplit = true : up to 128 rows, the streams on alternate token tiles of the same rows; their
-//                   (m, l, O) are added up at the unit's end.
+// so that the products of one stream run while the warps of the other take exponentials. A unit has
+// up to 256 rows. With more than 128 ("dual") both streams see every token tile, and one load of K
+// and V serves 256 rows; with fewer ("split") the streams take alternate token tiles of the same
+// rows, and their (m, l, O) are added up at the unit's end.
 // O stays unnormalised in tensor memory. It is scaled down only when a row's maximum has grown by
 // more than 2^8 since its last reference: until then P <= 2^8 relative to the reference, which
 // costs no precision in fp32 and 16-bit floats (their relative error does not depend on the size;
 // 2^8 is far inside fp16's range), and most tiles skip the round trip through the registers.
 //
-// Roles: warps 0-3 and 4-7 one stream each; warps 8-11 copy K and V tiles (TMA boxes
-// inside the pages, or 16-byte cp.async for any page size; 128-byte-swizzled rows) through a ring of
-// STAGES tiles; a thread of warp 12 issues the
-// products. The hand-offs are mbarriers; every wait is bounded, and when one expires the status
-// word says so and all roles run out.
+// Roles: warps 0-3 and 4-7 one stream each; warps 8-11 copy Q, K and V tiles (TMA boxes inside the
+// pages, or 16-byte cp.async for any page size; 128-byte-swizzled rows), K and V through a ring of
+// STAGES tiles, the next unit's Q as soon as the last scores of this one are done; an elected thread
+// of warp 12 issues the products. The hand-offs are mbarriers; every wait is bounded, and when one
+// expires the status word says so and all roles run out.
 #pragma once
 #include "gdn_attn_kernel.cuh"
 
 namespace gdn {
 
 constexpr int kTcTile = 128;  // tokens of a tile, and rows of a stream
+constexpr int kTcRows = 256;  // rows of a unit
 constexpr int kTcThreads = 416;
 constexpr float kTcGrowth = 8.f;  // log2 of the growth of a maximum that O is not scaled for
 
 template <int D>
 struct AttnTcPlan {
   static constexpr int TILE = kTcTile * D * 2;  // Q of a stream, or a tile of K or V
-  // the ring: as many tiles as fit beside Q; with D = 64 enough to keep the CTA alone on its SM,
-  // since it takes all of the tensor memory
-  static constexpr int STAGES = D == 128 ? 5 : 8;
-  static constexpr int LAG = 2;  // copies in flight behind the one just issued
+  // the ring: as many tiles as fit; with D = 64 enough to keep the CTA alone on its SM, since it
+  // takes all of the tensor memory
+  static constexpr int STAGES = D == 128 ? 4 : 8;
+  static constexpr int LAG = 2;  // cp.async tiles in flight behind the one just issued
   static constexpr int Q = 0;
-  static constexpr int RING = 2 * TILE;
+  static constexpr int PATCH = 32 * 64;  // of a warp, through which its rows go out
+  static constexpr int OUT = 2 * TILE;
+  static constexpr int RING = OUT + 8 * PATCH;
   static constexpr int BYTES = RING + STAGES * TILE;
   static constexpr int DYN_SMEM = BYTES + 1024;  // slack for 1024-byte alignment
   static constexpr uint32_t COL_S = 0, COL_O = 256, TMEM_COLS = 512;
   // mbarriers
   static constexpr int FULL = 0, FREE = STAGES, S_FULL = 2 * STAGES, P_FULL = S_FULL + 2, O_FULL = P_FULL + 2,
-                       Q_FULL = O_FULL + 2, X_FULL = Q_FULL + 1, X_FREE = X_FULL + 1, NBAR = X_FREE + 1;
+                       Q_FULL = O_FULL + 2, Q_FREE = Q_FULL + 1, JOIN = Q_FREE + 1, NBAR = JOIN + 1;
 };
 
 // Which of tokens tok .. tok + 31 the new row i of sequence s sees, as bits.
@@ -100,18 +102,18 @@ struct TcShared {
   }
 };
 
-template <typename T, int D, bool kSplit>
+template <typename T, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
 gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                    const AttnParams p) {
   using Plan = AttnTcPlan<D>;
-  constexpr int MT = kSplit ? kTcTile : 2 * kTcTile, TILE = Plan::TILE, NS = Plan::STAGES, LAG = Plan::LAG;
+  constexpr int MT = kTcRows, TILE = Plan::TILE, NS = Plan::STAGES, LAG = Plan::LAG;
   extern __shared__ uint8_t dyn[];
   __shared__ int64_t s_scan[kTcThreads / 32];
   __shared__ AttnStart s_start;
   __shared__ __align__(8) uint64_t s_bar[Plan::NBAR];
   __shared__ uint32_t s_tmem, s_abort;
-  __shared__ float s_ml[2][kTcTile];
+  __shared__ float2 s_ml[2][kTcTile];  // split units: (m, l) of both streams
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = tc::smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -130,9 +132,9 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
       tc::mbar_init(sh.bar(Plan::P_FULL + x), 4);
       tc::mbar_init(sh.bar(Plan::O_FULL + x), 1);
     }
-    tc::mbar_init(sh.bar(Plan::Q_FULL), 256);
-    tc::mbar_init(sh.bar(Plan::X_FULL), 128);
-    tc::mbar_init(sh.bar(Plan::X_FREE), 128);
+    tc::mbar_init(sh.bar(Plan::Q_FULL), 128);
+    tc::mbar_init(sh.bar(Plan::Q_FREE), 1);
+    tc::mbar_init(sh.bar(Plan::JOIN), 256);
     tc::mbar_fence_init();
     if (!p.whole) p.cut[run] = make_int4(0, 0, 0, -1);
   }
@@ -148,212 +150,236 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     // ---- one row a thread: softmax, and the unit's end -----------------------------------
     const int x = warp >> 2, lrow = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's quarter of the lanes
-    const uint32_t s_addr = tmem + lanes + Plan::COL_S + x * kTcTile, o_addr = tmem + lanes + Plan::COL_O + x * D;
+    const uint32_t s_addr = tmem + lanes + Plan::COL_S + x * kTcTile, o_addr = tmem + lanes + Plan::COL_O;
+    uint8_t* patch = smem + Plan::OUT + warp * Plan::PATCH;
+    auto patch_at = [](int r, int pc) { return r * 64 + ((pc ^ ((r >> 1) & 3)) << 4); };
     const float cl = p.scale_log2;
-    uint32_t s_ph = 0, o_ph = 0;
-    bool ok = true;
+    uint32_t s_ph = 0, o_ph = 0, j_ph = 0;
+    bool ok = true, pending = false;  // pending: the other stream may still read this one's O
     while (ok && w.next(p)) {
       const AttnSeq& s = w.s;
-      const int R = s.n * p.group, row = w.qt * MT + (kSplit ? 0 : x * kTcTile) + lrow;
+      const int R = s.n * p.group;
+      const bool split = R - w.qt * MT <= kTcTile;
+      const int row = w.qt * MT + (split ? 0 : x * kTcTile) + lrow;
       const bool has = row < R;
       const int i = has ? row / p.group : 0, g = has ? row - i * p.group : 0;
-      const int64_t head = (static_cast<int64_t>(s.first) + i) * p.q_stride + static_cast<int64_t>(w.kvh * p.group + g) * D;
-      {  // the row of Q (of its stream; or half of it each, where the streams share the rows)
-        constexpr int PER = kSplit ? D / 16 : D / 8;
-        uint8_t* q = smem + Plan::Q + (kSplit ? 0 : x * TILE);
-        const int c0 = kSplit ? x * PER : 0;
-        uint4 v[PER];
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-          v[j] = has ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + head + 8 * (c0 + j)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-          *reinterpret_cast<uint4*>(q + ((c0 + j) >> 3) * (kTcTile * 128) + tc::sw128(lrow, ((c0 + j) & 7) * 16)) = v[j];
-        tc::fence_proxy_async();
-        tc::mbar_arrive(sh.bar(Plan::Q_FULL));
-      }
-      const bool used = __any_sync(0xffffffffu, has);                       // any row of the warp
-      const bool mine = kSplit ? w.t0 + x < w.t1 : w.qt * MT + x * kTcTile < R;  // any tile of the stream
+      const bool used = __any_sync(0xffffffffu, has);  // any row of the warp
+      const int step = split ? 2 : 1;
       float m = -INFINITY, l = 0.f;
-      for (int t = w.t0 + (kSplit ? x : 0); mine && t < w.t1; t += kSplit ? 2 : 1) {
+      for (int t = w.t0 + (split ? x : 0); t < w.t1; t += step) {
         ok = sh.wait_warp(Plan::S_FULL + x, s_ph);
         s_ph ^= 1;
         if (!ok) break;
         tc::fence_after_sync();
         if (used) {
           const int tok = t * kTcTile;
-          const bool tail = tok + kTcTile > s.ctx || tok + kTcTile > s.len;
-          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint32_t r[32];
-          if (tail) {
-#pragma unroll
+          uint32_t r0[32], r1[32];
+          if (tok + kTcTile > s.ctx || tok + kTcTile > s.len) {  // scores of unseen tokens become -inf
+#pragma unroll 1
             for (int k = 0; k < 4; ++k) {
-              vis[k] = sees32(p, s, i, tok + 32 * k);
-              tc::tmem_ld32(s_addr + 32 * k, r);
-              tc::tmem_ld_wait();
+              const uint32_t vis = sees32(p, s, i, tok + 32 * k);
+              if (__all_sync(0xffffffffu, vis == ~0u)) continue;
+              tc::tmem_ld32(s_addr + 32 * k, r0);
+              tc::tmem_ld_wait32(r0);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], (vis[k] >> e) & 1 ? __uint_as_float(r[e]) : -INFINITY);
+              for (int e = 0; e < 32; ++e) r0[e] = (vis >> e) & 1 ? r0[e] : 0xFF800000u;
+              tc::tmem_st32(s_addr + 32 * k, r0);
             }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              tc::tmem_ld32(s_addr + 32 * k, r);
-              tc::tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(r[e]));
-            }
+            tc::tmem_st_wait();
           }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          float mx[2] = {-INFINITY, -INFINITY};
+          auto top_of = [&](const uint32_t (&r)[32]) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              mx[0] = fmaxf(mx[0], fmaxf(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
+              mx[1] = fmaxf(mx[1], fmaxf(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])));
+            }
+          };
+          tc::tmem_ld32(s_addr, r0);
+          tc::tmem_ld_wait32(r0);
+          tc::tmem_ld32(s_addr + 32, r1);
+          top_of(r0);
+          tc::tmem_ld_wait32(r1);
+          tc::tmem_ld32(s_addr + 64, r0);
+          top_of(r1);
+          tc::tmem_ld_wait32(r0);
+          tc::tmem_ld32(s_addr + 96, r1);
+          top_of(r0);
+          tc::tmem_ld_wait32(r1);
+          tc::tmem_ld32(s_addr, r0);  // the second pass begins
+          top_of(r1);
+          const float top = fmaxf(mx[0], mx[1]);
           // a new reference for the row where its maximum has outgrown the old one (or there is none)
           const bool grown = top * cl > m * cl + kTcGrowth, fresh = m == -INFINITY;
-          if (__any_sync(0xffffffffu, grown && !fresh)) {
-            const float f = grown && !fresh ? exp2_approx((m - top) * cl) : 1.f;
+          const float f = grown && !fresh ? exp2_approx((m - top) * cl) : 1.f;
+          if (grown || fresh) m = top;
+          if (__any_sync(0xffffffffu, f != 1.f)) {
             l *= f;
-#pragma unroll
+            tc::tmem_ld_wait32(r0);
+#pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
-              tc::tmem_ld32(o_addr + 32 * k, r);
-              tc::tmem_ld_wait();
+              tc::tmem_ld32(o_addr + x * D + 32 * k, r1);
+              tc::tmem_ld_wait32(r1);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-              tc::tmem_st32(o_addr + 32 * k, r);
+              for (int e = 0; e < 32; ++e) r1[e] = __float_as_uint(__uint_as_float(r1[e]) * f);
+              tc::tmem_st32(o_addr + x * D + 32 * k, r1);
             }
           }
-          if (grown || fresh) m = top;
           const float nb = m == -INFINITY ? 0.f : -m * cl;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            tc::tmem_ld32(s_addr + 32 * k, r);
-            tc::tmem_ld_wait();
+          float sum[2] = {0.f, 0.f};
+          auto weights = [&](const uint32_t (&r)[32], int k) {  // over a part of S that has been read
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              float a = exp2_approx(fmaf(__uint_as_float(r[e]), cl, nb));
-              float b = exp2_approx(fmaf(__uint_as_float(r[e + 1]), cl, nb));
-              if (tail) {
-                a = (vis[k] >> e) & 1 ? a : 0.f;
-                b = (vis[k] >> (e + 1)) & 1 ? b : 0.f;
-              }
-              sum[(e >> 1) & 3] += a + b;
+              const float a = exp2_approx(fmaf(__uint_as_float(r[e]), cl, nb));
+              const float b = exp2_approx(fmaf(__uint_as_float(r[e + 1]), cl, nb));
+              sum[0] += a;
+              sum[1] += b;
               pk[e >> 1] = pack2<T>(a, b);
             }
-            tc::tmem_st16u(s_addr + 16 * k, pk);  // over the part of S that has been read
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tc::tmem_st16u(s_addr + 16 * k, pk);
+          };
+          tc::tmem_ld_wait32(r0);
+          tc::tmem_ld32(s_addr + 32, r1);
+          weights(r0, 0);
+          tc::tmem_ld_wait32(r1);
+          tc::tmem_ld32(s_addr + 64, r0);
+          weights(r1, 1);
+          tc::tmem_ld_wait32(r0);
+          tc::tmem_ld32(s_addr + 96, r1);
+          weights(r0, 2);
+          tc::tmem_ld_wait32(r1);
+          weights(r1, 3);
+          l += sum[0] + sum[1];
           tc::tmem_st_wait();
+        }
+        if (pending) {  // the products that follow overwrite O
+          pending = false;
+          ok = sh.wait_warp(Plan::JOIN, j_ph ^ 1);
+          if (!ok) break;
         }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(sh.bar(Plan::P_FULL + x));
       }
       if (!ok) break;
+      if (pending) {  // a unit in which this stream had no tile
+        pending = false;
+        ok = sh.wait_warp(Plan::JOIN, j_ph ^ 1);
+        if (!ok) break;
+      }
+      // ---- the unit's end: rows out, or a piece of them into the workspace --------------------
+      const bool whole = w.t0 == 0 && w.t1 == s.tiles, two = split && w.t0 + 1 < w.t1;
       ok = sh.wait_warp(Plan::O_FULL + x, o_ph);
+      if (split && ok) {  // both streams' O, and both (m, l) for each stream's warps
+        s_ml[x][lrow] = make_float2(m, l);
+        tc::mbar_arrive(sh.bar(Plan::JOIN));
+        ok = sh.wait_warp(Plan::O_FULL + (x ^ 1), o_ph) && sh.wait_warp(Plan::JOIN, j_ph);
+        j_ph ^= 1;
+      }
       o_ph ^= 1;
       if (!ok) break;
       tc::fence_after_sync();
-      // ---- the unit's end: the row out, or a piece of it into the workspace
-      const bool whole = w.t0 == 0 && w.t1 == s.tiles, two = kSplit && w.t0 + 1 < w.t1;
-      const int64_t part = (static_cast<int64_t>(run) * 2 + (w.t0 == 0 ? 1 : 0)) * MT + (kSplit ? 0 : x * kTcTile) + lrow;
-      T* out = static_cast<T*>(p.out) + (static_cast<int64_t>(s.first) + i) * p.out_stride +
-               static_cast<int64_t>(w.kvh * p.group + g) * D;
-      float mm = m, ll = l, f0 = 1.f, f1 = 0.f;
-      constexpr int HALF = D / 2;  // columns that the second stream hands over at a time
-      float* xch = reinterpret_cast<float*>(smem + TILE);  // [HALF][128]
-      if (two) {
-        if (x == 1) {
-          s_ml[0][lrow] = m;
-          s_ml[1][lrow] = l;
-        }
+      float f0 = 1.f, f1 = 0.f;
+      if (split) {
+        const float2 a = s_ml[0][lrow], b = s_ml[1][lrow];
+        m = fmaxf(a.x, b.x);
+        const float base = m == -INFINITY ? 0.f : m;
+        f0 = exp2_approx((a.x - base) * cl);
+        f1 = exp2_approx((b.x - base) * cl);
+        l = a.y * f0 + b.y * f1;
       }
-      auto write32 = [&](int col, const float* a, float inv) {  // 32 columns of the row
-        if (!has) return;
-        if (whole) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(out + col + e) =
-                make_uint4(pack2<T>(a[e] * inv, a[e + 1] * inv), pack2<T>(a[e + 2] * inv, a[e + 3] * inv),
-                           pack2<T>(a[e + 4] * inv, a[e + 5] * inv), pack2<T>(a[e + 6] * inv, a[e + 7] * inv));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(p.part_o + part * D + col + e) = make_float4(a[e], a[e + 1], a[e + 2], a[e + 3]);
-        }
-      };
+      const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      f0 *= inv;
+      f1 *= inv;
+      // a dual stream has its rows; the warps of a split unit have half of the columns each
+      const int c0 = split ? x * (D / 2) : 0, c1 = split ? c0 + D / 2 : D, xo = split ? 0 : x;
+      const int64_t part = (static_cast<int64_t>(run) * 2 + (w.t0 == 0 ? 1 : 0)) * MT + (split ? 0 : x * kTcTile) + lrow;
+      char* mine;  // this lane's row
+      if (whole)
+        mine = reinterpret_cast<char*>(static_cast<T*>(p.out) + (static_cast<int64_t>(s.first) + i) * p.out_stride +
+                                       static_cast<int64_t>(w.kvh * p.group + g) * D);
+      else
+        mine = reinterpret_cast<char*>(p.part_o + part * D);
+      if (!has) mine = nullptr;
+      if (used) {
 #pragma unroll 1
-      for (int h = 0; h < 2 && ok; ++h) {
-        if (two && x == 1) {
-          if (h == 1) {  // the first half has been taken
-            ok = sh.wait_warp(Plan::X_FREE, 0);  // two phases a unit
-            if (!ok) break;
-          }
+        for (int col = c0; col < c1; col += 32) {
+          uint32_t r0[32];
+          float a[32];
+          tc::tmem_ld32(o_addr + xo * D + col, r0);
+          tc::tmem_ld_wait32(r0);
 #pragma unroll
-          for (int k = 0; k < HALF / 32; ++k) {
-            uint32_t r[32];
-            tc::tmem_ld32(o_addr + h * HALF + 32 * k, r);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) xch[(32 * k + e) * kTcTile + lrow] = __uint_as_float(r[e]);
-          }
-          tc::mbar_arrive(sh.bar(Plan::X_FULL));
-        } else if (mine && !(kSplit && x == 1)) {
+          for (int e = 0; e < 32; ++e) a[e] = __uint_as_float(r0[e]) * f0;
           if (two) {
-            ok = sh.wait_warp(Plan::X_FULL, h);
-            if (!ok) break;
-            if (h == 0) {
-              const float m1 = s_ml[0][lrow];
-              mm = fmaxf(m, m1);
-              const float base = mm == -INFINITY ? 0.f : mm;
-              f0 = exp2_approx((m - base) * cl);
-              f1 = exp2_approx((m1 - base) * cl);
-              ll = l * f0 + s_ml[1][lrow] * f1;
-            }
-          }
-          const float inv = ll > 0.f ? 1.f / ll : 0.f;
+            tc::tmem_ld32(o_addr + D + col, r0);
+            tc::tmem_ld_wait32(r0);
 #pragma unroll
-          for (int k = 0; k < HALF / 32; ++k) {
-            uint32_t r[32];
-            float a[32];
-            tc::tmem_ld32(o_addr + h * HALF + 32 * k, r);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              a[e] = __uint_as_float(r[e]);
-              if (two) a[e] = a[e] * f0 + xch[(32 * k + e) * kTcTile + lrow] * f1;
-            }
-            write32(h * HALF + 32 * k, a, inv);
+            for (int e = 0; e < 32; ++e) a[e] = fmaf(__uint_as_float(r0[e]), f1, a[e]);
           }
-          if (two) tc::mbar_arrive(sh.bar(Plan::X_FREE));
+          // through the warp's patch (rows of 64 bytes, pieces exchanged by row), so that the lanes
+          // store 64-byte runs of the rows: 32 16-bit values, or 16 fp32 ones and then the other 16
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (whole && h == 1) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint4 q = whole ? make_uint4(pack2<T>(a[8 * e], a[8 * e + 1]), pack2<T>(a[8 * e + 2], a[8 * e + 3]),
+                                                 pack2<T>(a[8 * e + 4], a[8 * e + 5]), pack2<T>(a[8 * e + 6], a[8 * e + 7]))
+                                    : make_uint4(__float_as_uint(a[16 * h + 4 * e]), __float_as_uint(a[16 * h + 4 * e + 1]),
+                                                 __float_as_uint(a[16 * h + 4 * e + 2]), __float_as_uint(a[16 * h + 4 * e + 3]));
+              *reinterpret_cast<uint4*>(patch + patch_at(lane, e)) = q;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int rr = 8 * e + (lane >> 2), pc = lane & 3;
+              const uint64_t dst = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), rr);
+              const uint4 q = *reinterpret_cast<const uint4*>(patch + patch_at(rr, pc));
+              if (dst) *reinterpret_cast<uint4*>(dst + (whole ? col * 2 : col * 4 + 64 * h) + 16 * pc) = q;
+            }
+            __syncwarp();
+          }
         }
       }
-      if (!ok) break;
-      if (two) {
-        // the streams leave together: Q and the hand-over space are free for both
-        ok = sh.wait_warp(Plan::X_FREE, 1);
-        if (!ok) break;
+      if (split) {  // this stream's warps have read the other's O
+        tc::fence_before_sync();
+        tc::mbar_arrive(sh.bar(Plan::JOIN));
+        pending = true;
+        j_ph ^= 1;
       }
-      if (has && !whole && mine && (!kSplit || x == 0)) {
-        p.part_ml[part * 2] = mm == -INFINITY ? mm : mm * cl;  // in units of log2 e, as the join takes them
-        p.part_ml[part * 2 + 1] = ll;
-      }
+      if (has && !whole && (!split || x == 0))  // m in units of log2 e, as the join takes it
+        *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(m == -INFINITY ? m : m * cl, l);
       if (threadIdx.x == 0 && w.t0 == 0 && w.t1 < s.tiles)
         p.cut[run] = make_int4(s.first, s.n, w.unit, run_of(st.end + (s.tiles - w.t1) - 1, st.total, st.runs));
     }
   } else if (warp < 12) {
-    // ---- copies of K and V -----------------------------------------------------------------
-    constexpr int CH = D / 8, ROWS = 32 / CH;
+    // ---- copies of Q, K and V --------------------------------------------------------------
     // A warp copies 32 tokens of every tile. Where a page holds whole boxes of p.box tokens and all
     // 32 tokens are there, a lane a box starts a TMA copy; else the warp copies by 16 bytes, with
     // zeros for the tokens that are not there.
+    constexpr int CH = D / 8, ROWS = 32 / CH;
     const int lw = warp - 8;
     int n = 0;       // tiles issued
     int landed = 0;  // tiles whose arrival is made; those of TMA copies are made at once
+    int units = 0;
     bool ok = true;
     auto land = [&](int upto) {
       tc::fence_proxy_async();
       for (; landed < upto; ++landed) tc::mbar_arrive(sh.bar(Plan::FULL + landed % NS));
     };
+    // 32 rows of 16-byte pieces to rows lw * 32 .. of the tile at dst; lane r knows row r's source (null: zeros)
+    auto copy_rows = [&](uint32_t dst, const T* mine) {
+#pragma unroll 4
+      for (int j = 0; j < 32 / ROWS; ++j) {
+        const int r = j * ROWS + lane / CH, ch = lane % CH;
+        const uint64_t src = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), r);
+        cp_async_16(dst + (ch >> 3) * (kTcTile * 128) + tc::sw128(lw * 32 + r, (ch & 7) * 16),
+                    reinterpret_cast<const T*>(src ? src : reinterpret_cast<uint64_t>(p.q)) + (src ? 8 * ch : 0), src != 0);
+      }
+    };
     while (ok && w.next(p)) {
+      const int R = w.s.n * p.group, left = R - w.qt * MT;  // rows of the unit: left, at most MT
       const int32_t* table = c.block_table + w.b * c.table_stride;
       const T* kbase = static_cast<const T*>(c.k) + w.kvh * c.k_head;
       const T* vbase = static_cast<const T*>(c.v) + w.kvh * c.v_head;
@@ -372,7 +398,7 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
           else tc::mbar_arrive(bar);
           __syncwarp();
           constexpr int HALVES = D / 64;
-          const int box = lane / HALVES, half = lane % HALVES, first = box * p.box & 31;
+          const int box = lane / HALVES, half = lane % HALVES, first = (box * p.box) & 31;
           const int page = __shfl_sync(0xffffffffu, place.page, first), at = __shfl_sync(0xffffffffu, place.place, first);
           if (box * p.box < 32)
             tc::tma_load_4d(dst + half * (kTcTile * 128) + (lw * 32 + first) * 128, map, 64 * half, w.kvh, at, page, bar);
@@ -380,14 +406,7 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
           ++landed;
           return;
         }
-#pragma unroll 4
-        for (int j = 0; j < 32 / ROWS; ++j) {
-          const int r = j * ROWS + lane / CH, ch = lane % CH;
-          const int page = __shfl_sync(0xffffffffu, place.page, r), at = __shfl_sync(0xffffffffu, place.place, r);
-          const bool real = page >= 0;
-          cp_async_16(dst + (ch >> 3) * (kTcTile * 128) + tc::sw128(lw * 32 + r, (ch & 7) * 16),
-                      base + (real ? page : 0) * page_stride + at * token_stride + 8 * ch, real);
-        }
+        copy_rows(dst, place.page >= 0 ? base + place.page * page_stride + place.place * token_stride : nullptr);
         tc::cp_async_commit();
         ++n;
         if (n - landed > LAG) {
@@ -395,11 +414,29 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
           land(n - LAG);
         }
       };
+      // the order of the tiles: K0, (Q), K1, V0, K2, V1, ..., V(n-1)
       TokenPlace next = token_place(p, table, w.t0 * kTcTile + lw * 32 + lane, w.s.len), prev = next;
       for (int t = w.t0; t <= w.t1 && ok; ++t) {
         const TokenPlace cur = next;
         next = token_place(p, table, (t + 1) * kTcTile + lw * 32 + lane, t + 1 < w.t1 ? w.s.len : 0);
         if (t < w.t1) load(&k_map, kbase, c.k_page, c.k_token, cur);
+        if (t == w.t0 && ok) {
+          ok = units == 0 || sh.wait_warp(Plan::Q_FREE, (units - 1) & 1);
+          if (!ok) break;
+#pragma unroll 1
+          for (int y = 0; y < (left > kTcTile ? 2 : 1); ++y) {
+            const int rr = y * kTcTile + lw * 32 + lane, row = w.qt * MT + rr, i = row / p.group;
+            copy_rows(sbase + Plan::Q + y * TILE,
+                      rr < left ? static_cast<const T*>(p.q) + (static_cast<int64_t>(w.s.first) + i) * p.q_stride +
+                                      static_cast<int64_t>(w.kvh * p.group + row - i * p.group) * D
+                                : nullptr);
+          }
+          tc::cp_async_commit();
+          tc::cp_async_wait_all();
+          land(n);
+          tc::mbar_arrive(sh.bar(Plan::Q_FULL));
+          ++units;
+        }
         if (t > w.t0 && ok) load(&v_map, vbase, c.v_page, c.v_token, prev);
         prev = cur;
       }
@@ -418,19 +455,19 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     bool ok = true;
     while (ok && w.next(p)) {
       const int n = w.t1 - w.t0;
-      const int streams = kSplit ? 2 : (w.qt * MT + kTcTile < w.s.n * p.group ? 2 : 1);
+      const bool split = w.s.n * p.group - w.qt * MT <= kTcTile;
       ok = sh.wait_warp(Plan::Q_FULL, q_ph);
       q_ph ^= 1;
-      // tiles are loaded in the order K0, K1, V0, K2, V1, ..., V(n-1)
       auto scores = [&](int x, int j) {
         if (!ok) return;
         const int at = base + (j == 0 ? 0 : 2 * j - 1), slot = at % NS;
         ok = sh.wait_warp(Plan::FULL + slot, (at / NS) & 1);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint64_t a = tc::desc_sw128(sbase + Plan::Q + (kSplit ? 0 : x * TILE), 16, 1024);
+        const uint64_t a = tc::desc_sw128(sbase + Plan::Q + (split ? 0 : x * TILE), 16, 1024);
         const uint64_t b = tc::desc_sw128(sbase + Plan::RING + slot * TILE, 16, 1024);
         const uint32_t d = tmem + Plan::COL_S + x * kTcTile;
+        const bool last = split || x == 1;  // of the stream(s) that use the tile
         if (tc::elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -438,7 +475,8 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             tc::mma_f16(d, a + off, b + off, id_s, k > 0);
           }
           tc::mma_commit(sh.bar(Plan::S_FULL + x));
-          if (kSplit || x == streams - 1) tc::mma_commit(sh.bar(Plan::FREE + slot));
+          if (last) tc::mma_commit(sh.bar(Plan::FREE + slot));
+          if (last && j == n - 1) tc::mma_commit(sh.bar(Plan::Q_FREE));
         }
         __syncwarp();
       };
@@ -451,18 +489,17 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         tc::fence_after_sync();
         const uint64_t b = tc::desc_sw128(sbase + Plan::RING + slot * TILE, kTcTile * 128, 1024);
         const uint32_t d = tmem + Plan::COL_O + x * D, a = tmem + Plan::COL_S + x * kTcTile;
-        const bool first = kSplit ? j < 2 : j == 0;
+        const bool first = split ? j < 2 : j == 0;
         if (tc::elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTcTile / 16; ++k) tc::mma_f16_ts(d, a + 8 * k, b + ((k * 2048) >> 4), id_o, !first || k > 0);
-          if (kSplit || x == streams - 1) tc::mma_commit(sh.bar(Plan::FREE + slot));
-          if (kSplit ? j + 2 >= n : j == n - 1) tc::mma_commit(sh.bar(Plan::O_FULL + x));
-          // a stream without tiles is told too: it must not run ahead into the next unit's Q
-          if (kSplit ? n == 1 : streams == 1 && j == n - 1) tc::mma_commit(sh.bar(Plan::O_FULL + 1));
+          if (split || x == 1) tc::mma_commit(sh.bar(Plan::FREE + slot));
+          if (split ? j + 2 >= n : j == n - 1) tc::mma_commit(sh.bar(Plan::O_FULL + x));
+          if (split && n == 1) tc::mma_commit(sh.bar(Plan::O_FULL + 1));  // a stream without tiles is told too
         }
         __syncwarp();
       };
-      if (kSplit) {
+      if (split) {
         scores(0, 0);
         if (n > 1) scores(1, 1);
         for (int j = 0; j < n && ok; ++j) {
@@ -470,9 +507,10 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
           if (j + 2 < n) scores(j & 1, j + 2);
         }
       } else {
-        for (int x = 0; x < streams; ++x) scores(x, 0);
+        scores(0, 0);
+        scores(1, 0);
         for (int j = 0; j < n && ok; ++j)
-          for (int x = 0; x < streams; ++x) {
+          for (int x = 0; x < 2; ++x) {
             values(x, j);
             if (j + 1 < n) scores(x, j + 1);
           }
