@@ -382,87 +382,90 @@ def backward(q, k, v, g, beta, h0, dout, dq, dk, dv, dg, dbeta, *, nk: int, nv: 
 
 
 # ---- the softmax-attention operators (include/gdn_attention.h) ----------------------------
+# A decode step makes several of these calls a layer, each a few microseconds on the GPU, so the
+# checks below touch every attribute of a tensor once and take the common layout first.
 
-def _stream(torch, stream, device):
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+_torch = None   # torch, once one of the calls below has been made
+_codes = {}     # torch dtype -> the ABI's number
+
+
+def _setup():
+    global _torch
+    import torch
+
+    load()
+    _codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    _torch = torch
+    return torch
+
+
+def _stream_of(stream, device):
+    if stream is None:  # the handle itself: a torch.cuda.Stream around it costs a sixth of a call
+        return _torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _dtype(torch, t, name, allowed):
-    """The ABI's number of an activation type."""
-    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(t.dtype)
-    if code is None or code not in allowed:
-        raise GdnError(GDN_ERR_ARG, f"{name} must be {' or '.join(('bfloat16', 'float16', 'float32')[a] for a in allowed)}, "
-                                    f"got {t.dtype}")
+def _act_code(t, name, most):
+    """The ABI's number of an activation type: bf16 0, fp16 1, fp32 2 (up to `most`)."""
+    code = _codes.get(t.dtype, 9)
+    if code > most:
+        raise GdnError(GDN_ERR_ARG, f"{name} must be {' or '.join(('bfloat16', 'float16', 'float32')[:most + 1])}, got {t.dtype}")
     return code
 
 
-def _check_like(torch, dt, named):
-    """Rows of one element type on the GPU."""
-    for name, t in named:
-        if t is not None and t.dtype != dt:
-            raise GdnError(GDN_ERR_ARG, f"{name} must be {dt}, got {t.dtype}")
-        if t is not None and not t.is_cuda:
-            raise GdnError(GDN_ERR_ARG, f"{name} must be a CUDA tensor")
+def _act(t, name, dtype, rows, inner):
+    """Checks [rows, ...] activations with `inner` contiguous elements a row; (address, row stride)."""
+    if t.dtype != dtype or not t.is_cuda:
+        raise GdnError(GDN_ERR_ARG, f"{name} must be a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != inner or strides[1] != 1 or rows < 2:  # not the common layout
+        if len(shape) < 2:
+            raise GdnError(GDN_ERR_ARG, f"{name} must be at least 2-D ([rows, ...])")
+        stride = _row_stride(t, name, inner)
+    else:
+        stride = strides[0]
+    if shape[0] != rows:
+        raise GdnError(GDN_ERR_ARG, f"{name} has {shape[0]} rows, need {rows}")
+    return t.data_ptr(), stride
 
 
-def _check_vector(t, name, dt, n):
-    """A contiguous CUDA vector of n elements, or None."""
-    if t is not None and (not t.is_cuda or t.dtype != dt or not t.is_contiguous() or t.numel() != n):
-        raise GdnError(GDN_ERR_ARG, f"{name} must be a contiguous {dt} CUDA tensor of {n} elements")
-
-
-def _rows_of(t, name, rows, inner):
-    if t.shape[0] != rows:
-        raise GdnError(GDN_ERR_ARG, f"{name} has {t.shape[0]} rows, need {rows}")
-    return _row_stride(t, name, inner)
-
-
-def _rope(torch, cos, sin, interleaved):
-    if (cos is None) != (sin is None):
-        raise GdnError(GDN_ERR_ARG, "cos and sin must be given together")
-    if cos is None:
+def _vector(t, name, dtype, n):
+    """The address of a contiguous CUDA vector of n elements, or None for None."""
+    if t is None:
         return None
-    for name, t in (("cos", cos), ("sin", sin)):
-        if not t.is_cuda or t.dtype != torch.float32 or t.dim() != 2 or t.shape != cos.shape or (
-                t.shape[1] > 1 and t.stride(1) != 1) or t.stride(0) != cos.stride(0):
-            raise GdnError(GDN_ERR_ARG, f"{name} must be an fp32 CUDA tensor [positions, rot/2], contiguous in a row, "
-                                        "cos and sin alike")
-    n, half = cos.shape
-    return Rope(cos.data_ptr(), sin.data_ptr(), cos.stride(0) if n > 1 else max(cos.stride(0), half), n, 2 * half,
-                1 if interleaved else 0)
+    if t.dtype != dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
+        raise GdnError(GDN_ERR_ARG, f"{name} must be a contiguous {dtype} CUDA tensor of {n} elements")
+    return t.data_ptr()
 
 
-def _check_workspace(workspace):
-    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
+def _rope(cos, sin, interleaved):
+    if cos is None or sin is None:
+        if cos is not sin:
+            raise GdnError(GDN_ERR_ARG, "cos and sin must be given together")
+        return None
+    f32, shape, st = _torch.float32, cos.shape, cos.stride()
+    if cos.dtype != f32 or sin.dtype != f32 or not cos.is_cuda or not sin.is_cuda or len(shape) != 2 or (
+            sin.shape != shape or sin.stride() != st or (st[1] != 1 and shape[1] > 1)):
+        raise GdnError(GDN_ERR_ARG, "cos and sin must be fp32 CUDA tensors [positions, rot/2], contiguous in a row, both alike")
+    n, half = shape
+    return Rope(cos.data_ptr(), sin.data_ptr(), st[0] if n > 1 else max(st[0], half), n, 2 * half, 1 if interleaved else 0)
+
+
+def _scratch(workspace):
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or not workspace.is_contiguous():
         raise GdnError(GDN_ERR_ARG, "workspace must be a contiguous CUDA tensor")
-    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _norm_args(torch, q, k, positions, cos, sin, outs, grads, nq, nkv, d, q_weight, k_weight, interleaved):
-    """Shared checks of head_norm_rope and its backward: (rows, dtype, rope, strides)."""
-    x = q if q is not None else k
-    if x is None:
-        raise GdnError(GDN_ERR_ARG, "q or k must be given")
-    if (q is None) != (nq == 0) or (k is None) != (nkv == 0):
-        raise GdnError(GDN_ERR_ARG, "q (k) is None just where nq (nkv) is 0")
-    code = _dtype(torch, x, "q" if q is not None else "k", (0, 1, 2))
-    rows, st = x.shape[0], []
-    for names, ts in ((("q", "k"), (q, k)), (("q_out", "k_out"), outs), (("q_grad", "k_grad"), grads)):
-        for name, t, heads in zip(names, ts, (nq, nkv)):
-            if heads and t is None:
-                raise GdnError(GDN_ERR_ARG, f"{name} is missing")
-            _check_like(torch, x.dtype, ((name, t),))
-            st.append(_rows_of(t, name, rows, heads * d) if heads else 0)
-    _check_vector(q_weight, "q_weight", torch.float32, d)
-    _check_vector(k_weight, "k_weight", torch.float32, d)
-    _check_vector(positions, "positions", torch.int32, rows)
-    return rows, code, _rope(torch, cos, sin, interleaved), NormStrides(*st)
+def _heads_given(q, k, nq, nkv):
+    if (q is None) != (nq == 0) or (k is None) != (nkv == 0) or (q is None and k is None):
+        raise GdnError(GDN_ERR_ARG, "q (k) is None just where nq (nkv) is 0, and one of them is given")
+    return q if q is not None else k
+
+
+_NONE = (None, 0)
 
 
 def head_norm_rope(q, k, positions, cos, sin, q_out, k_out, *, nq: int, nkv: int, head_dim: int = 128, q_weight=None,
@@ -475,14 +478,19 @@ def head_norm_rope(q, k, positions, cos, sin, q_out, k_out, *, nq: int, nkv: int
     ``k_weight``: fp32 [head_dim], shared by the heads (None: ones). ``positions``: int32 [rows] into the fp32
     tables ``cos``, ``sin`` [positions, rot/2] (both None: no rotation); the first ``rot`` values of a head are
     turned, in pairs (i, i + rot/2), or (2i, 2i + 1) if ``interleaved``. head_dim is 64 or 128."""
-    import torch
-
-    lib = load()
-    rows, code, rope, st = _norm_args(torch, q, k, positions, cos, sin, (q_out, k_out), (q, k), nq, nkv, head_dim,
-                                      q_weight, k_weight, interleaved)
-    rc = lib.gdn_head_norm_rope(_ptr(q), _ptr(k), _ptr(positions), rope, _ptr(q_weight), _ptr(k_weight), eps,
-                                _ptr(q_out), _ptr(k_out), rows, nq, nkv, head_dim, code, st,
-                                _stream(torch, stream, (q if q is not None else k).device))
+    torch = _torch or _setup()
+    x = _heads_given(q, k, nq, nkv)
+    code, rows, dt, wq, wk = _act_code(x, "q" if nq else "k", 2), x.shape[0], x.dtype, nq * head_dim, nkv * head_dim
+    if (nq and q_out is None) or (nkv and k_out is None):
+        raise GdnError(GDN_ERR_ARG, "q_out or k_out is missing")
+    qp, qs = _act(q, "q", dt, rows, wq) if nq else _NONE
+    kp, ks = _act(k, "k", dt, rows, wk) if nkv else _NONE
+    qo, qos = _act(q_out, "q_out", dt, rows, wq) if nq else _NONE
+    ko, kos = _act(k_out, "k_out", dt, rows, wk) if nkv else _NONE
+    rc = _lib.gdn_head_norm_rope(qp, kp, _vector(positions, "positions", torch.int32, rows), _rope(cos, sin, interleaved),
+                                 _vector(q_weight, "q_weight", torch.float32, head_dim),
+                                 _vector(k_weight, "k_weight", torch.float32, head_dim), eps, qo, ko, rows, nq, nkv,
+                                 head_dim, code, NormStrides(qs, ks, qos, kos, 0, 0), _stream_of(stream, x.device))
     if rc != GDN_OK:
         _raise(rc)
 
@@ -498,39 +506,42 @@ def head_norm_rope_backward(q, k, positions, cos, sin, q_grad, k_grad, dq, dk, d
     forward; ``q_grad``, ``k_grad``: dL/dq_out, dL/dk_out; outputs ``dq``, ``dk`` of the same type (may be
     q_grad, k_grad themselves) and, where given, ``dq_weight``, ``dk_weight``: fp32 [head_dim], overwritten with
     the sums over all rows and heads."""
-    import torch
-
-    lib = load()
-    rows, code, rope, st = _norm_args(torch, q, k, positions, cos, sin, (dq, dk), (q_grad, k_grad), nq, nkv, head_dim,
-                                      q_weight, k_weight, interleaved)
-    _check_vector(dq_weight, "dq_weight", torch.float32, head_dim)
-    _check_vector(dk_weight, "dk_weight", torch.float32, head_dim)
-    ws, size = _check_workspace(workspace)
-    rc = lib.gdn_head_norm_rope_backward(_ptr(q), _ptr(k), _ptr(positions), rope, _ptr(q_weight), _ptr(k_weight), eps,
-                                         _ptr(q_grad), _ptr(k_grad), _ptr(dq), _ptr(dk), _ptr(dq_weight),
-                                         _ptr(dk_weight), rows, nq, nkv, head_dim, code, st, ws, size,
-                                         _stream(torch, stream, (q if q is not None else k).device))
+    torch = _torch or _setup()
+    x = _heads_given(q, k, nq, nkv)
+    code, rows, dt, wq, wk = _act_code(x, "q" if nq else "k", 2), x.shape[0], x.dtype, nq * head_dim, nkv * head_dim
+    if (nq and (dq is None or q_grad is None)) or (nkv and (dk is None or k_grad is None)):
+        raise GdnError(GDN_ERR_ARG, "a gradient tensor is missing")
+    qp, qs = _act(q, "q", dt, rows, wq) if nq else _NONE
+    kp, ks = _act(k, "k", dt, rows, wk) if nkv else _NONE
+    gq, gqs = _act(q_grad, "q_grad", dt, rows, wq) if nq else _NONE
+    gk, gks = _act(k_grad, "k_grad", dt, rows, wk) if nkv else _NONE
+    dqp, dqs = _act(dq, "dq", dt, rows, wq) if nq else _NONE
+    dkp, dks = _act(dk, "dk", dt, rows, wk) if nkv else _NONE
+    ws, size = _scratch(workspace)
+    f32 = torch.float32
+    rc = _lib.gdn_head_norm_rope_backward(qp, kp, _vector(positions, "positions", torch.int32, rows), _rope(cos, sin, interleaved),
+                                          _vector(q_weight, "q_weight", f32, head_dim), _vector(k_weight, "k_weight", f32, head_dim),
+                                          eps, gq, gk, dqp, dkp, _vector(dq_weight, "dq_weight", f32, head_dim),
+                                          _vector(dk_weight, "dk_weight", f32, head_dim), rows, nq, nkv, head_dim, code,
+                                          NormStrides(qs, ks, dqs, dks, gqs, gks), ws, size, _stream_of(stream, x.device))
     if rc != GDN_OK:
         _raise(rc)
 
 
-def _paged(torch, x, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, d):
-    """The cache and the batch of rows x as the ABI's struct."""
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not t.is_cuda or t.dtype != x.dtype:
-            raise GdnError(GDN_ERR_ARG, f"{name} must be a {x.dtype} CUDA tensor")
-        if t.dim() != 4 or t.shape[2] != nkv or t.shape[3] != d or t.stride(3) != 1 or t.shape != k_cache.shape:
-            raise GdnError(GDN_ERR_ARG, f"{name} must be [pages, page_size, {nkv}, {d}], the last dimension contiguous")
-    if not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or (
-            block_table.shape[1] > 1 and block_table.stride(1) != 1):
+def _paged(x, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, d, rows):
+    """The cache and the batch of `rows` rows like x as the ABI's struct."""
+    dt, shape, ks, vs = x.dtype, k_cache.shape, k_cache.stride(), v_cache.stride()
+    if k_cache.dtype != dt or v_cache.dtype != dt or not k_cache.is_cuda or not v_cache.is_cuda:
+        raise GdnError(GDN_ERR_ARG, f"k_cache and v_cache must be {dt} CUDA tensors")
+    if len(shape) != 4 or shape[2] != nkv or shape[3] != d or v_cache.shape != shape or ks[3] != 1 or vs[3] != 1:
+        raise GdnError(GDN_ERR_ARG, f"k_cache and v_cache must be [pages, page_size, {nkv}, {d}], the last dimension contiguous")
+    i32, table, ts = _torch.int32, block_table.shape, block_table.stride()
+    if block_table.dtype != i32 or not block_table.is_cuda or len(table) != 2 or (ts[1] != 1 and table[1] > 1):
         raise GdnError(GDN_ERR_ARG, "block_table must be an int32 CUDA tensor [B, max_pages], contiguous in a row")
-    B, most = block_table.shape
-    _check_vector(ctx_lens, "ctx_lens", torch.int32, B)
-    _check_vector(cu_rows, "cu_rows", torch.int32, B + 1)
-    ks, vs = k_cache.stride(), v_cache.stride()
-    return Paged(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], k_cache.shape[0],
-                 k_cache.shape[1], block_table.data_ptr(), max(block_table.stride(0), most), most, B, x.shape[0],
-                 ctx_lens.data_ptr(), _ptr(cu_rows))
+    B, most = table
+    return Paged(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], shape[0], shape[1],
+                 block_table.data_ptr(), max(ts[0], most), most, B, rows, _vector(ctx_lens, "ctx_lens", i32, B),
+                 _vector(cu_rows, "cu_rows", i32, B + 1))
 
 
 def paged_append(k, v, k_cache, v_cache, block_table, ctx_lens, *, nkv: int, head_dim: int = 128, cu_rows=None,
@@ -544,19 +555,14 @@ def paged_append(k, v, k_cache, v_cache, block_table, ctx_lens, *, nkv: int, hea
     sequence's tokens before this call; cu_rows: int32 [B + 1], the rows of each sequence (None: row b belongs to
     sequence b). Row i of sequence b becomes its token ctx_lens[b] + i. ``positions``: int32 [rows] for the
     rotation (None: the token's index); ``cos``, ``sin``, ``interleaved``, ``k_weight``: as ``head_norm_rope``."""
-    import torch
-
-    lib = load()
-    code = _dtype(torch, k, "k", (0, 1))
-    _check_like(torch, k.dtype, (("k", k), ("v", v)))
-    rows = k.shape[0]
-    cache = _paged(torch, k, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, head_dim)
-    _check_vector(positions, "positions", torch.int32, rows)
-    _check_vector(k_weight, "k_weight", torch.float32, head_dim)
-    rc = lib.gdn_paged_append(_ptr(k), _ptr(v), cache, _ptr(positions), _rope(torch, cos, sin, interleaved),
-                              1 if norm else 0, _ptr(k_weight), eps, nkv, head_dim, code,
-                              _rows_of(k, "k", rows, nkv * head_dim), _rows_of(v, "v", rows, nkv * head_dim),
-                              _stream(torch, stream, k.device))
+    torch = _torch or _setup()
+    code, rows, w = _act_code(k, "k", 1), k.shape[0], nkv * head_dim
+    kp, ks = _act(k, "k", k.dtype, rows, w)
+    vp, vs = _act(v, "v", k.dtype, rows, w)
+    rc = _lib.gdn_paged_append(kp, vp, _paged(k, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, head_dim, rows),
+                               _vector(positions, "positions", torch.int32, rows), _rope(cos, sin, interleaved),
+                               1 if norm else 0, _vector(k_weight, "k_weight", torch.float32, head_dim), eps, nkv, head_dim,
+                               code, ks, vs, _stream_of(stream, k.device))
     if rc != GDN_OK:
         _raise(rc)
 
@@ -576,21 +582,20 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_lens, out, *, nq: int, 
     words], bit j % 64 of word j // 64 for new row j), or without a mask those up to itself. A row that sees
     nothing gives zeros. ``max_rows``: the most rows of a sequence, by which the kernel is chosen; ``scale``:
     1/sqrt(head_dim) by default; ``workspace``: uint8 CUDA tensor of ``tree_attention_workspace_bytes(...)``."""
-    import torch
-
-    lib = load()
-    code = _dtype(torch, q, "q", (0, 1))
-    _check_like(torch, q.dtype, (("q", q), ("out", out)))
-    rows = q.shape[0]
-    cache = _paged(torch, q, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, head_dim)
-    if mask is not None and (not mask.is_cuda or mask.dtype != torch.int64 or mask.dim() != 2
-                             or mask.shape[0] != rows or not mask.is_contiguous()):
-        raise GdnError(GDN_ERR_ARG, f"mask must be a contiguous int64 CUDA tensor [{rows}, words]")
-    ws, size = _check_workspace(workspace)
-    rc = lib.gdn_tree_attention(_ptr(q), cache, _ptr(mask), 0 if mask is None else mask.shape[1],
-                                head_dim ** -0.5 if scale is None else scale, _ptr(out), nq, nkv, head_dim, code,
-                                _rows_of(q, "q", rows, nq * head_dim), _rows_of(out, "out", rows, nq * head_dim),
-                                max_rows or 0, ws, size, _stream(torch, stream, q.device))
+    torch = _torch or _setup()
+    code, rows, w = _act_code(q, "q", 1), q.shape[0], nq * head_dim
+    qp, qs = _act(q, "q", q.dtype, rows, w)
+    op, os_ = _act(out, "out", q.dtype, rows, w)
+    cache = _paged(q, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, head_dim, rows)
+    words, mp = 0, None
+    if mask is not None:
+        shape = mask.shape
+        if mask.dtype != torch.int64 or not mask.is_cuda or len(shape) != 2 or shape[0] != rows or not mask.is_contiguous():
+            raise GdnError(GDN_ERR_ARG, f"mask must be a contiguous int64 CUDA tensor [{rows}, words]")
+        words, mp = shape[1], mask.data_ptr()
+    ws, size = _scratch(workspace)
+    rc = _lib.gdn_tree_attention(qp, cache, mp, words, head_dim ** -0.5 if scale is None else scale, op, nq, nkv, head_dim,
+                                 code, qs, os_, max_rows or 0, ws, size, _stream_of(stream, q.device))
     if rc != GDN_OK:
         _raise(rc)
 

@@ -187,5 +187,5 @@ def test_binding_refuses_what_the_library_cannot_see(gdn):
             f()
         assert e.value.code == gdn.GDN_ERR_ARG
     with pytest.raises(gdn.GdnError):
-        gdn._paged(torch, bf, cache.transpose(2, 3), cache, table, i, None, 2, 128)
+        gdn.paged_append(bf, bf, cache.transpose(2, 3), cache, table, i, nkv=2)
     assert ctypes.sizeof(gdn.Paged) == 8 * 8 + 8 + 8 + 8 + 16 + 16
