@@ -327,12 +327,12 @@ int gdn_head_norm_rope_backward(const void* q, const void* k, const int32_t* pos
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaMallocAsync(%zu): %s", need, cudaGetErrorString(e));
   }
   p.partials = static_cast<float*>(ws);
-  const int64_t warps = gdn::kNormThreads / 32, ctas = (static_cast<int64_t>(rows) * p.chunks + warps - 1) / warps;
+  const int64_t warps = gdn::kNormBwdThreads / 32, ctas = (static_cast<int64_t>(rows) * p.chunks + warps - 1) / warps;
   const int64_t slots = static_cast<int64_t>(dev->sms) * kNormBwdCtasPerSm;
   const int grid = static_cast<int>(ctas < slots ? ctas : slots);
   by_type(dtype, [&](auto t) {
     by_head(d, next, [&](auto dim, auto pairs) {
-      gdn::gdn_head_norm_rope_bwd_kernel<decltype(t), dim.value, pairs.value><<<grid, gdn::kNormThreads, 0, s>>>(p);
+      gdn::gdn_head_norm_rope_bwd_kernel<decltype(t), dim.value, pairs.value><<<grid, gdn::kNormBwdThreads, 0, s>>>(p);
     });
   });
   if (sums) {

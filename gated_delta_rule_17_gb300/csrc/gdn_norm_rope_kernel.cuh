@@ -25,8 +25,12 @@ namespace gdn {
 constexpr unsigned kStatusBadPosition = 8u;  // a rotation position outside the table
 constexpr unsigned kStatusBadPage = 16u;     // a page number or token index outside the cache or table
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 128;
+// Registers for 40 warps an SM keep enough loads under way (fp32 words take twice the room: 20).
+template <typename T>
+constexpr int kNormCtasPerSm = sizeof(T) == 4 ? 5 : 10;
 constexpr int kNormUnroll = 4;
+constexpr int kNormBwdThreads = 256;
 
 // ---- four consecutive values of a row -----------------------------------------------
 __device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
@@ -56,6 +60,20 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&f)[4]) {
 }
 __device__ __forceinline__ void store4(__half* p, const float (&f)[4]) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]));
+}
+
+// Four values as they lie in memory (held packed while their load is under way).
+template <typename T>
+struct Four {
+  using Word = uint2;
+};
+template <>
+struct Four<float> {
+  using Word = uint4;
+};
+template <typename T>
+__device__ __forceinline__ void unpack4(const typename Four<T>::Word& w, float (&f)[4]) {
+  load4(reinterpret_cast<const T*>(&w), f);
 }
 
 struct RopeParams {
@@ -125,6 +143,22 @@ struct HeadLane {
     load4(row + b, xb);
     to_pairs(xa, xb, u, v);
   }
+  // The same in two steps: the words, and the pairs in them.
+  template <typename T>
+  __device__ __forceinline__ void fetch(const T* row, bool real, typename Four<T>::Word (&w)[2]) const {
+    w[0] = w[1] = typename Four<T>::Word{};
+    if (real) {
+      w[0] = *reinterpret_cast<const typename Four<T>::Word*>(row + a);
+      w[1] = *reinterpret_cast<const typename Four<T>::Word*>(row + b);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void pairs(const typename Four<T>::Word (&w)[2], float (&u)[4], float (&v)[4]) const {
+    float xa[4], xb[4];
+    unpack4<T>(w[0], xa);
+    unpack4<T>(w[1], xb);
+    to_pairs(xa, xb, u, v);
+  }
   template <typename T>
   __device__ __forceinline__ void store(T* row, const float (&u)[4], const float (&v)[4]) const {
     float xa[4], xb[4];
@@ -150,26 +184,29 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// Norms (unless kNormed is off at run time) and rotates up to kNormUnroll x SLOTS heads of one
-// token row, from `src` to `dst` (head h at h * src_head, h * dst_head).
+// The words of up to kNormUnroll x SLOTS heads of one token row (head h at h * src_head): the first
+// loads of a warp, before it looks up where and how far to turn them.
 template <typename T, int D, bool kNext>
-__device__ __forceinline__ void norm_rope_heads(const T* src, T* dst, int64_t src_head, int64_t dst_head, int h0,
-                                                int heads, const float* weight, bool normed, float eps,
+__device__ __forceinline__ void fetch_heads(const T* src, int64_t src_head, int h0, int heads, int rot,
+                                            typename Four<T>::Word (&x)[kNormUnroll][2]) {
+  constexpr int LPH = D / 8, SLOTS = 32 / LPH;
+  const int lane = threadIdx.x & 31, slot = lane / LPH;
+  const HeadLane<D, kNext> hl(lane % LPH, rot);
+#pragma unroll
+  for (int i = 0; i < kNormUnroll; ++i) {
+    const int h = h0 + i * SLOTS + slot;
+    hl.fetch(src + h * src_head, h < heads, x[i]);
+  }
+}
+
+// Norms (where `normed`) and rotates them, and writes them to `dst` (head h at h * dst_head).
+template <typename T, int D, bool kNext>
+__device__ __forceinline__ void norm_rope_heads(const typename Four<T>::Word (&x)[kNormUnroll][2], T* dst, int64_t dst_head,
+                                                int h0, int heads, const float* weight, bool normed, float eps,
                                                 const RopeParams& rope, int64_t pos) {
   constexpr int LPH = D / 8, SLOTS = 32 / LPH;
   const int lane = threadIdx.x & 31, l = lane % LPH, slot = lane / LPH;
   const HeadLane<D, kNext> hl(l, rope.rot);
-  float u[kNormUnroll][4], v[kNormUnroll][4];
-#pragma unroll
-  for (int i = 0; i < kNormUnroll; ++i) {
-    const int h = h0 + i * SLOTS + slot;
-    if (h < heads) {
-      hl.load(src + h * src_head, u[i], v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[i][j] = v[i][j] = 0.f;
-    }
-  }
   float c[4], s[4], wu[4], wv[4];
   hl.angles(rope, pos, c, s);
   hl.weights(weight, wu, wv);
@@ -184,18 +221,19 @@ __device__ __forceinline__ void norm_rope_heads(const T* src, T* dst, int64_t sr
 #pragma unroll
   for (int i = 0; i < kNormUnroll; ++i) {
     const int h = h0 + i * SLOTS + slot;
-    float r = 1.f;
+    float u[4], v[4], r = 1.f;
+    hl.template pairs<T>(x[i], u, v);
     if (normed) {  // the same for the whole warp
       float q = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) q = fmaf(u[i][j], u[i][j], fmaf(v[i][j], v[i][j], q));
+      for (int j = 0; j < 4; ++j) q = fmaf(u[j], u[j], fmaf(v[j], v[j], q));
       r = rsqrtf(row_sum<LPH>(q) * (1.f / D) + eps);
     }
     float yu[4], yv[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      yu[j] = r * (u[i][j] * uc[j] - v[i][j] * vs[j]);
-      yv[j] = r * (v[i][j] * vc[j] + u[i][j] * us[j]);
+      yu[j] = r * (u[j] * uc[j] - v[j] * vs[j]);
+      yv[j] = r * (v[j] * vc[j] + u[j] * us[j]);
     }
     if (h < heads) hl.store(dst + h * dst_head, yu, yv);
   }
@@ -220,33 +258,29 @@ struct NormRopeParams {
   unsigned* status;
 };
 
-// The position of a row, or -1 (and the status bit) where the table does not hold it.
-__device__ __forceinline__ int64_t row_position(const int32_t* positions, int row, const RopeParams& rope,
-                                                unsigned* status) {
-  if (rope.rot == 0) return 0;
-  const int pos = positions[row];
-  if (pos < 0 || pos >= rope.positions) {
-    if ((threadIdx.x & 31) == 0) atomicOr(status, kStatusBadPosition);
-    return -1;
-  }
-  return pos;
+// Whether the table holds a row's position; reports it where not.
+__device__ __forceinline__ bool position_held(int64_t pos, const RopeParams& rope, unsigned* status) {
+  if (rope.rot == 0 || (pos >= 0 && pos < rope.positions)) return true;
+  if ((threadIdx.x & 31) == 0) atomicOr(status, kStatusBadPosition);
+  return false;
 }
 
 template <typename T, int D, bool kNext>
-__global__ void __launch_bounds__(kNormThreads) gdn_head_norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kNormThreads, kNormCtasPerSm<T>) gdn_head_norm_rope_kernel(const NormRopeParams p) {
   constexpr int PER = kNormUnroll * (32 / (D / 8));  // heads of an item
   const unsigned item = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
   const unsigned row = item / static_cast<unsigned>(p.chunks);
   if (row >= static_cast<unsigned>(p.rows)) return;
   const int ch = static_cast<int>(item - row * p.chunks);
-  const int64_t pos = row_position(p.positions, static_cast<int>(row), p.rope, p.status);
-  if (pos < 0) return;
-  if (ch < p.q_chunks)
-    norm_rope_heads<T, D, kNext>(static_cast<const T*>(p.q) + row * p.q_stride, static_cast<T*>(p.q_out) + row * p.q_out_stride,
-                                 D, D, ch * PER, p.nq, p.q_weight, true, p.eps, p.rope, pos);
-  else
-    norm_rope_heads<T, D, kNext>(static_cast<const T*>(p.k) + row * p.k_stride, static_cast<T*>(p.k_out) + row * p.k_out_stride,
-                                 D, D, (ch - p.q_chunks) * PER, p.nkv, p.k_weight, true, p.eps, p.rope, pos);
+  const bool is_q = ch < p.q_chunks;
+  const int h0 = (is_q ? ch : ch - p.q_chunks) * PER, heads = is_q ? p.nq : p.nkv;
+  const int pos = p.rope.rot ? p.positions[row] : 0;
+  typename Four<T>::Word x[kNormUnroll][2];
+  fetch_heads<T, D, kNext>(is_q ? static_cast<const T*>(p.q) + row * p.q_stride : static_cast<const T*>(p.k) + row * p.k_stride,
+                           D, h0, heads, p.rope.rot, x);
+  if (!position_held(pos, p.rope, p.status)) return;
+  norm_rope_heads<T, D, kNext>(x, is_q ? static_cast<T*>(p.q_out) + row * p.q_out_stride : static_cast<T*>(p.k_out) + row * p.k_out_stride,
+                               D, h0, heads, is_q ? p.q_weight : p.k_weight, true, p.eps, p.rope, pos);
 }
 
 // ---- backward ------------------------------------------------------------------------
@@ -303,8 +337,8 @@ __device__ __forceinline__ void norm_rope_heads_bwd(const T* x, const T* dy, T* 
 // A fixed grid walks the items, so that the weight gradients' sums stay in registers; each
 // CTA adds its warps' sums in a fixed order and writes one row of partials for q and for k.
 template <typename T, int D, bool kNext>
-__global__ void __launch_bounds__(kNormThreads) gdn_head_norm_rope_bwd_kernel(const NormRopeParams p) {
-  constexpr int LPH = D / 8, SLOTS = 32 / LPH, PER = kNormBwdUnroll * SLOTS, WARPS = kNormThreads / 32;
+__global__ void __launch_bounds__(kNormBwdThreads) gdn_head_norm_rope_bwd_kernel(const NormRopeParams p) {
+  constexpr int LPH = D / 8, SLOTS = 32 / LPH, PER = kNormBwdUnroll * SLOTS, WARPS = kNormBwdThreads / 32;
   __shared__ __align__(16) float s_sum[WARPS][2][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned items = static_cast<unsigned>(p.rows) * static_cast<unsigned>(p.chunks);
@@ -312,8 +346,8 @@ __global__ void __launch_bounds__(kNormThreads) gdn_head_norm_rope_bwd_kernel(co
   for (unsigned item = blockIdx.x * WARPS + warp; item < items; item += gridDim.x * WARPS) {
     const unsigned row = item / static_cast<unsigned>(p.chunks);
     const int ch = static_cast<int>(item - row * p.chunks);
-    const int64_t pos = row_position(p.positions, static_cast<int>(row), p.rope, p.status);
-    if (pos < 0) continue;
+    const int pos = p.rope.rot ? p.positions[row] : 0;
+    if (!position_held(pos, p.rope, p.status)) continue;
     if (ch < p.q_chunks)
       norm_rope_heads_bwd<T, D, kNext>(static_cast<const T*>(p.q) + row * p.q_stride,
                                        static_cast<const T*>(p.q_grad) + row * p.q_grad_stride,
@@ -342,7 +376,7 @@ __global__ void __launch_bounds__(kNormThreads) gdn_head_norm_rope_bwd_kernel(co
     hl.store(&s_sum[warp][1][0], ku, kv);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kNormThreads) {
+  for (int i = threadIdx.x; i < 2 * D; i += kNormBwdThreads) {
     float t = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) t += (&s_sum[w][0][0])[i];
@@ -416,7 +450,7 @@ struct AppendParams {
 };
 
 template <typename T, int D, bool kNext>
-__global__ void __launch_bounds__(kNormThreads) gdn_paged_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kNormThreads, kNormCtasPerSm<T>) gdn_paged_append_kernel(const AppendParams p) {
   constexpr int LPH = D / 8, SLOTS = 32 / LPH, PER = kNormUnroll * SLOTS;
   const unsigned per_row = 2u * static_cast<unsigned>(p.chunks);
   const unsigned item = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
@@ -424,8 +458,14 @@ __global__ void __launch_bounds__(kNormThreads) gdn_paged_append_kernel(const Ap
   const PagedParams& c = p.cache;
   if (row >= static_cast<unsigned>(c.rows)) return;
   int ch = static_cast<int>(item - row * per_row);
+  const bool is_k = ch < p.chunks;
+  if (!is_k) ch -= p.chunks;
   const int lane = threadIdx.x & 31;
-  // the token's place in the cache
+  // the heads first: their loads overlap the look-up of the token's place. Values are copied as
+  // they are, which is a key's way without a rotation.
+  typename Four<T>::Word x[kNormUnroll][2];
+  fetch_heads<T, D, kNext>(is_k ? static_cast<const T*>(p.k) + row * p.k_stride : static_cast<const T*>(p.v) + row * p.v_stride,
+                           D, ch * PER, p.nkv, is_k ? p.rope.rot : 0, x);
   const int b = c.cu_rows ? find_sequence(c.cu_rows, c.B, static_cast<int>(row)) : static_cast<int>(row);
   const int first = c.cu_rows ? c.cu_rows[b] : static_cast<int>(row);
   const int end = c.cu_rows ? c.cu_rows[b + 1] : static_cast<int>(row) + 1;
@@ -435,45 +475,31 @@ __global__ void __launch_bounds__(kNormThreads) gdn_paged_append_kernel(const Ap
     return;
   }
   const int64_t token = static_cast<int64_t>(ctx) + (static_cast<int>(row) - first);
-  const int64_t at = token / c.page_size;
-  const int page = at < c.max_pages ? c.block_table[b * c.table_stride + at] : -1;
+  // (below max_pages * page_size < 2^31 where it counts; the division is 32-bit then)
+  const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_size;
+  const unsigned at = token < room ? static_cast<unsigned>(token) / static_cast<unsigned>(c.page_size) : 0u;
+  const int page = token < room ? c.block_table[b * c.table_stride + at] : -1;
   if (page < 0 || page >= c.num_pages) {
     if (lane == 0) atomicOr(p.status, kStatusBadPage);
     return;
   }
-  const int64_t place = token - at * c.page_size;
-  if (ch < p.chunks) {
-    int64_t pos = 0;
-    if (p.rope.rot) {
-      pos = p.positions ? p.positions[row] : token;
-      if (pos < 0 || pos >= p.rope.positions) {
-        if (lane == 0) atomicOr(p.status, kStatusBadPosition);
-        return;
+  const int64_t place = token - static_cast<int64_t>(at) * c.page_size;
+  const int64_t pos = p.positions && p.rope.rot ? p.positions[row] : token;
+  if (!position_held(pos, p.rope, p.status)) return;  // the token is left out whole
+  if (is_k) {
+    norm_rope_heads<T, D, kNext>(x, static_cast<T*>(c.k) + page * c.k_page + place * c.k_token, c.k_head, ch * PER, p.nkv,
+                                 p.k_weight, p.norm != 0, p.eps, p.rope, pos);
+  } else {
+    const HeadLane<D, kNext> hl(lane % LPH, 0);
+    T* dst = static_cast<T*>(c.v) + page * c.v_page + place * c.v_token;
+#pragma unroll
+    for (int i = 0; i < kNormUnroll; ++i) {
+      const int h = ch * PER + i * SLOTS + lane / LPH;
+      if (h < p.nkv) {
+        *reinterpret_cast<typename Four<T>::Word*>(dst + h * c.v_head + hl.a) = x[i][0];
+        *reinterpret_cast<typename Four<T>::Word*>(dst + h * c.v_head + hl.b) = x[i][1];
       }
     }
-    norm_rope_heads<T, D, kNext>(static_cast<const T*>(p.k) + row * p.k_stride,
-                                 static_cast<T*>(c.k) + page * c.k_page + place * c.k_token, D, c.k_head, ch * PER, p.nkv,
-                                 p.k_weight, p.norm != 0, p.eps, p.rope, pos);
-    return;
-  }
-  ch -= p.chunks;
-  if (p.rope.rot) {  // a token with a bad position is left out whole
-    const int64_t pos = p.positions ? p.positions[row] : token;
-    if (pos < 0 || pos >= p.rope.positions) return;
-  }
-  const int l = lane % LPH, slot = lane / LPH;
-  const T* src = static_cast<const T*>(p.v) + row * p.v_stride + 8 * l;
-  T* dst = static_cast<T*>(c.v) + page * c.v_page + place * c.v_token + 8 * l;
-  uint4 x[kNormUnroll];
-#pragma unroll
-  for (int i = 0; i < kNormUnroll; ++i) {
-    const int h = ch * PER + i * SLOTS + slot;
-    if (h < p.nkv) x[i] = *reinterpret_cast<const uint4*>(src + h * D);
-  }
-#pragma unroll
-  for (int i = 0; i < kNormUnroll; ++i) {
-    const int h = ch * PER + i * SLOTS + slot;
-    if (h < p.nkv) *reinterpret_cast<uint4*>(dst + h * c.v_head) = x[i];
   }
 }
 
