@@ -47,8 +47,6 @@ int check_stride(int64_t stride, int64_t least, const char* name) {
   return GDN_OK;
 }
 
-constexpr int kNormBwdCtasPerSm = 4;
-
 int norm_chunks(int heads, int d, int unroll) {
   const int per = unroll * (32 / (d / 8));
   return (heads + per - 1) / per;
@@ -279,7 +277,7 @@ size_t gdn_head_norm_rope_backward_workspace_bytes(int rows, int nq, int nkv, in
   (void)nq;
   (void)nkv;
   if (rows <= 0 || (d != 64 && d != 128)) return 0;
-  return static_cast<size_t>(plan_sms()) * kNormBwdCtasPerSm * 2 * d * sizeof(float);
+  return (static_cast<size_t>(plan_sms()) * gdn::kNormBwdCtasPerSm + 2) * d * sizeof(float);
 }
 
 int gdn_head_norm_rope_backward(const void* q, const void* k, const int32_t* positions, const gdn_rope_t* rope,
@@ -292,7 +290,7 @@ int gdn_head_norm_rope_backward(const void* q, const void* k, const int32_t* pos
   gdn::NormRopeParams p;
   int next = 0;
   if (int rc = norm_setup(q, k, positions, rope, q_weight, k_weight, eps, dq, dk, rows, nq, nkv, d, dtype, strides,
-                          gdn::kNormBwdUnroll, &p, &next))
+                          gdn::kNormUnroll, &p, &next))
     return rc;
   if (nq)
     if (int rc = check_stride(p.q_grad_stride, static_cast<int64_t>(nq) * d, "q_grad")) return rc;
@@ -327,17 +325,43 @@ int gdn_head_norm_rope_backward(const void* q, const void* k, const int32_t* pos
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaMallocAsync(%zu): %s", need, cudaGetErrorString(e));
   }
   p.partials = static_cast<float*>(ws);
-  const int64_t warps = gdn::kNormBwdThreads / 32, ctas = (static_cast<int64_t>(rows) * p.chunks + warps - 1) / warps;
-  const int64_t slots = static_cast<int64_t>(dev->sms) * kNormBwdCtasPerSm;
-  const int grid = static_cast<int>(ctas < slots ? ctas : slots);
+  // the grid's CTAs in proportion to the heads, at least one each; a token's heads are cut into as
+  // many runs as it takes to give every warp one
+  const int slots = dev->sms * gdn::kNormBwdCtasPerSm, warps = gdn::kNormBwdThreads / 32;
+  auto side = [&](int heads, int* parts, int* per) -> int {
+    *parts = *per = 1;
+    if (!heads) return 0;
+    const int step = 256 / d * (dtype == GDN_F32 ? 1 : 2), steps = (heads + step - 1) / step;
+    int share = static_cast<int>(static_cast<int64_t>(slots) * heads / (nq + nkv));
+    if (share < 1) share = 1;
+    int64_t cuts = (static_cast<int64_t>(share) * warps + rows - 1) / rows;
+    if (cuts > steps) cuts = steps;
+    const int run = (steps + static_cast<int>(cuts) - 1) / static_cast<int>(cuts);
+    *per = run * step;
+    *parts = (steps + run - 1) / run;
+    const int64_t need = (static_cast<int64_t>(rows) * *parts + warps - 1) / warps;
+    return need < share ? static_cast<int>(need) : share;
+  };
+  p.q_ctas = side(nq, &p.q_parts, &p.q_per);
+  const int grid = p.q_ctas + side(nkv, &p.k_parts, &p.k_per);
   by_type(dtype, [&](auto t) {
     by_head(d, next, [&](auto dim, auto pairs) {
       gdn::gdn_head_norm_rope_bwd_kernel<decltype(t), dim.value, pairs.value><<<grid, gdn::kNormBwdThreads, 0, s>>>(p);
     });
   });
   if (sums) {
-    if (d == 64) gdn::gdn_norm_weight_sum_kernel<64><<<2, 1024, 0, s>>>(p.partials, grid, dq_weight, dk_weight);
-    else gdn::gdn_norm_weight_sum_kernel<128><<<2, 1024, 0, s>>>(p.partials, grid, dq_weight, dk_weight);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = a;
+    cfg.numAttrs = 1;
+    const float* parts = p.partials;
+    cudaLaunchKernelEx(&cfg, d == 64 ? gdn::gdn_norm_weight_sum_kernel<64> : gdn::gdn_norm_weight_sum_kernel<128>, parts,
+                       static_cast<int>(p.q_ctas), grid, dq_weight, dk_weight);  // a refusal is launched()'s to report
   }
   int rc = launched(sums ? 2 : 1);
   if (sums && !workspace) {

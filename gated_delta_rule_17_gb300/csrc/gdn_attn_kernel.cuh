@@ -58,11 +58,6 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// 16 bytes to shared memory, or zeros.
-__device__ __forceinline__ void cp_async_16(uint32_t dst_saddr, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_saddr), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-
 // Byte offset of 16-byte piece c of row r: pieces are exchanged within a row by the row's number,
 // so that eight rows' pieces c lie in different banks.
 template <int D>

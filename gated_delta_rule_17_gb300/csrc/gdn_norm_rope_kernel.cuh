@@ -30,7 +30,8 @@ constexpr int kNormThreads = 128;
 template <typename T>
 constexpr int kNormCtasPerSm = sizeof(T) == 4 ? 5 : 10;
 constexpr int kNormUnroll = 4;
-constexpr int kNormBwdThreads = 256;
+constexpr int kNormBwdThreads = 128;
+constexpr int kNormBwdCtasPerSm = 6;
 
 // ---- four consecutive values of a row -----------------------------------------------
 __device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
@@ -176,6 +177,14 @@ struct HeadLane {
   }
 };
 
+// 16 bytes to shared memory, or zeros; and through L1, for what several warps read.
+__device__ __forceinline__ void cp_async_16(uint32_t dst_saddr, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_saddr), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_16_ca(uint32_t dst_saddr, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst_saddr), "l"(src) : "memory");
+}
+
 // Sum over the LPH lanes that hold one head row.
 template <int LPH>
 __device__ __forceinline__ float row_sum(float x) {
@@ -250,7 +259,9 @@ struct NormRopeParams {
   RopeParams rope;
   const float* q_weight;
   const float* k_weight;
-  float* partials;  // backward: [grid][2][D] sums of the weight gradients, or null
+  float* partials;  // backward: [grid][D] sums of the weight gradients, or null
+  int q_ctas;       // backward: CTAs for q, and the runs that a token's heads are cut into
+  int q_parts, k_parts, q_per, k_per;
   int64_t q_stride, k_stride, q_out_stride, k_out_stride, q_grad_stride, k_grad_stride;
   int rows, nq, nkv;
   int q_chunks, chunks;  // warp items of a token: q_chunks for q's heads, the rest for k's
@@ -284,118 +295,248 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtasPerSm<T>) gdn_head_norm
 }
 
 // ---- backward ------------------------------------------------------------------------
-constexpr int kNormBwdUnroll = 2;
+// A fixed grid, the first q_ctas CTAs for q and the rest for k, so that the weight gradient's sums
+// stay in registers. A warp walks its share of (token, run of heads) items, U x SLOTS heads a step,
+// and copies x, dy and the angles of the next STAGES - 1 steps into its own ring in shared memory
+// (cp.async): with the words in registers instead, the loads under way were too few (294 us for 4 x
+// 8192 tokens of 32 + 8 heads) or spilled. What bounds it then is the issue of instructions (two
+// thirds of all slots at one head a lane group and step, 216 us), so a step has two heads and the
+// arithmetic goes in pairs of fp32. Each CTA adds its warps' sums in a fixed order and writes one
+// row of partials.
+template <typename T, int D>
+struct NormBwdPlan {
+  static constexpr int WARPS = kNormBwdThreads / 32, SLOTS = 256 / D, U = sizeof(T) == 4 ? 1 : 2;
+  static constexpr int ROW = D * static_cast<int>(sizeof(T));
+  static constexpr int HEADS = U * SLOTS * ROW;  // bytes of a step's x or dy
+  static constexpr int STEP = 2 * HEADS + 4 * D;  // and its cosines and sines
+  static constexpr int STAGES = 3;
+  static constexpr int BYTES = WARPS * STAGES * STEP;
+};
 
-// dx of up to kNormBwdUnroll x SLOTS heads of one token row; adds dz x r to the lane's sums.
-template <typename T, int D, bool kNext>
-__device__ __forceinline__ void norm_rope_heads_bwd(const T* x, const T* dy, T* dx, int h0, int heads,
-                                                    const float* weight, float eps, const RopeParams& rope,
-                                                    int64_t pos, float (&du)[4], float (&dv)[4]) {
-  constexpr int LPH = D / 8, SLOTS = 32 / LPH;
-  const int lane = threadIdx.x & 31, l = lane % LPH, slot = lane / LPH;
-  const HeadLane<D, kNext> hl(l, rope.rot);
-  float u[kNormBwdUnroll][4], v[kNormBwdUnroll][4], gu[kNormBwdUnroll][4], gv[kNormBwdUnroll][4];
-#pragma unroll
-  for (int i = 0; i < kNormBwdUnroll; ++i) {
-    const int h = h0 + i * SLOTS + slot;
-    if (h < heads) {
-      hl.load(x + h * D, u[i], v[i]);
-      hl.load(dy + h * D, gu[i], gv[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[i][j] = v[i][j] = gu[i][j] = gv[i][j] = 0.f;
-    }
-  }
-  float c[4], s[4], wu[4], wv[4];
-  hl.angles(rope, pos, c, s);
-  hl.weights(weight, wu, wv);
-#pragma unroll
-  for (int i = 0; i < kNormBwdUnroll; ++i) {
-    const int h = h0 + i * SLOTS + slot;
-    float zu[4], zv[4], q = 0.f, m = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      zu[j] = gu[i][j] * c[j] + gv[i][j] * s[j];
-      zv[j] = gv[i][j] * c[j] - gu[i][j] * s[j];
-      q = fmaf(u[i][j], u[i][j], fmaf(v[i][j], v[i][j], q));
-      m = fmaf(zu[j] * wu[j], u[i][j], fmaf(zv[j] * wv[j], v[i][j], m));
-    }
-    const float r = rsqrtf(row_sum<LPH>(q) * (1.f / D) + eps);
-    const float f = r * r * (row_sum<LPH>(m) * (1.f / D));
-    float xu[4], xv[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      du[j] = fmaf(zu[j], u[i][j] * r, du[j]);
-      dv[j] = fmaf(zv[j], v[i][j] * r, dv[j]);
-      xu[j] = r * (zu[j] * wu[j] - u[i][j] * f);
-      xv[j] = r * (zv[j] * wv[j] - v[i][j] * f);
-    }
-    if (h < heads) hl.store(dx + h * D, xu, xv);
-  }
+// Two fp32 values in one register pair, and the paired arithmetic of sm_100 and up.
+using Pair = uint64_t;
+__device__ __forceinline__ Pair pair_of(float a, float b) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void parts_of(Pair p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void to_pairs2(const float (&x)[4], Pair (&p)[2]) {
+  p[0] = pair_of(x[0], x[1]);
+  p[1] = pair_of(x[2], x[3]);
+}
+__device__ __forceinline__ void from_pairs2(const Pair (&p)[2], float (&x)[4]) {
+  parts_of(p[0], x[0], x[1]);
+  parts_of(p[1], x[2], x[3]);
 }
 
-// A fixed grid walks the items, so that the weight gradients' sums stay in registers; each
-// CTA adds its warps' sums in a fixed order and writes one row of partials for q and for k.
 template <typename T, int D, bool kNext>
-__global__ void __launch_bounds__(kNormBwdThreads) gdn_head_norm_rope_bwd_kernel(const NormRopeParams p) {
-  constexpr int LPH = D / 8, SLOTS = 32 / LPH, PER = kNormBwdUnroll * SLOTS, WARPS = kNormBwdThreads / 32;
-  __shared__ __align__(16) float s_sum[WARPS][2][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned items = static_cast<unsigned>(p.rows) * static_cast<unsigned>(p.chunks);
-  float qu[4] = {}, qv[4] = {}, ku[4] = {}, kv[4] = {};
-  for (unsigned item = blockIdx.x * WARPS + warp; item < items; item += gridDim.x * WARPS) {
-    const unsigned row = item / static_cast<unsigned>(p.chunks);
-    const int ch = static_cast<int>(item - row * p.chunks);
-    const int pos = p.rope.rot ? p.positions[row] : 0;
-    if (!position_held(pos, p.rope, p.status)) continue;
-    if (ch < p.q_chunks)
-      norm_rope_heads_bwd<T, D, kNext>(static_cast<const T*>(p.q) + row * p.q_stride,
-                                       static_cast<const T*>(p.q_grad) + row * p.q_grad_stride,
-                                       static_cast<T*>(p.q_out) + row * p.q_out_stride, ch * PER, p.nq, p.q_weight,
-                                       p.eps, p.rope, pos, qu, qv);
-    else
-      norm_rope_heads_bwd<T, D, kNext>(static_cast<const T*>(p.k) + row * p.k_stride,
-                                       static_cast<const T*>(p.k_grad) + row * p.k_grad_stride,
-                                       static_cast<T*>(p.k_out) + row * p.k_out_stride, (ch - p.q_chunks) * PER, p.nkv,
-                                       p.k_weight, p.eps, p.rope, pos, ku, kv);
+__global__ void __launch_bounds__(kNormBwdThreads, kNormBwdCtasPerSm)
+gdn_head_norm_rope_bwd_kernel(const NormRopeParams p) {
+  using Plan = NormBwdPlan<T, D>;
+  constexpr int LPH = D / 8, SLOTS = Plan::SLOTS, U = Plan::U, WARPS = Plan::WARPS, STAGES = Plan::STAGES, ROW = Plan::ROW;
+  __shared__ __align__(16) uint8_t s_ring[Plan::BYTES];
+  __shared__ __align__(16) float s_sum[WARPS][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPH, slot = lane / LPH;
+  uint8_t* ring = s_ring + warp * STAGES * Plan::STEP;
+  const bool is_q = static_cast<int>(blockIdx.x) < p.q_ctas;
+  const T* x = static_cast<const T*>(is_q ? p.q : p.k);
+  const T* dy = static_cast<const T*>(is_q ? p.q_grad : p.k_grad);
+  T* dx = static_cast<T*>(is_q ? p.q_out : p.k_out);
+  const int64_t xs = is_q ? p.q_stride : p.k_stride, gs = is_q ? p.q_grad_stride : p.k_grad_stride,
+                ds = is_q ? p.q_out_stride : p.k_out_stride;
+  const int heads = is_q ? p.nq : p.nkv;
+  const unsigned parts = is_q ? p.q_parts : p.k_parts, per = is_q ? p.q_per : p.k_per;
+  const unsigned items = static_cast<unsigned>(p.rows) * parts;
+  const unsigned stride = (is_q ? p.q_ctas : gridDim.x - p.q_ctas) * WARPS;
+  const HeadLane<D, kNext> hl(l, p.rope.rot);
+  Pair wu[2], wv[2], du[2] = {0, 0}, dv[2] = {0, 0};
+  {
+    float a[4], b[4];
+    hl.weights(is_q ? p.q_weight : p.k_weight, a, b);
+    to_pairs2(a, wu);
+    to_pairs2(b, wv);
   }
+
+  // Two walks over the steps: one fetches, one computes and writes.
+  unsigned f_item = (is_q ? blockIdx.x : blockIdx.x - p.q_ctas) * WARPS + warp, c_item = f_item;
+  int f_left = 0, c_left = 0, pos = 0;  // heads that the item still has
+  const uint8_t *f_x = nullptr, *f_g = nullptr;
+  const float* f_angle = nullptr;
+  T* c_dx = nullptr;
+  bool f_ok = false;
+  const int pieces = p.rope.rot >> 3;  // 16-byte pieces of the cosines, and of the sines
+  const bool sine = lane >= pieces;
+  const int piece = 4 * (sine ? lane - pieces : lane);
+  auto item_heads = [&](unsigned item, unsigned* row, int* h) {
+    *row = item / parts;
+    *h = static_cast<int>((item - *row * parts) * per);
+    return *h + static_cast<int>(per) < heads ? static_cast<int>(per) : heads - *h;
+  };
+  auto f_enter = [&] {
+    if (f_item >= items) return;
+    unsigned row;
+    int h;
+    f_left = item_heads(f_item, &row, &h);
+    if (p.rope.rot) {
+      pos = p.positions[row];
+      f_ok = position_held(pos, p.rope, p.status);
+      f_angle = (sine ? p.rope.sin : p.rope.cos) + static_cast<int64_t>(f_ok ? pos : 0) * p.rope.stride + piece;
+    } else {
+      f_ok = true;
+    }
+    f_x = reinterpret_cast<const uint8_t*>(x + row * xs + static_cast<int64_t>(h) * D);
+    f_g = reinterpret_cast<const uint8_t*>(dy + row * gs + static_cast<int64_t>(h) * D);
+  };
+  auto c_enter = [&] {
+    if (c_item >= items) return;
+    unsigned row;
+    int h;
+    c_left = item_heads(c_item, &row, &h);
+    c_dx = dx + row * ds + static_cast<int64_t>(h + slot) * D;
+  };
+  unsigned held = 0;  // a bit a fetched step, the newest last: its position is in the table
+  auto fetch = [&](int stage) {
+    held <<= 1;
+    if (f_item < items) {
+      const uint32_t dst = tc::smem_u32(ring) + stage * Plan::STEP;
+      held |= f_ok ? 1u : 0u;
+#pragma unroll
+      for (int b = 0; b < Plan::HEADS; b += 512) {
+        const int at = b + 16 * lane;
+        const bool real = f_ok && at / ROW < f_left;
+        cp_async_16(dst + at, f_x + (real ? at : 0), real);
+        cp_async_16(dst + Plan::HEADS + at, f_g + (real ? at : 0), real);
+      }
+      if (lane < 2 * pieces) cp_async_16_ca(dst + 2 * Plan::HEADS + (sine ? 2 * D : 0) + 4 * piece, f_angle);
+      f_x += Plan::HEADS;
+      f_g += Plan::HEADS;
+      f_left -= U * SLOTS;
+      if (f_left <= 0) {
+        f_item += stride;
+        f_enter();
+      }
+    }
+    tc::cp_async_commit();
+  };
+  f_enter();
+  c_enter();
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+  for (int stage = 0; c_item < items; stage = stage + 1 < STAGES ? stage + 1 : 0) {
+    fetch(stage == 0 ? STAGES - 1 : stage - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+    __syncwarp();
+    const uint8_t* src = ring + stage * Plan::STEP;
+    Pair c[2], s[2], ns[2];
+    {
+      const float* angles = reinterpret_cast<const float*>(src + 2 * Plan::HEADS);
+      float a[4], b[4];
+      hl.angles(RopeParams{angles, angles + D / 2, 0, 1, p.rope.rot}, 0, a, b);
+      to_pairs2(a, c);
+      to_pairs2(b, s);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) ns[j] = s[j] ^ 0x8000000080000000ull;
+    }
+    const bool ok = (held >> (STAGES - 1)) & 1;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      Pair u[2], v[2], gu[2], gv[2], zu[2], zv[2], tu[2], tv[2];
+      {
+        float a[4], b[4];
+        hl.load(reinterpret_cast<const T*>(src) + (i * SLOTS + slot) * D, a, b);
+        to_pairs2(a, u);
+        to_pairs2(b, v);
+        hl.load(reinterpret_cast<const T*>(src + Plan::HEADS) + (i * SLOTS + slot) * D, a, b);
+        to_pairs2(a, gu);
+        to_pairs2(b, gv);
+      }
+      Pair q2 = 0, m2 = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        zu[j] = fma2(gu[j], c[j], mul2(gv[j], s[j]));
+        zv[j] = fma2(gv[j], c[j], mul2(gu[j], ns[j]));
+        tu[j] = mul2(zu[j], wu[j]);
+        tv[j] = mul2(zv[j], wv[j]);
+        q2 = fma2(u[j], u[j], fma2(v[j], v[j], q2));
+        m2 = fma2(tu[j], u[j], fma2(tv[j], v[j], m2));
+      }
+      float qa, qb, ma, mb;
+      parts_of(q2, qa, qb);
+      parts_of(m2, ma, mb);
+      const float r = rsqrtf(row_sum<LPH>(qa + qb) * (1.f / D) + p.eps);
+      const float f = -r * r * r * (row_sum<LPH>(ma + mb) * (1.f / D));
+      if (ok && i * SLOTS + slot < c_left) {
+        const Pair rr = pair_of(r, r), ff = pair_of(f, f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          du[j] = fma2(zu[j], mul2(u[j], rr), du[j]);
+          dv[j] = fma2(zv[j], mul2(v[j], rr), dv[j]);
+          tu[j] = fma2(u[j], ff, mul2(tu[j], rr));
+          tv[j] = fma2(v[j], ff, mul2(tv[j], rr));
+        }
+        float a[4], b[4];
+        from_pairs2(tu, a);
+        from_pairs2(tv, b);
+        hl.store(c_dx + i * SLOTS * D, a, b);
+      }
+    }
+    __syncwarp();  // the stage is read before the next step's fetch overwrites it
+    c_dx += U * SLOTS * D;
+    c_left -= U * SLOTS;
+    if (c_left <= 0) {
+      c_item += stride;
+      c_enter();
+    }
+  }
+  float su[4], sv[4];
+  from_pairs2(du, su);
+  from_pairs2(dv, sv);
   if (!p.partials) return;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {  // over the head rows that a warp holds side by side
 #pragma unroll
     for (int o = LPH; o < 32; o <<= 1) {
-      qu[j] += __shfl_xor_sync(0xffffffffu, qu[j], o);
-      qv[j] += __shfl_xor_sync(0xffffffffu, qv[j], o);
-      ku[j] += __shfl_xor_sync(0xffffffffu, ku[j], o);
-      kv[j] += __shfl_xor_sync(0xffffffffu, kv[j], o);
+      su[j] += __shfl_xor_sync(0xffffffffu, su[j], o);
+      sv[j] += __shfl_xor_sync(0xffffffffu, sv[j], o);
     }
   }
-  if (lane < LPH) {
-    const HeadLane<D, kNext> hl(lane, p.rope.rot);
-    hl.store(&s_sum[warp][0][0], qu, qv);
-    hl.store(&s_sum[warp][1][0], ku, kv);
-  }
+  if (lane < LPH) hl.store(&s_sum[warp][0], su, sv);
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kNormBwdThreads) {
+  for (int i = threadIdx.x; i < D; i += kNormBwdThreads) {
     float t = 0.f;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) t += (&s_sum[w][0][0])[i];
-    p.partials[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = t;
+    for (int w = 0; w < WARPS; ++w) t += s_sum[w][i];
+    p.partials[static_cast<int64_t>(blockIdx.x) * D + i] = t;
   }
 }
 
-// dw[i] = sum over the grid's partials, in a fixed order: one CTA for q's and one for k's
-// weights, D threads wide and 1024 / D partials at a time.
+// dw[i] = sum over the partials of q's CTAs (block 0) or k's (block 1), in a fixed order: D threads
+// wide and 1024 / D partials at a time.
 template <int D>
-__global__ void __launch_bounds__(1024) gdn_norm_weight_sum_kernel(const float* partials, int n, float* dq_weight,
-                                                                  float* dk_weight) {
+__global__ void __launch_bounds__(1024) gdn_norm_weight_sum_kernel(const float* partials, int q_ctas, int ctas,
+                                                                  float* dq_weight, float* dk_weight) {
   constexpr int LANES = 1024 / D;
   __shared__ float s_part[LANES][D];
+  tc::grid_dependency_wait();
   const int i = threadIdx.x % D, g = threadIdx.x / D;
   float* dst = blockIdx.x == 0 ? dq_weight : dk_weight;
+  const int first = blockIdx.x == 0 ? 0 : q_ctas, end = blockIdx.x == 0 ? q_ctas : ctas;
   float t = 0.f;
-  if (dst)
-    for (int j = g; j < n; j += LANES) t += partials[static_cast<int64_t>(j) * 2 * D + blockIdx.x * D + i];
+  if (dst) {
+#pragma unroll 8
+    for (int j = first + g; j < end; j += LANES) t += partials[static_cast<int64_t>(j) * D + i];
+  }
   s_part[g][i] = t;
   __syncthreads();
   if (g == 0 && dst) {
