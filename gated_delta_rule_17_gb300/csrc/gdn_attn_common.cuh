@@ -3,18 +3,22 @@
 //
 // A unit is one tile of query rows of one (sequence, kv head). The rows of a kv head are
 // r = i (nq / nkv) + g for new token i and head g of its group, so that all heads that read
-// a key share its load. A unit walks its sequence's tokens in tiles of KT. The tiles of all
-// units in a row, (sequence, kv head, row tile, token tile), are cut into as many equal runs
-// as there are CTAs: the load is even whatever the lengths, one long sequence fills the
+// a key share its load. A unit walks its sequence's tokens in tiles of KT. The CTAs are dealt
+// out to members, by their work: member j of J (J = the most row tiles of a kv head, at most 8)
+// has the row tiles j, j + J, ... So CTAs that read the same keys for different rows run side by
+// side, and the second read finds them in L2. (In one order over (sequence, kv head, row tile) the
+// row tiles of a kv head came one after the other: with two of them every key came from HBM twice.)
+// A member's tiles in a row, (sequence, kv head, row tile, token tile), are cut into as many equal
+// runs as it has CTAs: the load is even whatever the lengths, one long sequence fills the
 // card, and no length is needed on the host. A unit that lies in one run is written by it. A
 // unit that is cut leaves a partial (m, l, o) of every piece in the workspace,
 //
 //     m = max_t x_t,   l = sum_t 2^(x_t - m),   o = sum_t 2^(x_t - m) v_t
 //
-// (x in units of log2 e), and gdn_attn_join_kernel adds the pieces up in their order,
-// with weights 2^(m_piece - max m). A run has at most two cut units, its first (slot 0)
-// and its last (slot 1), so the workspace does not grow with the batch. Where the block table
-// has room for few tokens only, the runs are cut at units and the join falls away.
+// (x in units of log2 e, m any reference near the maximum), and gdn_attn_join_kernel adds the
+// pieces up in their order, with weights 2^(m_piece - max m). A run has at most two cut units, its
+// first (slot 0) and its last (slot 1), so the workspace does not grow with the batch. Where the
+// block table has room for few tokens only, the runs are cut at units and the join falls away.
 #pragma once
 #include "gdn_norm_rope_kernel.cuh"
 
@@ -70,9 +74,16 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b, bool rep
   return s;
 }
 
+constexpr int kAttnMembers = 8;
+
+// Row tiles of a kv head that member j of `members` has.
+__device__ __forceinline__ int attn_member_tiles(const AttnSeq& s, int j, int members) {
+  return s.qtiles > j ? (s.qtiles - j - 1) / members + 1 : 0;
+}
+
 // What the runs count: token tiles, or units.
-__device__ __forceinline__ int64_t attn_cost(const AttnParams& p, const AttnSeq& s) {
-  return static_cast<int64_t>(p.whole ? 1 : s.tiles) * s.qtiles * p.nkv;
+__device__ __forceinline__ int64_t attn_cost(const AttnParams& p, const AttnSeq& s, int j, int members) {
+  return static_cast<int64_t>(p.whole ? 1 : s.tiles) * attn_member_tiles(s, j, members) * p.nkv;
 }
 
 // Inclusive prefix of `x` over the block's threads; *total is the sum. s_scan: a word a warp.
@@ -100,10 +111,11 @@ __device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t* s_scan, int6
 // Where a run starts: sequence, unit and tile of it, and how many tiles it has.
 struct AttnStart {
   int b;
+  int member, members;
   int64_t within;      // tiles of sequence b before the run
-  int64_t end, total;  // tiles up to the run's end, and of all runs
+  int64_t end, total;  // the member's tiles up to the run's end, and in all
   int64_t count;       // tiles of the run
-  int runs;            // runs that have tiles
+  int first, runs;     // the member's first run, and its runs that have tiles
 };
 
 // Run i of `runs` has the tiles [total i / runs, total (i + 1) / runs).
@@ -127,30 +139,61 @@ __device__ __forceinline__ int run_of(int64_t at, int64_t total, int runs) {
 template <int MT, int KT, int THREADS>
 __device__ __forceinline__ AttnStart attn_start(const AttnParams& p, int run, int64_t* s_scan, AttnStart* s_start) {
   const int B = p.cache.B, tid = threadIdx.x;
-  int64_t total = 0, cost = 0, upto = 0;
-  for (int b0 = 0; b0 < B; b0 += THREADS) {
-    int64_t sum;
-    cost = b0 + tid < B ? attn_cost(p, attn_seq<MT, KT>(p, b0 + tid, run == 0)) : 0;
-    upto = block_prefix<THREADS>(cost, s_scan, &sum);
-    total += sum;
+  // the most row tiles, and all members' work
+  int most = 0;
+  int64_t work = 0;
+  AttnSeq own{};  // the sequence of this thread where there is one a thread at most
+  for (int b = tid; b < B; b += THREADS) {
+    own = attn_seq<MT, KT>(p, b, run == 0);
+    most = own.qtiles > most ? own.qtiles : most;
+    work += attn_cost(p, own, 0, 1);
   }
-  const int runs = total < p.runs ? static_cast<int>(total) : p.runs;  // no run is empty
-  const bool works = run < runs;
-  const int64_t begin = works ? run_begin(run, total, runs) : 0, end = works ? run_begin(run + 1, total, runs) : 0;
-  if (tid == 0) *s_start = AttnStart{0, 0, end, total, 0, runs};
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (tid == 0) s_start->member = 0;
+  __syncthreads();
+  if ((tid & 31) == 0) atomicMax(&s_start->member, most);
+  int64_t all;
+  block_prefix<THREADS>(work, s_scan, &all);
+  most = s_start->member;
+  const int members = most < kAttnMembers ? most : kAttnMembers;
+  // member j has the runs j + floor((p.runs - members) work of members < j / all) and on, at least one
+  int64_t before = 0, total = 0;
+  int member = 0, first = 0, next = p.runs;
+  for (int j = 0; j < members; ++j) {
+    if (members > 1) {
+      int64_t sum = 0;
+      for (int b = tid; b < B; b += THREADS)
+        sum += attn_cost(p, B <= THREADS ? own : attn_seq<MT, KT>(p, b, false), j, members);
+      block_prefix<THREADS>(sum, s_scan, &total);
+    } else {
+      total = all;
+    }
+    const int begin = j + static_cast<int>((p.runs - members) * before / all);
+    before += total;
+    const int end = j + 1 + static_cast<int>((p.runs - members) * before / all);
+    if (run >= begin && run < end) {
+      member = j;
+      first = begin;
+      next = end;
+      break;  // the same for the whole block
+    }
+  }
+  const int runs = total < next - first ? static_cast<int>(total) : next - first;  // no run is empty
+  const bool works = run - first < runs;
+  const int64_t begin = works ? run_begin(run - first, total, runs) : 0, end = works ? run_begin(run - first + 1, total, runs) : 0;
+  __syncthreads();  // all have read s_start->member
+  if (tid == 0) *s_start = AttnStart{0, member, members, 0, end, total, 0, first, runs};
   __syncthreads();
   if (works) {
-    int64_t before = 0;
-    for (int b0 = 0; b0 < B && before <= begin; b0 += THREADS) {
-      if (B > THREADS) {  // else the first pass has left this thread's sequence
-        int64_t sum;
-        cost = b0 + tid < B ? attn_cost(p, attn_seq<MT, KT>(p, b0 + tid, false)) : 0;
-        upto = before + block_prefix<THREADS>(cost, s_scan, &sum);
-        before += sum;
-      }
-      if (upto > begin && upto - cost <= begin) {  // one thread's, at most
+    int64_t upto = 0;
+    for (int b0 = 0; b0 < B && upto <= begin; b0 += THREADS) {
+      int64_t sum, cost = 0;
+      if (b0 + tid < B) cost = attn_cost(p, B <= THREADS ? own : attn_seq<MT, KT>(p, b0 + tid, false), member, members);
+      const int64_t end_b = upto + block_prefix<THREADS>(cost, s_scan, &sum);
+      upto += sum;
+      if (end_b > begin && end_b - cost <= begin) {  // one thread's, at most
         s_start->b = b0 + tid;
-        s_start->within = begin - (upto - cost);
+        s_start->within = begin - (end_b - cost);
         s_start->count = end - begin;
       }
     }
@@ -162,22 +205,23 @@ __device__ __forceinline__ AttnStart attn_start(const AttnParams& p, int run, in
 // Walks a run: the unit pieces in their order. Every thread of a role walks by itself.
 template <int MT, int KT>
 struct AttnWalk {
-  int b;
+  int b, member, members;
   int64_t within, left;
-  AttnSeq s;      // the sequence
-  int unit;       // kv head and row tile
+  AttnSeq s;   // the sequence
   int kvh, qt;
-  int t0, t1;     // token tiles of the piece
-  __device__ __forceinline__ explicit AttnWalk(const AttnStart& st) : b(st.b), within(st.within), left(st.count) {}
+  int t0, t1;  // token tiles of the piece
+  __device__ __forceinline__ explicit AttnWalk(const AttnStart& st)
+      : b(st.b), member(st.member), members(st.members), within(st.within), left(st.count) {}
   __device__ __forceinline__ bool next(const AttnParams& p) {
     while (left > 0) {
       s = attn_seq<MT, KT>(p, b, false);
-      const int64_t cost = attn_cost(p, s);
+      const int64_t cost = attn_cost(p, s, member, members);
       if (within >= cost) {
         within -= cost;
         ++b;
         continue;
       }
+      int unit;
       if (p.whole) {
         unit = static_cast<int>(within);
         t0 = 0;
@@ -191,11 +235,17 @@ struct AttnWalk {
         within += t1 - t0;
         left -= t1 - t0;
       }
-      kvh = unit / s.qtiles;
-      qt = unit - kvh * s.qtiles;
+      const int mine = attn_member_tiles(s, member, members);
+      kvh = unit / mine;
+      qt = (unit - kvh * mine) * members + member;
       return true;
     }
     return false;
+  }
+  // What the join has to know where the unit begins in run `run` and is cut: first row, rows, kv
+  // head and row tile, last run.
+  __device__ __forceinline__ int4 cut(const AttnStart& st) const {
+    return make_int4(s.first, s.n, kvh * s.qtiles + qt, st.first + run_of(st.end + (s.tiles - t1) - 1, st.total, st.runs));
   }
 };
 

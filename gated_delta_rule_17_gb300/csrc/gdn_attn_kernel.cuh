@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
   AttnWalk<MT, kAttnTile> w(st);
   while (w.next(p)) {
     const AttnSeq& s = w.s;
-    const int b = w.b, unit = w.unit, kvh = w.kvh, qt = w.qt, t0 = w.t0, t1 = w.t1;
+    const int b = w.b, kvh = w.kvh, qt = w.qt, t0 = w.t0, t1 = w.t1;
     const int R = s.n * p.group;
     const int32_t* table = c.block_table + b * c.table_stride;
 
@@ -310,8 +310,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
       }
     }
     __syncthreads();  // the join buffer is done with
-    if (t0 == 0 && t1 < s.tiles && threadIdx.x == 0) 
-      p.cut[run] = make_int4(s.first, s.n, unit, run_of(st.end + (s.tiles - t1) - 1, st.total, st.runs));
+    if (t0 == 0 && t1 < s.tiles && threadIdx.x == 0) p.cut[run] = w.cut(st);
   }
 }
 

@@ -77,28 +77,30 @@ __device__ __forceinline__ uint32_t sees32(const AttnParams& p, const AttnSeq& s
   return lim < 32 ? w & ((1u << lim) - 1u) : w;
 }
 
+// A wait that did not succeed at once, with its time limit. Out of line: the roles' loops share the
+// instruction caches, and their size is what the issuing warp feels first.
+__device__ __noinline__ bool tc_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort, unsigned* status) {
+  const uint64_t t0 = tc::globaltimer_ns();
+  while (!tc::mbar_try_wait_hint(bar, parity, 100000u)) {
+    if (*abort) return false;
+    if (tc::globaltimer_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
 struct TcShared {
   uint32_t bars;  // shared address of the mbarriers
   volatile uint32_t* abort;
   unsigned* status;
   __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
-  // Bounded wait of one thread.
-  __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
-    if (tc::mbar_try_wait(bar(i), parity)) return true;
-    const uint64_t t0 = tc::globaltimer_ns();
-    while (!tc::mbar_try_wait_hint(bar(i), parity, 100000u)) {
-      if (*abort) return false;
-      if (tc::globaltimer_ns() - t0 > kWaitLimitNs) {
-        *abort = 1;
-        atomicOr(status, kStatusTimeout);
-        return false;
-      }
-    }
-    return true;
-  }
-  // The same by a whole warp, with one answer.
+  // Bounded wait by a whole warp, with one answer.
   __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
-    return __all_sync(0xffffffffu, wait(i, parity));
+    const bool ok = tc::mbar_try_wait(bar(i), parity);
+    return __all_sync(0xffffffffu, ok) || __all_sync(0xffffffffu, ok || tc_wait_slow(bar(i), parity, abort, status));
   }
 };
 
@@ -154,6 +156,7 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     uint8_t* patch = smem + Plan::OUT + warp * Plan::PATCH;
     auto patch_at = [](int r, int pc) { return r * 64 + ((pc ^ ((r >> 1) & 3)) << 4); };
     const float cl = p.scale_log2;
+    const Pair cl2 = pair_of(cl, cl);
     uint32_t s_ph = 0, o_ph = 0, j_ph = 0;
     bool ok = true, pending = false;  // pending: the other stream may still read this one's O
     while (ok && w.next(p)) {
@@ -226,15 +229,17 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             }
           }
           const float nb = m == -INFINITY ? 0.f : -m * cl;
-          float sum[2] = {0.f, 0.f};
+          const Pair nb2 = pair_of(nb, nb);
+          Pair sum[2] = {0, 0};
           auto weights = [&](const uint32_t (&r)[32], int k) {  // over a part of S that has been read
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float a = exp2_approx(fmaf(__uint_as_float(r[e]), cl, nb));
-              const float b = exp2_approx(fmaf(__uint_as_float(r[e + 1]), cl, nb));
-              sum[0] += a;
-              sum[1] += b;
+              float a, b;
+              parts_of(fma2(pair_of(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), cl2, nb2), a, b);
+              a = exp2_approx(a);
+              b = exp2_approx(b);
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair_of(a, b));
               pk[e >> 1] = pack2<T>(a, b);
             }
             tc::tmem_st16u(s_addr + 16 * k, pk);
@@ -250,7 +255,9 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
           weights(r0, 2);
           tc::tmem_ld_wait32(r1);
           weights(r1, 3);
-          l += sum[0] + sum[1];
+          float sa, sb;
+          parts_of(add2(sum[0], sum[1]), sa, sb);
+          l += sa + sb;
           tc::tmem_st_wait();
         }
         if (pending) {  // the products that follow overwrite O
@@ -351,7 +358,7 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
       if (has && !whole && (!split || x == 0))  // m in units of log2 e, as the join takes it
         *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(m == -INFINITY ? m : m * cl, l);
       if (threadIdx.x == 0 && w.t0 == 0 && w.t1 < s.tiles)
-        p.cut[run] = make_int4(s.first, s.n, w.unit, run_of(st.end + (s.tiles - w.t1) - 1, st.total, st.runs));
+        p.cut[run] = w.cut(st);
     }
   } else if (warp < 12) {
     // ---- copies of Q, K and V --------------------------------------------------------------
