@@ -468,6 +468,7 @@ int gdn_tree_attention(const void* q, const gdn_paged_t* cache, const uint64_t* 
   }
   p.q = q;
   p.out = out;
+  p.out_wide = reinterpret_cast<uintptr_t>(out) % 32 == 0 && p.out_stride % 16 == 0;
   p.mask = mask;
   p.mask_words = mask_words;
   p.nq = nq;

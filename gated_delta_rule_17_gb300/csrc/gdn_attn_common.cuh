@@ -33,6 +33,7 @@ struct AttnParams {
   int nq, nkv, group;
   float scale_log2;  // scale * log2 e
   int64_t q_stride, out_stride;
+  int out_wide;  // out's head rows lie on 32-byte boundaries
   int runs;        // CTAs of the attention kernel
   int box;         // tokens of a TMA box inside a page, 0: pages do not hold whole boxes
   int whole;       // runs are cut at units only: nothing to join
@@ -86,26 +87,27 @@ __device__ __forceinline__ int64_t attn_cost(const AttnParams& p, const AttnSeq&
   return static_cast<int64_t>(p.whole ? 1 : s.tiles) * attn_member_tiles(s, j, members) * p.nkv;
 }
 
-// Inclusive prefix of `x` over the block's threads; *total is the sum. s_scan: a word a warp.
-template <int THREADS>
-__device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t* s_scan, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive prefix of `x` over the warp, and the sum over it.
+__device__ __forceinline__ int64_t warp_prefix(int64_t x) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();  // the last use of s_scan is over
-  if (lane == 31) s_scan[warp] = x;
-  __syncthreads();
-  int64_t before = 0, all = 0;
+  return x;
+}
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += s_scan[w];
-    all += s_scan[w];
-  }
-  *total = all;
-  return x + before;
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// a * b / c for a, c >= 0, b > 0, in 32 bits where that holds the product.
+__device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
+  const uint64_t x = static_cast<uint64_t>(a) * static_cast<uint64_t>(b);
+  return (x | static_cast<uint64_t>(c)) >> 32 ? static_cast<int64_t>(x / static_cast<uint64_t>(c))
+                                              : static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(c));
 }
 
 // Where a run starts: sequence, unit and tile of it, and how many tiles it has.
@@ -119,100 +121,100 @@ struct AttnStart {
 };
 
 // Run i of `runs` has the tiles [total i / runs, total (i + 1) / runs).
-__device__ __forceinline__ int64_t run_begin(int64_t i, int64_t total, int runs) {
-  const uint64_t x = static_cast<uint64_t>(total) * static_cast<uint64_t>(i);
-  return x >> 32 ? static_cast<int64_t>(x / static_cast<uint64_t>(runs))
-                 : static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(runs));
-}
+__device__ __forceinline__ int64_t run_begin(int64_t i, int64_t total, int runs) { return mul_div(total, i, runs); }
 
 // The run that holds tile `at`.
 __device__ __forceinline__ int run_of(int64_t at, int64_t total, int runs) {
-  const uint64_t x = static_cast<uint64_t>(at) * static_cast<uint64_t>(runs);
-  int64_t i = (x | static_cast<uint64_t>(total)) >> 32 ? static_cast<int64_t>(x / static_cast<uint64_t>(total))
-                                                       : static_cast<uint32_t>(x) / static_cast<uint32_t>(total);
+  int64_t i = mul_div(at, runs, total);
   while (run_begin(i + 1, total, runs) <= at) ++i;
   while (run_begin(i, total, runs) > at) --i;
   return static_cast<int>(i);
 }
 
-// All threads of the block take part. s_scan: THREADS / 32 words; s_start: shared.
-template <int MT, int KT, int THREADS>
-__device__ __forceinline__ AttnStart attn_start(const AttnParams& p, int run, int64_t* s_scan, AttnStart* s_start) {
-  const int B = p.cache.B, tid = threadIdx.x;
+// Where the block's run starts, found by one warp, a lane a sequence (the block's barrier after its
+// set-up is then the only one; a search by all threads took several).
+template <int MT, int KT>
+__device__ __forceinline__ AttnStart attn_start(const AttnParams& p, int run) {
+  const int B = p.cache.B, lane = threadIdx.x & 31;
+  const bool report = run == 0;
   // the most row tiles, and all members' work
   int most = 0;
   int64_t work = 0;
-  AttnSeq own{};  // the sequence of this thread where there is one a thread at most
-  for (int b = tid; b < B; b += THREADS) {
-    own = attn_seq<MT, KT>(p, b, run == 0);
+  AttnSeq own{};  // this lane's sequence, where there are at most 32
+#pragma unroll 4
+  for (int b = lane; b < B; b += 32) {
+    own = attn_seq<MT, KT>(p, b, report);
     most = own.qtiles > most ? own.qtiles : most;
     work += attn_cost(p, own, 0, 1);
   }
   most = __reduce_max_sync(0xffffffffu, most);
-  if (tid == 0) s_start->member = 0;
-  __syncthreads();
-  if ((tid & 31) == 0) atomicMax(&s_start->member, most);
-  int64_t all;
-  block_prefix<THREADS>(work, s_scan, &all);
-  most = s_start->member;
+  const int64_t all = warp_sum(work);
   const int members = most < kAttnMembers ? most : kAttnMembers;
   // member j has the runs j + floor((p.runs - members) work of members < j / all) and on, at least one
   int64_t before = 0, total = 0;
   int member = 0, first = 0, next = p.runs;
-  for (int j = 0; j < members; ++j) {
-    if (members > 1) {
+  if (members == 1) {
+    total = all;
+  } else {
+    for (int j = 0; j < members; ++j) {
       int64_t sum = 0;
-      for (int b = tid; b < B; b += THREADS)
-        sum += attn_cost(p, B <= THREADS ? own : attn_seq<MT, KT>(p, b, false), j, members);
-      block_prefix<THREADS>(sum, s_scan, &total);
-    } else {
-      total = all;
-    }
-    const int begin = j + static_cast<int>((p.runs - members) * before / all);
-    before += total;
-    const int end = j + 1 + static_cast<int>((p.runs - members) * before / all);
-    if (run >= begin && run < end) {
-      member = j;
-      first = begin;
-      next = end;
-      break;  // the same for the whole block
-    }
-  }
-  const int runs = total < next - first ? static_cast<int>(total) : next - first;  // no run is empty
-  const bool works = run - first < runs;
-  const int64_t begin = works ? run_begin(run - first, total, runs) : 0, end = works ? run_begin(run - first + 1, total, runs) : 0;
-  __syncthreads();  // all have read s_start->member
-  if (tid == 0) *s_start = AttnStart{0, member, members, 0, end, total, 0, first, runs};
-  __syncthreads();
-  if (works) {
-    int64_t upto = 0;
-    for (int b0 = 0; b0 < B && upto <= begin; b0 += THREADS) {
-      int64_t sum, cost = 0;
-      if (b0 + tid < B) cost = attn_cost(p, B <= THREADS ? own : attn_seq<MT, KT>(p, b0 + tid, false), member, members);
-      const int64_t end_b = upto + block_prefix<THREADS>(cost, s_scan, &sum);
-      upto += sum;
-      if (end_b > begin && end_b - cost <= begin) {  // one thread's, at most
-        s_start->b = b0 + tid;
-        s_start->within = begin - (end_b - cost);
-        s_start->count = end - begin;
+      for (int b = lane; b < B; b += 32) sum += attn_cost(p, B <= 32 ? own : attn_seq<MT, KT>(p, b, false), j, members);
+      total = warp_sum(sum);
+      const int begin = j + static_cast<int>(mul_div(before, p.runs - members, all));
+      before += total;
+      const int end = j + 1 + static_cast<int>(mul_div(before, p.runs - members, all));
+      if (run >= begin && run < end) {
+        member = j;
+        first = begin;
+        next = end;
+        break;
       }
     }
   }
-  __syncthreads();
-  return *s_start;
+  const int runs = total < next - first ? static_cast<int>(total) : next - first;  // no run is empty
+  AttnStart st{0, member, members, 0, 0, total, 0, first, runs};
+  if (run - first >= runs) return st;
+  const int64_t begin = run_begin(run - first, total, runs);
+  st.end = run_begin(run - first + 1, total, runs);
+  st.count = st.end - begin;
+  int64_t upto = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    int64_t cost = 0;
+    if (b0 + lane < B) cost = attn_cost(p, B <= 32 ? own : attn_seq<MT, KT>(p, b0 + lane, false), member, members);
+    const int64_t end_b = upto + warp_prefix(cost);
+    const unsigned m = __ballot_sync(0xffffffffu, end_b > begin);
+    if (m) {  // the first sequence that ends behind the run's first tile
+      const int l = __ffs(m) - 1;
+      st.b = b0 + l;
+      st.within = begin - __shfl_sync(0xffffffffu, end_b - cost, l);
+      break;
+    }
+    upto = __shfl_sync(0xffffffffu, end_b, 31);
+  }
+  return st;
 }
 
-// Walks a run: the unit pieces in their order. Every thread of a role walks by itself.
+// Walks a run: the unit pieces in their order. The warp that has found the start takes the first
+// step; then every thread of a role walks by itself.
 template <int MT, int KT>
 struct AttnWalk {
-  int b, member, members;
+  AttnStart st;
+  int b;
   int64_t within, left;
-  AttnSeq s;   // the sequence
+  bool any;    // there is a piece
+  AttnSeq s;   // its sequence
   int kvh, qt;
-  int t0, t1;  // token tiles of the piece
-  __device__ __forceinline__ explicit AttnWalk(const AttnStart& st)
-      : b(st.b), member(st.member), members(st.members), within(st.within), left(st.count) {}
-  __device__ __forceinline__ bool next(const AttnParams& p) {
+  int t0, t1;  // its token tiles
+  __device__ __forceinline__ void begin(const AttnParams& p, const AttnStart& start) {
+    st = start;
+    b = st.b;
+    within = st.within;
+    left = st.count;
+    next(p);
+  }
+  __device__ __forceinline__ void next(const AttnParams& p) {
+    const int member = st.member, members = st.members;
+    any = left > 0;
     while (left > 0) {
       s = attn_seq<MT, KT>(p, b, false);
       const int64_t cost = attn_cost(p, s, member, members);
@@ -238,13 +240,12 @@ struct AttnWalk {
       const int mine = attn_member_tiles(s, member, members);
       kvh = unit / mine;
       qt = (unit - kvh * mine) * members + member;
-      return true;
+      return;
     }
-    return false;
   }
   // What the join has to know where the unit begins in run `run` and is cut: first row, rows, kv
   // head and row tile, last run.
-  __device__ __forceinline__ int4 cut(const AttnStart& st) const {
+  __device__ __forceinline__ int4 cut() const {
     return make_int4(s.first, s.n, kvh * s.qtiles + qt, st.first + run_of(st.end + (s.tiles - t1) - 1, st.total, st.runs));
   }
 };

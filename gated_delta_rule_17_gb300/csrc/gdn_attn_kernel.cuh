@@ -88,8 +88,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
   using Plan = AttnPlan<D, MB>;
   constexpr int MT = Plan::MT, KS = D / 16, NT = D / 8, CH = D / 8, STAGES = Plan::STAGES;
   extern __shared__ uint8_t dyn[];
-  __shared__ int64_t s_scan[kAttnWarps];
-  __shared__ AttnStart s_start;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 127) & ~static_cast<uintptr_t>(127));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gr = lane >> 2, tc = lane & 3;  // fragment row and column pair
@@ -97,11 +95,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
   const PagedParams& c = p.cache;
   const int run = blockIdx.x;
 
-  const AttnStart st = attn_start<MT, kAttnTile, kAttnThreads>(p, run, s_scan, &s_start);
+  __shared__ AttnWalk<MT, kAttnTile> s_walk;
+  if (warp == 0) {
+    AttnWalk<MT, kAttnTile> found;
+    found.begin(p, attn_start<MT, kAttnTile>(p, run));
+    if (lane == 0) s_walk = found;
+  }
+  __syncthreads();
   tc::allow_dependent_launch();  // the join waits for this grid's end before it reads anything
   if (threadIdx.x == 0 && !p.whole) p.cut[run] = make_int4(0, 0, 0, -1);
-  AttnWalk<MT, kAttnTile> w(st);
-  while (w.next(p)) {
+  AttnWalk<MT, kAttnTile> w = s_walk;
+  for (; w.any; w.next(p)) {
     const AttnSeq& s = w.s;
     const int b = w.b, kvh = w.kvh, qt = w.qt, t0 = w.t0, t1 = w.t1;
     const int R = s.n * p.group;
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
       }
     }
     __syncthreads();  // the join buffer is done with
-    if (t0 == 0 && t1 < s.tiles && threadIdx.x == 0) p.cut[run] = w.cut(st);
+    if (t0 == 0 && t1 < s.tiles && threadIdx.x == 0) p.cut[run] = w.cut();
   }
 }
 

@@ -41,9 +41,7 @@ struct AttnTcPlan {
   static constexpr int STAGES = D == 128 ? 4 : 8;
   static constexpr int LAG = 2;  // cp.async tiles in flight behind the one just issued
   static constexpr int Q = 0;
-  static constexpr int PATCH = 32 * 64;  // of a warp, through which its rows go out
-  static constexpr int OUT = 2 * TILE;
-  static constexpr int RING = OUT + 8 * PATCH;
+  static constexpr int RING = 2 * TILE;
   static constexpr int BYTES = RING + STAGES * TILE;
   static constexpr int DYN_SMEM = BYTES + 1024;  // slack for 1024-byte alignment
   static constexpr uint32_t COL_S = 0, COL_O = 256, TMEM_COLS = 512;
@@ -92,6 +90,18 @@ __device__ __noinline__ bool tc_wait_slow(uint32_t bar, uint32_t parity, volatil
   return true;
 }
 
+// 32 bytes to global memory: as one sector, or in two halves where dst is only 16-byte aligned.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* r, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(dst)), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  }
+}
+
 struct TcShared {
   uint32_t bars;  // shared address of the mbarriers
   volatile uint32_t* abort;
@@ -111,10 +121,9 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
   using Plan = AttnTcPlan<D>;
   constexpr int MT = kTcRows, TILE = Plan::TILE, NS = Plan::STAGES, LAG = Plan::LAG;
   extern __shared__ uint8_t dyn[];
-  __shared__ int64_t s_scan[kTcThreads / 32];
-  __shared__ AttnStart s_start;
   __shared__ __align__(8) uint64_t s_bar[Plan::NBAR];
   __shared__ uint32_t s_tmem, s_abort;
+  __shared__ AttnWalk<MT, kTcTile> s_walk;
   __shared__ float2 s_ml[2][kTcTile];  // split units: (m, l) of both streams
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = tc::smem_u32(smem);
@@ -123,7 +132,12 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
   const int run = blockIdx.x;
   const TcShared sh{tc::smem_u32(s_bar), &s_abort, p.status};
 
-  if (threadIdx.x == 0) {
+  if (warp == 0) {
+    AttnWalk<MT, kTcTile> found;
+    found.begin(p, attn_start<MT, kTcTile>(p, run));
+    if (lane == 0) s_walk = found;
+  }
+  if (threadIdx.x == 32) {
     s_abort = 0;
     for (int i = 0; i < NS; ++i) {
       tc::mbar_init(sh.bar(Plan::FULL + i), 128);
@@ -138,28 +152,26 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     tc::mbar_init(sh.bar(Plan::Q_FREE), 1);
     tc::mbar_init(sh.bar(Plan::JOIN), 256);
     tc::mbar_fence_init();
-    if (!p.whole) p.cut[run] = make_int4(0, 0, 0, -1);
   }
+  if (threadIdx.x == 0 && !p.whole) p.cut[run] = make_int4(0, 0, 0, -1);
   if (warp == 12) tc::tmem_alloc(tc::smem_u32(&s_tmem), Plan::TMEM_COLS);
   tc::fence_before_sync();
-  const AttnStart st = attn_start<MT, kTcTile, kTcThreads>(p, run, s_scan, &s_start);
+  __syncthreads();
   tc::fence_after_sync();
   tc::allow_dependent_launch();  // the join waits for this grid's end before it reads anything
   const uint32_t tmem = s_tmem;
-  AttnWalk<MT, kTcTile> w(st);
+  AttnWalk<MT, kTcTile> w = s_walk;
 
   if (warp < 8) {
     // ---- one row a thread: softmax, and the unit's end -----------------------------------
     const int x = warp >> 2, lrow = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's quarter of the lanes
     const uint32_t s_addr = tmem + lanes + Plan::COL_S + x * kTcTile, o_addr = tmem + lanes + Plan::COL_O;
-    uint8_t* patch = smem + Plan::OUT + warp * Plan::PATCH;
-    auto patch_at = [](int r, int pc) { return r * 64 + ((pc ^ ((r >> 1) & 3)) << 4); };
     const float cl = p.scale_log2;
     const Pair cl2 = pair_of(cl, cl);
     uint32_t s_ph = 0, o_ph = 0, j_ph = 0;
     bool ok = true, pending = false;  // pending: the other stream may still read this one's O
-    while (ok && w.next(p)) {
+    for (; ok && w.any; w.next(p)) {
       const AttnSeq& s = w.s;
       const int R = s.n * p.group;
       const bool split = R - w.qt * MT <= kTcTile;
@@ -302,50 +314,33 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
       // a dual stream has its rows; the warps of a split unit have half of the columns each
       const int c0 = split ? x * (D / 2) : 0, c1 = split ? c0 + D / 2 : D, xo = split ? 0 : x;
       const int64_t part = (static_cast<int64_t>(run) * 2 + (w.t0 == 0 ? 1 : 0)) * MT + (split ? 0 : x * kTcTile) + lrow;
-      char* mine;  // this lane's row
-      if (whole)
-        mine = reinterpret_cast<char*>(static_cast<T*>(p.out) + (static_cast<int64_t>(s.first) + i) * p.out_stride +
-                                       static_cast<int64_t>(w.kvh * p.group + g) * D);
-      else
-        mine = reinterpret_cast<char*>(p.part_o + part * D);
-      if (!has) mine = nullptr;
+      // each lane stores whole 32-byte sectors of its own row
+      char* dst = whole ? reinterpret_cast<char*>(static_cast<T*>(p.out) + (static_cast<int64_t>(s.first) + i) * p.out_stride +
+                                                  static_cast<int64_t>(w.kvh * p.group + g) * D)
+                        : reinterpret_cast<char*>(p.part_o + part * D);
+      const bool wide = !whole || p.out_wide;
       if (used) {
 #pragma unroll 1
-        for (int col = c0; col < c1; col += 32) {
-          uint32_t r0[32];
-          float a[32];
-          tc::tmem_ld32(o_addr + xo * D + col, r0);
-          tc::tmem_ld_wait32(r0);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) a[e] = __uint_as_float(r0[e]) * f0;
+        for (int col = c0; col < c1; col += 16) {
+          uint32_t r[16], o2[16];
+          tc::tmem_ld16u(o_addr + xo * D + col, r);
+          if (two) tc::tmem_ld16u(o_addr + D + col, o2);
+          tc::tmem_ld_wait16(r);
           if (two) {
-            tc::tmem_ld32(o_addr + D + col, r0);
-            tc::tmem_ld_wait32(r0);
+            tc::tmem_ld_wait16(o2);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) a[e] = fmaf(__uint_as_float(r0[e]), f1, a[e]);
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(fmaf(__uint_as_float(o2[e]), f1, __uint_as_float(r[e]) * f0));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f0);
           }
-          // through the warp's patch (rows of 64 bytes, pieces exchanged by row), so that the lanes
-          // store 64-byte runs of the rows: 32 16-bit values, or 16 fp32 ones and then the other 16
+          if (whole) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (whole && h == 1) break;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint4 q = whole ? make_uint4(pack2<T>(a[8 * e], a[8 * e + 1]), pack2<T>(a[8 * e + 2], a[8 * e + 3]),
-                                                 pack2<T>(a[8 * e + 4], a[8 * e + 5]), pack2<T>(a[8 * e + 6], a[8 * e + 7]))
-                                    : make_uint4(__float_as_uint(a[16 * h + 4 * e]), __float_as_uint(a[16 * h + 4 * e + 1]),
-                                                 __float_as_uint(a[16 * h + 4 * e + 2]), __float_as_uint(a[16 * h + 4 * e + 3]));
-              *reinterpret_cast<uint4*>(patch + patch_at(lane, e)) = q;
-            }
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int rr = 8 * e + (lane >> 2), pc = lane & 3;
-              const uint64_t dst = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), rr);
-              const uint4 q = *reinterpret_cast<const uint4*>(patch + patch_at(rr, pc));
-              if (dst) *reinterpret_cast<uint4*>(dst + (whole ? col * 2 : col * 4 + 64 * h) + 16 * pc) = q;
-            }
-            __syncwarp();
+            for (int e = 0; e < 8; ++e) r[e] = pack2<T>(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+          }
+          if (has) {
+            store32(dst + col * (whole ? 2 : 4), r, wide);
+            if (!whole) store32(dst + col * 4 + 32, r + 8, true);
           }
         }
       }
@@ -358,7 +353,7 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
       if (has && !whole && (!split || x == 0))  // m in units of log2 e, as the join takes it
         *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(m == -INFINITY ? m : m * cl, l);
       if (threadIdx.x == 0 && w.t0 == 0 && w.t1 < s.tiles)
-        p.cut[run] = w.cut(st);
+        p.cut[run] = w.cut();
     }
   } else if (warp < 12) {
     // ---- copies of Q, K and V --------------------------------------------------------------
@@ -385,7 +380,7 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     reinterpret_cast<const T*>(src ? src : reinterpret_cast<uint64_t>(p.q)) + (src ? 8 * ch : 0), src != 0);
       }
     };
-    while (ok && w.next(p)) {
+    for (; ok && w.any; w.next(p)) {
       const int R = w.s.n * p.group, left = R - w.qt * MT;  // rows of the unit: left, at most MT
       const int32_t* table = c.block_table + w.b * c.table_stride;
       const T* kbase = static_cast<const T*>(c.k) + w.kvh * c.k_head;
@@ -427,7 +422,7 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         const TokenPlace cur = next;
         next = token_place(p, table, (t + 1) * kTcTile + lw * 32 + lane, t + 1 < w.t1 ? w.s.len : 0);
         if (t < w.t1) load(&k_map, kbase, c.k_page, c.k_token, cur);
-        if (t == w.t0 && ok) {
+        if (t == w.t0 && ok) {  // the first tile is under way meanwhile
           ok = units == 0 || sh.wait_warp(Plan::Q_FREE, (units - 1) & 1);
           if (!ok) break;
 #pragma unroll 1
@@ -460,7 +455,7 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     int base = 0;
     uint32_t q_ph = 0, p_ph = 0;  // p_ph: a bit a stream
     bool ok = true;
-    while (ok && w.next(p)) {
+    for (; ok && w.any; w.next(p)) {
       const int n = w.t1 - w.t0;
       const bool split = w.s.n * p.group - w.qt * MT <= kTcTile;
       ok = sh.wait_warp(Plan::Q_FULL, q_ph);
