@@ -215,33 +215,41 @@ bool cache_map(CUtensorMap* m, const void* base, int64_t page, int64_t token, in
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, int MT>
-cudaError_t launch_join(const gdn::AttnParams& p, cudaStream_t s) {
-  if (p.whole) return cudaSuccess;
+// A launch that may start while the kernel before it in the stream ends: all of these kernels wait
+// for it (tc::grid_dependency_wait) before they read or write global memory.
+template <typename... A, typename... B>
+cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t s, const B&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.runs), MT / gdn::kJoinWarps);
-  cfg.blockDim = dim3(32 * gdn::kJoinWarps);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gdn::gdn_attn_join_kernel<T, D, MT>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T, int D, int MT>
+cudaError_t launch_join(cudaError_t e, const gdn::AttnParams& p, cudaStream_t s) {
+  if (e != cudaSuccess || p.whole) return e;
+  return launch_early(gdn::gdn_attn_join_kernel<T, D, MT>, dim3(static_cast<unsigned>(p.runs), MT / gdn::kJoinWarps),
+                      32 * gdn::kJoinWarps, 0, s, p);
 }
 
 template <typename T, int D>
 cudaError_t launch_attn(AttnKind kind, const gdn::AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
-  if (kind == kAttn16) {
-    gdn::gdn_attn_kernel<T, D, 1><<<p.runs, gdn::kAttnThreads, gdn::AttnPlan<D, 1>::DYN_SMEM, s>>>(p);
-    return launch_join<T, D, 16>(p, s);
-  }
-  if (kind == kAttn32) {
-    gdn::gdn_attn_kernel<T, D, 2><<<p.runs, gdn::kAttnThreads, gdn::AttnPlan<D, 2>::DYN_SMEM, s>>>(p);
-    return launch_join<T, D, 32>(p, s);
-  }
-  gdn::gdn_attn_tc_kernel<T, D><<<p.runs, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s>>>(k, v, p);
-  return launch_join<T, D, gdn::kTcRows>(p, s);
+  const dim3 grid(static_cast<unsigned>(p.runs));
+  if (kind == kAttn16)
+    return launch_join<T, D, 16>(
+        launch_early(gdn::gdn_attn_kernel<T, D, 1>, grid, gdn::kAttnThreads, gdn::AttnPlan<D, 1>::DYN_SMEM, s, p), p, s);
+  if (kind == kAttn32)
+    return launch_join<T, D, 32>(
+        launch_early(gdn::gdn_attn_kernel<T, D, 2>, grid, gdn::kAttnThreads, gdn::AttnPlan<D, 2>::DYN_SMEM, s, p), p, s);
+  return launch_join<T, D, gdn::kTcRows>(
+      launch_early(gdn::gdn_attn_tc_kernel<T, D>, grid, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s, k, v, p), p, s);
 }
 
 }  // namespace
@@ -350,18 +358,9 @@ int gdn_head_norm_rope_backward(const void* q, const void* k, const int32_t* pos
     });
   });
   if (sums) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = s;
-    cudaLaunchAttribute a[1];
-    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = a;
-    cfg.numAttrs = 1;
     const float* parts = p.partials;
-    cudaLaunchKernelEx(&cfg, d == 64 ? gdn::gdn_norm_weight_sum_kernel<64> : gdn::gdn_norm_weight_sum_kernel<128>, parts,
-                       static_cast<int>(p.q_ctas), grid, dq_weight, dk_weight);  // a refusal is launched()'s to report
+    launch_early(d == 64 ? gdn::gdn_norm_weight_sum_kernel<64> : gdn::gdn_norm_weight_sum_kernel<128>, dim3(2), 1024, 0, s,
+                 parts, p.q_ctas, grid, dq_weight, dk_weight);  // a refusal is launched()'s to report
   }
   int rc = launched(sums ? 2 : 1);
   if (sums && !workspace) {

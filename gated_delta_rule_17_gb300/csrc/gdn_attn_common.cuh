@@ -87,6 +87,17 @@ __device__ __forceinline__ int64_t attn_cost(const AttnParams& p, const AttnSeq&
   return static_cast<int64_t>(p.whole ? 1 : s.tiles) * attn_member_tiles(s, j, members) * p.nkv;
 }
 
+// The same as time, by which the members get their CTAs: in gdn_attn_tc_kernel a tile costs a
+// row tile that fills more than one stream about 3/2 of another (3000 and 1950 cycles).
+template <int MT, int KT>
+__device__ __forceinline__ int64_t attn_weight(const AttnParams& p, const AttnSeq& s, int j, int members) {
+  const int64_t cost = attn_cost(p, s, j, members);
+  if (MT <= KT || cost == 0) return cost;
+  const int last = s.qtiles - 1;
+  const bool small = last % members == j && s.n * p.group - last * MT <= MT / 2;
+  return 3 * cost - (small ? attn_cost(p, s, last, last + 1) : 0);
+}
+
 // Inclusive prefix of `x` over the warp, and the sum over it.
 __device__ __forceinline__ int64_t warp_prefix(int64_t x) {
   const int lane = threadIdx.x & 31;
@@ -137,7 +148,7 @@ template <int MT, int KT>
 __device__ __forceinline__ AttnStart attn_start(const AttnParams& p, int run) {
   const int B = p.cache.B, lane = threadIdx.x & 31;
   const bool report = run == 0;
-  // the most row tiles, and all members' work
+  // the most row tiles, and all members' weight
   int most = 0;
   int64_t work = 0;
   AttnSeq own{};  // this lane's sequence, where there are at most 32
@@ -145,23 +156,29 @@ __device__ __forceinline__ AttnStart attn_start(const AttnParams& p, int run) {
   for (int b = lane; b < B; b += 32) {
     own = attn_seq<MT, KT>(p, b, report);
     most = own.qtiles > most ? own.qtiles : most;
-    work += attn_cost(p, own, 0, 1);
+    work += attn_weight<MT, KT>(p, own, 0, 1);
   }
   most = __reduce_max_sync(0xffffffffu, most);
   const int64_t all = warp_sum(work);
   const int members = most < kAttnMembers ? most : kAttnMembers;
-  // member j has the runs j + floor((p.runs - members) work of members < j / all) and on, at least one
+  // member j has the runs j + floor((p.runs - members) weight of members < j / all) and on, at least one
   int64_t before = 0, total = 0;
   int member = 0, first = 0, next = p.runs;
   if (members == 1) {
-    total = all;
+    int64_t cost = 0;
+    for (int b = lane; b < B; b += 32) cost += attn_cost(p, B <= 32 ? own : attn_seq<MT, KT>(p, b, false), 0, 1);
+    total = warp_sum(cost);
   } else {
     for (int j = 0; j < members; ++j) {
-      int64_t sum = 0;
-      for (int b = lane; b < B; b += 32) sum += attn_cost(p, B <= 32 ? own : attn_seq<MT, KT>(p, b, false), j, members);
-      total = warp_sum(sum);
+      int64_t weight = 0, cost = 0;
+      for (int b = lane; b < B; b += 32) {
+        const AttnSeq s = B <= 32 ? own : attn_seq<MT, KT>(p, b, false);
+        weight += attn_weight<MT, KT>(p, s, j, members);
+        cost += attn_cost(p, s, j, members);
+      }
+      total = warp_sum(cost);
       const int begin = j + static_cast<int>(mul_div(before, p.runs - members, all));
-      before += total;
+      before += warp_sum(weight);
       const int end = j + 1 + static_cast<int>(mul_div(before, p.runs - members, all));
       if (run >= begin && run < end) {
         member = j;

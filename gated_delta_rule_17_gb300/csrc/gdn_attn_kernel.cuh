@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
   const int run = blockIdx.x;
 
   __shared__ AttnWalk<MT, kAttnTile> s_walk;
+  tc::grid_dependency_wait();
   if (warp == 0) {
     AttnWalk<MT, kAttnTile> found;
     found.begin(p, attn_start<MT, kAttnTile>(p, run));
@@ -323,6 +324,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
 constexpr int kJoinWarps = 8;
 template <typename T, int D, int MT>
 __global__ void __launch_bounds__(32 * kJoinWarps) gdn_attn_join_kernel(const AttnParams p) {
+  tc::allow_dependent_launch();
   tc::grid_dependency_wait();
   const int run = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + warp;
   const int4 cut = p.cut[run];

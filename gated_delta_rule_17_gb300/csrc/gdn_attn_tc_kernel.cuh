@@ -132,12 +132,7 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
   const int run = blockIdx.x;
   const TcShared sh{tc::smem_u32(s_bar), &s_abort, p.status};
 
-  if (warp == 0) {
-    AttnWalk<MT, kTcTile> found;
-    found.begin(p, attn_start<MT, kTcTile>(p, run));
-    if (lane == 0) s_walk = found;
-  }
-  if (threadIdx.x == 32) {
+  if (threadIdx.x == 0) {
     s_abort = 0;
     for (int i = 0; i < NS; ++i) {
       tc::mbar_init(sh.bar(Plan::FULL + i), 128);
@@ -153,8 +148,14 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     tc::mbar_init(sh.bar(Plan::JOIN), 256);
     tc::mbar_fence_init();
   }
-  if (threadIdx.x == 0 && !p.whole) p.cut[run] = make_int4(0, 0, 0, -1);
   if (warp == 12) tc::tmem_alloc(tc::smem_u32(&s_tmem), Plan::TMEM_COLS);
+  tc::grid_dependency_wait();  // so far nothing has touched global memory
+  if (warp == 0) {
+    AttnWalk<MT, kTcTile> found;
+    found.begin(p, attn_start<MT, kTcTile>(p, run));
+    if (lane == 0) s_walk = found;
+  }
+  if (threadIdx.x == 0 && !p.whole) p.cut[run] = make_int4(0, 0, 0, -1);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
