@@ -104,14 +104,10 @@ int device_info(DeviceInfo** out) {
     const std::pair<const void*, int> bwd[] = {
         {reinterpret_cast<const void*>(gdn::gdn_bwd_dstates_tc_kernel), gdn::DsPlan::DYN_SMEM},
         {reinterpret_cast<const void*>(gdn::gdn_bwd_grads_tc_kernel), gdn::GtPlan::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__nv_bfloat16, 64, 1>), gdn::AttnPlan<64, 1>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__nv_bfloat16, 64, 2>), gdn::AttnPlan<64, 2>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__nv_bfloat16, 128, 1>), gdn::AttnPlan<128, 1>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__nv_bfloat16, 128, 2>), gdn::AttnPlan<128, 2>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 64, 1>), gdn::AttnPlan<64, 1>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 64, 2>), gdn::AttnPlan<64, 2>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 128, 1>), gdn::AttnPlan<128, 1>::DYN_SMEM},
-        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 128, 2>), gdn::AttnPlan<128, 2>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__nv_bfloat16, 64>), gdn::AttnPlan<64>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__nv_bfloat16, 128>), gdn::AttnPlan<128>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 64>), gdn::AttnPlan<64>::DYN_SMEM},
+        {reinterpret_cast<const void*>(gdn::gdn_attn_kernel<__half, 128>), gdn::AttnPlan<128>::DYN_SMEM},
         {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__nv_bfloat16, 64>), gdn::AttnTcPlan<64>::DYN_SMEM},
         {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__nv_bfloat16, 128>), gdn::AttnTcPlan<128>::DYN_SMEM},
         {reinterpret_cast<const void*>(gdn::gdn_attn_tc_kernel<__half, 64>), gdn::AttnTcPlan<64>::DYN_SMEM},

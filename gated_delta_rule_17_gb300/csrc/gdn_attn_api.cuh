@@ -164,14 +164,17 @@ int check_paged(const gdn_paged_t* c, int nkv, int d, gdn::PagedParams* p) {
 // ---- attention -----------------------------------------------------------------------
 constexpr int kAttnCtasPerSm = 2;  // of gdn_attn_kernel; gdn_attn_tc_kernel has an SM to itself
 
-// The kernel for the rows that a kv head may have (new rows of a sequence x heads of a group).
-enum AttnKind { kAttn16, kAttn32, kAttnTc };
-constexpr int kAttnKindRows[] = {16, 32, gdn::kTcRows};
+// The kernel for the rows that a kv head may have (new rows of a sequence x heads of a group). With
+// 16 or fewer one block of register products does: 79 us against 82 on tcgen05 at 16 rows, 16
+// sequences of 4096 to 8192 tokens, 8 kv heads; 58 against 72 for 128 sequences of 200 to 400. Above,
+// tcgen05 does: 83 against 112 (two blocks of 16) or 106 (blocks of 32) at 24 rows.
+enum AttnKind { kAttn16, kAttnTc };
+constexpr int kAttnKindRows[] = {gdn::kAttnRows, gdn::kTcRows};
 AttnKind attn_kind(int64_t rows, float scale) {
-  if (rows <= 16) return kAttn16;
   // the tensor-core kernel keeps its maxima in unscaled scores, which a scale <= 0 would turn round
-  return rows <= 32 || !(scale > 0.f) ? kAttn32 : kAttnTc;
+  return rows <= gdn::kAttnRows || !(scale > 0.f) ? kAttn16 : kAttnTc;
 }
+
 // A block table with room for at most this many tokens a sequence is not split over the CTAs: a
 // unit of them costs less than the join that a split needs.
 constexpr int64_t kAttnWholeTokens = 512;
@@ -232,10 +235,10 @@ cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, int smem,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename T, int D, int MT>
+template <typename T, int D, int MT, int W>
 cudaError_t launch_join(cudaError_t e, const gdn::AttnParams& p, cudaStream_t s) {
   if (e != cudaSuccess || p.whole) return e;
-  return launch_early(gdn::gdn_attn_join_kernel<T, D, MT>, dim3(static_cast<unsigned>(p.runs), MT / gdn::kJoinWarps),
+  return launch_early(gdn::gdn_attn_join_kernel<T, D, MT, W>, dim3(static_cast<unsigned>(p.runs), MT * W / gdn::kJoinWarps),
                       32 * gdn::kJoinWarps, 0, s, p);
 }
 
@@ -243,12 +246,9 @@ template <typename T, int D>
 cudaError_t launch_attn(AttnKind kind, const gdn::AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.runs));
   if (kind == kAttn16)
-    return launch_join<T, D, 16>(
-        launch_early(gdn::gdn_attn_kernel<T, D, 1>, grid, gdn::kAttnThreads, gdn::AttnPlan<D, 1>::DYN_SMEM, s, p), p, s);
-  if (kind == kAttn32)
-    return launch_join<T, D, 32>(
-        launch_early(gdn::gdn_attn_kernel<T, D, 2>, grid, gdn::kAttnThreads, gdn::AttnPlan<D, 2>::DYN_SMEM, s, p), p, s);
-  return launch_join<T, D, gdn::kTcRows>(
+    return launch_join<T, D, gdn::kAttnRows, 4>(
+        launch_early(gdn::gdn_attn_kernel<T, D>, grid, gdn::kAttnThreads, gdn::AttnPlan<D>::DYN_SMEM, s, p), p, s);
+  return launch_join<T, D, gdn::kTcRows, 1>(
       launch_early(gdn::gdn_attn_tc_kernel<T, D>, grid, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s, k, v, p), p, s);
 }
 
@@ -420,7 +420,7 @@ int gdn_paged_append(const void* k, const void* v, const gdn_paged_t* cache, con
 size_t gdn_tree_attention_workspace_bytes(int nq, int nkv, int d) {
   if (nq <= 0 || nkv <= 0 || (d != 64 && d != 128)) return 0;
   size_t most = 0;
-  for (AttnKind kind : {kAttn16, kAttn32, kAttnTc}) {
+  for (AttnKind kind : {kAttn16, kAttnTc}) {
     const size_t n = attn_layout(kind, plan_sms(), d).total;
     if (n > most) most = n;
   }

@@ -4,8 +4,8 @@
 // byte of the cache, far below the 289 flops a byte at which the card's tensor rate meets
 // its bandwidth, so it is bound by reading K and V once. Every warp is on its own: it
 // streams 16-token slabs of K and V through its private ring in shared memory (16-byte
-// cp.async from the tokens' places in the pages, any page size), and has all MB x 16 query
-// rows against them with register tensor products: scores S = Q K^T, running maximum and sum, O += P V.
+// cp.async from the tokens' places in the pages, any page size), and has 16 query rows against
+// them with register tensor products: scores S = Q K^T, running maximum and sum, O += P V.
 // No barrier is needed in the loop; the warps' (m, l, O) are added up at a unit's end.
 #pragma once
 #include "gdn_attn_common.cuh"
@@ -14,12 +14,13 @@ namespace gdn {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kAttnRows = 16;                      // query rows of a unit
 constexpr int kAttnSlab = 16;                      // tokens of a warp's step
 constexpr int kAttnTile = kAttnWarps * kAttnSlab;  // tokens of a CTA's step
 
-template <int D, int MB>
+template <int D>
 struct AttnPlan {
-  static constexpr int MT = 16 * MB;
+  static constexpr int MT = kAttnRows;
   static constexpr int ROW = D * 2;                        // bytes of a key or value
   static constexpr int SLAB = kAttnSlab * ROW;             // bytes of a slab of K or V
   static constexpr int STAGES = 3 * 128 / D;
@@ -83,9 +84,9 @@ __device__ __forceinline__ TokenPlace token_place(const AttnParams& p, const int
   return r;
 }
 
-template <typename T, int D, int MB>
+template <typename T, int D>
 __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnParams p) {
-  using Plan = AttnPlan<D, MB>;
+  using Plan = AttnPlan<D>;
   constexpr int MT = Plan::MT, KS = D / 16, NT = D / 8, CH = D / 8, STAGES = Plan::STAGES;
   extern __shared__ uint8_t dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 127) & ~static_cast<uintptr_t>(127));
@@ -112,34 +113,27 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
     const int R = s.n * p.group;
     const int32_t* table = c.block_table + b * c.table_stride;
 
-    // Q fragments: row gr (+8) of each block of 16
-    uint32_t qf[MB][KS][4];
-    int node[MB][2];  // the new token of each of this thread's rows, -1 for none
+    // Q fragments: rows gr and gr + 8
+    uint32_t qf[KS][4];
+    int node[2];  // the new token of either row, -1 for none
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = qt * MT + hf * 8 + gr;
+      const int i = r < R ? r / p.group : 0, g = r < R ? r - i * p.group : 0;
+      node[hf] = r < R ? i : -1;
+      const T* src = static_cast<const T*>(p.q) + (static_cast<int64_t>(s.first) + i) * p.q_stride +
+                     static_cast<int64_t>(kvh * p.group + g) * D + 2 * tc;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = qt * MT + mb * 16 + hf * 8 + gr;
-        node[mb][hf] = r < R ? r / p.group : -1;
-        const int i = r < R ? r / p.group : 0, g = r < R ? r - i * p.group : 0;
-        const T* src = static_cast<const T*>(p.q) + (static_cast<int64_t>(s.first) + i) * p.q_stride +
-                       static_cast<int64_t>(kvh * p.group + g) * D + 2 * tc;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          qf[mb][ks][hf] = r < R ? *reinterpret_cast<const uint32_t*>(src + 16 * ks) : 0u;
-          qf[mb][ks][2 + hf] = r < R ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 8) : 0u;
-        }
+      for (int ks = 0; ks < KS; ++ks) {
+        qf[ks][hf] = r < R ? *reinterpret_cast<const uint32_t*>(src + 16 * ks) : 0u;
+        qf[ks][2 + hf] = r < R ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 8) : 0u;
       }
-    float o[MB][NT][4], m[MB][2], l[MB][2];
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-      m[mb][0] = m[mb][1] = -INFINITY;
-      l[mb][0] = l[mb][1] = 0.f;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[mb][nt][j] = 0.f;
     }
+    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[nt][j] = 0.f;
 
     const T* kbase = static_cast<const T*>(c.k) + kvh * c.k_head;
     const T* vbase = static_cast<const T*>(c.v) + kvh * c.v_head;
@@ -178,79 +172,68 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
       const int tok = t * kAttnTile + warp * kAttnSlab;
       if (tok >= s.len) continue;  // the whole warp: nothing of its slab is there
 
-      float sc[MB][2][4];
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sc[mb][nt][j] = 0.f;
+      float sc[2][4] = {};
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t kf[4];
         ldmatrix4(ks_addr + attn_sw<D>((lane >> 4) * 8 + (lane & 7), 2 * ks + ((lane >> 3) & 1)), kf);
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          mma16816<T>(sc[mb][0], qf[mb][ks], kf[0], kf[1]);
-          mma16816<T>(sc[mb][1], qf[mb][ks], kf[2], kf[3]);
-        }
+        mma16816<T>(sc[0], qf[ks], kf[0], kf[1]);
+        mma16816<T>(sc[1], qf[ks], kf[2], kf[3]);
       }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[nt][j] *= p.scale_log2;  // before the mask: the scale may be negative
       // tokens that a row does not see; before the new tokens every row sees all
       if (tok + kAttnSlab > s.ctx) {
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
+        for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int at = tok + nt * 8 + 2 * tc + (j & 1), i = node[mb][j >> 1], x = at - s.ctx;
-              bool sees = at < s.len;
-              if (sees && x >= 0) {
-                if (!p.mask)
-                  sees = x <= i;
-                else
-                  sees = i >= 0 && (x >> 6) < p.mask_words &&
-                         ((p.mask[(static_cast<int64_t>(s.first) + i) * p.mask_words + (x >> 6)] >> (x & 63)) & 1);
-              }
-              if (!sees) sc[mb][nt][j] = -INFINITY;
+          for (int j = 0; j < 4; ++j) {
+            const int at = tok + nt * 8 + 2 * tc + (j & 1), i = node[j >> 1], x = at - s.ctx;
+            bool sees = at < s.len;
+            if (sees && x >= 0) {
+              if (!p.mask)
+                sees = x <= i;
+              else
+                sees = i >= 0 && (x >> 6) < p.mask_words &&
+                       ((p.mask[(static_cast<int64_t>(s.first) + i) * p.mask_words + (x >> 6)] >> (x & 63)) & 1);
             }
+            if (!sees) sc[nt][j] = -INFINITY;
+          }
+      }
+      uint32_t pf[4];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float x0 = sc[0][2 * hf], x1 = sc[0][2 * hf + 1], x2 = sc[1][2 * hf], x3 = sc[1][2 * hf + 1];
+        float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[hf], mx), base = mn == -INFINITY ? 0.f : mn;
+        if (__any_sync(0xffffffffu, mn > m[hf])) {
+          const float f = exp2_approx(m[hf] - base);
+          l[hf] *= f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            o[nt][2 * hf] *= f;
+            o[nt][2 * hf + 1] *= f;
+          }
+          m[hf] = mn;
+        }
+        x0 = exp2_approx(x0 - base);
+        x1 = exp2_approx(x1 - base);
+        x2 = exp2_approx(x2 - base);
+        x3 = exp2_approx(x3 - base);
+        l[hf] += (x0 + x1) + (x2 + x3);  // this thread's tokens; over the row at the end
+        pf[hf] = pack2<T>(x0, x1);
+        pf[2 + hf] = pack2<T>(x2, x3);
       }
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        uint32_t pf[4];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float x0 = sc[mb][0][2 * hf] * p.scale_log2, x1 = sc[mb][0][2 * hf + 1] * p.scale_log2;
-          float x2 = sc[mb][1][2 * hf] * p.scale_log2, x3 = sc[mb][1][2 * hf + 1] * p.scale_log2;
-          float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[mb][hf], mx), base = mn == -INFINITY ? 0.f : mn;
-          if (__any_sync(0xffffffffu, mn > m[mb][hf])) {
-            const float f = exp2_approx(m[mb][hf] - base);
-            l[mb][hf] *= f;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              o[mb][nt][2 * hf] *= f;
-              o[mb][nt][2 * hf + 1] *= f;
-            }
-            m[mb][hf] = mn;
-          }
-          x0 = exp2_approx(x0 - base);
-          x1 = exp2_approx(x1 - base);
-          x2 = exp2_approx(x2 - base);
-          x3 = exp2_approx(x3 - base);
-          l[mb][hf] += (x0 + x1) + (x2 + x3);  // this thread's tokens; over the row at the end
-          pf[hf] = pack2<T>(x0, x1);
-          pf[2 + hf] = pack2<T>(x2, x3);
-        }
-#pragma unroll
-        for (int cp = 0; cp < NT / 2; ++cp) {
-          uint32_t vf[4];
-          ldmatrix4_trans(vs_addr + attn_sw<D>(((lane >> 3) & 1) * 8 + (lane & 7), 2 * cp + (lane >> 4)), vf);
-          mma16816<T>(o[mb][2 * cp], pf, vf[0], vf[1]);
-          mma16816<T>(o[mb][2 * cp + 1], pf, vf[2], vf[3]);
-        }
+      for (int cp = 0; cp < NT / 2; ++cp) {
+        uint32_t vf[4];
+        ldmatrix4_trans(vs_addr + attn_sw<D>(((lane >> 3) & 1) * 8 + (lane & 7), 2 * cp + (lane >> 4)), vf);
+        mma16816<T>(o[2 * cp], pf, vf[0], vf[1]);
+        mma16816<T>(o[2 * cp + 1], pf, vf[2], vf[3]);
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -260,22 +243,19 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
     float* jml = jo + kAttnWarps * MT * D;            // [warp][MT][2]
     __syncthreads();                                  // the rings are done with
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = mb * 16 + hf * 8 + gr;
-        float ll = l[mb][hf];
-        ll += __shfl_xor_sync(0xffffffffu, ll, 1);
-        ll += __shfl_xor_sync(0xffffffffu, ll, 2);
-        if (tc == 0) {
-          jml[(warp * MT + r) * 2] = m[mb][hf];
-          jml[(warp * MT + r) * 2 + 1] = ll;
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          *reinterpret_cast<float2*>(jo + (warp * MT + r) * D + nt * 8 + 2 * tc) =
-              make_float2(o[mb][nt][2 * hf], o[mb][nt][2 * hf + 1]);
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = hf * 8 + gr;
+      float ll = l[hf];
+      ll += __shfl_xor_sync(0xffffffffu, ll, 1);
+      ll += __shfl_xor_sync(0xffffffffu, ll, 2);
+      if (tc == 0) {
+        jml[(warp * MT + r) * 2] = m[hf];
+        jml[(warp * MT + r) * 2 + 1] = ll;
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        *reinterpret_cast<float2*>(jo + (warp * MT + r) * D + nt * 8 + 2 * tc) = make_float2(o[nt][2 * hf], o[nt][2 * hf + 1]);
+    }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == s.tiles;
     const int slot = t0 == 0 ? 1 : 0;
@@ -319,22 +299,26 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
   }
 }
 
-// Joins the pieces of the unit that begins in run blockIdx.x and goes on in the next runs: a warp a
-// row, kJoinWarps rows a CTA, several pieces' loads in flight.
+// Joins the pieces of the unit that begins in run blockIdx.x and goes on in the next runs: W warps a
+// row, each every W-th group of U pieces, whose loads are under way together. A unit of few rows may
+// have a hundred pieces and more (one long sequence alone), so its rows get four warps.
 constexpr int kJoinWarps = 8;
-template <typename T, int D, int MT>
+template <typename T, int D, int MT, int W>
 __global__ void __launch_bounds__(32 * kJoinWarps) gdn_attn_join_kernel(const AttnParams p) {
+  constexpr int ROWS = kJoinWarps / W, V = D / 32, U = 8;  // rows of a CTA, values of a lane, pieces in flight
+  __shared__ float s_ml[kJoinWarps][2];
+  __shared__ float s_o[kJoinWarps][D];
   tc::allow_dependent_launch();
   tc::grid_dependency_wait();
-  const int run = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + warp;
+  const int run = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * ROWS + warp / W, sub = warp % W;
   const int4 cut = p.cut[run];
   if (cut.w < 0) return;
   const int unit_qtiles = (cut.y * p.group + MT - 1) / MT;
   const int kvh = cut.z / unit_qtiles, qt = cut.z - kvh * unit_qtiles, row = qt * MT + r;
-  if (row >= cut.y * p.group) return;
-  constexpr int V = D / 32, U = 8;  // values of a lane, pieces in flight
+  const bool has = row < cut.y * p.group;
   float m = -INFINITY, l = 0.f, o[V] = {};
-  for (int i0 = run; i0 <= cut.w; i0 += U) {
+  for (int i0 = run + sub * U; has && i0 <= cut.w; i0 += W * U) {
     float pm[U], pl[U], v[U][V];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -371,6 +355,29 @@ __global__ void __launch_bounds__(32 * kJoinWarps) gdn_attn_join_kernel(const At
       for (int j = 0; j < V; ++j) o[j] = fmaf(v[u][j], g, o[j]);
     }
   }
+  if (W > 1) {
+    s_ml[warp][0] = m;
+    s_ml[warp][1] = l;
+#pragma unroll
+    for (int j = 0; j < V; ++j) s_o[warp][V * lane + j] = o[j];
+    __syncthreads();
+    if (sub != 0) return;
+    float mn = m;
+#pragma unroll
+    for (int w = 1; w < W; ++w) mn = fmaxf(mn, s_ml[warp + w][0]);
+    const float base = mn == -INFINITY ? 0.f : mn, f = exp2_approx(m - base);
+    l *= f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] *= f;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      const float g = exp2_approx(s_ml[warp + w][0] - base);
+      l = fmaf(s_ml[warp + w][1], g, l);
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] = fmaf(s_o[warp + w][V * lane + j], g, o[j]);
+    }
+  }
+  if (!has) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int i = row / p.group, g = row - i * p.group;
   T* dst = static_cast<T*>(p.out) + (static_cast<int64_t>(cut.x) + i) * p.out_stride +

@@ -95,7 +95,7 @@ def attention(q, k, v, ctx, mask, scale):
             out[i, h] = p @ vv
             spread[i, h] = p @ vv.abs()
             # fp32 scores: d products, their sum, the scaling and the exponential's argument
-            size[i, h] = scale * ((d + 4) * (kk.abs() @ q[i, h].abs())).max() + 4 * x.abs().max()
+            size[i, h] = abs(scale) * ((d + 4) * (kk.abs() @ q[i, h].abs())).max() + 4 * x.abs().max()
     # the sums over the tokens in fp32, and 2^x to 2^-22
     slack = 2 * FP32 * (size[..., None] + (ctx + n) + 16)
     return out, spread, slack

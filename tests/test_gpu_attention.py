@@ -535,6 +535,36 @@ def test_scores_far_apart(n):
     _check_attention(c, q, out.cpu(), ks, vs, None, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 1e-30, 5.0])
+@pytest.mark.parametrize("n", [2, 30])
+def test_any_scale(n, scale):
+    import gated_delta_rule_17_gb300 as gdn
+
+    c = Cache(40, [300, 50], [n, n], 2, 128, 16, BF)
+    ks, vs = c.fill_tokens()
+    q = randn(c.g, c.rows, 8, 128)
+    out = torch.empty(c.rows, 8 * 128, dtype=BF, device="cuda")
+    gdn.tree_attention(q.cuda(), *c.plan(), out, nq=8, nkv=2, cu_rows=c.cu.cuda(), max_rows=n, scale=scale)
+    gdn.check()
+    _check_attention(c, q, out.cpu(), ks, vs, None, scale)
+
+
+def test_output_rows_on_16_byte_boundaries():
+    # rows that whole 32-byte sectors do not fit; on tcgen05 and not
+    import gated_delta_rule_17_gb300 as gdn
+
+    for n in (3, 40):
+        c = Cache(41, [70, 0], [n, n], 2, 64, 16, HF)
+        ks, vs = c.fill_tokens()
+        q = randn(c.g, c.rows, 8, 64, dtype=HF)
+        wide = torch.full((c.rows, 8 * 64 + 24), 9.0, dtype=HF, device="cuda")
+        out = wide[:, 8:8 + 8 * 64]
+        gdn.tree_attention(q.cuda(), *c.plan(), out, nq=8, nkv=2, head_dim=64, cu_rows=c.cu.cuda(), max_rows=n)
+        gdn.check()
+        _check_attention(c, q, out.cpu(), ks, vs, None, 0.125)
+        assert (wide[:, :8] == 9).all() and (wide[:, 8 + 8 * 64:] == 9).all()
+
+
 @pytest.mark.parametrize("n", [1, 20])
 def test_cache_past_four_gigabytes(n):
     # pages whose first element is past 2^31: 64-bit offsets, in the append and the attention
