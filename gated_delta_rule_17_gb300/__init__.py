@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 __all__ = ["prefill", "prefill_noalloc", "prefill_host", "host_scratch_bytes", "NOALLOC_MAX_SEQS", "workspace_bytes", "check", "last_launch_count",
@@ -102,7 +103,7 @@ def load():
             lib.gdn_prefill_backward.argtypes = [vp] * 14 + [i] * 6 + [ctypes.POINTER(Strides), vp, vp, sz, vp]
             lib.gdn_prefill_backward.restype = i
             f32 = ctypes.c_float
-            rope, norm_st, paged = (ctypes.POINTER(x) for x in (Rope, NormStrides, Paged))
+            rope = norm_st = paged = vp  # Rope, NormStrides, Paged: by address
             lib.gdn_head_norm_rope.argtypes = [vp, vp, vp, rope, vp, vp, f32, vp, vp] + [i] * 5 + [norm_st, vp]
             lib.gdn_head_norm_rope.restype = i
             lib.gdn_head_norm_rope_backward_workspace_bytes.argtypes = [i] * 4
@@ -387,6 +388,10 @@ def backward(q, k, v, g, beta, h0, dout, dq, dk, dv, dg, dbeta, *, nk: int, nv: 
 
 _torch = None   # torch, once one of the calls below has been made
 _codes = {}     # torch dtype -> the ABI's number
+# The ABI's structs, packed: the bytes of Rope, NormStrides and Paged (a fraction of a ctypes object's cost)
+_ROPE = struct.Struct("@QQqiii4x").pack
+_STRIDES = struct.Struct("@6q").pack
+_PAGED = struct.Struct("@QQqqqqqqiiQqiii4xQQ").pack
 
 
 def _setup():
@@ -415,17 +420,13 @@ def _act_code(t, name, most):
 
 def _act(t, name, dtype, rows, inner):
     """Checks [rows, ...] activations with `inner` contiguous elements a row; (address, row stride)."""
-    if t.dtype != dtype or not t.is_cuda:
+    if t.dtype is not dtype or not t.is_cuda:
         raise GdnError(GDN_ERR_ARG, f"{name} must be a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
-    shape, strides = t.shape, t.stride()
-    if len(shape) != 2 or shape[1] != inner or strides[1] != 1 or rows < 2:  # not the common layout
-        if len(shape) < 2:
-            raise GdnError(GDN_ERR_ARG, f"{name} must be at least 2-D ([rows, ...])")
-        stride = _row_stride(t, name, inner)
-    else:
-        stride = strides[0]
-    if shape[0] != rows:
-        raise GdnError(GDN_ERR_ARG, f"{name} has {shape[0]} rows, need {rows}")
+    if t.numel() == rows * inner and t.is_contiguous() and t.dim() > 1 and t.size(0) == rows:  # packed rows
+        return t.data_ptr(), inner
+    stride = _row_stride(t, name, inner)
+    if t.size(0) != rows:
+        raise GdnError(GDN_ERR_ARG, f"{name} has {t.size(0)} rows, need {rows}")
     return t.data_ptr(), stride
 
 
@@ -433,22 +434,28 @@ def _vector(t, name, dtype, n):
     """The address of a contiguous CUDA vector of n elements, or None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
         raise GdnError(GDN_ERR_ARG, f"{name} must be a contiguous {dtype} CUDA tensor of {n} elements")
     return t.data_ptr()
 
 
 def _rope(cos, sin, interleaved):
+    """The tables as the ABI's struct, packed."""
     if cos is None or sin is None:
         if cos is not sin:
             raise GdnError(GDN_ERR_ARG, "cos and sin must be given together")
         return None
-    f32, shape, st = _torch.float32, cos.shape, cos.stride()
-    if cos.dtype != f32 or sin.dtype != f32 or not cos.is_cuda or not sin.is_cuda or len(shape) != 2 or (
-            sin.shape != shape or sin.stride() != st or (st[1] != 1 and shape[1] > 1)):
-        raise GdnError(GDN_ERR_ARG, "cos and sin must be fp32 CUDA tensors [positions, rot/2], contiguous in a row, both alike")
+    f32, shape = _torch.float32, cos.shape
+    if cos.dtype is not f32 or sin.dtype is not f32 or not cos.is_cuda or not sin.is_cuda or len(shape) != 2 or sin.shape != shape:
+        raise GdnError(GDN_ERR_ARG, "cos and sin must be fp32 CUDA tensors [positions, rot/2], both alike")
     n, half = shape
-    return Rope(cos.data_ptr(), sin.data_ptr(), st[0] if n > 1 else max(st[0], half), n, 2 * half, 1 if interleaved else 0)
+    stride = half
+    if not (cos.is_contiguous() and sin.is_contiguous()):
+        st = cos.stride()
+        if sin.stride() != st or (st[1] != 1 and half > 1):
+            raise GdnError(GDN_ERR_ARG, "cos and sin must be contiguous in a row, with the same row stride")
+        stride = st[0] if n > 1 else max(st[0], half)
+    return _ROPE(cos.data_ptr(), sin.data_ptr(), stride, n, 2 * half, 1 if interleaved else 0)
 
 
 def _scratch(workspace):
@@ -490,7 +497,7 @@ def head_norm_rope(q, k, positions, cos, sin, q_out, k_out, *, nq: int, nkv: int
     rc = _lib.gdn_head_norm_rope(qp, kp, _vector(positions, "positions", torch.int32, rows), _rope(cos, sin, interleaved),
                                  _vector(q_weight, "q_weight", torch.float32, head_dim),
                                  _vector(k_weight, "k_weight", torch.float32, head_dim), eps, qo, ko, rows, nq, nkv,
-                                 head_dim, code, NormStrides(qs, ks, qos, kos, 0, 0), _stream_of(stream, x.device))
+                                 head_dim, code, _STRIDES(qs, ks, qos, kos, 0, 0), _stream_of(stream, x.device))
     if rc != GDN_OK:
         _raise(rc)
 
@@ -523,7 +530,7 @@ def head_norm_rope_backward(q, k, positions, cos, sin, q_grad, k_grad, dq, dk, d
                                           _vector(q_weight, "q_weight", f32, head_dim), _vector(k_weight, "k_weight", f32, head_dim),
                                           eps, gq, gk, dqp, dkp, _vector(dq_weight, "dq_weight", f32, head_dim),
                                           _vector(dk_weight, "dk_weight", f32, head_dim), rows, nq, nkv, head_dim, code,
-                                          NormStrides(qs, ks, dqs, dks, gqs, gks), ws, size, _stream_of(stream, x.device))
+                                          _STRIDES(qs, ks, dqs, dks, gqs, gks), ws, size, _stream_of(stream, x.device))
     if rc != GDN_OK:
         _raise(rc)
 
@@ -531,17 +538,23 @@ def head_norm_rope_backward(q, k, positions, cos, sin, q_grad, k_grad, dq, dk, d
 def _paged(x, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, d, rows):
     """The cache and the batch of `rows` rows like x as the ABI's struct."""
     dt, shape, ks, vs = x.dtype, k_cache.shape, k_cache.stride(), v_cache.stride()
-    if k_cache.dtype != dt or v_cache.dtype != dt or not k_cache.is_cuda or not v_cache.is_cuda:
+    if k_cache.dtype is not dt or v_cache.dtype is not dt or not k_cache.is_cuda or not v_cache.is_cuda:
         raise GdnError(GDN_ERR_ARG, f"k_cache and v_cache must be {dt} CUDA tensors")
     if len(shape) != 4 or shape[2] != nkv or shape[3] != d or v_cache.shape != shape or ks[3] != 1 or vs[3] != 1:
         raise GdnError(GDN_ERR_ARG, f"k_cache and v_cache must be [pages, page_size, {nkv}, {d}], the last dimension contiguous")
-    i32, table, ts = _torch.int32, block_table.shape, block_table.stride()
-    if block_table.dtype != i32 or not block_table.is_cuda or len(table) != 2 or (ts[1] != 1 and table[1] > 1):
-        raise GdnError(GDN_ERR_ARG, "block_table must be an int32 CUDA tensor [B, max_pages], contiguous in a row")
+    i32, table = _torch.int32, block_table.shape
+    if block_table.dtype is not i32 or not block_table.is_cuda or len(table) != 2:
+        raise GdnError(GDN_ERR_ARG, "block_table must be an int32 CUDA tensor [B, max_pages]")
     B, most = table
-    return Paged(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], shape[0], shape[1],
-                 block_table.data_ptr(), max(ts[0], most), most, B, rows, _vector(ctx_lens, "ctx_lens", i32, B),
-                 _vector(cu_rows, "cu_rows", i32, B + 1))
+    stride = most
+    if not block_table.is_contiguous():
+        ts = block_table.stride()
+        if ts[1] != 1 and most > 1:
+            raise GdnError(GDN_ERR_ARG, "block_table must be contiguous in a row")
+        stride = max(ts[0], most) if B < 2 else ts[0]
+    return _PAGED(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], shape[0], shape[1],
+                  block_table.data_ptr(), stride, most, B, rows, _vector(ctx_lens, "ctx_lens", i32, B) or 0,
+                  _vector(cu_rows, "cu_rows", i32, B + 1) or 0)
 
 
 def paged_append(k, v, k_cache, v_cache, block_table, ctx_lens, *, nkv: int, head_dim: int = 128, cu_rows=None,

@@ -33,6 +33,11 @@ def test_every_declared_symbol_is_exported(gdn):
 P = 256  # an aligned address that no check dereferences
 
 
+def at(x):
+    """The address of a ctypes struct, kept alive by the caller; None for None."""
+    return None if x is None else ctypes.addressof(x)
+
+
 def rope(gdn, **kw):
     f = dict(cos=P, sin=P, stride=64, positions=10, rot=128, interleaved=0)
     f.update(kw)
@@ -40,7 +45,7 @@ def rope(gdn, **kw):
 
 
 def norm(gdn, q=P, k=P, pos=P, r=None, qw=None, kw=None, eps=1e-6, qo=P, ko=P, rows=4, nq=4, nkv=2, d=128, dtype=0, st=None):
-    rc = gdn.load().gdn_head_norm_rope(q, k, pos, r, qw, kw, eps, qo, ko, rows, nq, nkv, d, dtype, st, None)
+    rc = gdn.load().gdn_head_norm_rope(q, k, pos, at(r), qw, kw, eps, qo, ko, rows, nq, nkv, d, dtype, at(st), None)
     return rc, gdn.load().gdn_last_error().decode()
 
 
@@ -85,7 +90,7 @@ def test_norm_rope_backward_refusals(gdn):
     lib = gdn.load()
 
     def call(gq=P, gk=P, dq=P, rows=4, st=None, ws=None, size=0, dw=P):
-        rc = lib.gdn_head_norm_rope_backward(P, P, None, None, None, None, 1e-6, gq, gk, dq, P, dw, dw, rows, 4, 2, 128, 0, st, ws, size, None)
+        rc = lib.gdn_head_norm_rope_backward(P, P, None, None, None, None, 1e-6, gq, gk, dq, P, dw, dw, rows, 4, 2, 128, 0, at(st), ws, size, None)
         return rc, lib.gdn_last_error().decode()
 
     for words, kw in (("gradient", dict(gq=None)), ("aligned", dict(gk=P + 2)), ("NULL", dict(dq=None)),
@@ -109,13 +114,15 @@ def paged(gdn, **kw):
 
 def append(gdn, k=P, v=P, c=None, r=None, n=0, kw=None, eps=1e-6, nkv=2, d=128, dtype=0, ks=0, vs=0):
     lib = gdn.load()
-    rc = lib.gdn_paged_append(k, v, c if c is not None else paged(gdn), None, r, n, kw, eps, nkv, d, dtype, ks, vs, None)
+    c = c if c is not None else paged(gdn)
+    rc = lib.gdn_paged_append(k, v, at(c), None, at(r), n, kw, eps, nkv, d, dtype, ks, vs, None)
     return rc, lib.gdn_last_error().decode()
 
 
 def attend(gdn, q=P, c=None, mask=None, words=0, scale=0.1, out=P, nq=4, nkv=2, d=128, dtype=0, qs=0, os_=0, most=0, ws=None, size=0):
     lib = gdn.load()
-    rc = lib.gdn_tree_attention(q, c if c is not None else paged(gdn), mask, words, scale, out, nq, nkv, d, dtype, qs, os_, most, ws, size, None)
+    c = c if c is not None else paged(gdn)
+    rc = lib.gdn_tree_attention(q, at(c), mask, words, scale, out, nq, nkv, d, dtype, qs, os_, most, ws, size, None)
     return rc, lib.gdn_last_error().decode()
 
 
@@ -188,4 +195,13 @@ def test_binding_refuses_what_the_library_cannot_see(gdn):
         assert e.value.code == gdn.GDN_ERR_ARG
     with pytest.raises(gdn.GdnError):
         gdn.paged_append(bf, bf, cache.transpose(2, 3), cache, table, i, nkv=2)
-    assert ctypes.sizeof(gdn.Paged) == 8 * 8 + 8 + 8 + 8 + 16 + 16
+
+
+def test_packed_structs_are_the_declared_ones(gdn):
+    values = list(range(1, 18))
+    for cls, pack in ((gdn.Rope, gdn._ROPE), (gdn.NormStrides, gdn._STRIDES), (gdn.Paged, gdn._PAGED)):
+        n = len(cls._fields_)
+        raw = pack(*values[:n])
+        assert len(raw) == ctypes.sizeof(cls)
+        back = cls.from_buffer_copy(raw)
+        assert [getattr(back, f[0]) for f in cls._fields_] == values[:n]
