@@ -47,6 +47,22 @@ int check_stride(int64_t stride, int64_t least, const char* name) {
   return GDN_OK;
 }
 
+template <int N>
+using IntC = std::integral_constant<int, N>;
+
+// Head rows a lane group takes of a token with `heads` heads at most.
+int norm_unroll(int heads, int d) {
+  const int slots = 256 / d;
+  return heads <= slots ? 1 : heads <= 2 * slots ? 2 : gdn::kNormUnroll;
+}
+// Calls f with it at compile time.
+template <typename F>
+void by_unroll(int unroll, F&& f) {
+  if (unroll == 1) f(IntC<1>{});
+  else if (unroll == 2) f(IntC<2>{});
+  else f(IntC<gdn::kNormUnroll>{});
+}
+
 int norm_chunks(int heads, int d, int unroll) {
   const int per = unroll * (32 / (d / 8));
   return (heads + per - 1) / per;
@@ -104,8 +120,6 @@ int norm_setup(const void* q, const void* k, const int32_t* positions, const gdn
 }
 
 // Calls f(T{}, D, interleaved) with compile-time element type, head size and pairing.
-template <int N>
-using IntC = std::integral_constant<int, N>;
 template <typename F>
 void by_head(int d, int interleaved, F&& f) {
   if (d == 64) interleaved ? f(IntC<64>{}, std::true_type{}) : f(IntC<64>{}, std::false_type{});
@@ -263,8 +277,9 @@ int gdn_head_norm_rope(const void* q, const void* k, const int32_t* positions, c
   g_launches = 0;
   gdn::NormRopeParams p;
   int next = 0;
+  const int unroll = norm_unroll(nq > nkv ? nq : nkv, d);
   if (int rc = norm_setup(q, k, positions, rope, q_weight, k_weight, eps, q_out, k_out, rows, nq, nkv, d, dtype, strides,
-                          gdn::kNormUnroll, &p, &next))
+                          unroll, &p, &next))
     return rc;
   if (rows == 0) return GDN_OK;
   DeviceInfo* dev = nullptr;
@@ -275,7 +290,9 @@ int gdn_head_norm_rope(const void* q, const void* k, const int32_t* positions, c
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   by_type(dtype, [&](auto t) {
     by_head(d, next, [&](auto dim, auto pairs) {
-      gdn::gdn_head_norm_rope_kernel<decltype(t), dim.value, pairs.value><<<grid, gdn::kNormThreads, 0, s>>>(p);
+      by_unroll(unroll, [&](auto u) {
+        gdn::gdn_head_norm_rope_kernel<decltype(t), dim.value, pairs.value, u.value><<<grid, gdn::kNormThreads, 0, s>>>(p);
+      });
     });
   });
   return launched(1);
@@ -390,8 +407,9 @@ int gdn_paged_append(const void* k, const void* v, const gdn_paged_t* cache, con
   p.v_stride = v_stride ? v_stride : w;
   if (int rc = check_stride(p.k_stride, w, "k")) return rc;
   if (int rc = check_stride(p.v_stride, w, "v")) return rc;
-  p.chunks = norm_chunks(nkv, d, gdn::kNormUnroll);
-  const int64_t items = static_cast<int64_t>(cache->rows) * p.chunks * 2;
+  const int unroll = norm_unroll(nkv, d);
+  p.chunks = norm_chunks(nkv, d, unroll);
+  const int64_t items = static_cast<int64_t>(cache->rows) * p.chunks;
   if (items > INT32_MAX - (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "%d rows of %d heads exceed the item range", cache->rows, nkv);
   if (cache->rows == 0) return GDN_OK;
   if (!k || !v) return fail(GDN_ERR_ARG, "a required pointer is NULL");
@@ -411,7 +429,9 @@ int gdn_paged_append(const void* k, const void* v, const gdn_paged_t* cache, con
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   by_type16(dtype, [&](auto t) {
     by_head(d, next, [&](auto dim, auto pairs) {
-      gdn::gdn_paged_append_kernel<decltype(t), dim.value, pairs.value><<<grid, gdn::kNormThreads, 0, s>>>(p);
+      by_unroll(unroll, [&](auto u) {
+        gdn::gdn_paged_append_kernel<decltype(t), dim.value, pairs.value, u.value><<<grid, gdn::kNormThreads, 0, s>>>(p);
+      });
     });
   });
   return launched(1);

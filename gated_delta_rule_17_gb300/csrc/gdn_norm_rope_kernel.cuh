@@ -29,6 +29,9 @@ constexpr int kNormThreads = 128;
 // Registers for 40 warps an SM keep enough loads under way (fp32 words take twice the room: 20).
 template <typename T>
 constexpr int kNormCtasPerSm = sizeof(T) == 4 ? 5 : 10;
+constexpr int kAppendCtasPerSm = 9;
+// Head rows a lane group of a warp: four, or two or one for tokens of so few heads that the rest would
+// idle (append of 94 sequences of 258 to 516 tokens with one kv head: 40 us with four, 19 with one).
 constexpr int kNormUnroll = 4;
 constexpr int kNormBwdThreads = 128;
 constexpr int kNormBwdCtasPerSm = 6;
@@ -193,24 +196,24 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// The words of up to kNormUnroll x SLOTS heads of one token row (head h at h * src_head): the first
+// The words of up to U x SLOTS heads of one token row (head h at h * src_head): the first
 // loads of a warp, before it looks up where and how far to turn them.
-template <typename T, int D, bool kNext>
+template <typename T, int D, bool kNext, int U>
 __device__ __forceinline__ void fetch_heads(const T* src, int64_t src_head, int h0, int heads, int rot,
-                                            typename Four<T>::Word (&x)[kNormUnroll][2]) {
+                                            typename Four<T>::Word (&x)[U][2]) {
   constexpr int LPH = D / 8, SLOTS = 32 / LPH;
   const int lane = threadIdx.x & 31, slot = lane / LPH;
   const HeadLane<D, kNext> hl(lane % LPH, rot);
 #pragma unroll
-  for (int i = 0; i < kNormUnroll; ++i) {
+  for (int i = 0; i < U; ++i) {
     const int h = h0 + i * SLOTS + slot;
     hl.fetch(src + h * src_head, h < heads, x[i]);
   }
 }
 
 // Norms (where `normed`) and rotates them, and writes them to `dst` (head h at h * dst_head).
-template <typename T, int D, bool kNext>
-__device__ __forceinline__ void norm_rope_heads(const typename Four<T>::Word (&x)[kNormUnroll][2], T* dst, int64_t dst_head,
+template <typename T, int D, bool kNext, int U>
+__device__ __forceinline__ void norm_rope_heads(const typename Four<T>::Word (&x)[U][2], T* dst, int64_t dst_head,
                                                 int h0, int heads, const float* weight, bool normed, float eps,
                                                 const RopeParams& rope, int64_t pos) {
   constexpr int LPH = D / 8, SLOTS = 32 / LPH;
@@ -228,7 +231,7 @@ __device__ __forceinline__ void norm_rope_heads(const typename Four<T>::Word (&x
     vs[j] = wv[j] * s[j];
   }
 #pragma unroll
-  for (int i = 0; i < kNormUnroll; ++i) {
+  for (int i = 0; i < U; ++i) {
     const int h = h0 + i * SLOTS + slot;
     float u[4], v[4], r = 1.f;
     hl.template pairs<T>(x[i], u, v);
@@ -276,9 +279,9 @@ __device__ __forceinline__ bool position_held(int64_t pos, const RopeParams& rop
   return false;
 }
 
-template <typename T, int D, bool kNext>
+template <typename T, int D, bool kNext, int U>
 __global__ void __launch_bounds__(kNormThreads, kNormCtasPerSm<T>) gdn_head_norm_rope_kernel(const NormRopeParams p) {
-  constexpr int PER = kNormUnroll * (32 / (D / 8));  // heads of an item
+  constexpr int PER = U * (32 / (D / 8));  // heads of an item
   const unsigned item = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
   const unsigned row = item / static_cast<unsigned>(p.chunks);
   if (row >= static_cast<unsigned>(p.rows)) return;
@@ -286,11 +289,11 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtasPerSm<T>) gdn_head_norm
   const bool is_q = ch < p.q_chunks;
   const int h0 = (is_q ? ch : ch - p.q_chunks) * PER, heads = is_q ? p.nq : p.nkv;
   const int pos = p.rope.rot ? p.positions[row] : 0;
-  typename Four<T>::Word x[kNormUnroll][2];
-  fetch_heads<T, D, kNext>(is_q ? static_cast<const T*>(p.q) + row * p.q_stride : static_cast<const T*>(p.k) + row * p.k_stride,
+  typename Four<T>::Word x[U][2];
+  fetch_heads<T, D, kNext, U>(is_q ? static_cast<const T*>(p.q) + row * p.q_stride : static_cast<const T*>(p.k) + row * p.k_stride,
                            D, h0, heads, p.rope.rot, x);
   if (!position_held(pos, p.rope, p.status)) return;
-  norm_rope_heads<T, D, kNext>(x, is_q ? static_cast<T*>(p.q_out) + row * p.q_out_stride : static_cast<T*>(p.k_out) + row * p.k_out_stride,
+  norm_rope_heads<T, D, kNext, U>(x, is_q ? static_cast<T*>(p.q_out) + row * p.q_out_stride : static_cast<T*>(p.k_out) + row * p.k_out_stride,
                                D, h0, heads, is_q ? p.q_weight : p.k_weight, true, p.eps, p.rope, pos);
 }
 
@@ -589,29 +592,33 @@ struct AppendParams {
   RopeParams rope;
   const float* k_weight;
   int64_t k_stride, v_stride;
-  int nkv, chunks;  // warp items of a token: `chunks` for k's heads, as many for v's
+  int nkv, chunks;  // warp items of a token
   int norm;
   float eps;
   unsigned* status;
 };
 
-template <typename T, int D, bool kNext>
-__global__ void __launch_bounds__(kNormThreads, kNormCtasPerSm<T>) gdn_paged_append_kernel(const AppendParams p) {
-  constexpr int LPH = D / 8, SLOTS = 32 / LPH, PER = kNormUnroll * SLOTS;
-  const unsigned per_row = 2u * static_cast<unsigned>(p.chunks);
+template <typename T, int D, bool kNext, int U>
+__global__ void __launch_bounds__(kNormThreads, kAppendCtasPerSm) gdn_paged_append_kernel(const AppendParams p) {
+  constexpr int LPH = D / 8, SLOTS = 32 / LPH, PER = U * SLOTS;
   const unsigned item = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
-  const unsigned row = item / per_row;
+  const unsigned row = item / static_cast<unsigned>(p.chunks);
   const PagedParams& c = p.cache;
   if (row >= static_cast<unsigned>(c.rows)) return;
-  int ch = static_cast<int>(item - row * per_row);
-  const bool is_k = ch < p.chunks;
-  if (!is_k) ch -= p.chunks;
-  const int lane = threadIdx.x & 31;
-  // the heads first: their loads overlap the look-up of the token's place. Values are copied as
-  // they are, which is a key's way without a rotation.
-  typename Four<T>::Word x[kNormUnroll][2];
-  fetch_heads<T, D, kNext>(is_k ? static_cast<const T*>(p.k) + row * p.k_stride : static_cast<const T*>(p.v) + row * p.v_stride,
-                           D, ch * PER, p.nkv, is_k ? p.rope.rot : 0, x);
+  const int h0 = static_cast<int>(item - row * p.chunks) * PER;
+  const int lane = threadIdx.x & 31, slot = lane / LPH, at8 = 8 * (lane % LPH);
+  // the heads first, keys and values: their loads overlap the look-up of the token's place
+  typename Four<T>::Word x[U][2];
+  fetch_heads<T, D, kNext, U>(static_cast<const T*>(p.k) + row * p.k_stride, D, h0, p.nkv, p.rope.rot, x);
+  uint4 v[U];
+  {
+    const T* src = static_cast<const T*>(p.v) + row * p.v_stride + at8;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * SLOTS + slot;
+      v[i] = h < p.nkv ? *reinterpret_cast<const uint4*>(src + h * D) : make_uint4(0, 0, 0, 0);
+    }
+  }
   const int b = c.cu_rows ? find_sequence(c.cu_rows, c.B, static_cast<int>(row)) : static_cast<int>(row);
   const int first = c.cu_rows ? c.cu_rows[b] : static_cast<int>(row);
   const int end = c.cu_rows ? c.cu_rows[b + 1] : static_cast<int>(row) + 1;
@@ -632,21 +639,14 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtasPerSm<T>) gdn_paged_app
   const int64_t place = token - static_cast<int64_t>(at) * c.page_size;
   const int64_t pos = p.positions && p.rope.rot ? p.positions[row] : token;
   if (!position_held(pos, p.rope, p.status)) return;  // the token is left out whole
-  if (is_k) {
-    norm_rope_heads<T, D, kNext>(x, static_cast<T*>(c.k) + page * c.k_page + place * c.k_token, c.k_head, ch * PER, p.nkv,
-                                 p.k_weight, p.norm != 0, p.eps, p.rope, pos);
-  } else {
-    const HeadLane<D, kNext> hl(lane % LPH, 0);
-    T* dst = static_cast<T*>(c.v) + page * c.v_page + place * c.v_token;
+  T* dst = static_cast<T*>(c.v) + page * c.v_page + place * c.v_token + at8;
 #pragma unroll
-    for (int i = 0; i < kNormUnroll; ++i) {
-      const int h = ch * PER + i * SLOTS + lane / LPH;
-      if (h < p.nkv) {
-        *reinterpret_cast<typename Four<T>::Word*>(dst + h * c.v_head + hl.a) = x[i][0];
-        *reinterpret_cast<typename Four<T>::Word*>(dst + h * c.v_head + hl.b) = x[i][1];
-      }
-    }
+  for (int i = 0; i < U; ++i) {
+    const int h = h0 + i * SLOTS + slot;
+    if (h < p.nkv) *reinterpret_cast<uint4*>(dst + h * c.v_head) = v[i];
   }
+  norm_rope_heads<T, D, kNext, U>(x, static_cast<T*>(c.k) + page * c.k_page + place * c.k_token, c.k_head, h0, p.nkv,
+                               p.k_weight, p.norm != 0, p.eps, p.rope, pos);
 }
 
 }  // namespace gdn
