@@ -350,14 +350,15 @@ int gdn_head_norm_rope_backward(const void* q, const void* k, const int32_t* pos
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaMallocAsync(%zu): %s", need, cudaGetErrorString(e));
   }
   p.partials = static_cast<float*>(ws);
-  // the grid's CTAs in proportion to the heads, at least one each; a token's heads are cut into as
-  // many runs as it takes to give every warp one
+  // the grid's CTAs in proportion to the steps that a token's heads take, at least one each; a token's
+  // heads are cut into as many runs as it takes to give every warp one
   const int slots = dev->sms * gdn::kNormBwdCtasPerSm, warps = gdn::kNormBwdThreads / 32;
-  auto side = [&](int heads, int* parts, int* per) -> int {
+  const int step = 256 / d * (dtype == GDN_F32 ? 1 : 2);
+  const int q_steps = (nq + step - 1) / step, k_steps = (nkv + step - 1) / step;
+  auto side = [&](int steps, int* parts, int* per) -> int {
     *parts = *per = 1;
-    if (!heads) return 0;
-    const int step = 256 / d * (dtype == GDN_F32 ? 1 : 2), steps = (heads + step - 1) / step;
-    int share = static_cast<int>(static_cast<int64_t>(slots) * heads / (nq + nkv));
+    if (!steps) return 0;
+    int share = static_cast<int>(static_cast<int64_t>(slots) * steps / (q_steps + k_steps));
     if (share < 1) share = 1;
     int64_t cuts = (static_cast<int64_t>(share) * warps + rows - 1) / rows;
     if (cuts > steps) cuts = steps;
@@ -367,8 +368,8 @@ int gdn_head_norm_rope_backward(const void* q, const void* k, const int32_t* pos
     const int64_t need = (static_cast<int64_t>(rows) * *parts + warps - 1) / warps;
     return need < share ? static_cast<int>(need) : share;
   };
-  p.q_ctas = side(nq, &p.q_parts, &p.q_per);
-  const int grid = p.q_ctas + side(nkv, &p.k_parts, &p.k_per);
+  p.q_ctas = side(q_steps, &p.q_parts, &p.q_per);
+  const int grid = p.q_ctas + side(k_steps, &p.k_parts, &p.k_per);
   by_type(dtype, [&](auto t) {
     by_head(d, next, [&](auto dim, auto pairs) {
       gdn::gdn_head_norm_rope_bwd_kernel<decltype(t), dim.value, pairs.value><<<grid, gdn::kNormBwdThreads, 0, s>>>(p);

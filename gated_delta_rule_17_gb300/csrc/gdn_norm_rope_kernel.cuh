@@ -378,7 +378,11 @@ gdn_head_norm_rope_bwd_kernel(const NormRopeParams p) {
 
   // Two walks over the steps: one fetches, one computes and writes.
   unsigned f_item = (is_q ? blockIdx.x : blockIdx.x - p.q_ctas) * WARPS + warp, c_item = f_item;
-  int f_left = 0, c_left = 0, pos = 0;  // heads that the item still has
+  int f_left = 0, c_left = 0;  // heads that the item still has
+  // the position of the item to fetch next, loaded an item ahead: its latency would else stand
+  // before every item's angles
+  auto position = [&](unsigned item) { return p.rope.rot && item < items ? p.positions[parts == 1 ? item : item / parts] : 0; };
+  int pos = position(f_item);
   const uint8_t *f_x = nullptr, *f_g = nullptr;
   const float* f_angle = nullptr;
   T* c_dx = nullptr;
@@ -387,7 +391,7 @@ gdn_head_norm_rope_bwd_kernel(const NormRopeParams p) {
   const bool sine = lane >= pieces;
   const int piece = 4 * (sine ? lane - pieces : lane);
   auto item_heads = [&](unsigned item, unsigned* row, int* h) {
-    *row = item / parts;
+    *row = parts == 1 ? item : item / parts;
     *h = static_cast<int>((item - *row * parts) * per);
     return *h + static_cast<int>(per) < heads ? static_cast<int>(per) : heads - *h;
   };
@@ -397,9 +401,9 @@ gdn_head_norm_rope_bwd_kernel(const NormRopeParams p) {
     int h;
     f_left = item_heads(f_item, &row, &h);
     if (p.rope.rot) {
-      pos = p.positions[row];
       f_ok = position_held(pos, p.rope, p.status);
       f_angle = (sine ? p.rope.sin : p.rope.cos) + static_cast<int64_t>(f_ok ? pos : 0) * p.rope.stride + piece;
+      pos = position(f_item + stride);
     } else {
       f_ok = true;
     }
