@@ -377,8 +377,8 @@ int gdn_head_norm_rope_backward(const void* q, const void* k, const int32_t* pos
   });
   if (sums) {
     const float* parts = p.partials;
-    launch_early(d == 64 ? gdn::gdn_norm_weight_sum_kernel<64> : gdn::gdn_norm_weight_sum_kernel<128>, dim3(2), 1024, 0, s,
-                 parts, p.q_ctas, grid, dq_weight, dk_weight);  // a refusal is launched()'s to report
+    launch_early(gdn::gdn_norm_weight_sum_kernel, dim3(static_cast<unsigned>(d / 32), 2), 1024, 0, s, parts, d, p.q_ctas,
+                 grid, dq_weight, dk_weight);  // a refusal is launched()'s to report
   }
   int rc = launched(sums ? 2 : 1);
   if (sums && !workspace) {

@@ -533,29 +533,25 @@ gdn_head_norm_rope_bwd_kernel(const NormRopeParams p) {
   }
 }
 
-// dw[i] = sum over the partials of q's CTAs (block 0) or k's (block 1), in a fixed order: D threads
-// wide and 1024 / D partials at a time.
-template <int D>
-__global__ void __launch_bounds__(1024) gdn_norm_weight_sum_kernel(const float* partials, int q_ctas, int ctas,
+// dw[i] = sum over the partials of q's CTAs (blockIdx.y 0) or k's (1), in a fixed order: 32 values a
+// CTA, a warp every 32nd partial.
+__global__ void __launch_bounds__(1024) gdn_norm_weight_sum_kernel(const float* partials, int d, int q_ctas, int ctas,
                                                                   float* dq_weight, float* dk_weight) {
-  constexpr int LANES = 1024 / D;
-  __shared__ float s_part[LANES][D];
+  __shared__ float s_part[32][33];
   tc::grid_dependency_wait();
-  const int i = threadIdx.x % D, g = threadIdx.x / D;
-  float* dst = blockIdx.x == 0 ? dq_weight : dk_weight;
-  const int first = blockIdx.x == 0 ? 0 : q_ctas, end = blockIdx.x == 0 ? q_ctas : ctas;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
+  float* dst = blockIdx.y == 0 ? dq_weight : dk_weight;
+  if (!dst) return;
+  const int first = blockIdx.y == 0 ? 0 : q_ctas, end = blockIdx.y == 0 ? q_ctas : ctas;
   float t = 0.f;
-  if (dst) {
 #pragma unroll 8
-    for (int j = first + g; j < end; j += LANES) t += partials[static_cast<int64_t>(j) * D + i];
-  }
-  s_part[g][i] = t;
+  for (int j = first + warp; j < end; j += 32) t += partials[static_cast<int64_t>(j) * d + i];
+  s_part[warp][lane] = t;
   __syncthreads();
-  if (g == 0 && dst) {
+  t = s_part[lane][warp];  // warp w adds value w's 32 sums
 #pragma unroll
-    for (int j = 1; j < LANES; ++j) t += s_part[j][i];
-    dst[i] = t;
-  }
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if (lane == 0) dst[blockIdx.x * 32 + warp] = t;
 }
 
 // ---- paged cache -----------------------------------------------------------------------
