@@ -27,7 +27,7 @@
 // What bounds it: the chain of a stream from one tile's scores to the next's, about 3000 cycles (softmax
 // 1500, the products of both kinds 1024 one after the other because P lies over S, hand-offs the
 // rest), of which two streams fill the tensor pipe to 59%: trees of 64 in 8 sequences of 32768, 32
-// heads on 4: 203 us, 1.34 PFLOP/s, 68% of the measured cuBLAS rate. With few rows HBM and the
+// heads on 4: 203 to 218 us, 1.25 to 1.34 PFLOP/s, 64 to 68% of the measured cuBLAS rate. With few rows HBM and the
 // ends: trees of 3 to 16 in 16 sequences of 500 to 8192, 32 heads on 8: 66 us, 4.5 TB/s. Tensor
 // memory is full (S and O of two streams), so a third stream, or P beside S, has no room; one pass
 // over the scores instead of two, the row in registers, two warps a row and handing P over in halves

@@ -17,9 +17,9 @@
 // apart, 8l and 8l + 4 for neighbouring pairs and for values past `rot`. A warp takes up to
 // kNormUnroll x (32 lanes / lanes a row) heads of one token, all loads first, with the
 // products of weight and cosine or sine in registers for all of them. At 4 x 8192 tokens
-// of 32 + 8 heads of 128, bf16: forward 107 us (6.4 TB/s, 95% of the measured copy
-// rate), backward 175 us (5.9 TB/s, 86%); the append of 8 prompts of 100 to 16000 tokens,
-// 8 kv heads: 94 us (6.5 TB/s, 95%).
+// of 32 + 8 heads of 128, bf16: forward 106 us (6.5 TB/s, 95% of the measured copy
+// rate), backward 173 us (5.9 TB/s, 87%); the append of 8 prompts of 100 to 16000 tokens,
+// 8 kv heads: 92 us (6.6 TB/s, 97%).
 #pragma once
 #include "gdn_common.cuh"
 
