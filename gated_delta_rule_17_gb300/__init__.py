@@ -404,9 +404,9 @@ def _setup():
     return torch
 
 
-def _stream_of(stream, device):
+def _stream_of(stream, t):
     if stream is None:  # the handle itself: a torch.cuda.Stream around it costs a sixth of a call
-        return _torch._C._cuda_getCurrentRawStream(device.index)
+        return _torch._C._cuda_getCurrentRawStream(t.get_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -422,11 +422,11 @@ def _act(t, name, dtype, rows, inner):
     """Checks [rows, ...] activations with `inner` contiguous elements a row; (address, row stride)."""
     if t.dtype is not dtype or not t.is_cuda:
         raise GdnError(GDN_ERR_ARG, f"{name} must be a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
-    if t.numel() == rows * inner and t.is_contiguous() and t.dim() > 1 and t.size(0) == rows:  # packed rows
+    if t.numel() == rows * inner and t.is_contiguous():  # packed rows, however they are split up
         return t.data_ptr(), inner
     stride = _row_stride(t, name, inner)
-    if t.size(0) != rows:
-        raise GdnError(GDN_ERR_ARG, f"{name} has {t.size(0)} rows, need {rows}")
+    if t.shape[0] != rows:
+        raise GdnError(GDN_ERR_ARG, f"{name} has {t.shape[0]} rows, need {rows}")
     return t.data_ptr(), stride
 
 
@@ -497,7 +497,7 @@ def head_norm_rope(q, k, positions, cos, sin, q_out, k_out, *, nq: int, nkv: int
     rc = _lib.gdn_head_norm_rope(qp, kp, _vector(positions, "positions", torch.int32, rows), _rope(cos, sin, interleaved),
                                  _vector(q_weight, "q_weight", torch.float32, head_dim),
                                  _vector(k_weight, "k_weight", torch.float32, head_dim), eps, qo, ko, rows, nq, nkv,
-                                 head_dim, code, _STRIDES(qs, ks, qos, kos, 0, 0), _stream_of(stream, x.device))
+                                 head_dim, code, _STRIDES(qs, ks, qos, kos, 0, 0), _stream_of(stream, x))
     if rc != GDN_OK:
         _raise(rc)
 
@@ -530,7 +530,7 @@ def head_norm_rope_backward(q, k, positions, cos, sin, q_grad, k_grad, dq, dk, d
                                           _vector(q_weight, "q_weight", f32, head_dim), _vector(k_weight, "k_weight", f32, head_dim),
                                           eps, gq, gk, dqp, dkp, _vector(dq_weight, "dq_weight", f32, head_dim),
                                           _vector(dk_weight, "dk_weight", f32, head_dim), rows, nq, nkv, head_dim, code,
-                                          _STRIDES(qs, ks, dqs, dks, gqs, gks), ws, size, _stream_of(stream, x.device))
+                                          _STRIDES(qs, ks, dqs, dks, gqs, gks), ws, size, _stream_of(stream, x))
     if rc != GDN_OK:
         _raise(rc)
 
@@ -575,7 +575,7 @@ def paged_append(k, v, k_cache, v_cache, block_table, ctx_lens, *, nkv: int, hea
     rc = _lib.gdn_paged_append(kp, vp, _paged(k, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, head_dim, rows),
                                _vector(positions, "positions", torch.int32, rows), _rope(cos, sin, interleaved),
                                1 if norm else 0, _vector(k_weight, "k_weight", torch.float32, head_dim), eps, nkv, head_dim,
-                               code, ks, vs, _stream_of(stream, k.device))
+                               code, ks, vs, _stream_of(stream, k))
     if rc != GDN_OK:
         _raise(rc)
 
@@ -608,7 +608,7 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_lens, out, *, nq: int, 
         words, mp = shape[1], mask.data_ptr()
     ws, size = _scratch(workspace)
     rc = _lib.gdn_tree_attention(qp, cache, mp, words, head_dim ** -0.5 if scale is None else scale, op, nq, nkv, head_dim,
-                                 code, qs, os_, max_rows or 0, ws, size, _stream_of(stream, q.device))
+                                 code, qs, os_, max_rows or 0, ws, size, _stream_of(stream, q))
     if rc != GDN_OK:
         _raise(rc)
 
