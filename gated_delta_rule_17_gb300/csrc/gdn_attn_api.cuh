@@ -189,7 +189,10 @@ AttnKind attn_kind(int64_t rows, float scale) {
   return rows <= gdn::kAttnRows || !(scale > 0.f) ? kAttn16 : kAttnTc;
 }
 
-int attn_runs(AttnKind kind, int sms) { return kind != kAttnTc ? sms * kAttnCtasPerSm : sms; }
+int attn_runs(AttnKind kind, int sms) {
+  const int runs = kind != kAttnTc ? sms * kAttnCtasPerSm : sms;
+  return runs < gdn::kJoinRuns ? runs : gdn::kJoinRuns;
+}
 
 // Whether to give the CTAs whole units. That costs the tiles by which the busiest CTA then has more
 // than an even share (and what the units' lengths differ by, which the host does not know: hence
@@ -264,21 +267,21 @@ cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, int smem,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename T, int D, int MT, int W>
-cudaError_t launch_join(cudaError_t e, const gdn::AttnParams& p, cudaStream_t s) {
+template <typename T, int D, int MT>
+cudaError_t launch_join(cudaError_t e, int sms, const gdn::AttnParams& p, cudaStream_t s) {
   if (e != cudaSuccess || p.whole) return e;
-  return launch_early(gdn::gdn_attn_join_kernel<T, D, MT, W>, dim3(static_cast<unsigned>(p.runs), MT * W / gdn::kJoinWarps),
+  return launch_early(gdn::gdn_attn_join_kernel<T, D, MT>, dim3(static_cast<unsigned>(sms * gdn::kJoinCtasPerSm)),
                       32 * gdn::kJoinWarps, 0, s, p);
 }
 
 template <typename T, int D>
-cudaError_t launch_attn(AttnKind kind, const gdn::AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+cudaError_t launch_attn(AttnKind kind, int sms, const gdn::AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.runs));
   if (kind == kAttn16)
-    return launch_join<T, D, gdn::kAttnRows, 4>(
-        launch_early(gdn::gdn_attn_kernel<T, D>, grid, gdn::kAttnThreads, gdn::AttnPlan<D>::DYN_SMEM, s, p), p, s);
-  return launch_join<T, D, gdn::kTcRows, 1>(
-      launch_early(gdn::gdn_attn_tc_kernel<T, D>, grid, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s, k, v, p), p, s);
+    return launch_join<T, D, gdn::kAttnRows>(
+        launch_early(gdn::gdn_attn_kernel<T, D>, grid, gdn::kAttnThreads, gdn::AttnPlan<D>::DYN_SMEM, s, p), sms, p, s);
+  return launch_join<T, D, gdn::kTcRows>(
+      launch_early(gdn::gdn_attn_tc_kernel<T, D>, grid, gdn::kTcThreads, gdn::AttnTcPlan<D>::DYN_SMEM, s, k, v, p), sms, p, s);
 }
 
 }  // namespace
@@ -529,8 +532,8 @@ int gdn_tree_attention(const void* q, const gdn_paged_t* cache, const uint64_t* 
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + l.o);
   cudaError_t e = cudaSuccess;
   by_type16(dtype, [&](auto t) {
-    e = d == 64 ? launch_attn<decltype(t), 64>(kind, p, maps[0], maps[1], s)
-                : launch_attn<decltype(t), 128>(kind, p, maps[0], maps[1], s);
+    e = d == 64 ? launch_attn<decltype(t), 64>(kind, dev->sms, p, maps[0], maps[1], s)
+                : launch_attn<decltype(t), 128>(kind, dev->sms, p, maps[0], maps[1], s);
   });
   int rc = e != cudaSuccess ? fail(GDN_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e)) : launched(p.whole ? 1 : 2);
   if (!workspace) {

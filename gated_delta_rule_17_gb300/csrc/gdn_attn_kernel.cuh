@@ -302,91 +302,183 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
   }
 }
 
-// Joins the pieces of the unit that begins in run blockIdx.x and goes on in the next runs: W warps a
-// row, each every W-th group of U pieces, whose loads are under way together. A unit of few rows may
-// have a hundred pieces and more (one long sequence alone), so its rows get four warps.
+// Joins the pieces of the units that were cut. Every CTA reads the list of them and takes its share of
+// their rows, in pairs: a grid of rows by runs had thousands of CTAs that only found nothing to do, and
+// one warp for a row of fifty pieces (one long sequence alone). Where there are more pairs than warps a
+// warp takes whole pairs; where rows are few, 2, 4 or 8 warps share one, each every W-th group of
+// kJoinPieces pieces. All loads of a group are under way together.
 constexpr int kJoinWarps = 8;
-template <typename T, int D, int MT, int W>
-__global__ void __launch_bounds__(32 * kJoinWarps) gdn_attn_join_kernel(const AttnParams p) {
-  constexpr int ROWS = kJoinWarps / W, V = D / 32, U = 8;  // rows of a CTA, values of a lane, pieces in flight
+constexpr int kJoinCtasPerSm = 3;
+constexpr int kJoinPieces = 8;
+constexpr int kJoinRuns = 512;  // runs whose units a CTA can list
+
+// Adds to (m, l, o) of NR rows from r on (the last one is row `end` - 1) U pieces each at a time:
+// runs first + from .. last, `step` apart.
+template <int D, int MT, int NR, int U>
+__device__ __forceinline__ void join_pieces(const AttnParams& p, int first, int last, int r, int end, int from, int step,
+                                            float (&m)[NR], float (&l)[NR], float (&o)[NR][D / 32]) {
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31;
+  for (int i0 = first + from; i0 <= last; i0 += step) {
+    float2 ml[NR][U];
+    float v[NR][U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        ml[n][u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[n][u][j] = 0.f;
+        if (i0 + u <= last) {
+          const int64_t at = (static_cast<int64_t>(i0 + u) * 2 + (i0 + u == first ? 1 : 0)) * MT + (r + n < end ? r + n : end - 1);
+          ml[n][u] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+          const float* src = p.part_o + at * D + V * lane;
+          if constexpr (V == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            v[n][u][0] = x.x, v[n][u][1] = x.y, v[n][u][2] = x.z, v[n][u][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            v[n][u][0] = x.x, v[n][u][1] = x.y;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      float mn = m[n];
+#pragma unroll
+      for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[n][u].x);
+      const float base = mn == -INFINITY ? 0.f : mn, f = exp2_approx(m[n] - base);
+      m[n] = mn;
+      l[n] *= f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[n][j] *= f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float g = exp2_approx(ml[n][u].x - base);
+        l[n] = fmaf(ml[n][u].y, g, l[n]);
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[n][j] = fmaf(v[n][u][j], g, o[n][j]);
+      }
+    }
+  }
+}
+
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(32 * kJoinWarps, kJoinCtasPerSm) gdn_attn_join_kernel(const AttnParams p) {
+  constexpr int V = D / 32;
+  __shared__ int4 s_cut[kJoinRuns];
+  __shared__ int s_end[kJoinRuns];  // pairs of rows up to and with a run's unit
+  __shared__ int s_sum[kJoinWarps];
   __shared__ float s_ml[kJoinWarps][2];
   __shared__ float s_o[kJoinWarps][D];
   tc::allow_dependent_launch();
   tc::grid_dependency_wait();
-  const int run = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.y * ROWS + warp / W, sub = warp % W;
-  const int4 cut = p.cut[run];
-  if (cut.w < 0) return;
-  const int unit_qtiles = (cut.y * p.group + MT - 1) / MT;
-  const int kvh = cut.z / unit_qtiles, qt = cut.z - kvh * unit_qtiles, row = qt * MT + r;
-  const bool has = row < cut.y * p.group;
-  float m = -INFINITY, l = 0.f, o[V] = {};
-  for (int i0 = run + sub * U; has && i0 <= cut.w; i0 += W * U) {
-    float pm[U], pl[U], v[U][V];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto rows_of = [&](const int4& cut) {  // of the unit: first row of its kv head's, and rows
+    const int all = cut.y * p.group, qt = cut.z % ((all + MT - 1) / MT);
+    return make_int2(qt * MT, all - qt * MT < MT ? all - qt * MT : MT);
+  };
+  int total = 0;
+  for (int c0 = 0; c0 < p.runs; c0 += 32 * kJoinWarps) {
+    const int run = c0 + threadIdx.x;
+    int pairs = 0;
+    if (run < p.runs) {
+      const int4 cut = p.cut[run];
+      s_cut[run] = cut;
+      if (cut.w >= 0) pairs = (rows_of(cut).y + 1) / 2;
+    }
+    int upto = pairs;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      pm[u] = -INFINITY;
-      pl[u] = 0.f;
+    for (int k = 1; k < 32; k <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, k);
+      if (lane >= k) upto += y;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    int all = 0;
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[u][j] = 0.f;
-      if (i0 + u <= cut.w) {
-        const int64_t at = (static_cast<int64_t>(i0 + u) * 2 + (i0 + u == run ? 1 : 0)) * MT + r;
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-        pm[u] = ml.x;
-        pl[u] = ml.y;
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const int x = s_sum[w];
+      if (w < warp) upto += x;
+      all += x;
+    }
+    if (run < p.runs) s_end[run] = total + upto;
+    total += all;
+    __syncthreads();
+  }
+  auto unit_of = [&](int pair) {  // the first run with more pairs up to it
+    int lo = 0, hi = p.runs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_end[mid] > pair) hi = mid;
+      else lo = mid + 1;
+    }
+    return lo;
+  };
+  auto store = [&](const int4& cut, int row, float l, const float (&o)[V]) {  // row: of the kv head's
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int kvh = cut.z / ((cut.y * p.group + MT - 1) / MT), i = row / p.group, g = row - i * p.group;
+    T* dst = static_cast<T*>(p.out) + (static_cast<int64_t>(cut.x) + i) * p.out_stride +
+             static_cast<int64_t>(kvh * p.group + g) * D + V * lane;
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-          const float2 x = *reinterpret_cast<const float2*>(p.part_o + at * D + V * lane + j);
-          v[u][j] = x.x;
-          v[u][j + 1] = x.y;
+    for (int j = 0; j < V; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack2<T>(o[j] * inv, o[j + 1] * inv);
+  };
+  const int ctas = gridDim.x;
+  if (2 * total > 4 * ctas) {
+    for (int pair = blockIdx.x * kJoinWarps + warp; pair < total; pair += ctas * kJoinWarps) {
+      const int run = unit_of(pair);
+      const int4 cut = s_cut[run];
+      const int2 rows = rows_of(cut);
+      const int r = 2 * (pair - (run ? s_end[run - 1] : 0));
+      if (cut.w - run < kJoinPieces / 2) {
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {}, o[2][V] = {};
+        join_pieces<D, MT, 2, kJoinPieces / 2>(p, run, cut.w, r, rows.y, 0, kJoinPieces / 2, m, l, o);
+        store(cut, rows.x + r, l[0], o[0]);
+        if (r + 1 < rows.y) store(cut, rows.x + r + 1, l[1], o[1]);
+      } else {
+        for (int n = r; n < r + 2 && n < rows.y; ++n) {
+          float m[1] = {-INFINITY}, l[1] = {}, o[1][V] = {};
+          join_pieces<D, MT, 1, kJoinPieces>(p, run, cut.w, n, rows.y, 0, kJoinPieces, m, l, o);
+          store(cut, rows.x + n, l[0], o[0]);
         }
       }
     }
-    float mn = m;
-#pragma unroll
-    for (int u = 0; u < U; ++u) mn = fmaxf(mn, pm[u]);
-    const float base = mn == -INFINITY ? 0.f : mn, f = exp2_approx(m - base);
-    m = mn;
-    l *= f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) o[j] *= f;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float g = exp2_approx(pm[u] - base);
-      l = fmaf(pl[u], g, l);
-#pragma unroll
-      for (int j = 0; j < V; ++j) o[j] = fmaf(v[u][j], g, o[j]);
-    }
+    return;
   }
-  if (W > 1) {
-    s_ml[warp][0] = m;
-    s_ml[warp][1] = l;
-#pragma unroll
-    for (int j = 0; j < V; ++j) s_o[warp][V * lane + j] = o[j];
-    __syncthreads();
-    if (sub != 0) return;
-    float mn = m;
-#pragma unroll
-    for (int w = 1; w < W; ++w) mn = fmaxf(mn, s_ml[warp + w][0]);
-    const float base = mn == -INFINITY ? 0.f : mn, f = exp2_approx(m - base);
-    l *= f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) o[j] *= f;
-#pragma unroll
-    for (int w = 1; w < W; ++w) {
-      const float g = exp2_approx(s_ml[warp + w][0] - base);
-      l = fmaf(s_ml[warp + w][1], g, l);
-#pragma unroll
-      for (int j = 0; j < V; ++j) o[j] = fmaf(s_o[warp + w][V * lane + j], g, o[j]);
-    }
+  const int W = 2 * total <= ctas ? 8 : 2 * total <= 2 * ctas ? 4 : 2;  // warps of a row; every row has its own
+  const int at = blockIdx.x * (kJoinWarps / W) + warp / W, sub = warp % W, pair = at >> 1;
+  int run = 0, r = 0;
+  int4 cut = make_int4(0, 0, 0, -1);
+  int2 rows = make_int2(0, 0);
+  if (pair < total) {
+    run = unit_of(pair);
+    cut = s_cut[run];
+    rows = rows_of(cut);
+    r = 2 * (pair - (run ? s_end[run - 1] : 0)) + (at & 1);
   }
-  if (!has) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int i = row / p.group, g = row - i * p.group;
-  T* dst = static_cast<T*>(p.out) + (static_cast<int64_t>(cut.x) + i) * p.out_stride +
-           static_cast<int64_t>(kvh * p.group + g) * D + V * lane;
+  const bool has = r < rows.y;
+  float m[1] = {-INFINITY}, l[1] = {}, o[1][V] = {};
+  if (has) join_pieces<D, MT, 1, kJoinPieces>(p, run, cut.w, r, rows.y, sub * kJoinPieces, W * kJoinPieces, m, l, o);
+  s_ml[warp][0] = m[0];
+  s_ml[warp][1] = l[0];
 #pragma unroll
-  for (int j = 0; j < V; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack2<T>(o[j] * inv, o[j + 1] * inv);
+  for (int j = 0; j < V; ++j) s_o[warp][V * lane + j] = o[0][j];
+  __syncthreads();
+  if (!has || sub != 0) return;
+  float mn = m[0];
+  for (int w = 1; w < W; ++w) mn = fmaxf(mn, s_ml[warp + w][0]);
+  const float base = mn == -INFINITY ? 0.f : mn, f = exp2_approx(m[0] - base);
+  l[0] *= f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) o[0][j] *= f;
+  for (int w = 1; w < W; ++w) {
+    const float g = exp2_approx(s_ml[warp + w][0] - base);
+    l[0] = fmaf(s_ml[warp + w][1], g, l[0]);
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[0][j] = fmaf(s_o[warp + w][V * lane + j], g, o[0][j]);
+  }
+  store(cut, rows.x + r, l[0], o[0]);
 }
 
 }  // namespace gdn
