@@ -38,8 +38,8 @@ struct AttnParams {
   int box;         // tokens of a TMA box inside a page, 0: pages do not hold whole boxes
   int whole;       // runs are cut at units only: nothing to join
   float* part_ml;  // [runs][2][MT][2]: m and l
-  float* part_o;   // [runs][2][MT][D]
-  int4* cut;       // [runs]: the unit that begins in the run and is cut: first row, rows, kv head and row tile, last run (-1: none)
+  float* part_o;   // [runs][2][D / 8][MT][8]
+  int4* cut;       // [runs]: the unit that begins in the run and is cut (AttnWalk::cut; w < 0: none)
   unsigned* status;
 };
 
@@ -260,10 +260,12 @@ struct AttnWalk {
       return;
     }
   }
-  // What the join has to know where the unit begins in run `run` and is cut: first row, rows, kv
-  // head and row tile, last run.
-  __device__ __forceinline__ int4 cut() const {
-    return make_int4(s.first, s.n, kvh * s.qtiles + qt, st.first + run_of(st.end + (s.tiles - t1) - 1, st.total, st.runs));
+  // What the join has to know where the unit begins in run `run` and is cut: the sequence's first row, kv
+  // head, first of its rows there, and the rows of the unit (from bit 16) with the last run.
+  __device__ __forceinline__ int4 cut(const AttnParams& p) const {
+    const int left = s.n * p.group - qt * MT;
+    return make_int4(s.first, kvh, qt * MT,
+                     (left < MT ? left : MT) << 16 | (st.first + run_of(st.end + (s.tiles - t1) - 1, st.total, st.runs)));
   }
 };
 
@@ -285,6 +287,34 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// ---- pieces of cut units ----------------------------------------------------------------
+// A piece's o in the workspace: [D / 8][MT][8], so that threads with a row each write whole lines.
+template <int MT>
+__device__ __forceinline__ int attn_piece_at(int row, int col) {
+  return ((col >> 3) * MT + row) * 8 + (col & 7);
+}
+
+// Adds U pieces to (m, l, o), in their order.
+template <int U>
+__device__ __forceinline__ void attn_join(const float2 (&ml)[U], const float4 (&v)[U], float& m, float& l, float4& o) {
+  float mn = m;
+#pragma unroll
+  for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
+  const float base = mn == -INFINITY ? 0.f : mn, f = exp2_approx(m - base);
+  m = mn;
+  l *= f;
+  o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float g = exp2_approx(ml[u].x - base);
+    l = fmaf(ml[u].y, g, l);
+    o.x = fmaf(v[u].x, g, o.x);
+    o.y = fmaf(v[u].y, g, o.y);
+    o.z = fmaf(v[u].z, g, o.z);
+    o.w = fmaf(v[u].w, g, o.w);
+  }
 }
 
 }  // namespace gdn

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
         *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(a[0] * inv, a[1] * inv), pack2<T>(a[2] * inv, a[3] * inv));
       } else {
         const int64_t at = (static_cast<int64_t>(run) * 2 + slot) * MT + r;
-        *reinterpret_cast<float4*>(p.part_o + at * D + d4) = make_float4(a[0], a[1], a[2], a[3]);
+        *reinterpret_cast<float4*>(p.part_o + (at - r) * D + attn_piece_at<MT>(r, d4)) = make_float4(a[0], a[1], a[2], a[3]);
         if (d4 == 0) {
           p.part_ml[at * 2] = mm;
           p.part_ml[at * 2 + 1] = ll;
@@ -298,97 +298,42 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
       }
     }
     __syncthreads();  // the join buffer is done with
-    if (t0 == 0 && t1 < s.tiles && threadIdx.x == 0) p.cut[run] = w.cut();
+    if (t0 == 0 && t1 < s.tiles && threadIdx.x == 0) p.cut[run] = w.cut(p);
   }
 }
 
 // Joins the pieces of the units that were cut. Every CTA reads the list of them and takes its share of
-// their rows, in pairs: a grid of rows by runs had thousands of CTAs that only found nothing to do, and
-// one warp for a row of fifty pieces (one long sequence alone). Where there are more pairs than warps a
-// warp takes whole pairs; where rows are few, 2, 4 or 8 warps share one, each every W-th group of
-// kJoinPieces pieces. All loads of a group are under way together.
+// their parts of 8 rows by 16 columns, a value of a row and four columns a lane: a grid of rows by runs
+// had thousands of CTAs that only found nothing to do, and one warp for the fifty pieces of a row (one
+// long sequence alone). Where there are more parts than warps a warp takes whole parts; where there are
+// few, 2, 4 or 8 warps share one, each every W-th group of kJoinPieces pieces, whose loads are under
+// way together.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinCtasPerSm = 3;
 constexpr int kJoinPieces = 8;
 constexpr int kJoinRuns = 512;  // runs whose units a CTA can list
 
-// Adds to (m, l, o) of NR rows from r on (the last one is row `end` - 1) U pieces each at a time:
-// runs first + from .. last, `step` apart.
-template <int D, int MT, int NR, int U>
-__device__ __forceinline__ void join_pieces(const AttnParams& p, int first, int last, int r, int end, int from, int step,
-                                            float (&m)[NR], float (&l)[NR], float (&o)[NR][D / 32]) {
-  constexpr int V = D / 32;
-  const int lane = threadIdx.x & 31;
-  for (int i0 = first + from; i0 <= last; i0 += step) {
-    float2 ml[NR][U];
-    float v[NR][U][V];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        ml[n][u] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[n][u][j] = 0.f;
-        if (i0 + u <= last) {
-          const int64_t at = (static_cast<int64_t>(i0 + u) * 2 + (i0 + u == first ? 1 : 0)) * MT + (r + n < end ? r + n : end - 1);
-          ml[n][u] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-          const float* src = p.part_o + at * D + V * lane;
-          if constexpr (V == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(src);
-            v[n][u][0] = x.x, v[n][u][1] = x.y, v[n][u][2] = x.z, v[n][u][3] = x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(src);
-            v[n][u][0] = x.x, v[n][u][1] = x.y;
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      float mn = m[n];
-#pragma unroll
-      for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[n][u].x);
-      const float base = mn == -INFINITY ? 0.f : mn, f = exp2_approx(m[n] - base);
-      m[n] = mn;
-      l[n] *= f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) o[n][j] *= f;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float g = exp2_approx(ml[n][u].x - base);
-        l[n] = fmaf(ml[n][u].y, g, l[n]);
-#pragma unroll
-        for (int j = 0; j < V; ++j) o[n][j] = fmaf(v[n][u][j], g, o[n][j]);
-      }
-    }
-  }
-}
-
 template <typename T, int D, int MT>
 __global__ void __launch_bounds__(32 * kJoinWarps, kJoinCtasPerSm) gdn_attn_join_kernel(const AttnParams p) {
-  constexpr int V = D / 32;
+  constexpr int U = kJoinPieces, CT = D / 16;
   __shared__ int4 s_cut[kJoinRuns];
-  __shared__ int s_end[kJoinRuns];  // pairs of rows up to and with a run's unit
+  __shared__ int s_end[kJoinRuns];  // groups of 8 rows up to and with a run's unit
   __shared__ int s_sum[kJoinWarps];
-  __shared__ float s_ml[kJoinWarps][2];
-  __shared__ float s_o[kJoinWarps][D];
+  __shared__ float2 s_ml[kJoinWarps][32];
+  __shared__ float4 s_o[kJoinWarps][32];
   tc::allow_dependent_launch();
   tc::grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto rows_of = [&](const int4& cut) {  // of the unit: first row of its kv head's, and rows
-    const int all = cut.y * p.group, qt = cut.z % ((all + MT - 1) / MT);
-    return make_int2(qt * MT, all - qt * MT < MT ? all - qt * MT : MT);
-  };
   int total = 0;
   for (int c0 = 0; c0 < p.runs; c0 += 32 * kJoinWarps) {
     const int run = c0 + threadIdx.x;
-    int pairs = 0;
+    int groups = 0;
     if (run < p.runs) {
       const int4 cut = p.cut[run];
       s_cut[run] = cut;
-      if (cut.w >= 0) pairs = (rows_of(cut).y + 1) / 2;
+      if (cut.w >= 0) groups = ((cut.w >> 16) + 7) / 8;
     }
-    int upto = pairs;
+    int upto = groups;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, upto, k);
@@ -407,78 +352,64 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinCtasPerSm) gdn_attn_join
     total += all;
     __syncthreads();
   }
-  auto unit_of = [&](int pair) {  // the first run with more pairs up to it
-    int lo = 0, hi = p.runs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (s_end[mid] > pair) hi = mid;
-      else lo = mid + 1;
-    }
-    return lo;
-  };
-  auto store = [&](const int4& cut, int row, float l, const float (&o)[V]) {  // row: of the kv head's
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int kvh = cut.z / ((cut.y * p.group + MT - 1) / MT), i = row / p.group, g = row - i * p.group;
-    T* dst = static_cast<T*>(p.out) + (static_cast<int64_t>(cut.x) + i) * p.out_stride +
-             static_cast<int64_t>(kvh * p.group + g) * D + V * lane;
+  const int parts = total * CT, ctas = gridDim.x;
+  const int W = parts <= ctas ? 8 : parts <= 2 * ctas ? 4 : parts <= 4 * ctas ? 2 : 1;  // warps of a part
+  const int sub = warp & (W - 1);
+  // with W > 1 every part has its warps, and all warps take part in the one step
+  for (int part = (blockIdx.x * kJoinWarps + warp) / W; part < parts || W > 1; part += ctas * kJoinWarps) {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    int4 cut = make_int4(0, 0, 0, 0);
+    int row = 0;
+    const int col = (part % CT) * 16 + (lane & 3) * 4;
+    if (part < parts) {
+      const int group = part / CT;
+      int run = 0, hi = p.runs - 1;  // the first run with more groups up to it
+      while (run < hi) {
+        const int mid = (run + hi) >> 1;
+        if (s_end[mid] > group) hi = mid;
+        else run = mid + 1;
+      }
+      cut = s_cut[run];
+      const int rows = cut.w >> 16, last = cut.w & 0xffff;
+      row = (group - (run ? s_end[run - 1] : 0)) * 8 + (lane >> 2);
+      const int r = row < rows ? row : rows - 1;
+      for (int i0 = run + sub * U; i0 <= last; i0 += W * U) {
+        float2 ml[U];
+        float4 v[U];
 #pragma unroll
-    for (int j = 0; j < V; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack2<T>(o[j] * inv, o[j + 1] * inv);
-  };
-  const int ctas = gridDim.x;
-  if (2 * total > 4 * ctas) {
-    for (int pair = blockIdx.x * kJoinWarps + warp; pair < total; pair += ctas * kJoinWarps) {
-      const int run = unit_of(pair);
-      const int4 cut = s_cut[run];
-      const int2 rows = rows_of(cut);
-      const int r = 2 * (pair - (run ? s_end[run - 1] : 0));
-      if (cut.w - run < kJoinPieces / 2) {
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {}, o[2][V] = {};
-        join_pieces<D, MT, 2, kJoinPieces / 2>(p, run, cut.w, r, rows.y, 0, kJoinPieces / 2, m, l, o);
-        store(cut, rows.x + r, l[0], o[0]);
-        if (r + 1 < rows.y) store(cut, rows.x + r + 1, l[1], o[1]);
-      } else {
-        for (int n = r; n < r + 2 && n < rows.y; ++n) {
-          float m[1] = {-INFINITY}, l[1] = {}, o[1][V] = {};
-          join_pieces<D, MT, 1, kJoinPieces>(p, run, cut.w, n, rows.y, 0, kJoinPieces, m, l, o);
-          store(cut, rows.x + n, l[0], o[0]);
+        for (int u = 0; u < U; ++u) {
+          ml[u] = make_float2(-INFINITY, 0.f);
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i0 + u <= last) {
+            const int64_t at = (static_cast<int64_t>(i0 + u) * 2 + (i0 + u == run ? 1 : 0)) * MT;
+            ml[u] = *reinterpret_cast<const float2*>(p.part_ml + (at + r) * 2);
+            v[u] = *reinterpret_cast<const float4*>(p.part_o + at * D + attn_piece_at<MT>(r, col));
+          }
         }
+        attn_join<U>(ml, v, m, l, o);
       }
     }
-    return;
+    if (W > 1) {
+      s_ml[warp][lane] = make_float2(m, l);
+      s_o[warp][lane] = o;
+      __syncthreads();
+      if (sub != 0 || part >= parts) return;
+      for (int w = 1; w < W; ++w) {
+        const float2 ml[1] = {s_ml[warp + w][lane]};
+        const float4 v[1] = {s_o[warp + w][lane]};
+        attn_join<1>(ml, v, m, l, o);
+      }
+    }
+    if (row < cut.w >> 16) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int at = cut.z + row, i = at / p.group, g = at - i * p.group;
+      T* dst = static_cast<T*>(p.out) + (static_cast<int64_t>(cut.x) + i) * p.out_stride +
+               static_cast<int64_t>(cut.y * p.group + g) * D + col;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+    }
+    if (W > 1) return;
   }
-  const int W = 2 * total <= ctas ? 8 : 2 * total <= 2 * ctas ? 4 : 2;  // warps of a row; every row has its own
-  const int at = blockIdx.x * (kJoinWarps / W) + warp / W, sub = warp % W, pair = at >> 1;
-  int run = 0, r = 0;
-  int4 cut = make_int4(0, 0, 0, -1);
-  int2 rows = make_int2(0, 0);
-  if (pair < total) {
-    run = unit_of(pair);
-    cut = s_cut[run];
-    rows = rows_of(cut);
-    r = 2 * (pair - (run ? s_end[run - 1] : 0)) + (at & 1);
-  }
-  const bool has = r < rows.y;
-  float m[1] = {-INFINITY}, l[1] = {}, o[1][V] = {};
-  if (has) join_pieces<D, MT, 1, kJoinPieces>(p, run, cut.w, r, rows.y, sub * kJoinPieces, W * kJoinPieces, m, l, o);
-  s_ml[warp][0] = m[0];
-  s_ml[warp][1] = l[0];
-#pragma unroll
-  for (int j = 0; j < V; ++j) s_o[warp][V * lane + j] = o[0][j];
-  __syncthreads();
-  if (!has || sub != 0) return;
-  float mn = m[0];
-  for (int w = 1; w < W; ++w) mn = fmaxf(mn, s_ml[warp + w][0]);
-  const float base = mn == -INFINITY ? 0.f : mn, f = exp2_approx(m[0] - base);
-  l[0] *= f;
-#pragma unroll
-  for (int j = 0; j < V; ++j) o[0][j] *= f;
-  for (int w = 1; w < W; ++w) {
-    const float g = exp2_approx(s_ml[warp + w][0] - base);
-    l[0] = fmaf(s_ml[warp + w][1], g, l[0]);
-#pragma unroll
-    for (int j = 0; j < V; ++j) o[0][j] = fmaf(s_o[warp + w][V * lane + j], g, o[0][j]);
-  }
-  store(cut, rows.x + r, l[0], o[0]);
 }
 
 }  // namespace gdn

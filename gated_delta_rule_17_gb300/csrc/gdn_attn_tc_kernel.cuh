@@ -323,11 +323,12 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
       f1 *= inv;
       // a dual stream has its rows; the warps of a split unit have half of the columns each
       const int c0 = split ? x * (D / 2) : 0, c1 = split ? c0 + D / 2 : D, xo = split ? 0 : x;
-      const int64_t part = (static_cast<int64_t>(run) * 2 + (w.t0 == 0 ? 1 : 0)) * MT + (split ? 0 : x * kTcTile) + lrow;
+      const int prow = (split ? 0 : x * kTcTile) + lrow;
+      const int64_t part = (static_cast<int64_t>(run) * 2 + (w.t0 == 0 ? 1 : 0)) * MT + prow;
       // each lane stores whole 32-byte sectors of its own row
       char* dst = whole ? reinterpret_cast<char*>(static_cast<T*>(p.out) + (static_cast<int64_t>(s.first) + i) * p.out_stride +
                                                   static_cast<int64_t>(w.kvh * p.group + g) * D)
-                        : reinterpret_cast<char*>(p.part_o + part * D);
+                        : reinterpret_cast<char*>(p.part_o + (part - prow) * D + attn_piece_at<MT>(prow, 0));
       const bool wide = !whole || p.out_wide;
       if (used) {
 #pragma unroll 1
@@ -349,8 +350,8 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             for (int e = 0; e < 8; ++e) r[e] = pack2<T>(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
           }
           if (has) {
-            store32(dst + col * (whole ? 2 : 4), r, wide);
-            if (!whole) store32(dst + col * 4 + 32, r + 8, true);
+            store32(dst + col * (whole ? 2 : MT * 4), r, wide);
+            if (!whole) store32(dst + (col + 8) * (MT * 4), r + 8, true);
           }
         }
       }
@@ -363,7 +364,7 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
       if (has && !whole && (!split || x == 0))  // m in units of log2 e, as the join takes it
         *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(m == -INFINITY ? m : m * cl, l);
       if (threadIdx.x == 0 && w.t0 == 0 && w.t1 < s.tiles)
-        p.cut[run] = w.cut();
+        p.cut[run] = w.cut(p);
     }
   } else if (warp < 12) {
     // ---- copies of Q, K and V --------------------------------------------------------------
