@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
 // way together.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinCtasPerSm = 3;
-constexpr int kJoinPieces = 8;
+constexpr int kJoinPieces = 4;
 constexpr int kJoinRuns = 512;  // runs whose units a CTA can list
 
 template <typename T, int D, int MT>
