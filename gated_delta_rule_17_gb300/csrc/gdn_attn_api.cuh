@@ -198,8 +198,8 @@ int attn_runs(AttnKind kind, int sms) {
 // than an even share (and what the units' lengths differ by, which the host does not know: hence
 // the limit on them), and saves the join and the pieces' way through memory, worth about seven
 // tiles. Measured whole and cut, graph replays: 8 sequences of 500 tokens, 8 kv heads, one row each
-// 12.5 and 14.6 us, 64 of up to 500 27 and 32, one of 500 12.3 and 9.3, 8 of 1000 19 and 16; trees of
-// 16 in 32 sequences of up to 1000 31 and 43, in 8 of 500 12 and 21.
+// 12.3 and 12.9 us, 64 of 500 32 and 35, one of 500 12.3 and 10.5, 8 of 1000 19 and 15; trees of 16 in
+// 32 sequences of 980 31 and 36, in 8 of 480 11.5 and 16.4.
 bool attn_whole(AttnKind kind, int sms, const gdn::AttnParams& p, int most) {
   const int64_t tile = kind == kAttn16 ? gdn::kAttnTile : gdn::kTcTile;
   const int64_t tiles = (static_cast<int64_t>(p.cache.max_pages) * p.cache.page_size + tile - 1) / tile;
