@@ -473,6 +473,35 @@ def test_tree_attention(case, hint):
     assert torch.equal(again.cpu(), got)
 
 
+# Long sequences among many short ones: a CTA's share may end in front of a sequence's first tile, hold many
+# whole sequences, or a part of one; a row is joined from few parts or from many, by one warp or by several.
+UNEVEN_CASES = [
+    dict(ctx=[3000] + [(13 * i) % 200 for i in range(120)] + [2500], new=[1] * 122, nq=8, nkv=2, d=128, page=64, dtype=BF),
+    dict(ctx=[(29 * i) % 500 for i in range(40)] + [5000], new=[2] * 41, nq=8, nkv=8, d=64, page=16, dtype=HF),
+    dict(ctx=[2100] + [(17 * i) % 300 for i in range(30)], new=[20] * 31, nq=8, nkv=1, d=128, page=64, dtype=BF),
+    dict(ctx=[2600, 10, 2300], new=[40, 40, 33], nq=16, nkv=1, d=128, page=32, dtype=HF),
+    dict(ctx=[5, 12000], new=[1, 9], nq=9, nkv=1, d=64, page=64, dtype=BF),
+]
+
+
+@pytest.mark.parametrize("case", UNEVEN_CASES, ids=[str(i) for i in range(len(UNEVEN_CASES))])
+def test_uneven_sequences(case):
+    import gated_delta_rule_17_gb300 as gdn
+
+    case = dict(case)
+    nq = case.pop("nq")
+    c = Cache(47, fill=float("nan"), **case)
+    ks, vs = c.fill_tokens()
+    q = (1.5 * randn(c.g, c.rows, nq, c.d, dtype=F32)).to(c.dtype)
+    masks = [_tree(c.g, n) for n in c.new]
+    out = torch.full_like(q, float("nan"), device="cuda")
+    gdn.tree_attention(q.cuda(), *c.plan(), out, nq=nq, nkv=c.nkv, head_dim=c.d, cu_rows=c.cu.cuda(), max_rows=max(c.new),
+                       mask=_words(masks, c.rows).cuda())
+    assert gdn.last_launch_count() == 2  # cut and joined
+    gdn.check()
+    _check_attention(c, q, out.cpu(), ks, vs, masks, c.d ** -0.5)
+
+
 def test_tree_attention_without_cu_rows():
     import gated_delta_rule_17_gb300 as gdn
 
