@@ -295,6 +295,7 @@ int gdn_head_norm_rope(const void* q, const void* k, const int32_t* positions, c
   g_launches = 0;
   gdn::NormRopeParams p;
   int next = 0;
+  if (int rc = check_head_dim(d)) return rc;  // norm_unroll divides by it
   const int unroll = norm_unroll(nq > nkv ? nq : nkv, d);
   if (int rc = norm_setup(q, k, positions, rope, q_weight, k_weight, eps, q_out, k_out, rows, nq, nkv, d, dtype, strides,
                           unroll, &p, &next))

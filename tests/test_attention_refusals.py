@@ -1,0 +1,45 @@
+"""Calls that the softmax-attention entry points have to refuse, by name and before anything is launched. No GPU."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    from gated_delta_rule_17_gb300 import build
+
+    build.build()
+    import gated_delta_rule_17_gb300 as gdn
+
+    gdn.load()
+    return gdn
+
+
+# Run by a process of its own: what is refused here once ended the process (a division by zero).
+HEAD_SIZE = """
+import ctypes
+import gated_delta_rule_17_gb300 as gdn
+lib, P, d = gdn.load(), 256, {d}
+cache = gdn.Paged(P, P, 4096, 256, 128, 4096, 256, 128, 9, 16, P, 4, 4, 3, 5, P, P)
+at = ctypes.addressof(cache)
+calls = dict(
+    head_norm_rope=lambda: lib.gdn_head_norm_rope(P, P, P, None, None, None, 1e-6, P, P, 4, 4, 2, d, 0, None, None),
+    head_norm_rope_backward=lambda: lib.gdn_head_norm_rope_backward(P, P, P, None, None, None, 1e-6, P, P, P, P, P, P, 4, 4, 2, d, 0,
+                                                                    None, None, 0, None),
+    paged_append=lambda: lib.gdn_paged_append(P, P, at, None, None, 0, None, 1e-6, 2, d, 0, 0, 0, None),
+    tree_attention=lambda: lib.gdn_tree_attention(P, at, None, 0, 0.1, P, 4, 2, d, 0, 0, 0, 0, None, 0, None))
+for name, call in calls.items():
+    rc = call()
+    assert rc == gdn.GDN_ERR_UNSUPPORTED and b"head_dim" in lib.gdn_last_error(), (name, rc, lib.gdn_last_error())
+assert lib.gdn_head_norm_rope_backward_workspace_bytes(4, 4, 2, d) == 0 and lib.gdn_tree_attention_workspace_bytes(4, 2, d) == 0
+"""
+
+
+@pytest.mark.parametrize("d", [0, -1, -128, 96, 1 << 30])
+def test_head_sizes(gdn, d):
+    r = subprocess.run([sys.executable, "-c", HEAD_SIZE.format(d=d)], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stderr[-500:])
