@@ -607,7 +607,7 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_lens, out, *, nq: int, 
             raise GdnError(GDN_ERR_ARG, f"mask must be a contiguous int64 CUDA tensor [{rows}, words]")
         words, mp = shape[1], mask.data_ptr()
     ws, size = _scratch(workspace)
-    rc = _lib.gdn_tree_attention(qp, cache, mp, words, head_dim ** -0.5 if scale is None else scale, op, nq, nkv, head_dim,
+    rc = _lib.gdn_tree_attention(qp, cache, mp, words, max(head_dim, 1) ** -0.5 if scale is None else scale, op, nq, nkv, head_dim,
                                  code, qs, os_, max_rows or 0, ws, size, _stream_of(stream, q))
     if rc != GDN_OK:
         _raise(rc)

@@ -43,3 +43,41 @@ assert lib.gdn_head_norm_rope_backward_workspace_bytes(4, 4, 2, d) == 0 and lib.
 def test_head_sizes(gdn, d):
     r = subprocess.run([sys.executable, "-c", HEAD_SIZE.format(d=d)], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, (r.returncode, r.stderr[-500:])
+
+
+class OnCard:
+    """A tensor's layout with an address that nothing may follow, as if it lay on a card: what is tested is refused
+    before it is read."""
+
+    is_cuda = True
+
+    def __init__(self, *shape, dtype="bfloat16", card=0):
+        import torch
+
+        self.layout, self.card = torch.empty(*shape, dtype=getattr(torch, dtype), device="meta"), card
+
+    def get_device(self):
+        return self.card
+
+    def data_ptr(self):
+        return 256 if self.layout.numel() else 0
+
+    def __getattr__(self, name):
+        return getattr(self.layout, name)
+
+
+def refused(gdn, call, words):
+    with pytest.raises(gdn.GdnError) as e:
+        call()
+    assert e.value.code in (gdn.GDN_ERR_ARG, gdn.GDN_ERR_UNSUPPORTED) and words in str(e.value), str(e.value)
+
+
+def attend(gdn, rows=4, d=128, **kw):
+    a = dict(q=OnCard(rows, 4 * d), k_cache=OnCard(3, 16, 2, d), v_cache=OnCard(3, 16, 2, d), block_table=OnCard(rows, 2, dtype="int32"),
+             ctx_lens=OnCard(rows, dtype="int32"), out=OnCard(rows, 4 * d), nq=4, nkv=2, head_dim=d, stream=0)
+    a.update(kw)
+    return gdn.tree_attention(**a)
+
+
+def test_attention_over_heads_of_nothing(gdn):
+    refused(gdn, lambda: attend(gdn, d=0), "head_dim")
