@@ -606,6 +606,8 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_lens, out, *, nq: int, 
         if mask.dtype != torch.int64 or not mask.is_cuda or len(shape) != 2 or shape[0] != rows or not mask.is_contiguous():
             raise GdnError(GDN_ERR_ARG, f"mask must be a contiguous int64 CUDA tensor [{rows}, words]")
         words, mp = shape[1], mask.data_ptr()
+        if words == 0 and rows:  # no address either, which the library takes for no mask
+            raise GdnError(GDN_ERR_ARG, "mask must have at least one word a row")
     ws, size = _scratch(workspace)
     rc = _lib.gdn_tree_attention(qp, cache, mp, words, max(head_dim, 1) ** -0.5 if scale is None else scale, op, nq, nkv, head_dim,
                                  code, qs, os_, max_rows or 0, ws, size, _stream_of(stream, q))

@@ -81,3 +81,11 @@ def attend(gdn, rows=4, d=128, **kw):
 
 def test_attention_over_heads_of_nothing(gdn):
     refused(gdn, lambda: attend(gdn, d=0), "head_dim")
+
+
+def test_a_mask_of_no_words_is_not_no_mask(gdn):
+    # such a tensor has no address, which the library would take for "each row sees those up to itself"
+    refused(gdn, lambda: attend(gdn, mask=OnCard(4, 0, dtype="int64")), "word")
+    attend(gdn, rows=0, mask=OnCard(0, 0, dtype="int64"))  # no rows: nothing to see, with or without words
+    attend(gdn, rows=0, mask=OnCard(0, 2, dtype="int64"))
+    assert gdn.last_launch_count() == 0
