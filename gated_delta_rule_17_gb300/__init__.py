@@ -427,6 +427,8 @@ def _act(t, name, dtype, rows, inner):
     stride = _row_stride(t, name, inner)
     if t.shape[0] != rows:
         raise GdnError(GDN_ERR_ARG, f"{name} has {t.shape[0]} rows, need {rows}")
+    if t.numel() != rows * inner:  # [B, T, ...] in place of [B * T, ...], or heads that no one would touch
+        raise GdnError(GDN_ERR_ARG, f"{name}: rows hold {t.numel() // rows} elements, need just {inner}")
     return t.data_ptr(), stride
 
 

@@ -89,3 +89,24 @@ def test_a_mask_of_no_words_is_not_no_mask(gdn):
     attend(gdn, rows=0, mask=OnCard(0, 0, dtype="int64"))  # no rows: nothing to see, with or without words
     attend(gdn, rows=0, mask=OnCard(0, 2, dtype="int64"))
     assert gdn.last_launch_count() == 0
+
+
+def norm(gdn, q, q_out=None, **kw):
+    return gdn.head_norm_rope(q, None, None, None, None, q_out if q_out is not None else q, None, nq=2, nkv=0, stream=0, **kw)
+
+
+def test_rows_that_hold_more_than_the_heads(gdn):
+    # a batch of sequences in place of their rows: only the first token of each would be worked on
+    batch, grad = OnCard(2, 5, 256), OnCard(2, 5, 256, dtype="float32")
+    refused(gdn, lambda: norm(gdn, batch), "elements")
+    refused(gdn, lambda: norm(gdn, OnCard(2, 256), batch), "elements")
+    refused(gdn, lambda: gdn.head_norm_rope_backward(grad, None, None, None, None, grad, None, grad, None, nq=2, nkv=0, stream=0), "elements")
+    kc, table, lens = OnCard(3, 16, 2, 128), OnCard(2, 2, dtype="int32"), OnCard(2, dtype="int32")
+    refused(gdn, lambda: gdn.paged_append(batch, batch, kc, kc, table, lens, nkv=2, stream=0), "elements")
+    refused(gdn, lambda: gdn.paged_append(OnCard(2, 256), batch, kc, kc, table, lens, nkv=2, stream=0), "elements")
+    refused(gdn, lambda: attend(gdn, rows=2, q=OnCard(2, 5, 4 * 128)), "elements")
+    refused(gdn, lambda: attend(gdn, rows=2, out=OnCard(2, 5, 4 * 128)), "elements")
+    # and a row with more heads than are worked on, in place of a slice of it
+    refused(gdn, lambda: norm(gdn, OnCard(4, 3, 128)), "elements")
+    refused(gdn, lambda: norm(gdn, OnCard(4, 1, 128)), "elements")
+    refused(gdn, lambda: norm(gdn, OnCard(4 * 256)), "2-D")
