@@ -16,7 +16,11 @@ def gdn():
     import gated_delta_rule_17_gb300 as gdn
 
     gdn.load()
-    return gdn
+    import torch
+
+    with pytest.MonkeyPatch.context() as m:  # the current device, which a machine without a card does not have
+        m.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+        yield gdn
 
 
 # Run by a process of its own: what is refused here once ended the process (a division by zero).
@@ -110,3 +114,29 @@ def test_rows_that_hold_more_than_the_heads(gdn):
     refused(gdn, lambda: norm(gdn, OnCard(4, 3, 128)), "elements")
     refused(gdn, lambda: norm(gdn, OnCard(4, 1, 128)), "elements")
     refused(gdn, lambda: norm(gdn, OnCard(4 * 256)), "2-D")
+
+
+NORM = dict(q=(4, 256), k=(4, 128), positions=(4, "int32"), cos=(9, 64, "float32"), sin=(9, 64, "float32"), q_out=(4, 256),
+            k_out=(4, 128), q_weight=(128, "float32"), k_weight=(128, "float32"))
+BACK = {n: s for n, s in NORM.items() if not n.endswith("_out")}
+BACK.update(q_grad=(4, 256), k_grad=(4, 128), dq=(4, 256), dk=(4, 128), dq_weight=(128, "float32"), dk_weight=(128, "float32"),
+            workspace=(1 << 24, "uint8"))
+CACHE = dict(k_cache=(3, 16, 1, 128), v_cache=(3, 16, 1, 128), block_table=(2, 2, "int32"), ctx_lens=(2, "int32"), cu_rows=(3, "int32"))
+APPEND = dict(CACHE, k=(4, 128), v=(4, 128), positions=(4, "int32"), cos=(9, 64, "float32"), sin=(9, 64, "float32"), k_weight=(128, "float32"))
+ATTEND = dict(CACHE, q=(4, 256), out=(4, 256), mask=(4, 1, "int64"), workspace=(1 << 24, "uint8"))
+CALLS = [("head_norm_rope", NORM, dict(nq=2, nkv=1)), ("head_norm_rope_backward", BACK, dict(nq=2, nkv=1)),
+         ("paged_append", APPEND, dict(nkv=1, norm=True)), ("tree_attention", ATTEND, dict(nq=2, nkv=1))]
+
+
+@pytest.mark.parametrize("name,tensors,kw", CALLS, ids=[c[0] for c in CALLS])
+def test_tensors_on_another_card(gdn, name, tensors, kw):
+    # the launch goes to the current card, and a kernel there cannot take another's addresses
+    def call(**cards):
+        ts = {n: OnCard(*(x for x in s if not isinstance(x, str)), dtype=s[-1] if isinstance(s[-1], str) else "bfloat16",
+                        card=cards.get(n, cards.get("all", 0))) for n, s in tensors.items()}
+        return getattr(gdn, name)(**ts, **kw, stream=0)
+
+    for n in tensors:
+        refused(gdn, lambda: call(**{n: 1}), "cuda:0" if n not in ("q", "k") else n)
+        refused(gdn, lambda: call(**{n: -1}), "cuda:0" if n not in ("q", "k") else n)
+    refused(gdn, lambda: call(all=1), "current device")
