@@ -489,16 +489,19 @@ gdn_head_norm_rope_bwd_kernel(const NormRopeParams p) {
       float qa, qb, ma, mb;
       parts_of(q2, qa, qb);
       parts_of(m2, ma, mb);
+      // dx = r (t - (x r) (r mean(t x))): the powers of r stay with what they scale, since r^3 by itself leaves
+      // fp32 for rows far from 1 (of 1e13 and more, below 1e-13 without eps) whose gradient does not
       const float r = rsqrtf(row_sum<LPH>(qa + qb) * (1.f / D) + p.eps);
-      const float f = -r * r * r * (row_sum<LPH>(ma + mb) * (1.f / D));
+      const float f = -r * (row_sum<LPH>(ma + mb) * (1.f / D));
       if (ok && i * SLOTS + slot < c_left) {
         const Pair rr = pair_of(r, r), ff = pair_of(f, f);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          du[j] = fma2(zu[j], mul2(u[j], rr), du[j]);
-          dv[j] = fma2(zv[j], mul2(v[j], rr), dv[j]);
-          tu[j] = fma2(u[j], ff, mul2(tu[j], rr));
-          tv[j] = fma2(v[j], ff, mul2(tv[j], rr));
+          const Pair xu = mul2(u[j], rr), xv = mul2(v[j], rr);
+          du[j] = fma2(zu[j], xu, du[j]);
+          dv[j] = fma2(zv[j], xv, dv[j]);
+          tu[j] = mul2(fma2(xu, ff, tu[j]), rr);
+          tv[j] = mul2(fma2(xv, ff, tv[j]), rr);
         }
         float a[4], b[4];
         from_pairs2(tu, a);

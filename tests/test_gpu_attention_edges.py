@@ -1,0 +1,47 @@
+"""GPU tests of the softmax-attention operators at sizes and values where their arithmetic or their schedule could go
+wrong, against plain 64-bit forms, with bounds that follow from the kernels' roundings."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import attention_reference as ref  # noqa: E402
+from tests.test_gpu_attention import BF, F32, HF, Cache, _built, _check_attention, _cuda, gen, padded, randn  # noqa: E402, F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- the backward of norm and rotation -----------------------------------------------------
+
+
+def _backward(x, dy, w, cos, sin, pos, eps, interleaved=False):
+    """dq and the weight's gradient of q alone, x and dy [rows, heads, d] on the host."""
+    import gated_delta_rule_17_gb300 as gdn
+
+    rows, heads, d = x.shape
+    dx, dw = torch.empty(rows, heads * d, dtype=x.dtype, device="cuda"), torch.empty(d, device="cuda")
+    gdn.head_norm_rope_backward(x.cuda().flatten(1), None, _cuda(pos), _cuda(cos), _cuda(sin), dy.cuda().flatten(1), None, dx, None, dw,
+                                nq=heads, nkv=0, head_dim=d, q_weight=_cuda(w), eps=eps, interleaved=interleaved)
+    gdn.check()
+    return dx.cpu().double().view(rows, heads, d), dw.cpu().double()
+
+
+# rows of these sizes: the sum of their squares is inside fp32, the cube of their root mean square is not
+@pytest.mark.parametrize("size,eps", [(1e12, 1e-6), (1e15, 1e-6), (1e17, 1e-6), (1e-13, 0.0), (1e-15, 0.0)])
+@pytest.mark.parametrize("dtype,rot", [(F32, 0), (F32, 128), (BF, 128)])
+def test_norm_rope_backward_of_rows_of_any_size(size, eps, dtype, rot):
+    g = gen(61)
+    x, dy = (size * randn(g, 6, 3, 128, dtype=F32)).to(dtype), randn(g, 6, 3, 128, dtype=dtype)
+    w = 1 + 0.2 * torch.randn(128, generator=g)
+    cos, sin = ref.rope_tables(9, rot) if rot else (None, None)
+    pos = torch.randint(0, 9, (6,), generator=g, dtype=torch.int32)
+    got, gotw = _backward(x, dy, w, cos, sin, pos, eps)
+    at = pos.long()
+    want, wsum, wsize, room = ref.norm_rope_backward(x.double(), dy.double(), w, None if cos is None else cos[at],
+                                                     None if sin is None else sin[at], eps, False)
+    # fp32: two row sums (<= 16 additions in a chain), rsqrt, about ten products and sums
+    bound = ref.ROUNDING[dtype] * want.abs() + 64 * ref.FP32 * room
+    assert ((got - want).abs() <= bound).all(), float(((got - want).abs() / bound).max())
+    # 18 terms: each a rotated value, which is a difference of two, times x r; and their sum
+    both = dy.double().abs() if cos is None else ref.rotate_sizes(dy.double(), rot, False)
+    wroom = (both * x.double().abs() / torch.sqrt((x.double() ** 2).mean(-1, keepdim=True) + eps)).sum((0, 1))
+    assert ((gotw - wsum).abs() <= (18 + 32) * ref.FP32 * wroom).all()
