@@ -384,11 +384,11 @@ def backward(q, k, v, g, beta, h0, dout, dq, dk, dv, dg, dbeta, *, nk: int, nv: 
 
 # ---- the softmax-attention operators (include/gdn_attention.h) ----------------------------
 # A decode step makes several of these calls a layer, each a few microseconds on the GPU, so the
-# checks below touch every attribute of a tensor once and take the common layout first. All tensors are
-# on the current device, where the launch goes.
+# checks below touch every attribute of a tensor once and take the common layout first.
 
 _torch = None   # torch, once one of the calls below has been made
 _codes = {}     # torch dtype -> the ABI's number
+_cards = 0      # devices of this process
 # The ABI's structs, packed: the bytes of Rope, NormStrides and Paged (a fraction of a ctypes object's cost)
 _ROPE = struct.Struct("@QQqiii4x").pack
 _STRIDES = struct.Struct("@6q").pack
@@ -396,19 +396,29 @@ _PAGED = struct.Struct("@QQqqqqqqiiQqiii4xQQ").pack
 
 
 def _setup():
-    global _torch
+    global _torch, _cards
     import torch
 
     load()
+    _cards = torch.cuda.device_count()
     _codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
     _torch = torch
     return torch
 
 
-def _stream_of(stream, card):
+def _stream_of(stream, t):
     if stream is None:  # the handle itself: a torch.cuda.Stream around it costs a sixth of a call
-        return _torch._C._cuda_getCurrentRawStream(card)
+        return _torch._C._cuda_getCurrentRawStream(t.get_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _one_card(**tensors):
+    """All tensors have to be on the current device, where the launch goes. Asked where there are several devices; else
+    a CUDA tensor has nowhere else to be, and the question costs up to a tenth of a call."""
+    here = _torch._C._cuda_getDevice()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != here:
+            raise GdnError(GDN_ERR_ARG, f"{name} is on {t.device}, the current device is cuda:{here}")
 
 
 def _act_code(t, name, most):
@@ -419,18 +429,10 @@ def _act_code(t, name, most):
     return code
 
 
-def _card(t, name):
-    """The number of the current device, which `t` has to be on: the launch goes there."""
-    card = t.get_device()
-    if card < 0 or card != _torch._C._cuda_getDevice():
-        raise GdnError(GDN_ERR_ARG, f"{name} must be a CUDA tensor on the current device, got one on {t.device}")
-    return card
-
-
-def _act(t, name, dtype, card, rows, inner):
+def _act(t, name, dtype, rows, inner):
     """Checks [rows, ...] activations with `inner` contiguous elements a row; (address, row stride)."""
-    if t.dtype is not dtype or t.get_device() != card:
-        raise GdnError(GDN_ERR_ARG, f"{name} must be a {dtype} tensor on cuda:{card}, got {t.dtype} on {t.device}")
+    if t.dtype is not dtype or not t.is_cuda:
+        raise GdnError(GDN_ERR_ARG, f"{name} must be a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
     if t.numel() == rows * inner and t.is_contiguous():  # packed rows, however they are split up
         return t.data_ptr(), inner
     stride = _row_stride(t, name, inner)
@@ -441,24 +443,24 @@ def _act(t, name, dtype, card, rows, inner):
     return t.data_ptr(), stride
 
 
-def _vector(t, name, dtype, card, n):
-    """The address of a contiguous vector of n elements, or None for None."""
+def _vector(t, name, dtype, n):
+    """The address of a contiguous CUDA vector of n elements, or None for None."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.get_device() != card or t.numel() != n or not t.is_contiguous():
-        raise GdnError(GDN_ERR_ARG, f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{card}")
+    if t.dtype is not dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
+        raise GdnError(GDN_ERR_ARG, f"{name} must be a contiguous {dtype} CUDA tensor of {n} elements")
     return t.data_ptr()
 
 
-def _rope(cos, sin, card, interleaved):
+def _rope(cos, sin, interleaved):
     """The tables as the ABI's struct, packed."""
     if cos is None or sin is None:
         if cos is not sin:
             raise GdnError(GDN_ERR_ARG, "cos and sin must be given together")
         return None
     f32, shape = _torch.float32, cos.shape
-    if cos.dtype is not f32 or sin.dtype is not f32 or cos.get_device() != card or sin.get_device() != card or len(shape) != 2 or sin.shape != shape:
-        raise GdnError(GDN_ERR_ARG, f"cos and sin must be fp32 tensors [positions, rot/2] on cuda:{card}, both alike")
+    if cos.dtype is not f32 or sin.dtype is not f32 or not cos.is_cuda or not sin.is_cuda or len(shape) != 2 or sin.shape != shape:
+        raise GdnError(GDN_ERR_ARG, "cos and sin must be fp32 CUDA tensors [positions, rot/2], both alike")
     n, half = shape
     stride = half
     if not (cos.is_contiguous() and sin.is_contiguous()):
@@ -469,11 +471,11 @@ def _rope(cos, sin, card, interleaved):
     return _ROPE(cos.data_ptr(), sin.data_ptr(), stride, n, 2 * half, 1 if interleaved else 0)
 
 
-def _scratch(workspace, card):
+def _scratch(workspace):
     if workspace is None:
         return None, 0
-    if workspace.get_device() != card or not workspace.is_contiguous():
-        raise GdnError(GDN_ERR_ARG, f"workspace must be a contiguous tensor on cuda:{card}")
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise GdnError(GDN_ERR_ARG, "workspace must be a contiguous CUDA tensor")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -498,18 +500,19 @@ def head_norm_rope(q, k, positions, cos, sin, q_out, k_out, *, nq: int, nkv: int
     turned, in pairs (i, i + rot/2), or (2i, 2i + 1) if ``interleaved``. head_dim is 64 or 128."""
     torch = _torch or _setup()
     x = _heads_given(q, k, nq, nkv)
+    if _cards > 1:
+        _one_card(q=q, k=k, positions=positions, cos=cos, sin=sin, q_out=q_out, k_out=k_out, q_weight=q_weight, k_weight=k_weight)
     code, rows, dt, wq, wk = _act_code(x, "q" if nq else "k", 2), x.shape[0], x.dtype, nq * head_dim, nkv * head_dim
-    card = _card(x, "q" if nq else "k")
     if (nq and q_out is None) or (nkv and k_out is None):
         raise GdnError(GDN_ERR_ARG, "q_out or k_out is missing")
-    qp, qs = _act(q, "q", dt, card, rows, wq) if nq else _NONE
-    kp, ks = _act(k, "k", dt, card, rows, wk) if nkv else _NONE
-    qo, qos = _act(q_out, "q_out", dt, card, rows, wq) if nq else _NONE
-    ko, kos = _act(k_out, "k_out", dt, card, rows, wk) if nkv else _NONE
-    rc = _lib.gdn_head_norm_rope(qp, kp, _vector(positions, "positions", torch.int32, card, rows), _rope(cos, sin, card, interleaved),
-                                 _vector(q_weight, "q_weight", torch.float32, card, head_dim),
-                                 _vector(k_weight, "k_weight", torch.float32, card, head_dim), eps, qo, ko, rows, nq, nkv,
-                                 head_dim, code, _STRIDES(qs, ks, qos, kos, 0, 0), _stream_of(stream, card))
+    qp, qs = _act(q, "q", dt, rows, wq) if nq else _NONE
+    kp, ks = _act(k, "k", dt, rows, wk) if nkv else _NONE
+    qo, qos = _act(q_out, "q_out", dt, rows, wq) if nq else _NONE
+    ko, kos = _act(k_out, "k_out", dt, rows, wk) if nkv else _NONE
+    rc = _lib.gdn_head_norm_rope(qp, kp, _vector(positions, "positions", torch.int32, rows), _rope(cos, sin, interleaved),
+                                 _vector(q_weight, "q_weight", torch.float32, head_dim),
+                                 _vector(k_weight, "k_weight", torch.float32, head_dim), eps, qo, ko, rows, nq, nkv,
+                                 head_dim, code, _STRIDES(qs, ks, qos, kos, 0, 0), _stream_of(stream, x))
     if rc != GDN_OK:
         _raise(rc)
 
@@ -527,37 +530,39 @@ def head_norm_rope_backward(q, k, positions, cos, sin, q_grad, k_grad, dq, dk, d
     the sums over all rows and heads."""
     torch = _torch or _setup()
     x = _heads_given(q, k, nq, nkv)
+    if _cards > 1:
+        _one_card(q=q, k=k, positions=positions, cos=cos, sin=sin, q_grad=q_grad, k_grad=k_grad, dq=dq, dk=dk, dq_weight=dq_weight,
+                  dk_weight=dk_weight, q_weight=q_weight, k_weight=k_weight, workspace=workspace)
     code, rows, dt, wq, wk = _act_code(x, "q" if nq else "k", 2), x.shape[0], x.dtype, nq * head_dim, nkv * head_dim
-    card = _card(x, "q" if nq else "k")
     if (nq and (dq is None or q_grad is None)) or (nkv and (dk is None or k_grad is None)):
         raise GdnError(GDN_ERR_ARG, "a gradient tensor is missing")
-    qp, qs = _act(q, "q", dt, card, rows, wq) if nq else _NONE
-    kp, ks = _act(k, "k", dt, card, rows, wk) if nkv else _NONE
-    gq, gqs = _act(q_grad, "q_grad", dt, card, rows, wq) if nq else _NONE
-    gk, gks = _act(k_grad, "k_grad", dt, card, rows, wk) if nkv else _NONE
-    dqp, dqs = _act(dq, "dq", dt, card, rows, wq) if nq else _NONE
-    dkp, dks = _act(dk, "dk", dt, card, rows, wk) if nkv else _NONE
-    ws, size = _scratch(workspace, card)
+    qp, qs = _act(q, "q", dt, rows, wq) if nq else _NONE
+    kp, ks = _act(k, "k", dt, rows, wk) if nkv else _NONE
+    gq, gqs = _act(q_grad, "q_grad", dt, rows, wq) if nq else _NONE
+    gk, gks = _act(k_grad, "k_grad", dt, rows, wk) if nkv else _NONE
+    dqp, dqs = _act(dq, "dq", dt, rows, wq) if nq else _NONE
+    dkp, dks = _act(dk, "dk", dt, rows, wk) if nkv else _NONE
+    ws, size = _scratch(workspace)
     f32 = torch.float32
-    rc = _lib.gdn_head_norm_rope_backward(qp, kp, _vector(positions, "positions", torch.int32, card, rows), _rope(cos, sin, card, interleaved),
-                                          _vector(q_weight, "q_weight", f32, card, head_dim), _vector(k_weight, "k_weight", f32, card, head_dim),
-                                          eps, gq, gk, dqp, dkp, _vector(dq_weight, "dq_weight", f32, card, head_dim),
-                                          _vector(dk_weight, "dk_weight", f32, card, head_dim), rows, nq, nkv, head_dim, code,
-                                          _STRIDES(qs, ks, dqs, dks, gqs, gks), ws, size, _stream_of(stream, card))
+    rc = _lib.gdn_head_norm_rope_backward(qp, kp, _vector(positions, "positions", torch.int32, rows), _rope(cos, sin, interleaved),
+                                          _vector(q_weight, "q_weight", f32, head_dim), _vector(k_weight, "k_weight", f32, head_dim),
+                                          eps, gq, gk, dqp, dkp, _vector(dq_weight, "dq_weight", f32, head_dim),
+                                          _vector(dk_weight, "dk_weight", f32, head_dim), rows, nq, nkv, head_dim, code,
+                                          _STRIDES(qs, ks, dqs, dks, gqs, gks), ws, size, _stream_of(stream, x))
     if rc != GDN_OK:
         _raise(rc)
 
 
-def _paged(x, card, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, d, rows):
+def _paged(x, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, d, rows):
     """The cache and the batch of `rows` rows like x as the ABI's struct."""
     dt, shape, ks, vs = x.dtype, k_cache.shape, k_cache.stride(), v_cache.stride()
-    if k_cache.dtype is not dt or v_cache.dtype is not dt or k_cache.get_device() != card or v_cache.get_device() != card:
-        raise GdnError(GDN_ERR_ARG, f"k_cache and v_cache must be {dt} tensors on cuda:{card}")
+    if k_cache.dtype is not dt or v_cache.dtype is not dt or not k_cache.is_cuda or not v_cache.is_cuda:
+        raise GdnError(GDN_ERR_ARG, f"k_cache and v_cache must be {dt} CUDA tensors")
     if len(shape) != 4 or shape[2] != nkv or shape[3] != d or v_cache.shape != shape or ks[3] != 1 or vs[3] != 1:
         raise GdnError(GDN_ERR_ARG, f"k_cache and v_cache must be [pages, page_size, {nkv}, {d}], the last dimension contiguous")
     i32, table = _torch.int32, block_table.shape
-    if block_table.dtype is not i32 or block_table.get_device() != card or len(table) != 2:
-        raise GdnError(GDN_ERR_ARG, f"block_table must be an int32 tensor [B, max_pages] on cuda:{card}")
+    if block_table.dtype is not i32 or not block_table.is_cuda or len(table) != 2:
+        raise GdnError(GDN_ERR_ARG, "block_table must be an int32 CUDA tensor [B, max_pages]")
     B, most = table
     stride = most
     if not block_table.is_contiguous():
@@ -566,8 +571,8 @@ def _paged(x, card, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, d, ro
             raise GdnError(GDN_ERR_ARG, "block_table must be contiguous in a row")
         stride = max(ts[0], most) if B < 2 else ts[0]
     return _PAGED(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], shape[0], shape[1],
-                  block_table.data_ptr(), stride, most, B, rows, _vector(ctx_lens, "ctx_lens", i32, card, B) or 0,
-                  _vector(cu_rows, "cu_rows", i32, card, B + 1) or 0)
+                  block_table.data_ptr(), stride, most, B, rows, _vector(ctx_lens, "ctx_lens", i32, B) or 0,
+                  _vector(cu_rows, "cu_rows", i32, B + 1) or 0)
 
 
 def paged_append(k, v, k_cache, v_cache, block_table, ctx_lens, *, nkv: int, head_dim: int = 128, cu_rows=None,
@@ -582,14 +587,16 @@ def paged_append(k, v, k_cache, v_cache, block_table, ctx_lens, *, nkv: int, hea
     sequence b). Row i of sequence b becomes its token ctx_lens[b] + i. ``positions``: int32 [rows] for the
     rotation (None: the token's index); ``cos``, ``sin``, ``interleaved``, ``k_weight``: as ``head_norm_rope``."""
     torch = _torch or _setup()
+    if _cards > 1:
+        _one_card(k=k, v=v, k_cache=k_cache, v_cache=v_cache, block_table=block_table, ctx_lens=ctx_lens, cu_rows=cu_rows,
+                  positions=positions, cos=cos, sin=sin, k_weight=k_weight)
     code, rows, w = _act_code(k, "k", 1), k.shape[0], nkv * head_dim
-    card = _card(k, "k")
-    kp, ks = _act(k, "k", k.dtype, card, rows, w)
-    vp, vs = _act(v, "v", k.dtype, card, rows, w)
-    rc = _lib.gdn_paged_append(kp, vp, _paged(k, card, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, head_dim, rows),
-                               _vector(positions, "positions", torch.int32, card, rows), _rope(cos, sin, card, interleaved),
-                               1 if norm else 0, _vector(k_weight, "k_weight", torch.float32, card, head_dim), eps, nkv, head_dim,
-                               code, ks, vs, _stream_of(stream, card))
+    kp, ks = _act(k, "k", k.dtype, rows, w)
+    vp, vs = _act(v, "v", k.dtype, rows, w)
+    rc = _lib.gdn_paged_append(kp, vp, _paged(k, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, head_dim, rows),
+                               _vector(positions, "positions", torch.int32, rows), _rope(cos, sin, interleaved),
+                               1 if norm else 0, _vector(k_weight, "k_weight", torch.float32, head_dim), eps, nkv, head_dim,
+                               code, ks, vs, _stream_of(stream, k))
     if rc != GDN_OK:
         _raise(rc)
 
@@ -610,22 +617,24 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_lens, out, *, nq: int, 
     nothing gives zeros. ``max_rows``: the most rows of a sequence, by which the kernel is chosen; ``scale``:
     1/sqrt(head_dim) by default; ``workspace``: uint8 CUDA tensor of ``tree_attention_workspace_bytes(...)``."""
     torch = _torch or _setup()
+    if _cards > 1:
+        _one_card(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, ctx_lens=ctx_lens, out=out, cu_rows=cu_rows,
+                  mask=mask, workspace=workspace)
     code, rows, w = _act_code(q, "q", 1), q.shape[0], nq * head_dim
-    card = _card(q, "q")
-    qp, qs = _act(q, "q", q.dtype, card, rows, w)
-    op, os_ = _act(out, "out", q.dtype, card, rows, w)
-    cache = _paged(q, card, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, head_dim, rows)
+    qp, qs = _act(q, "q", q.dtype, rows, w)
+    op, os_ = _act(out, "out", q.dtype, rows, w)
+    cache = _paged(q, k_cache, v_cache, block_table, ctx_lens, cu_rows, nkv, head_dim, rows)
     words, mp = 0, None
     if mask is not None:
         shape = mask.shape
-        if mask.dtype != torch.int64 or mask.get_device() != card or len(shape) != 2 or shape[0] != rows or not mask.is_contiguous():
-            raise GdnError(GDN_ERR_ARG, f"mask must be a contiguous int64 tensor [{rows}, words] on cuda:{card}")
+        if mask.dtype != torch.int64 or not mask.is_cuda or len(shape) != 2 or shape[0] != rows or not mask.is_contiguous():
+            raise GdnError(GDN_ERR_ARG, f"mask must be a contiguous int64 CUDA tensor [{rows}, words]")
         words, mp = shape[1], mask.data_ptr()
         if words == 0 and rows:  # no address either, which the library takes for no mask
             raise GdnError(GDN_ERR_ARG, "mask must have at least one word a row")
-    ws, size = _scratch(workspace, card)
+    ws, size = _scratch(workspace)
     rc = _lib.gdn_tree_attention(qp, cache, mp, words, max(head_dim, 1) ** -0.5 if scale is None else scale, op, nq, nkv, head_dim,
-                                 code, qs, os_, max_rows or 0, ws, size, _stream_of(stream, card))
+                                 code, qs, os_, max_rows or 0, ws, size, _stream_of(stream, q))
     if rc != GDN_OK:
         _raise(rc)
 

@@ -16,11 +16,7 @@ def gdn():
     import gated_delta_rule_17_gb300 as gdn
 
     gdn.load()
-    import torch
-
-    with pytest.MonkeyPatch.context() as m:  # the current device, which a machine without a card does not have
-        m.setattr(torch._C, "_cuda_getDevice", lambda: 0)
-        yield gdn
+    return gdn
 
 
 # Run by a process of its own: what is refused here once ended the process (a division by zero).
@@ -129,14 +125,20 @@ CALLS = [("head_norm_rope", NORM, dict(nq=2, nkv=1)), ("head_norm_rope_backward"
 
 
 @pytest.mark.parametrize("name,tensors,kw", CALLS, ids=[c[0] for c in CALLS])
-def test_tensors_on_another_card(gdn, name, tensors, kw):
+def test_tensors_on_another_card(gdn, monkeypatch, name, tensors, kw):
     # the launch goes to the current card, and a kernel there cannot take another's addresses
+    import torch
+
+    gdn._setup()
+    monkeypatch.setattr(gdn, "_cards", 2)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+
     def call(**cards):
         ts = {n: OnCard(*(x for x in s if not isinstance(x, str)), dtype=s[-1] if isinstance(s[-1], str) else "bfloat16",
                         card=cards.get(n, cards.get("all", 0))) for n, s in tensors.items()}
         return getattr(gdn, name)(**ts, **kw, stream=0)
 
     for n in tensors:
-        refused(gdn, lambda: call(**{n: 1}), "cuda:0" if n not in ("q", "k") else n)
-        refused(gdn, lambda: call(**{n: -1}), "cuda:0" if n not in ("q", "k") else n)
-    refused(gdn, lambda: call(all=1), "current device")
+        refused(gdn, lambda: call(**{n: 1}), f"{n} is on")
+        refused(gdn, lambda: call(**{n: -1}), f"{n} is on")
+    refused(gdn, lambda: call(all=1), "the current device is cuda:0")
