@@ -223,10 +223,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) gdn_attn_kernel(const AttnPar
           }
           m[hf] = mn;
         }
-        x0 = exp2_approx(x0 - base);
-        x1 = exp2_approx(x1 - base);
-        x2 = exp2_approx(x2 - base);
-        x3 = exp2_approx(x3 - base);
+        const float one = base - kWeightLog2<T>;
+        x0 = exp2_approx(x0 - one);
+        x1 = exp2_approx(x1 - one);
+        x2 = exp2_approx(x2 - one);
+        x3 = exp2_approx(x3 - one);
         l[hf] += (x0 + x1) + (x2 + x3);  // this thread's tokens; over the row at the end
         pf[hf] = pack2<T>(x0, x1);
         pf[2 + hf] = pack2<T>(x2, x3);

@@ -16,7 +16,7 @@
 // O stays unnormalised in tensor memory. It is scaled down only when a row's maximum has grown by
 // more than 2^8 since its last reference: until then P <= 2^8 relative to the reference, which
 // costs no precision in fp32 and 16-bit floats (their relative error does not depend on the size;
-// 2^8 is far inside fp16's range), and most tiles skip the round trip through the registers.
+// 2^8 and kWeightLog2 together are inside fp16's range), and most tiles skip the round trip through the registers.
 //
 // Roles: warps 0-3 and 4-7 one stream each; warps 8-11 copy Q, K and V tiles (TMA boxes inside the
 // pages, or 16-byte cp.async for any page size; 128-byte-swizzled rows), K and V through a ring of
@@ -251,7 +251,7 @@ gdn_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
               tc::tmem_st32(o_addr + x * D + 32 * k, r1);
             }
           }
-          const float nb = m == -INFINITY ? 0.f : -m * cl;
+          const float nb = m == -INFINITY ? 0.f : (kWeightLog2<T> == 0.f ? -m * cl : kWeightLog2<T> - m * cl);
           const Pair nb2 = pair_of(nb, nb);
           Pair sum[2] = {0, 0};
           auto weights = [&](const uint32_t (&r)[32], int k) {  // over a part of S that has been read

@@ -45,3 +45,40 @@ def test_norm_rope_backward_of_rows_of_any_size(size, eps, dtype, rot):
     both = dy.double().abs() if cos is None else ref.rotate_sizes(dy.double(), rot, False)
     wroom = (both * x.double().abs() / torch.sqrt((x.double() ** 2).mean(-1, keepdim=True) + eps)).sum((0, 1))
     assert ((gotw - wsum).abs() <= (18 + 32) * ref.FP32 * wroom).all()
+
+
+# ---- attention -----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("peak", ["first", "last"])
+@pytest.mark.parametrize("nq,n", [(1, 1), (8, 5)])
+def test_fp16_sums_of_many_small_weights(nq, n, peak):
+    # One token outweighs each of 40000 others by 2^26, and has a value of zero: what the others add up to, 0.06% of the
+    # weight, is the output. As fp16 numbers below 1 their weights of 2^-26 would be gone. As many sequences (of the same
+    # pages) as there are CTAs, so that one CTA has a sequence's tokens and one maximum for many of them.
+    import gated_delta_rule_17_gb300 as gdn
+
+    tokens, d, page = 40000, 64, 64
+    B = torch.cuda.get_device_properties(0).multi_processor_count * (2 if nq * n <= 16 else 1)
+    g = gen(64)
+    k, v = torch.zeros(tokens, 1, d, dtype=HF), (256 + 128 * torch.rand(tokens, 1, d, generator=g)).to(HF)
+    at = 0 if peak == "first" else tokens - n
+    k[at, 0, 0] = 26 * 0.6931471805599453 * 8 / 4  # times q's 4 and 1 / sqrt(d): 26 in units of log 2
+    v[at] = 0
+    kc, vc = k.cuda().view(-1, page, 1, d), v.cuda().view(-1, page, 1, d)
+    table = torch.arange(tokens // page, dtype=torch.int32, device="cuda").repeat(B, 1)
+    lens = torch.full((B,), tokens - n, dtype=torch.int32, device="cuda")
+    cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    q = torch.zeros(n, nq, d, dtype=HF)
+    q[:, :, 0] = 4
+    out = torch.empty(B * n, nq * d, dtype=HF, device="cuda")
+    gdn.tree_attention(q.cuda().repeat(B, 1, 1), kc, vc, table, lens, out, nq=nq, nkv=1, head_dim=d, cu_rows=cu, max_rows=n)
+    gdn.check()
+    want, spread, slack = ref.attention(q.double(), k.double(), v.double(), tokens - n, None, 0.125)
+    assert float(want.min()) > 0.15
+    # u for the rounded output and u for the rounded weights, which are fractions of a row's largest, 2^6, or of more:
+    # down to 2^-14 they have fp16's relative rounding, below they are off by up to 2^-25 of 2^6 each
+    u = ref.ROUNDING[HF]
+    bound = u * want.abs() + (u + slack) * spread * (1 + 2 * u) + (tokens + 1) * 2.0 ** -31 * float(v.abs().max()) + 2.0 ** -25
+    err = (out.cpu().double().view(B, n, nq, d) - want).abs()
+    assert (err <= bound).all(), float((err / bound).max())
