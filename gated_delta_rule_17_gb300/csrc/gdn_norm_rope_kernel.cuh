@@ -405,7 +405,7 @@ gdn_head_norm_rope_bwd_kernel(const NormRopeParams p) {
     f_left = item_heads(f_item, &row, &h);
     if (p.rope.rot) {
       f_ok = position_held(pos, p.rope, p.status);
-      f_angle = (sine ? p.rope.sin : p.rope.cos) + static_cast<int64_t>(f_ok ? pos : 0) * p.rope.stride + piece;
+      f_angle = (sine ? p.rope.sin : p.rope.cos) + static_cast<int64_t>(pos) * p.rope.stride + piece;
       pos = position(f_item + stride);
     } else {
       f_ok = true;
@@ -433,7 +433,8 @@ gdn_head_norm_rope_bwd_kernel(const NormRopeParams p) {
         cp_async_16(dst + at, f_x + (real ? at : 0), real);
         cp_async_16(dst + Plan::HEADS + at, f_g + (real ? at : 0), real);
       }
-      if (lane < 2 * pieces) cp_async_16_ca(dst + 2 * Plan::HEADS + (sine ? 2 * D : 0) + 4 * piece, f_angle);
+      // (nothing of the table for a position outside it: it may have no rows; what the step then works out is dropped)
+      if (f_ok && lane < 2 * pieces) cp_async_16_ca(dst + 2 * Plan::HEADS + (sine ? 2 * D : 0) + 4 * piece, f_angle);
       f_x += Plan::HEADS;
       f_g += Plan::HEADS;
       f_left -= U * SLOTS;

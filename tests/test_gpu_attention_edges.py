@@ -47,6 +47,43 @@ def test_norm_rope_backward_of_rows_of_any_size(size, eps, dtype, rot):
     assert ((gotw - wsum).abs() <= (18 + 32) * ref.FP32 * wroom).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("held", [50, 0])
+def test_norm_rope_backward_of_positions_outside_the_table(dtype, held):
+    # reported and left out, of the weights' gradients too; a table without rows is not read
+    import ctypes
+
+    import gated_delta_rule_17_gb300 as gdn
+
+    g = gen(62)
+    x, dy = randn(g, 12, 5, 128, dtype=dtype), randn(g, 12, 5, 128, dtype=dtype)
+    cos, sin = ref.rope_tables(50, 128)
+    pos = torch.randint(0, 50, (12,), generator=g, dtype=torch.int32)
+    pos[3], pos[7] = 50, -1
+    good = [i for i in range(12) if 0 <= pos[i] < held]
+    dev = dict(x=x.cuda(), dy=dy.cuda(), cos=cos.cuda(), sin=sin.cuda(), pos=pos.cuda(), dx=torch.full_like(x, 7.0, device="cuda"),
+               dw=torch.full((128,), float("nan"), device="cuda"))
+    at = {n: t.data_ptr() for n, t in dev.items()}
+    rope = gdn.Rope(at["cos"], at["sin"], 64, held, 128, 0)
+    rc = gdn.load().gdn_head_norm_rope_backward(at["x"], None, at["pos"], ctypes.addressof(rope), None, None, 1e-6, at["dy"], None, at["dx"],
+                                                None, at["dw"], None, 12, 5, 0, 128, 2 if dtype is F32 else 0, None, None, 0, 0)
+    assert rc == gdn.GDN_OK
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.check(0)
+    assert e.value.code == gdn.GDN_ERR_DEVICE_STATUS and "position" in str(e.value)
+    bad = [i for i in range(12) if i not in good]
+    dx, dw = dev["dx"].cpu(), dev["dw"].cpu().double()
+    assert (dx[bad] == 7.0).all()
+    if not good:
+        assert (dw == 0).all()
+        return
+    xs, ys, ps = x[good].double(), dy[good].double(), pos[good].long()
+    want, wsum, _, room = ref.norm_rope_backward(xs, ys, None, cos[ps], sin[ps], 1e-6, False)
+    assert ((dx[good].double() - want).abs() <= ref.ROUNDING[dtype] * want.abs() + 64 * ref.FP32 * room).all()
+    wroom = (ref.rotate_sizes(ys, 128, False) * xs.abs() / torch.sqrt((xs ** 2).mean(-1, keepdim=True) + 1e-6)).sum((0, 1))
+    assert ((dw - wsum).abs() <= (50 + 32) * ref.FP32 * wroom).all()
+
+
 # ---- attention -----------------------------------------------------------------------------
 
 
