@@ -84,6 +84,21 @@ def test_norm_rope_backward_of_positions_outside_the_table(dtype, held):
     assert ((dw - wsum).abs() <= (50 + 32) * ref.FP32 * wroom).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, HF])
+@pytest.mark.parametrize("rows,heads,d", [(1, 1, 128), (3, 7, 64), (40, 9, 128), (999, 3, 64), (1100, 12, 128), (2500, 32, 64)])
+def test_no_row_is_lost_from_the_weight_gradients(rows, heads, d, dtype):
+    # x of +-1 has r = 1 (up to rsqrt's two units in the last place), so that dw sums whole numbers, exactly
+    g = gen(68)
+    x = (torch.randint(0, 2, (rows, heads, d), generator=g) * 2 - 1).to(dtype)
+    dy = torch.randint(1, 4, (rows, heads, d), generator=g).to(dtype) * x  # each term is 1, 2 or 3
+    _, dw = _backward(x, dy, None, None, None, None, 0.0)
+    want = (x.double() * dy.double()).sum((0, 1))
+    # Where r is not quite 1: its two units, and the roundings of sums that are no whole numbers then. At the largest case
+    # here a lane adds 8 head rows, a warp's lanes 2 more, 4 warps, 29 partials a warp of the last sum, 5 steps over these.
+    assert ((dw - want).abs() <= (4 + 60) * ref.FP32 * want).all()
+    assert float((4 + 60) * ref.FP32 * want.max()) < 1  # and no term is as small
+
+
 # ---- attention -----------------------------------------------------------------------------
 
 
@@ -119,3 +134,87 @@ def test_fp16_sums_of_many_small_weights(nq, n, peak):
     bound = u * want.abs() + (u + slack) * spread * (1 + 2 * u) + (tokens + 1) * 2.0 ** -31 * float(v.abs().max()) + 2.0 ** -25
     err = (out.cpu().double().view(B, n, nq, d) - want).abs()
     assert (err <= bound).all(), float((err / bound).max())
+
+
+def _attention_on_the_card(c, q, ks, vs, scale):
+    """Causal attention of every row in 64 bits, and its error bound (as attention_reference.attention has it)."""
+    wants, bounds, at = [], [], 0
+    nq, group = q.shape[1], q.shape[1] // c.nkv
+    for b, (a, n) in enumerate(zip(c.ctx, c.new)):
+        want = torch.zeros(n, nq, c.d, dtype=torch.float64, device="cuda")
+        bound = torch.zeros_like(want)
+        unseen = torch.arange(a + n, device="cuda") > a + torch.arange(n, device="cuda")[:, None]
+        for h in range(nq):
+            k, v, qh = (x.double().cuda() for x in (ks[b][:, h // group], vs[b][:, h // group], q[at:at + n, h]))
+            x = scale * (qh @ k.T)
+            p = torch.softmax(x.masked_fill(unseen, float("-inf")), -1)
+            want[:, h] = p @ v
+            size = abs(scale) * (c.d + 4) * (qh.abs() @ k.abs().T).masked_fill(unseen, 0).amax(-1) + 4 * x.abs().masked_fill(unseen, 0).amax(-1)
+            slack = 2 * ref.FP32 * (size[:, None] + a + n + 16)
+            bound[:, h] = ref.attention_bound(want[:, h], p @ v.abs(), slack, c.dtype, a + n, float(v.abs().max()))
+        wants.append(want)
+        bounds.append(bound)
+        at += n
+    return torch.cat(wants), torch.cat(bounds)
+
+
+# Chunks of a prompt with more row tiles of a kv head than there are groups of CTAs (8): a group then has several.
+CHUNKS = [
+    dict(ctx=[0], new=[700], nq=8, nkv=2, d=128, page=64, dtype=BF),  # 11 row tiles of 256, whole units
+    dict(ctx=[3000, 10, 500], new=[560, 3, 1030], nq=4, nkv=1, d=128, page=16, dtype=BF),  # 9, 1 and 17, cut
+    dict(ctx=[900], new=[2100], nq=2, nkv=1, d=64, page=24, dtype=HF),
+]
+
+
+@pytest.mark.parametrize("case", CHUNKS, ids=[str(i) for i in range(len(CHUNKS))])
+@pytest.mark.parametrize("hint", ["exact", "too low"])
+def test_many_row_tiles(case, hint):
+    # max_rows below a sequence's rows: the kernel for few rows then has them in tiles of 16
+    import gated_delta_rule_17_gb300 as gdn
+
+    case = dict(case)
+    nq = case.pop("nq")
+    c = Cache(65, fill=float("nan"), **case)
+    ks, vs = c.fill_tokens()
+    q = (1.5 * randn(c.g, c.rows, nq, c.d, dtype=F32)).to(c.dtype)
+    out = torch.full((c.rows, nq * c.d), float("nan"), dtype=c.dtype, device="cuda")
+    gdn.tree_attention(q.cuda(), *c.plan(), out, nq=nq, nkv=c.nkv, head_dim=c.d, cu_rows=c.cu.cuda(),
+                       max_rows=max(c.new) if hint == "exact" else 1)
+    gdn.check()
+    want, bound = _attention_on_the_card(c, q, ks, vs, c.d ** -0.5)
+    err = (out.double().view_as(want) - want).abs()
+    assert (err <= bound).all(), float((err / bound).max())
+
+
+@pytest.mark.parametrize("page,d", [(8, 128), (24, 128), (40, 64), (48, 64)])
+def test_pages_of_small_boxes_on_the_tensor_cores(page, d):
+    # copies of 8 and 16 tokens inside the pages
+    import gated_delta_rule_17_gb300 as gdn
+
+    c = Cache(66, [500, 3, 129], [20, 33, 8], 2, d, page, BF, fill=float("nan"))
+    ks, vs = c.fill_tokens()
+    q = (1.5 * randn(c.g, c.rows, 8, d, dtype=F32)).to(BF)
+    out = torch.empty(c.rows, 8 * d, dtype=BF, device="cuda")
+    gdn.tree_attention(q.cuda(), *c.plan(), out, nq=8, nkv=2, head_dim=d, cu_rows=c.cu.cuda(), max_rows=33)
+    gdn.check()
+    _check_attention(c, q, out.cpu(), ks, vs, None, d ** -0.5)
+
+
+@pytest.mark.parametrize("page", [8, 64])
+@pytest.mark.parametrize("number", [-1, 10 ** 6])
+def test_a_bad_page_on_the_tensor_cores(page, number):
+    # its tokens have keys and values of zeros, and the status says so
+    import gated_delta_rule_17_gb300 as gdn
+
+    c = Cache(67, [300, 70], [20, 25], 2, 128, page, BF, fill=float("nan"))
+    ks, vs = c.fill_tokens()
+    q = randn(c.g, c.rows, 8, 128)
+    kc, vc, table, lens = c.plan()
+    table[0, 1] = number
+    out = torch.empty(c.rows, 8 * 128, dtype=BF, device="cuda")
+    gdn.tree_attention(q.cuda(), kc, vc, table, lens, out, nq=8, nkv=2, cu_rows=c.cu.cuda(), max_rows=25)
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.check()
+    assert e.value.code == gdn.GDN_ERR_DEVICE_STATUS and "page" in str(e.value)
+    there = ((torch.arange(320) // page) != 1)[:, None, None]
+    _check_attention(c, q, out.cpu(), [ks[0] * there, ks[1]], [vs[0] * there, vs[1]], None, 128 ** -0.5)
