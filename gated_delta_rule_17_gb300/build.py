@@ -1,7 +1,7 @@
 """Builds the CUDA library in-tree: ``_lib/libgdn_gb300.so`` for sm_103a.
 
 One translation unit (``csrc/gdn_api.cu``, which includes the kernels), so a
-build takes a few seconds on either the x86 build host or the Arm GPU host.
+build takes 20 to 30 seconds on either the x86 build host or the Arm GPU host.
 """
 from __future__ import annotations
 

@@ -7,8 +7,8 @@
 // cp.async from the tokens' places in the pages, any page size), and has 16 query rows against
 // them with register tensor products: scores S = Q K^T, running maximum and sum, O += P V.
 // No barrier is needed in the loop; the warps' (m, l, O) are added up at a unit's end.
-// One token each of 64 sequences of 100 to 16000 tokens, 32 heads on 8 kv heads of 128: 332 to
-// 338 us with the join, 6.2 to 6.4 TB/s, 92 to 94% of the measured copy rate; the loads' latency at the units' ends and the
+// One token each of 64 sequences of 100 to 16000 tokens, 32 heads on 8 kv heads of 128: 326 to
+// 335 us with the join, 6.3 to 6.5 TB/s, 93 to 95% of the measured copy rate; the loads' latency at the units' ends and the
 // join are the rest.
 #pragma once
 #include "gdn_attn_common.cuh"

@@ -27,8 +27,9 @@
 // What bounds it: with many rows the chain of a stream from one tile's scores to the next's, about 3000
 // cycles (softmax 1500, the products of both kinds 1024 one after the other because P lies over S,
 // hand-offs the rest), of which two streams fill the tensor pipe to 59%, and the start, the pieces of cut
-// units and the join. Trees of 64 in 8 sequences of 32768, 32 heads on 4: 198 to 216 us, 1.26 to 1.37
-// PFLOP/s, 64 to 70% of the measured cuBLAS rate (173 us for each 32768 tokens more, 81%). With few
+// units and the join. Trees of 64 in 8 sequences of 32768, 32 heads on 4: 215 to 222 us, 1.22 to 1.26
+// PFLOP/s, 62 to 65% of the measured cuBLAS rate, the clock held down by the power limit; 196 to 202 us in loops too
+// short for that (173 us for each 32768 tokens more, 81%). With few
 // rows HBM and the ends: trees of 3 to 16 in 16 sequences of 500 to 8192, 32 heads on 8: 58 us, 5.1
 // TB/s. Tensor memory is full (S and O of two streams), so a third stream, or P beside S, has no room;
 // one pass over the scores instead of two, the row in registers, two warps a row, handing P over in

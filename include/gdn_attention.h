@@ -128,8 +128,8 @@ int gdn_paged_append(const void* k, const void* v, const gdn_paged_t* cache, con
  *   workspace: gdn_tree_attention_workspace_bytes() bytes, 256-byte aligned, or NULL
  *              to allocate it stream-ordered. Calls that overlap need one each.
  * d is 64 or 128. Products take 16-bit operands (the softmax's weights are
- * rounded to dtype for the second product), scores, statistics and sums are
- * fp32. The keys and values of every token below ctx_lens[b] + (rows of b) must
+ * rounded to dtype for the second product; fp16 weights below 2^-31 of a row's
+ * largest count as zero there), scores, statistics and sums are fp32. The keys and values of every token below ctx_lens[b] + (rows of b) must
  * be finite, seen or not; what lies past them, in a page or outside, is not
  * used. The same inputs give the same bits. At most two launches. */
 size_t gdn_tree_attention_workspace_bytes(int nq, int nkv, int d);
