@@ -1,8 +1,9 @@
-"""GB300-native chunked gated-delta-rule (GDN) prefill forward, and the softmax-attention
-operators that stand next to it in a hybrid model.
+"""GB300-native chunked gated-delta-rule (GDN) prefill forward, the operators around and
+beside it in a linear-attention layer, and the softmax-attention operators that stand next
+to it in a hybrid model.
 
-A thin ctypes binding over the C ABI in ``include/gdn_prefill.h`` and
-``include/gdn_attention.h``; every step
+A thin ctypes binding over the C ABI in ``include/gdn_prefill.h``,
+``include/gdn_recurrent.h`` and ``include/gdn_attention.h``; every step
 of the computation runs in the library's CUDA kernels. PyTorch only supplies
 device memory and the current stream. There is no fallback: if the compiled
 library is missing, importing works but every call raises ``GdnError``.
@@ -18,6 +19,9 @@ __all__ = ["prefill", "prefill_noalloc", "prefill_host", "host_scratch_bytes", "
            "backward", "backward_workspace_bytes",
            "head_norm_rope", "head_norm_rope_backward", "head_norm_rope_backward_workspace_bytes", "paged_append",
            "tree_attention", "tree_attention_workspace_bytes",
+           "causal_conv", "causal_conv_backward", "causal_conv_backward_workspace_bytes", "ssm_scan",
+           "ssm_scan_workspace_bytes", "ssm_decode", "layer_norm", "layer_norm_backward",
+           "layer_norm_backward_workspace_bytes",
            "set_timing_events", "set_test_hooks", "decode", "lib_path", "load", "GdnError",
            "Strides", "Rope", "NormStrides", "Paged", "GDN_OK", "GDN_ERR_ARG", "GDN_ERR_UNSUPPORTED", "GDN_ERR_CUDA",
            "GDN_ERR_DEVICE_STATUS", "GDN_ERR_TIMEOUT", "GDN_ERR_RANGE"]
@@ -117,6 +121,25 @@ def load():
             lib.gdn_tree_attention_workspace_bytes.restype = sz
             lib.gdn_tree_attention.argtypes = [vp, paged, vp, i, f32, vp, i, i, i, i, i64, i64, i, vp, sz, vp]
             lib.gdn_tree_attention.restype = i
+            lib.gdn_causal_conv.argtypes = [vp] * 5 + [i] * 7 + [i64, i64, vp, vp]
+            lib.gdn_causal_conv.restype = i
+            lib.gdn_causal_conv_backward_workspace_bytes.argtypes = [i] * 3
+            lib.gdn_causal_conv_backward_workspace_bytes.restype = sz
+            lib.gdn_causal_conv_backward.argtypes = [vp] * 10 + [i] * 6 + [i64] * 3 + [vp, vp, sz, vp]
+            lib.gdn_causal_conv_backward.restype = i
+            ssm = vp  # the options, by address
+            lib.gdn_ssm_scan_workspace_bytes.argtypes = [i] * 6
+            lib.gdn_ssm_scan_workspace_bytes.restype = sz
+            lib.gdn_ssm_scan.argtypes = [vp] * 9 + [i] * 6 + [ssm, vp, vp, sz, vp]
+            lib.gdn_ssm_scan.restype = i
+            lib.gdn_ssm_decode.argtypes = [vp] * 9 + [i] * 5 + [ssm, vp]
+            lib.gdn_ssm_decode.restype = i
+            lib.gdn_layer_norm.argtypes = [vp] * 4 + [f32, vp] + [i] * 6 + [norm_st, vp]
+            lib.gdn_layer_norm.restype = i
+            lib.gdn_layer_norm_backward_workspace_bytes.argtypes = [i] * 3
+            lib.gdn_layer_norm_backward_workspace_bytes.restype = sz
+            lib.gdn_layer_norm_backward.argtypes = [vp] * 4 + [f32] + [vp] * 5 + [i] * 6 + [norm_st, vp, sz, vp]
+            lib.gdn_layer_norm_backward.restype = i
             lib.gdn_set_timing_events.argtypes = [vp, vp, vp]
             lib.gdn_set_timing_events.restype = None
             lib.gdn_set_test_hooks.argtypes = [i64, i64, i]
@@ -393,6 +416,8 @@ _cards = 0      # devices of this process
 _ROPE = struct.Struct("@QQqiii4x").pack
 _STRIDES = struct.Struct("@6q").pack
 _PAGED = struct.Struct("@QQqqqqqqiiQqiii4xQQ").pack
+_SSM = struct.Struct("@5q3i4x").pack
+_LAYER_NORM = struct.Struct("@5q").pack
 
 
 def _setup():
@@ -438,6 +463,8 @@ def _act(t, name, dtype, rows, inner):
     stride = _row_stride(t, name, inner)
     if t.shape[0] != rows:
         raise GdnError(GDN_ERR_ARG, f"{name} has {t.shape[0]} rows, need {rows}")
+    if stride < inner:  # rows over one another, as expand() gives; 0 means packed rows to the library
+        raise GdnError(GDN_ERR_ARG, f"{name}: a row stride of {stride} elements is below the {inner} of a row")
     if t.numel() != rows * inner:  # [B, T, ...] in place of [B * T, ...], or heads that no one would touch
         raise GdnError(GDN_ERR_ARG, f"{name}: rows hold {t.numel() // rows} elements, need just {inner}")
     return t.data_ptr(), stride
@@ -635,6 +662,216 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_lens, out, *, nq: int, 
     ws, size = _scratch(workspace)
     rc = _lib.gdn_tree_attention(qp, cache, mp, words, max(head_dim, 1) ** -0.5 if scale is None else scale, op, nq, nkv, head_dim,
                                  code, qs, os_, max_rows or 0, ws, size, _stream_of(stream, q))
+    if rc != GDN_OK:
+        _raise(rc)
+
+
+# ---- the operators around and beside the recurrence (include/gdn_recurrent.h) -------------
+
+def _batch(rows, B, T, cu_seqlens):
+    """B, the library's T and the address of cu_seqlens, for `rows` packed or B * T dense rows."""
+    if cu_seqlens is not None:
+        if B is not None or T is not None:
+            raise GdnError(GDN_ERR_ARG, "B and T go with dense batches, cu_seqlens with packed ones")
+        n = cu_seqlens.numel()
+        if n < 1:
+            raise GdnError(GDN_ERR_ARG, "cu_seqlens needs one element at least")
+        return n - 1, rows, _vector(cu_seqlens, "cu_seqlens", _torch.int32, n)
+    if B is None or T is None:
+        raise GdnError(GDN_ERR_ARG, "dense batches need B and T")
+    if B < 0 or T < 0 or B * T != rows:
+        raise GdnError(GDN_ERR_ARG, f"{rows} rows are not B = {B} sequences of T = {T}")
+    return B, T, None
+
+
+def _kept(t, name, dtype, shape, table=False):
+    """The address of a contiguous CUDA tensor of that shape, or (table) of an int64 table of addresses; None for None."""
+    if t is None:
+        return None
+    if table:
+        return _vector(t, f"a {name} table", _torch.int64, shape[0])
+    n = 1
+    for d in shape:
+        n *= d
+    if t.dtype is not dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
+        raise GdnError(GDN_ERR_ARG, f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)}")
+    return t.data_ptr()
+
+
+def _conv_args(x, weight, bias):
+    code, rows = _act_code(x, "x", 2), x.shape[0]
+    if len(weight.shape) != 2:
+        raise GdnError(GDN_ERR_ARG, "weight must be [channels, width]")
+    D, width = weight.shape
+    xp, xs = _act(x, "x", x.dtype, rows, D)
+    return code, rows, D, width, xp, xs, _vector(weight, "weight", _torch.float32, D * width), _vector(bias, "bias", _torch.float32, D)
+
+
+def causal_conv(x, weight, out, *, bias=None, state=None, B: int | None = None, T: int | None = None, cu_seqlens=None,
+                state_is_table: bool = False, silu: bool = True, stream=None) -> None:
+    """The short causal convolution of every channel (``gdn_causal_conv``), with its silu: the stage before the
+    recurrence, whose q, k and v are slices of its output rows.
+
+    x, out: [rows, D] bf16, fp16 or fp32, out of x's type and not overlapping it; ``weight``: fp32 [D, width], width 2 to
+    4; ``bias``: fp32 [D]. Batches as for ``prefill``: dense (``B``, ``T``) or packed (``cu_seqlens``). ``state``: the
+    width - 1 inputs before each sequence, [B, width - 1, D] of x's type, updated in place (None: zeros, nothing kept), or
+    (``state_is_table``) an int64 CUDA tensor of B addresses. A decode step is a batch with T = 1."""
+    torch = _torch or _setup()
+    if _cards > 1:
+        _one_card(x=x, weight=weight, out=out, bias=bias, state=state, cu_seqlens=cu_seqlens)
+    code, rows, D, width, xp, xs, wp, bp = _conv_args(x, weight, bias)
+    op, os_ = _act(out, "out", x.dtype, rows, D)
+    B, T, cu = _batch(rows, B, T, cu_seqlens)
+    sp = _kept(state, "state", x.dtype, (B, width - 1, D), state_is_table)
+    rc = _lib.gdn_causal_conv(xp, wp, bp, sp, op, B, T, D, width, 1 if silu else 0, code, 1 if state_is_table else 0, xs, os_,
+                              cu, _stream_of(stream, x))
+    if rc != GDN_OK:
+        _raise(rc)
+
+
+def causal_conv_backward_workspace_bytes(rows, D, width) -> int:
+    return int(load().gdn_causal_conv_backward_workspace_bytes(rows, D, width))
+
+
+def causal_conv_backward(x, weight, dout, dx, dweight=None, dbias=None, *, bias=None, h0=None, dST=None, dh0=None,
+                         B: int | None = None, T: int | None = None, cu_seqlens=None, silu: bool = True, workspace=None,
+                         stream=None) -> None:
+    """The backward of ``causal_conv`` (``gdn_causal_conv_backward``). x, weight, bias and the batch as given to the
+    forward, ``h0`` the state that it started from; ``dout``: dL/dout, ``dST``: dL/d(state after the call). Outputs ``dx``
+    of x's type (not overlapping x or dout) and, where given, ``dweight`` fp32 [D, width], ``dbias`` fp32 [D] and ``dh0``
+    like h0; all overwritten."""
+    torch = _torch or _setup()
+    if _cards > 1:
+        _one_card(x=x, weight=weight, dout=dout, dx=dx, dweight=dweight, dbias=dbias, bias=bias, h0=h0, dST=dST, dh0=dh0,
+                  cu_seqlens=cu_seqlens, workspace=workspace)
+    code, rows, D, width, xp, xs, wp, bp = _conv_args(x, weight, bias)
+    gp, gs = _act(dout, "dout", x.dtype, rows, D)
+    dp, ds = _act(dx, "dx", x.dtype, rows, D)
+    B, T, cu = _batch(rows, B, T, cu_seqlens)
+    hp, tp, fp = (_kept(t, name, x.dtype, (B, width - 1, D)) for t, name in ((h0, "h0"), (dST, "dST"), (dh0, "dh0")))
+    ws, size = _scratch(workspace)
+    rc = _lib.gdn_causal_conv_backward(xp, wp, bp, hp, gp, tp, dp, _vector(dweight, "dweight", torch.float32, D * width),
+                                       _vector(dbias, "dbias", torch.float32, D), fp, B, T, D, width, 1 if silu else 0, code,
+                                       xs, gs, ds, cu, ws, size, _stream_of(stream, x))
+    if rc != GDN_OK:
+        _raise(rc)
+
+
+def _ssm_args(q, k, v, dt, a, out, rows, nk, nv, dk, dv, dt_bias, skip, state_is_table, softplus):
+    """The addresses in the ABI's order, up to skip, then out's and the packed options."""
+    bf16, f32 = _torch.bfloat16, _torch.float32
+    qp, qs = _act(q, "q", bf16, rows, nk * dk)
+    kp, ks = _act(k, "k", bf16, rows, nk * dk)
+    vp, vs = _act(v, "v", bf16, rows, nv * dv)
+    op, os_ = _act(out, "out", bf16, rows, nv * dv)
+    if dt.dtype is not f32 and dt.dtype is not bf16:
+        raise GdnError(GDN_ERR_ARG, f"dt must be float32 or bfloat16, got {dt.dtype}")
+    tp, ts = _act(dt, "dt", dt.dtype, rows, nv)
+    head = [qp, kp, vp, tp, _vector(a, "a", f32, nv), _vector(dt_bias, "dt_bias", f32, nv), _vector(skip, "skip", f32, nv)]
+    return head, op, _SSM(qs, ks, vs, ts, os_, 1 if state_is_table else 0, 1 if dt.dtype is bf16 else 0, 1 if softplus else 0)
+
+
+def ssm_scan_workspace_bytes(B, T, nv, varlen, dk=128, dv=128) -> int:
+    return int(load().gdn_ssm_scan_workspace_bytes(B, T, nv, dk, dv, 1 if varlen else 0))
+
+
+def ssm_scan(q, k, v, dt, a, state, out, *, nk: int, nv: int, dk: int = 128, dv: int = 128, dt_bias=None,
+             softplus: bool = True, skip=None, B: int | None = None, T: int | None = None, cu_seqlens=None,
+             state_is_table: bool = False, workspace=None, stream=None) -> None:
+    """The selective state space scan (``gdn_ssm_scan``): the recurrence with a scalar decay per head and no erase,
+
+        d = softplus(dt + dt_bias);  S <- e^(d a) S + k (d v)^T;  o = S^T q + skip v
+
+    q, k: bf16 [rows, nk*dk] (C and B in state space terms); v, out: bf16 [rows, nv*dv]; dt: fp32 or bf16 [rows, nv];
+    ``a`` (<= 0), ``dt_bias``, ``skip``: fp32 [nv], the last two or None. ``softplus=False`` takes dt + dt_bias as it is.
+    ``state``, batches, ``state_is_table`` and ``workspace`` (``ssm_scan_workspace_bytes``) as for ``prefill``. dk and dv are 64 or 128."""
+    torch = _torch or _setup()
+    if _cards > 1:
+        _one_card(q=q, k=k, v=v, dt=dt, a=a, state=state, out=out, dt_bias=dt_bias, skip=skip, cu_seqlens=cu_seqlens, workspace=workspace)
+    rows = q.shape[0]
+    head, op, opt = _ssm_args(q, k, v, dt, a, out, rows, nk, nv, dk, dv, dt_bias, skip, state_is_table, softplus)
+    B, T, cu = _batch(rows, B, T, cu_seqlens)
+    ws, size = _scratch(workspace)
+    rc = _lib.gdn_ssm_scan(*head, _kept(state, "state", torch.float32, (B, nv, dk, dv), state_is_table), op, B, T, nk, nv, dk, dv,
+                           opt, cu, ws, size, _stream_of(stream, q))
+    if rc != GDN_OK:
+        _raise(rc)
+
+
+def ssm_decode(q, k, v, dt, a, state, out, *, nk: int, nv: int, dk: int = 128, dv: int = 128, dt_bias=None,
+               softplus: bool = True, skip=None, state_is_table: bool = False, stream=None) -> None:
+    """One token of ``ssm_scan`` for every row (sequence) b: ``state[b]`` (or the b-th address of a table) is advanced by
+    it and its output written to ``out[b]`` (``gdn_ssm_decode``)."""
+    torch = _torch or _setup()
+    if _cards > 1:
+        _one_card(q=q, k=k, v=v, dt=dt, a=a, state=state, out=out, dt_bias=dt_bias, skip=skip)
+    rows = q.shape[0]
+    head, op, opt = _ssm_args(q, k, v, dt, a, out, rows, nk, nv, dk, dv, dt_bias, skip, state_is_table, softplus)
+    rc = _lib.gdn_ssm_decode(*head, _kept(state, "state", torch.float32, (rows, nv, dk, dv), state_is_table), op, rows, nk, nv,
+                             dk, dv, opt, _stream_of(stream, q))
+    if rc != GDN_OK:
+        _raise(rc)
+
+
+def _grouped(x, dim):
+    """Rows and groups of x: [rows, groups * dim] (or [rows, groups, dim])."""
+    if dim < 1 or x.dim() < 2:
+        raise GdnError(GDN_ERR_ARG, f"x must be [rows, groups * dim] with dim = {dim} positive")
+    inner = 1
+    for d in x.shape[1:]:
+        inner *= d
+    if inner == 0 or inner % dim:
+        raise GdnError(GDN_ERR_ARG, f"x: rows hold {inner} elements, not groups of {dim}")
+    return x.shape[0], inner // dim
+
+
+def layer_norm(x, out, *, dim: int, weight=None, bias=None, gate=None, gate_first: bool = False, rms: bool = False,
+               eps: float = 1e-5, stream=None) -> None:
+    """Layer norm (or RMS norm, ``rms``) of every group of ``dim`` values in the rows of x (``gdn_layer_norm``), the stage
+    after the recurrence: out = h * weight + bias, times silu(gate) where there is a ``gate``, or with ``gate_first`` the
+    norm of x silu(gate).
+
+    x, out, gate: [rows, groups*dim] (or [rows, groups, dim]) bf16, fp16 or fp32, all alike; out may be x or gate itself.
+    ``weight``, ``bias``: fp32 [dim], shared by the groups (None: ones, zeros). dim is a multiple of 8 up to 8192."""
+    torch = _torch or _setup()
+    if _cards > 1:
+        _one_card(x=x, out=out, weight=weight, bias=bias, gate=gate)
+    code, (rows, groups), dt, f32 = _act_code(x, "x", 2), _grouped(x, dim), x.dtype, torch.float32
+    w = groups * dim
+    xp, xs = _act(x, "x", dt, rows, w)
+    op, os_ = _act(out, "out", dt, rows, w)
+    zp, zs = _act(gate, "gate", dt, rows, w) if gate is not None else _NONE
+    rc = _lib.gdn_layer_norm(xp, zp, _vector(weight, "weight", f32, dim), _vector(bias, "bias", f32, dim), eps, op, rows, groups,
+                             dim, code, 1 if rms else 0, 1 if gate_first else 0, _LAYER_NORM(xs, zs, os_, 0, 0),
+                             _stream_of(stream, x))
+    if rc != GDN_OK:
+        _raise(rc)
+
+
+def layer_norm_backward_workspace_bytes(rows, groups, dim) -> int:
+    return int(load().gdn_layer_norm_backward_workspace_bytes(rows, groups, dim))
+
+
+def layer_norm_backward(x, dout, dx, dweight=None, dbias=None, *, dim: int, weight=None, bias=None, gate=None, dgate=None,
+                        gate_first: bool = False, rms: bool = False, eps: float = 1e-5, workspace=None, stream=None) -> None:
+    """The backward of ``layer_norm`` (``gdn_layer_norm_backward``). x, weight, bias, gate and the rest as given to the
+    forward; ``dout``: dL/dout. Outputs ``dx`` (may be x or dout itself), ``dgate`` (wherever there is a gate; may be gate)
+    and, where given, ``dweight``, ``dbias``: fp32 [dim], overwritten with the sums over rows and groups."""
+    torch = _torch or _setup()
+    if _cards > 1:
+        _one_card(x=x, dout=dout, dx=dx, dweight=dweight, dbias=dbias, weight=weight, bias=bias, gate=gate, dgate=dgate, workspace=workspace)
+    code, (rows, groups), dt, f32 = _act_code(x, "x", 2), _grouped(x, dim), x.dtype, torch.float32
+    w = groups * dim
+    xp, xs = _act(x, "x", dt, rows, w)
+    gp, gs = _act(dout, "dout", dt, rows, w)
+    dp, ds = _act(dx, "dx", dt, rows, w)
+    zp, zs = _act(gate, "gate", dt, rows, w) if gate is not None else _NONE
+    ep, es = _act(dgate, "dgate", dt, rows, w) if dgate is not None else _NONE
+    ws, size = _scratch(workspace)
+    rc = _lib.gdn_layer_norm_backward(xp, zp, _vector(weight, "weight", f32, dim), _vector(bias, "bias", f32, dim), eps, gp, dp, ep,
+                                      _vector(dweight, "dweight", f32, dim), _vector(dbias, "dbias", f32, dim), rows, groups, dim,
+                                      code, 1 if rms else 0, 1 if gate_first else 0, _LAYER_NORM(xs, zs, ds, gs, es), ws, size,
+                                      _stream_of(stream, x))
     if rc != GDN_OK:
         _raise(rc)
 

@@ -1,26 +1,23 @@
 """Builds the CUDA library in-tree: ``_lib/libgdn_gb300.so`` for sm_103a.
 
-One translation unit (``csrc/gdn_api.cu``, which includes the kernels), so a
-build takes 20 to 30 seconds on either the x86 build host or the Arm GPU host.
+Two translation units (``csrc/gdn_api.cu`` and ``csrc/gdn_recurrent.cu``, which include the
+kernels), compiled side by side, so a build takes about half a minute on either the x86 build
+host or the Arm GPU host.
 """
 from __future__ import annotations
 
+import glob
 import os
 import shutil
 import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-SRC = os.path.join(HERE, "csrc", "gdn_api.cu")
-DEPS = [os.path.join(HERE, "csrc", f) for f in ("gdn_api.cu", "gdn_common.cuh", "gdn_prefill_kernel.cuh", "gdn_decode_kernel.cuh",
-                                                           "gdn_wy_kernel.cuh", "gdn_bwd_common.cuh", "gdn_bwd_dstates_tc.cuh", "gdn_bwd_grads_tc.cuh",
-                                                           "tc.cuh", "gdn_norm_rope_kernel.cuh", "gdn_attn_common.cuh",
-                                                           "gdn_attn_kernel.cuh", "gdn_attn_tc_kernel.cuh", "gdn_attn_api.cuh")] + [
-    os.path.join(os.path.dirname(HERE), "include", f) for f in ("gdn_prefill.h", "gdn_attention.h")]
+INCLUDE = os.path.join(os.path.dirname(HERE), "include")
+UNITS = ("gdn_api", "gdn_recurrent")
 OUT_DIR = os.path.join(HERE, "_lib")
 OUT = os.path.join(OUT_DIR, "libgdn_gb300.so")
 
-NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared", "-I", os.path.join(os.path.dirname(HERE), "include")]
+NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 
 
 def nvcc() -> str:
@@ -30,17 +27,32 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def sources():
+    return [f for pattern in ("csrc/*.cu", "csrc/*.cuh", "csrc/*.h") for f in glob.glob(os.path.join(HERE, pattern))] + \
+        glob.glob(os.path.join(INCLUDE, "*.h"))
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     if not force and os.path.exists(OUT):
-        newest = max(os.path.getmtime(d) for d in DEPS)
+        newest = max(os.path.getmtime(d) for d in sources())
         if os.path.getmtime(OUT) >= newest:
             return OUT
     tmp = OUT + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, "-o", tmp, SRC]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
+    extra = ["-Xptxas=-v"] if verbose else []
+    objects = [f"{tmp}.{u}.o" for u in UNITS]
+    jobs = [subprocess.Popen([nvcc(), *extra, *NVCC_FLAGS, "-c", "-o", o, os.path.join(HERE, "csrc", u + ".cu")])
+            for u, o in zip(UNITS, objects)]
+    codes = [j.wait() for j in jobs]
+    try:
+        for job, code in zip(jobs, codes):
+            if code:
+                raise subprocess.CalledProcessError(code, job.args)
+        subprocess.run([nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *objects], check=True)
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, OUT)
     return OUT
 

@@ -20,6 +20,7 @@
 
 #include "gdn_attention.h"
 #include "gdn_prefill.h"
+#include "gdn_host.h"
 #include "gdn_prefill_kernel.cuh"
 #include "gdn_wy_kernel.cuh"
 #include "gdn_decode_kernel.cuh"
@@ -1174,3 +1175,22 @@ void gdn_set_timing_events(void* before_wy, void* before_spine, void* after_spin
 }  // extern "C"
 
 #include "gdn_attn_api.cuh"
+
+// ---- for the other translation units -------------------------------------------------
+namespace gdn_host {
+void begin() {
+  g_err[0] = 0;
+  g_launches = 0;
+}
+int refuse(int code, const char* message) { return fail(code, "%s", message); }
+void count(int launches) { g_launches = launches; }
+int device(int* sms, unsigned** status) {
+  DeviceInfo* d = nullptr;
+  if (int rc = device_info(&d)) return rc;
+  *sms = d->sms;
+  *status = d->status;
+  return GDN_OK;
+}
+int plan_sms() { return ::plan_sms(); }
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() { return ::encode_fn(); }
+}  // namespace gdn_host

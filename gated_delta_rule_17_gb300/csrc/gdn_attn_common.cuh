@@ -282,18 +282,6 @@ struct AttnWalk {
 };
 
 // ---- 16-bit element types ---------------------------------------------------------------
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&x);
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-  return pack_half2(a, b);
-}
-
 // The weights 2^(x - m) are rounded to the cache's type for the second product, the only form in which the
 // tensor cores take them beside 16-bit values; l sums them in fp32 before. That costs up to 2^-8 (bf16) or
 // 2^-11 (fp16) of a weight: against 64 bits the output of 64 drafted rows over 32768 is off by 2.3e-3 of its

@@ -21,7 +21,7 @@
 // rate), backward 173 us (5.9 TB/s, 87%); the append of 8 prompts of 100 to 16000 tokens,
 // 8 kv heads: 92 us (6.6 TB/s, 97%).
 #pragma once
-#include "gdn_common.cuh"
+#include "gdn_row_common.cuh"
 
 namespace gdn {
 
@@ -38,50 +38,6 @@ constexpr int kAppendCtasPerSm = 9;
 constexpr int kNormUnroll = 4;
 constexpr int kNormBwdThreads = 128;
 constexpr int kNormBwdCtasPerSm = 6;
-
-// ---- four consecutive values of a row -----------------------------------------------
-__device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&f)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  f[0] = __uint_as_float(v.x << 16);
-  f[1] = __uint_as_float(v.x & 0xFFFF0000u);
-  f[2] = __uint_as_float(v.y << 16);
-  f[3] = __uint_as_float(v.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void load4(const __half* p, float (&f)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-  f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
-}
-__device__ __forceinline__ void store4(float* p, const float (&f)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&f)[4]) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
-  *reinterpret_cast<uint2*>(p) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-__device__ __forceinline__ void store4(__half* p, const float (&f)[4]) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]));
-}
-
-// Four values as they lie in memory (held packed while their load is under way).
-template <typename T>
-struct Four {
-  using Word = uint2;
-};
-template <>
-struct Four<float> {
-  using Word = uint4;
-};
-template <typename T>
-__device__ __forceinline__ void unpack4(const typename Four<T>::Word& w, float (&f)[4]) {
-  load4(reinterpret_cast<const T*>(&w), f);
-}
 
 struct RopeParams {
   const float* cos;
@@ -319,29 +275,6 @@ struct NormBwdPlan {
   static constexpr int BYTES = WARPS * STAGES * STEP;
 };
 
-// Two fp32 values in one register pair, and the paired arithmetic of sm_100 and up.
-using Pair = uint64_t;
-__device__ __forceinline__ Pair pair_of(float a, float b) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void parts_of(Pair p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-  Pair r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ void to_pairs2(const float (&x)[4], Pair (&p)[2]) {
   p[0] = pair_of(x[0], x[1]);
   p[1] = pair_of(x[2], x[3]);

@@ -1,0 +1,492 @@
+// Host side of the entry points in include/gdn_recurrent.h: argument checks (each rejection names the
+// guard) and launches. A translation unit of its own, compiled beside gdn_api.cu.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdarg>
+#include <cstdio>
+#include <type_traits>
+
+#include "gdn_recurrent.h"
+#include "gdn_host.h"
+#include "gdn_conv_kernel.cuh"
+#include "gdn_layer_norm_kernel.cuh"
+#include "gdn_ssm_scan_kernel.cuh"
+
+namespace {
+
+int fail(int code, const char* fmt, ...) {
+  char text[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(text, sizeof text, fmt, ap);
+  va_end(ap);
+  return gdn_host::refuse(code, text);
+}
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int launched(int launches) {
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+  gdn_host::count(launches);
+  return GDN_OK;
+}
+
+template <int N>
+using IntC = std::integral_constant<int, N>;
+
+template <typename F>
+void by_type(int dtype, F&& f) {
+  if (dtype == GDN_F32) f(float{});
+  else if (dtype == GDN_F16) f(__half{});
+  else f(__nv_bfloat16{});
+}
+
+int check_type(int dtype) {
+  if (dtype != GDN_BF16 && dtype != GDN_F16 && dtype != GDN_F32) return fail(GDN_ERR_UNSUPPORTED, "dtype %d is unknown", dtype);
+  return GDN_OK;
+}
+
+// A row stride (0: packed) that holds `least` elements and keeps rows on 16 bytes.
+int take_stride(int64_t given, int64_t least, const char* name, int64_t* out) {
+  *out = given ? given : least;
+  if (*out < least || *out % 8)
+    return fail(GDN_ERR_ARG, "%s row stride %lld must be >= %lld and a multiple of 8", name, (long long)*out, (long long)least);
+  return GDN_OK;
+}
+
+int check_flag(int value, const char* name) {
+  if (value != 0 && value != 1) return fail(GDN_ERR_ARG, "%s must be 0 or 1", name);
+  return GDN_OK;
+}
+
+int check_batch(int B, int T, const int32_t* cu, gdn::Rows* out) {
+  if (B < 0 || T < 0) return fail(GDN_ERR_ARG, "B = %d or T = %d is negative", B, T);
+  const int64_t rows = cu ? T : static_cast<int64_t>(B) * T;
+  if (rows > INT32_MAX - 65536) return fail(GDN_ERR_UNSUPPORTED, "%lld rows exceed the 2^31 row range", (long long)rows);
+  *out = gdn::Rows{cu, B, T, static_cast<int>(rows)};
+  return GDN_OK;
+}
+
+int check_workspace(const void* ws, size_t given, size_t need) {
+  if (!ws) return GDN_OK;
+  if (given < need) return fail(GDN_ERR_ARG, "workspace of %zu bytes is smaller than the %zu required", given, need);
+  if (!aligned(ws, 256)) return fail(GDN_ERR_ARG, "workspace must be 256-byte aligned");
+  return GDN_OK;
+}
+
+// The caller's workspace, or one from the stream's pool that release() gives back.
+int acquire(void* given, size_t need, cudaStream_t s, void** ws) {
+  *ws = given;
+  if (given || !need) return GDN_OK;
+  cudaError_t e = cudaMallocAsync(ws, need, s);
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaMallocAsync(%zu): %s", need, cudaGetErrorString(e));
+  return GDN_OK;
+}
+int release(void* given, void* ws, cudaStream_t s, int rc) {
+  if (given || !ws) return rc;
+  cudaError_t e = cudaFreeAsync(ws, s);
+  if (e != cudaSuccess && rc == GDN_OK) rc = fail(GDN_ERR_CUDA, "cudaFreeAsync: %s", cudaGetErrorString(e));
+  return rc;
+}
+
+int zero(float* p, int64_t n, cudaStream_t s) {
+  if (!p) return GDN_OK;
+  cudaError_t e = cudaMemsetAsync(p, 0, static_cast<size_t>(n) * sizeof(float), s);
+  return e == cudaSuccess ? GDN_OK : fail(GDN_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(e));
+}
+
+// A launch that may start while the kernel before it in the stream ends; these kernels wait for that
+// one (tc::grid_dependency_wait) before they read or write global memory.
+template <typename... A, typename... B>
+void launch_early(void (*kernel)(A...), int64_t grid, int threads, cudaStream_t s, const B&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = s;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, args...);  // a refusal is launched()'s to report
+}
+
+// ---- convolution ---------------------------------------------------------------------
+
+template <typename F>
+void by_width(int width, F&& f) {
+  if (width == 2) f(IntC<2>{});
+  else if (width == 3) f(IntC<3>{});
+  else f(IntC<4>{});
+}
+
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// Rows of a forward thread's strip: as few as give every SM 2048 threads, at most 64, where the rows
+// before a strip (read again) no longer count.
+int conv_strip(int64_t rows, int words, int sms) {
+  const int64_t strip = rows * words / (static_cast<int64_t>(sms) * 2048);
+  return static_cast<int>(strip < 1 ? 1 : strip > 64 ? 64 : strip);
+}
+// And of a backward thread's, which walks width - 1 rows more and leaves partial sums.
+int conv_bwd_strip(int64_t rows, int words, int sms) {
+  const int64_t strip = rows * words / (static_cast<int64_t>(sms) * 1024);
+  return static_cast<int>(strip < 16 ? 16 : strip);
+}
+
+int conv_setup(const void* x, const float* weight, const float* bias, int D, int width, int silu, int dtype, int64_t x_stride,
+               gdn::ConvParams* p) {
+  if (D < 1 || D % 8) return fail(GDN_ERR_UNSUPPORTED, "D = %d is not a positive multiple of 8", D);
+  if (width < 2 || width > 4) return fail(GDN_ERR_UNSUPPORTED, "width = %d is not 2, 3 or 4", width);
+  if (int rc = check_type(dtype)) return rc;
+  if (int rc = check_flag(silu, "silu")) return rc;
+  if (int rc = take_stride(x_stride, D, "x", &p->x_stride)) return rc;
+  if (!weight) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if (!aligned(x, 16) || !aligned(weight, 4) || !aligned(bias, 4)) return fail(GDN_ERR_ARG, "x must be 16-byte aligned, weight and bias 4-byte");
+  p->x = x;
+  p->weight = weight;
+  p->bias = bias;
+  p->D = D;
+  p->silu = silu;
+  return GDN_OK;
+}
+
+// ---- layer norm ----------------------------------------------------------------------
+
+constexpr int kNormMaxDim = 8192;
+
+// Calls f with the lanes of a group and the words of eight values that each holds.
+template <typename F>
+void by_dim(int dim, F&& f) {
+  if (dim <= 16) f(IntC<2>{}, IntC<1>{});
+  else if (dim <= 64) f(IntC<8>{}, IntC<1>{});
+  else if (dim <= 128) f(IntC<16>{}, IntC<1>{});
+  else if (dim <= 256) f(IntC<32>{}, IntC<1>{});
+  else if (dim <= 1024) f(IntC<32>{}, IntC<4>{});
+  else if (dim <= 4096) f(IntC<128>{}, IntC<4>{});
+  else f(IntC<256>{}, IntC<4>{});
+}
+// The backward keeps the columns' sums too, so a group takes more lanes.
+template <typename F>
+void by_dim_backward(int dim, F&& f) {
+  if (dim <= 16) f(IntC<2>{}, IntC<1>{});
+  else if (dim <= 64) f(IntC<8>{}, IntC<1>{});
+  else if (dim <= 128) f(IntC<16>{}, IntC<1>{});
+  else if (dim <= 256) f(IntC<32>{}, IntC<1>{});
+  else if (dim <= 1024) f(IntC<128>{}, IntC<1>{});
+  else if (dim <= 4096) f(IntC<512>{}, IntC<1>{});
+  else f(IntC<512>{}, IntC<2>{});
+}
+
+int norm_bwd_ctas(int64_t items, int dim, int sms) {
+  int ctas = 0;
+  by_dim_backward(dim, [&](auto lanes, auto) {
+    const int slots = gdn::norm_threads<lanes.value> / lanes.value;
+    const int64_t need = (items + slots - 1) / slots, most = static_cast<int64_t>(sms) * (lanes.value > 128 ? 2 : 8);
+    ctas = static_cast<int>(need < most ? need : most);
+  });
+  return ctas;
+}
+
+int layer_norm_setup(const void* x, const void* gate, const float* weight, const float* bias, float eps, int rows, int groups, int dim,
+                     int dtype, int rms, int gate_first, const gdn_layer_norm_strides_t* st, gdn::LayerNormParams* p) {
+  *p = gdn::LayerNormParams{};
+  if (rows < 0) return fail(GDN_ERR_ARG, "rows = %d is negative", rows);
+  if (groups < 1) return fail(GDN_ERR_ARG, "groups = %d must be positive", groups);
+  if (dim < 8 || dim % 8 || dim > kNormMaxDim)
+    return fail(GDN_ERR_UNSUPPORTED, "dim = %d is not a multiple of 8 in 8..%d", dim, kNormMaxDim);
+  if (int rc = check_type(dtype)) return rc;
+  if (int rc = check_flag(rms, "rms")) return rc;
+  if (int rc = check_flag(gate_first, "gate_first")) return rc;
+  if (gate_first && !gate) return fail(GDN_ERR_ARG, "gate_first without a gate");
+  if (!(eps >= 0.f)) return fail(GDN_ERR_ARG, "eps must not be negative");
+  const int64_t width = static_cast<int64_t>(groups) * dim;
+  if (int rc = take_stride(st ? st->x : 0, width, "x", &p->x_stride)) return rc;
+  if (gate)
+    if (int rc = take_stride(st ? st->gate : 0, width, "gate", &p->gate_stride)) return rc;
+  if (int rc = take_stride(st ? st->out : 0, width, "out", &p->out_stride)) return rc;
+  if (!aligned(x, 16) || !aligned(gate, 16) || !aligned(weight, 16) || !aligned(bias, 16))
+    return fail(GDN_ERR_ARG, "x, gate, weight and bias must be 16-byte aligned");
+  p->items = static_cast<int64_t>(rows) * groups;
+  if (p->items > INT32_MAX - 65536) return fail(GDN_ERR_UNSUPPORTED, "%d rows of %d groups exceed the item range", rows, groups);
+  if (rows && !x) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  p->x = x;
+  p->gate = gate;
+  p->weight = weight;
+  p->bias = bias;
+  p->groups = groups;
+  p->dim = dim;
+  p->rms = rms;
+  p->gate_first = gate_first;
+  p->eps = eps;
+  return GDN_OK;
+}
+
+// ---- state space scan ----------------------------------------------------------------
+
+template <typename F>
+void by_state(int dk, int dv, F&& f) {
+  if (dk == 64) dv == 64 ? f(IntC<64>{}, IntC<64>{}) : f(IntC<64>{}, IntC<128>{});
+  else dv == 64 ? f(IntC<128>{}, IntC<64>{}) : f(IntC<128>{}, IntC<128>{});
+}
+
+int ssm_setup(const void* q, const void* k, const void* v, const void* dt, const float* a, const float* dt_bias, const float* skip,
+              void* state, void* out, int nk, int nv, int dk, int dv, const gdn_ssm_options_t* o, int64_t rows, gdn::SsmParams* p) {
+  if (nk < 1 || nv < 1) return fail(GDN_ERR_ARG, "head counts nk = %d, nv = %d must be positive", nk, nv);
+  if (nv % nk) return fail(GDN_ERR_UNSUPPORTED, "nv = %d is not a multiple of nk = %d", nv, nk);
+  if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return fail(GDN_ERR_UNSUPPORTED, "dk = %d or dv = %d is neither 64 nor 128", dk, dv);
+  const int64_t wk = static_cast<int64_t>(nk) * dk, wv = static_cast<int64_t>(nv) * dv;
+  if (int rc = take_stride(o ? o->q : 0, wk, "q", &p->q_stride)) return rc;
+  if (int rc = take_stride(o ? o->k : 0, wk, "k", &p->k_stride)) return rc;
+  if (int rc = take_stride(o ? o->v : 0, wv, "v", &p->v_stride)) return rc;
+  if (int rc = take_stride(o ? o->out : 0, wv, "out", &p->out_stride)) return rc;
+  p->dt_stride = o && o->dt ? o->dt : nv;
+  if (p->dt_stride < nv) return fail(GDN_ERR_ARG, "dt row stride %lld must be >= nv = %d", (long long)p->dt_stride, nv);
+  p->state_is_table = o ? o->state_is_table : 0;
+  p->dt_bf16 = o ? o->dt_bf16 : 0;
+  p->softplus = o ? o->softplus : 1;
+  if (int rc = check_flag(p->state_is_table, "state_is_table")) return rc;
+  if (int rc = check_flag(p->dt_bf16, "dt_bf16")) return rc;
+  if (int rc = check_flag(p->softplus, "softplus")) return rc;
+  if (rows == 0) return GDN_OK;
+  if (!q || !k || !v || !dt || !a || !state || !out) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(state, p->state_is_table ? 8 : 16))
+    return fail(GDN_ERR_ARG, "q, k, v, out and state must be 16-byte aligned");
+  if (!aligned(dt, p->dt_bf16 ? 2 : 4) || !aligned(a, 4) || !aligned(dt_bias, 4) || !aligned(skip, 4))
+    return fail(GDN_ERR_ARG, "dt, a, dt_bias and skip must be aligned to their elements");
+  p->q = static_cast<const __nv_bfloat16*>(q);
+  p->k = static_cast<const __nv_bfloat16*>(k);
+  p->v = static_cast<const __nv_bfloat16*>(v);
+  p->dt = dt;
+  p->a = a;
+  p->dt_bias = dt_bias;
+  p->skip = skip;
+  p->state = state;
+  p->out = static_cast<__nv_bfloat16*>(out);
+  p->nk = nk;
+  p->nv = nv;
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_causal_conv(const void* x, const float* weight, const float* bias, void* state, void* out, int B, int T, int D, int width,
+                    int silu, int dtype, int state_is_table, int64_t x_stride, int64_t out_stride, const int32_t* cu_seqlens,
+                    void* stream) {
+  gdn_host::begin();
+  gdn::ConvParams p{};
+  if (int rc = check_batch(B, T, cu_seqlens, &p.batch)) return rc;
+  if (int rc = conv_setup(x, weight, bias, D, width, silu, dtype, x_stride, &p)) return rc;
+  if (int rc = take_stride(out_stride, D, "out", &p.out_stride)) return rc;
+  if (int rc = check_flag(state_is_table, "state_is_table")) return rc;
+  if (state_is_table && !state) return fail(GDN_ERR_ARG, "a state table without its pointer");
+  if (B == 0 || p.batch.rows == 0) return GDN_OK;
+  if (!x || !out) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if (x == out) return fail(GDN_ERR_ARG, "out must not be x: a row's inputs are read by several threads");
+  if (!aligned(out, 16) || !aligned(state, state_is_table ? 8 : 16)) return fail(GDN_ERR_ARG, "out and state must be 16-byte aligned");
+  p.state = state;
+  p.out = out;
+  p.state_is_table = state_is_table;
+  int sms = 0;
+  if (int rc = gdn_host::device(&sms, &p.status)) return rc;
+  const int words = D / (dtype == GDN_F32 ? 4 : 8), rows = p.batch.rows;
+  p.strip = conv_strip(rows, words, sms);
+  if (!cu_seqlens) {  // whole sequences in a strip where they are short
+    if (p.strip < T && T <= 16) p.strip = T;
+    if (p.strip >= T) {
+      p.strip -= p.strip % T;
+      p.state_here = 1;
+    }
+  }
+  p.strips = ceil_div(rows, p.strip);
+  const int64_t threads = static_cast<int64_t>(p.strips) * words;
+  if (threads > static_cast<int64_t>(INT32_MAX) * 64) return fail(GDN_ERR_UNSUPPORTED, "%d rows of %d channels exceed the item range", rows, D);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool after = state && !p.state_here;
+  by_type(dtype, [&](auto t) {
+    by_width(width, [&](auto w) {
+      gdn::gdn_conv_kernel<decltype(t), w.value><<<ceil_div(threads, gdn::kConvThreads), gdn::kConvThreads, 0, s>>>(p);
+      if (after)
+        launch_early(gdn::gdn_conv_state_kernel<decltype(t), w.value>, ceil_div(static_cast<int64_t>(B) * words, gdn::kConvThreads),
+                     gdn::kConvThreads, s, p);
+    });
+  });
+  return launched(after ? 2 : 1);
+}
+
+size_t gdn_causal_conv_backward_workspace_bytes(int rows, int D, int width) {
+  if (rows <= 0 || D < 1 || D % 8 || width < 2 || width > 4) return 0;
+  const int strip = conv_bwd_strip(rows, D / 4, gdn_host::plan_sms());
+  return static_cast<size_t>(ceil_div(rows, strip)) * (width + 1) * D * sizeof(float);
+}
+
+int gdn_causal_conv_backward(const void* x, const float* weight, const float* bias, const void* h0, const void* dout,
+                             const void* dST, void* dx, float* dweight, float* dbias, void* dh0, int B, int T, int D, int width,
+                             int silu, int dtype, int64_t x_stride, int64_t dout_stride, int64_t dx_stride,
+                             const int32_t* cu_seqlens, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_host::begin();
+  gdn::ConvParams p{};
+  if (int rc = check_batch(B, T, cu_seqlens, &p.batch)) return rc;
+  if (int rc = conv_setup(x, weight, bias, D, width, silu, dtype, x_stride, &p)) return rc;
+  if (int rc = take_stride(dout_stride, D, "dout", &p.dout_stride)) return rc;
+  if (int rc = take_stride(dx_stride, D, "dx", &p.dx_stride)) return rc;
+  const int rows = B == 0 ? 0 : p.batch.rows;
+  if (rows && (!x || !dout || !dx)) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if (rows && (dx == x || dx == dout)) return fail(GDN_ERR_ARG, "dx must not be x or dout: a row's are read by several threads");
+  if (!aligned(dout, 16) || !aligned(dx, 16) || !aligned(h0, 16) || !aligned(dST, 16) || !aligned(dh0, 16))
+    return fail(GDN_ERR_ARG, "dout, dx, h0, dST and dh0 must be 16-byte aligned");
+  const bool sums = dweight || dbias;
+  const size_t need = sums ? gdn_causal_conv_backward_workspace_bytes(rows, D, width) : 0;
+  if (need)
+    if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
+  int sms = 0;
+  if (int rc = gdn_host::device(&sms, &p.status)) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {  // sums over no rows
+    if (int rc = zero(dweight, static_cast<int64_t>(D) * width, s)) return rc;
+    if (int rc = zero(dbias, D, s)) return rc;
+  }
+  p.state = const_cast<void*>(h0);
+  p.dout = dout;
+  p.dx = dx;
+  p.dlast = dST;
+  p.dfirst = dh0;
+  p.dweight = dweight;
+  p.dbias = dbias;
+  const int words = D / 4;
+  p.strip = conv_bwd_strip(rows, words, sms);
+  p.strips = ceil_div(rows, p.strip);
+  void* ws = nullptr;
+  if (int rc = acquire(need ? workspace : nullptr, need, s, &ws)) return rc;
+  p.partials = static_cast<float*>(ws);
+  const int sum_ctas = need ? ceil_div(static_cast<int64_t>(width + 1) * D, 32) : 0;
+  const int end_ctas = dh0 ? ceil_div(static_cast<int64_t>(B) * words, gdn::kConvSumThreads) : 0;
+  by_type(dtype, [&](auto t) {
+    by_width(width, [&](auto w) {
+      if (rows)
+        gdn::gdn_conv_bwd_kernel<decltype(t), w.value>
+            <<<ceil_div(static_cast<int64_t>(p.strips) * words, gdn::kConvThreads), gdn::kConvThreads, 0, s>>>(p);
+      if (sum_ctas + end_ctas)
+        launch_early(gdn::gdn_conv_bwd_ends_kernel<decltype(t), w.value>, sum_ctas + end_ctas, gdn::kConvSumThreads, s, p, sum_ctas);
+    });
+  });
+  return release(need ? workspace : nullptr, ws, s, launched((rows > 0) + (sum_ctas + end_ctas > 0)));
+}
+
+size_t gdn_ssm_scan_workspace_bytes(int B, int T, int nv, int dk, int dv, int varlen) {
+  (void)B; (void)T; (void)nv; (void)dk; (void)dv; (void)varlen;
+  return 0;
+}
+
+int gdn_ssm_scan(const void* q, const void* k, const void* v, const void* dt, const float* a, const float* dt_bias, const float* skip,
+                 void* state, void* out, int B, int T, int nk, int nv, int dk, int dv, const gdn_ssm_options_t* options,
+                 const int32_t* cu_seqlens, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_host::begin();
+  gdn::SsmParams p{};
+  if (int rc = check_batch(B, T, cu_seqlens, &p.batch)) return rc;
+  const int rows = B == 0 ? 0 : p.batch.rows;
+  if (int rc = ssm_setup(q, k, v, dt, a, dt_bias, skip, state, out, nk, nv, dk, dv, options, rows, &p)) return rc;
+  if (static_cast<int64_t>(B) * nv > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%d sequences of %d heads exceed the item range", B, nv);
+  if (rows == 0) return GDN_OK;
+  if (int rc = check_workspace(workspace, workspace_bytes, 0)) return rc;
+  int sms = 0;
+  if (int rc = gdn_host::device(&sms, &p.status)) return rc;
+  by_state(dk, dv, [&](auto K, auto V) {
+    gdn::gdn_ssm_scan_kernel<K.value, V.value><<<B * nv, gdn::ssm_threads<K.value, V.value>, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  });
+  return launched(1);
+}
+
+int gdn_ssm_decode(const void* q, const void* k, const void* v, const void* dt, const float* a, const float* dt_bias, const float* skip,
+                   void* state, void* out, int B, int nk, int nv, int dk, int dv, const gdn_ssm_options_t* options, void* stream) {
+  gdn_host::begin();
+  gdn::SsmParams p{};
+  if (int rc = check_batch(B, 1, nullptr, &p.batch)) return rc;
+  if (int rc = ssm_setup(q, k, v, dt, a, dt_bias, skip, state, out, nk, nv, dk, dv, options, B, &p)) return rc;
+  if (static_cast<int64_t>(B) * nv > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%d sequences of %d heads exceed the item range", B, nv);
+  if (B == 0) return GDN_OK;
+  int sms = 0;
+  if (int rc = gdn_host::device(&sms, &p.status)) return rc;
+  by_state(dk, dv, [&](auto K, auto V) {
+    gdn::gdn_ssm_decode_kernel<K.value, V.value><<<B * nv, gdn::ssm_threads<K.value, V.value>, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  });
+  return launched(1);
+}
+
+int gdn_layer_norm(const void* x, const void* gate, const float* weight, const float* bias, float eps, void* out, int rows, int groups,
+                   int dim, int dtype, int rms, int gate_first, const gdn_layer_norm_strides_t* strides, void* stream) {
+  gdn_host::begin();
+  gdn::LayerNormParams p;
+  if (int rc = layer_norm_setup(x, gate, weight, bias, eps, rows, groups, dim, dtype, rms, gate_first, strides, &p)) return rc;
+  if (rows == 0) return GDN_OK;
+  if (!out) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if (!aligned(out, 16)) return fail(GDN_ERR_ARG, "out must be 16-byte aligned");
+  int sms = 0;
+  unsigned* status = nullptr;
+  if (int rc = gdn_host::device(&sms, &status)) return rc;
+  p.out = out;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  by_type(dtype, [&](auto t) {
+    by_dim(dim, [&](auto lanes, auto words) {
+      constexpr int L = lanes.value, threads = gdn::norm_threads<L>;
+      const int grid = ceil_div(p.items, threads / L);
+      if (gate) gdn::gdn_layer_norm_kernel<decltype(t), L, words.value, true><<<grid, threads, 0, s>>>(p);
+      else gdn::gdn_layer_norm_kernel<decltype(t), L, words.value, false><<<grid, threads, 0, s>>>(p);
+    });
+  });
+  return launched(1);
+}
+
+size_t gdn_layer_norm_backward_workspace_bytes(int rows, int groups, int dim) {
+  if (rows <= 0 || groups < 1 || dim < 8 || dim % 8 || dim > kNormMaxDim) return 0;
+  return static_cast<size_t>(norm_bwd_ctas(static_cast<int64_t>(rows) * groups, dim, gdn_host::plan_sms())) * 2 * dim * sizeof(float);
+}
+
+int gdn_layer_norm_backward(const void* x, const void* gate, const float* weight, const float* bias, float eps, const void* dout, void* dx,
+                            void* dgate, float* dweight, float* dbias, int rows, int groups, int dim, int dtype, int rms, int gate_first,
+                            const gdn_layer_norm_strides_t* strides, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_host::begin();
+  gdn::LayerNormParams p;
+  if (int rc = layer_norm_setup(x, gate, weight, bias, eps, rows, groups, dim, dtype, rms, gate_first, strides, &p)) return rc;
+  const int64_t width = static_cast<int64_t>(groups) * dim;
+  if (int rc = take_stride(strides ? strides->dout : 0, width, "dout", &p.dout_stride)) return rc;
+  if (gate)
+    if (int rc = take_stride(strides ? strides->dgate : 0, width, "dgate", &p.dgate_stride)) return rc;
+  if (!gate && dgate) return fail(GDN_ERR_ARG, "dgate without a gate");
+  if (rows && (!dout || !dx || (gate && !dgate))) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if (!aligned(dout, 16) || !aligned(dx, 16) || !aligned(dgate, 16)) return fail(GDN_ERR_ARG, "dout, dx and dgate must be 16-byte aligned");
+  const bool sums = dweight || dbias;
+  const size_t need = sums ? gdn_layer_norm_backward_workspace_bytes(rows, groups, dim) : 0;
+  if (need)
+    if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
+  int sms = 0;
+  unsigned* status = nullptr;
+  if (int rc = gdn_host::device(&sms, &status)) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {  // sums over no rows
+    if (int rc = zero(dweight, dim, s)) return rc;
+    return zero(dbias, dim, s);
+  }
+  p.dout = dout;
+  p.out = dx;
+  p.dgate = dgate;
+  void* ws = nullptr;
+  if (int rc = acquire(need ? workspace : nullptr, need, s, &ws)) return rc;
+  p.partials = static_cast<float*>(ws);
+  const int ctas = norm_bwd_ctas(p.items, dim, sms);
+  by_type(dtype, [&](auto t) {
+    by_dim_backward(dim, [&](auto lanes, auto words) {
+      constexpr int L = lanes.value, threads = gdn::norm_threads<L>;
+      if (gate) gdn::gdn_layer_norm_bwd_kernel<decltype(t), L, words.value, true><<<ctas, threads, 0, s>>>(p);
+      else gdn::gdn_layer_norm_bwd_kernel<decltype(t), L, words.value, false><<<ctas, threads, 0, s>>>(p);
+    });
+  });
+  if (sums) launch_early(gdn::gdn_layer_norm_sum_kernel, ceil_div(2 * dim, 32), 1024, s, static_cast<const float*>(p.partials), ctas, dim, dweight, dbias);
+  return release(need ? workspace : nullptr, ws, s, launched(sums ? 2 : 1));
+}
+
+}  // extern "C"
