@@ -101,18 +101,6 @@ __device__ __noinline__ bool tc_wait_slow(uint32_t bar, uint32_t parity, volatil
   return true;
 }
 
-// 32 bytes to global memory: as one sector, or in two halves where dst is only 16-byte aligned.
-__device__ __forceinline__ void store32(void* dst, const uint32_t* r, bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(dst)), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
-  }
-}
-
 struct TcShared {
   uint32_t bars;  // shared address of the mbarriers
   volatile uint32_t* abort;

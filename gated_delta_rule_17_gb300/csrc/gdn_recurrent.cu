@@ -5,6 +5,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <mutex>
 #include <type_traits>
 
 #include "gdn_recurrent.h"
@@ -270,6 +271,38 @@ int ssm_setup(const void* q, const void* k, const void* v, const void* dt, const
   return GDN_OK;
 }
 
+// [rows][heads * d] bf16 rows as boxes of 64 values and a chunk of tokens.
+int ssm_map(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int64_t stride, const char* name) {
+  auto fn = gdn_host::encode_fn();
+  if (!fn) return fail(GDN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[2] = {64, gdn::kSsmChunk}, estr[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(GDN_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed (%d)", name, static_cast<int>(r));
+  return GDN_OK;
+}
+
+// Shared memory of the scan's kernels, once a device.
+int ssm_attributes() {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lk(mu);
+  if (e == cudaSuccess && dev < 64 && done[dev]) return GDN_OK;
+  for (int dk : {64, 128})
+    for (int dv : {64, 128})
+      by_state(dk, dv, [&](auto K, auto V) {
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(gdn::gdn_ssm_scan_kernel<K.value, V.value>, cudaFuncAttributeMaxDynamicSharedMemorySize, gdn::SsmPlan::DYN_SMEM);
+      });
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  if (dev < 64) done[dev] = true;
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -390,13 +423,23 @@ int gdn_ssm_scan(const void* q, const void* k, const void* v, const void* dt, co
   if (int rc = check_batch(B, T, cu_seqlens, &p.batch)) return rc;
   const int rows = B == 0 ? 0 : p.batch.rows;
   if (int rc = ssm_setup(q, k, v, dt, a, dt_bias, skip, state, out, nk, nv, dk, dv, options, rows, &p)) return rc;
-  if (static_cast<int64_t>(B) * nv > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%d sequences of %d heads exceed the item range", B, nv);
   if (rows == 0) return GDN_OK;
   if (int rc = check_workspace(workspace, workspace_bytes, 0)) return rc;
   int sms = 0;
   if (int rc = gdn_host::device(&sms, &p.status)) return rc;
+  if (int rc = ssm_attributes()) return rc;
+  CUtensorMap q_map, k_map, v_map, out_map;
+  if (int rc = ssm_map(&q_map, q, static_cast<int64_t>(nk) * dk, rows, p.q_stride, "q")) return rc;
+  if (int rc = ssm_map(&k_map, k, static_cast<int64_t>(nk) * dk, rows, p.k_stride, "k")) return rc;
+  if (int rc = ssm_map(&v_map, v, static_cast<int64_t>(nv) * dv, rows, p.v_stride, "v")) return rc;
+  if (int rc = ssm_map(&out_map, out, static_cast<int64_t>(nv) * dv, rows, p.out_stride, "out")) return rc;
+  gdn::SsmScanParams sp{};
+  sp.s = p;
+  sp.pairs = nk * ((nv / nk * (dv / 64) + 1) / 2);
+  if (static_cast<int64_t>(B) * sp.pairs > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%d sequences of %d heads exceed the item range", B, nv);
   by_state(dk, dv, [&](auto K, auto V) {
-    gdn::gdn_ssm_scan_kernel<K.value, V.value><<<B * nv, gdn::ssm_threads<K.value, V.value>, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    gdn::gdn_ssm_scan_kernel<K.value, V.value>
+        <<<B * sp.pairs, gdn::kSsmThreads, gdn::SsmPlan::DYN_SMEM, static_cast<cudaStream_t>(stream)>>>(q_map, k_map, v_map, out_map, sp);
   });
   return launched(1);
 }

@@ -127,6 +127,31 @@ __device__ __forceinline__ void floats16(const uint4 w, float (&f)[Word16<T>::N]
   for (int i = 0; i < Word16<T>::PAIRS; ++i) parts_of(p[i], f[2 * i], f[2 * i + 1]);
 }
 
+// 32 bytes to global memory: as one sector, or in two halves where dst is only 16-byte aligned.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* r, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(dst)), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  }
+}
+
+// 32 bytes from global memory, likewise.
+__device__ __forceinline__ void load32(const void* src, uint32_t* r, bool wide) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(__cvta_generic_to_global(src)));
+  } else {
+    const uint4 a = reinterpret_cast<const uint4*>(src)[0], b = reinterpret_cast<const uint4*>(src)[1];
+    r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
+    r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
+  }
+}
+
 // 1 / (1 + e^-y). e^-y past fp32's range gives 0, as does a sum that the division cannot take.
 __device__ __forceinline__ float sigmoid(float y) { return __fdividef(1.f, 1.f + __expf(-y)); }
 __device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }

@@ -1,0 +1,517 @@
+// The scan over prompts in chunks of 128 tokens on the tensor cores (tcgen05), for sm_103a.
+//
+// Within a chunk, with g_t = d_t a, suf_t = sum of g over the chunk's tokens behind t, and total their sum:
+//
+//     o_i = e^{total - suf_i} q_i S + sum_{j <= i} (q_i . k_j) e^{suf_j - suf_i} d_j v_j + skip v_i
+//     S  <- e^{total} S + sum_j k_j (d_j e^{suf_j} v_j)^T
+//
+// A unit is 64 value columns of a head, and a CTA takes two units of one key head (two halves of a head of
+// 128, or two heads of 64) through a sequence, or a segment of one. Their products share the operands:
+//
+//     G = Q K^T (128 x 128)      once for both units
+//     O2 = Q S16                 N = 128: both units side by side
+//     O1 = A V                   A = G under the mask
+//     L = K^T V'                 V' = d e^{suf} v as bf16 hi + lo, so that the fp32 state keeps 16 bits of it
+//
+// The decays need no exponential a pair (i, j): with V = V' (hi) and e^{-suf_i} on the rows of O1, A is
+// the same for both heads, and bf16 has fp32's exponents. That holds while the chunk's decay stays within
+// kSsmSpan; in chunks that decay further each unit has an A of its own, with d_j e^{suf_j - suf_i} pair by pair,
+// and V = v. Operands of 16 bits cost the output what its own rounding does: 2.2e-3 of its size in
+// bf16, 1.7e-3 if it were rounded only once; the state is off by under 1e-5.
+//
+// Roles: warps 0-7, a thread a row of S and of the outputs (warps 0-3 unit 0, 4-7 unit 1), S in registers; warps 8-15 make
+// the operands, V' of their unit and half of A; warp 16 copies Q and K (TMA) and issues the products. Order on the tensor
+// pipe: O2, O1, L of a chunk, then G of the next. So the update of S, the only step that the next chunk's O2 waits
+// for, runs under G, making A under O2, the rows' way out under L.
+#pragma once
+#include "/root/repo/gated_delta_rule_17_gb300/csrc/gdn_ssm_common.cuh"
+
+namespace gdn {
+
+constexpr int kSsmChunk = 128;
+constexpr int kSsmThreads = 640;
+// Registers of a thread by role. Five warpgroups are launched with 96 each, which they share out: 2 x 120 + 2 x 96 + 48 = 5 x 96.
+constexpr int kSsmRowRegs = 120, kSsmOperandRegs = 96, kSsmIssueRegs = 48;
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+constexpr float kSsmSpan = 140.f;  // nats that a chunk may decay for its decays to go into its operands
+
+// What the roles tell one another beside tiles.
+struct SsmSmall {
+  uint64_t bar[14];
+  float suf[2][kSsmChunk], d[2][kSsmChunk];  // of each unit's tokens
+  float total[2][2];                         // by chunk parity: each unit's decay
+  uint32_t tmem, abort;
+};
+
+struct SsmPlan {
+  static constexpr int BLOCK = 128 * 128;  // 128 rows of 64 16-bit values
+  static constexpr int Q = 0, K = 2 * BLOCK, VHI = K + 4 * BLOCK, VLO = VHI + 2 * BLOCK, S16 = VLO + 2 * BLOCK, ROWS = S16 + 2 * BLOCK,
+                       SMALL = ROWS + 2 * BLOCK, DYN_SMEM = SMALL + static_cast<int>(sizeof(SsmSmall));
+  static constexpr uint32_t COL_G = 0, COL_O = 128, COL_L = 384, TMEM_COLS = 512;  // O: a buffer of 128 for even and odd chunks
+  // mbarriers: copies (Q_FULL, K_FULL + buffer), products (G_FULL, Q_FREE, L_FULL) and warps' signals
+  static constexpr int Q_FULL = 0, K_FULL = 1, G_FULL = 3, Q_FREE = 4, L_FULL = 5, GATES = 6, V_READY = 7, A_READY = 8, S_READY = 9,
+                       GATES_READ = 10, O_READ = 11, NBAR = 13;
+};
+
+struct SsmScanParams {
+  SsmParams s;
+  int pairs;             // CTAs of a sequence
+  int v_wide, out_wide;  // whether the rows of v and out lie on 32-byte boundaries
+};
+
+constexpr int kSsmWaits = 1 << 18;  // tries of up to 10 us each before a wait gives up
+
+struct SsmShared {
+  uint32_t bars;
+  volatile uint32_t* abort;
+  __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
+  // Bounded wait by a whole warp, with one answer. A warp that gave up waits no more but walks on, so that
+  // the barriers among warps still fill. (Counted, not timed: the clock and a call cost every wait code, of which
+  // the roles share the instruction caches.)
+  __device__ __forceinline__ void wait(int i, uint32_t parity, bool& ok) const {
+    if (!ok) return;
+    bool there = tc::mbar_try_wait(bar(i), parity);
+#pragma unroll 1
+    for (int k = 0; k < kSsmWaits && !there && !*abort; ++k) there = tc::mbar_try_wait_hint(bar(i), parity, 10000u);
+    ok = __all_sync(0xffffffffu, there);
+    if (!ok) *abort = 1;
+  }
+  __device__ __forceinline__ void arrive(int i) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar(i));
+  }
+};
+
+// A value that the compiler takes to change, so that it does not write a role's loop twice for the two of a flag.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+__device__ __forceinline__ float ssm_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Whether either unit's chunk decays by more than kSsmSpan (the same for all roles).
+__device__ __forceinline__ bool ssm_wide(const float (&total)[2]) { return !(fminf(total[0], total[1]) >= -kSsmSpan); }
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kSsmThreads, 1)
+gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                    const SsmScanParams params) {
+  using P = SsmPlan;
+  constexpr int SLICES = DV / 64, KB = DK / 64;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = tc::smem_u32(smem);
+  SsmSmall& small = *reinterpret_cast<SsmSmall*>(smem + P::SMALL);
+  const SsmParams& p = params.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const SsmShared sh{tc::smem_u32(small.bar), &small.abort};
+
+  const int pair = static_cast<int>(blockIdx.x % static_cast<unsigned>(params.pairs)), seq = static_cast<int>(blockIdx.x / static_cast<unsigned>(params.pairs));
+  const int heads = p.nv / p.nk, units = heads * SLICES, per_key = (units + 1) / 2;  // of a key head
+  const int kh = pair / per_key;
+  const int start = p.batch.start(seq), end = p.batch.end(seq);
+  if (pair == 0 && threadIdx.x == 0) p.batch.report(seq, p.status);
+  if (!rows_held(start, end, p.batch.rows) || start == end) return;
+  if (sbase & 1023) {  // the swizzled tiles' place; the linker keeps it
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+    return;
+  }
+  const int tokens = end - start, chunks = (tokens + kSsmChunk - 1) / kSsmChunk;
+
+  if (threadIdx.x == 0) {
+    small.abort = 0;
+    for (int i = 0; i < P::NBAR; ++i) tc::mbar_init(sh.bar(i), i < P::GATES ? 1 : i == P::GATES ? 2 : 8);
+    tc::mbar_fence_init();
+  }
+  if (warp == 16) tc::tmem_alloc(tc::smem_u32(&small.tmem), P::TMEM_COLS);
+  if (KB == 1)  // keys of 64: the products of K^T take 128 rows, the second half zeros
+    for (int i = threadIdx.x; i < 2 * P::BLOCK / 16; i += kSsmThreads)
+      *reinterpret_cast<uint4*>(smem + P::K + (i / (P::BLOCK / 16) * 2 + 1) * P::BLOCK + i % (P::BLOCK / 16) * 16) = make_uint4(0, 0, 0, 0);
+  tc::fence_proxy_async();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = small.tmem;
+  bool ok = true;
+
+  if (warp < 16) {
+    const int group = warp >> 3, x = (warp >> 2) & 1, t = threadIdx.x & 127;  // the unit, and the row of it
+    const int is_real = 2 * (pair % per_key) + x < units;
+    const bool real = is_real;
+    const int unit = 2 * (pair % per_key) + (real ? x : 0), h = kh * heads + unit / SLICES, col = h * DV + unit % SLICES * 64;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's quarter of the lanes
+    if (group == 0) {
+      // ---- a row of S, and of the outputs ------------------------------------------------
+      more_registers<kSsmRowRegs>();
+      float* S = ssm_state<DK, DV>(p, seq, h) + static_cast<int64_t>(t) * DV + unit % SLICES * 64;
+      float s[64];
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (real && t < DK) v = *reinterpret_cast<const float4*>(S + i);
+        s[i] = v.x;
+        s[i + 1] = v.y;
+        s[i + 2] = v.z;
+        s[i + 3] = v.w;
+      }
+      uint8_t* s16 = smem + P::S16 + x * P::BLOCK;
+      float f1 = 0.f, f2 = 0.f;  // the factors of the row's outputs in the chunk before
+      bool wide = false;
+      for (int c = 0; c <= chunks; ++c) {
+        const uint32_t ph = c & 1;
+        float keep = 0.f, grow = 0.f, r1 = 0.f, r2 = 0.f;
+        bool now_wide = false;
+        if (c < chunks) {  // S for the products, with what it decays by beside V' where they share an accumulator
+          sh.wait(P::GATES, ph, ok);
+          const float suf = small.suf[x][t], total = small.total[ph][x];
+          now_wide = ssm_wide(small.total[ph]);
+          sh.arrive(P::GATES_READ);
+          const float mid = now_wide ? 0.f : 0.5f * total;
+          r1 = now_wide ? 1.f : __expf(mid - suf);
+          r2 = __expf(total - suf);
+          keep = __expf(total);
+          grow = __expf(mid);
+          const float to16 = now_wide ? 1.f : grow;  // e^{total - mid}
+          const Pair by = pair_of(to16, to16);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) parts_of(mul2(pair_of(s[8 * i + 2 * e], s[8 * i + 2 * e + 1]), by), y[2 * e], y[2 * e + 1]);
+            *reinterpret_cast<uint4*>(s16 + tc::sw128(t, 16 * i)) = pack16<__nv_bfloat16>(y);
+          }
+          tc::fence_proxy_async();
+          tc::fence_before_sync();
+          sh.arrive(P::S_READY);
+        }
+        if (c > 0) {  // the rows of the chunk before
+          const int at = (c - 1) * kSsmChunk + t;
+          const uint32_t from = tmem + lanes + P::COL_O + 64 * x, off = (c & 1) ? 0 : 128;  // its buffer
+          __nv_bfloat16* out = p.out + (start + at) * p.out_stride + col;
+          const Pair by = pair_of(wide ? f2 : f1, wide ? f2 : f1);  // (its O is complete: L was, which comes after)
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[16], w[8];
+            tc::tmem_ld16u(from + off + 16 * i, o);
+            tc::tmem_ld_wait16(o);
+            Pair v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = mul2(pair_of(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), by);
+            if (wide) {
+              tc::tmem_ld16u(from + (off ^ 128) + 16 * i, o);
+              tc::tmem_ld_wait16(o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = add2(pair_of(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), v[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float y[2];
+              parts_of(v[e], y[0], y[1]);
+              w[e] = pack2<__nv_bfloat16>(y[0], y[1]);
+            }
+            if (ok && opaque(is_real) && at < tokens) store32(out + 16 * i, w, params.out_wide);
+          }
+          tc::fence_before_sync();
+          sh.arrive(P::O_READ + (ph ^ 1));
+        }
+        f1 = r1;
+        f2 = r2;
+        wide = now_wide;
+        if (c < chunks) {
+          sh.wait(P::L_FULL, ph, ok);
+          tc::fence_after_sync();
+          const Pair by = pair_of(keep, keep), in = pair_of(grow, grow);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t l[32];
+            tc::tmem_ld32(tmem + lanes + P::COL_L + 64 * x + 32 * i, l);
+            tc::tmem_ld_wait32(l);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              parts_of(fma2(pair_of(s[32 * i + e], s[32 * i + e + 1]), by, mul2(pair_of(__uint_as_float(l[e]), __uint_as_float(l[e + 1])), in)),
+                       s[32 * i + e], s[32 * i + e + 1]);
+          }
+        }
+      }
+      if (ok && real && t < DK) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) *reinterpret_cast<float4*>(S + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+      }
+    } else {
+      // ---- operands --------------------------------------------------------------------------
+      more_registers<kSsmOperandRegs>();
+      const int quarter = warp & 3;
+      const float skip = p.skip ? p.skip[h] : 0.f;
+      const __nv_bfloat16* v = p.v + static_cast<int64_t>(start) * p.v_stride + col;
+      uint8_t* hi = smem + P::VHI + x * P::BLOCK;
+      uint8_t* lo = smem + P::VLO + x * P::BLOCK;
+      uint8_t* rows = smem + P::ROWS + x * P::BLOCK;
+      uint32_t word[32];  // the thread's row of v, a chunk ahead
+      auto fetch = [&](int c) {
+        const int r = c * kSsmChunk + t;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) word[i] = 0;
+        if (opaque(is_real) && r < tokens) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load32(v + r * p.v_stride + 16 * i, word + 8 * i, params.v_wide);
+        }
+      };
+      fetch(0);
+      bool was_wide = false;
+      for (int c = 0; c < chunks; ++c) {
+        const uint32_t ph = c & 1;
+        const int n = min(kSsmChunk, tokens - c * kSsmChunk);
+        if (n < kSsmChunk) {  // rows of K behind the sequence are someone else's, or nobody's: as zeros they are no NaN
+          sh.wait(P::K_FULL + ph, (c >> 1) & 1, ok);
+#pragma unroll 1
+          for (int i = threadIdx.x - 256; i < (kSsmChunk - n) * 8 * KB; i += 256) {
+            const int r = n + i / (8 * KB), w = i % (8 * KB);
+            *reinterpret_cast<uint4*>(smem + P::K + (2 * ph + w / 8) * P::BLOCK + r * 128 + w % 8 * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        sh.wait(P::GATES, ph, ok);
+        const bool wide = ssm_wide(small.total[ph]);
+        const float suf = small.suf[x][t], f = small.d[x][t] * __expf(wide ? suf : fmaf(-0.5f, small.total[ph][x], suf));
+        const float f_hi = __bfloat162float(__float2bfloat16_rn(f));
+        const __nv_bfloat162 fh = __float2bfloat162_rn(f_hi), fl = __float2bfloat162_rn(f - f_hi);
+        const float start_o = wide ? skip : skip * __expf(fmaf(-0.5f, small.total[ph][x], suf));  // skip / r1
+        const Pair by_o = pair_of(start_o, start_o);
+        if (c > 1) sh.wait(P::O_READ + ph, ((c >> 1) - 1) & 1, ok);
+        if (c > 0 && (wide || was_wide)) sh.wait(P::O_READ + (ph ^ 1), ((c - 1) >> 1) & 1, ok);
+        was_wide = wide;
+        if (c > 0) sh.wait(P::L_FULL, ph ^ 1, ok);  // V is free
+        tc::fence_after_sync();
+        const uint32_t o = tmem + lanes + P::COL_O + (wide ? ph ^ 1 : ph) * 128 + 64 * x;
+        // V' = v f in pairs of bf16: with f = f_hi + f_lo, hi = v f_hi rounded, lo = (v f_hi - hi, exact) + v f_lo. And what O
+        // starts from: skip v
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t a8[8], b8[8];
+          float first[16];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const __nv_bfloat162 e = as_bf162(word[8 * i + k]), high = __hmul2_rn(e, fh);
+            a8[k] = as_u32(high);
+            b8[k] = as_u32(__hfma2(e, fl, __hfma2(e, fh, __hneg2(high))));
+            parts_of(mul2(pair_of(__uint_as_float(word[8 * i + k] << 16), __uint_as_float(word[8 * i + k] & 0xFFFF0000u)), by_o), first[2 * k],
+                     first[2 * k + 1]);
+          }
+          tc::tmem_st16(o + 16 * i, first);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t at = tc::sw128(t, 32 * i + 16 * k);
+            *reinterpret_cast<uint4*>(hi + at) = make_uint4(a8[4 * k], a8[4 * k + 1], a8[4 * k + 2], a8[4 * k + 3]);
+            *reinterpret_cast<uint4*>(lo + at) = make_uint4(b8[4 * k], b8[4 * k + 1], b8[4 * k + 2], b8[4 * k + 3]);
+            if (wide)
+              *reinterpret_cast<uint4*>(rows + at) =
+                  make_uint4(word[8 * i + 4 * k], word[8 * i + 4 * k + 1], word[8 * i + 4 * k + 2], word[8 * i + 4 * k + 3]);
+          }
+        }
+        if (c + 1 < chunks) fetch(c + 1);
+        tc::fence_proxy_async();
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        sh.arrive(P::V_READY);
+        sh.wait(P::G_FULL, ph, ok);
+        // A: row t, columns 16 i .. 16 i + 15, of which it sees those up to itself. Half of it in place of this half of G;
+        // where the decay is wide all of the unit's own, in place of its L, once that has been read.
+        if (wide) sh.wait(P::S_READY, ph, ok);
+        tc::fence_after_sync();
+        const int first = wide ? 0 : 4 * x, last = wide ? 8 : first + 4;
+        const uint32_t to = tmem + lanes + (wide ? P::COL_L + 64 * x : P::COL_G + 32 * x);
+        const float own = suf * kLog2e;
+#pragma unroll 1
+        for (int i = first; i < last; ++i) {
+          uint32_t r[16], k16[8];
+          const int seen = t - 16 * i;
+          if (i <= 2 * quarter + 1) {
+            tc::tmem_ld16u(tmem + lanes + P::COL_G + 16 * i, r);
+            tc::tmem_ld_wait16(r);
+            if (wide) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                r[e] = __float_as_uint(__uint_as_float(r[e]) * (small.d[x][16 * i + e] * ssm_exp2(fmaf(small.suf[x][16 * i + e], kLog2e, -own))));
+            }
+            if (i >= 2 * quarter) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = e <= seen ? r[e] : 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) k16[e / 2] = pack2<__nv_bfloat16>(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) k16[e] = 0;
+          }
+          tc::tmem_st8(to + 8 * i, k16);
+        }
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        sh.arrive(P::A_READY);
+      }
+    }
+  } else {
+    // ---- copies and products, by one warp of the last four ----------------------------------------
+    fewer_registers<kSsmIssueRegs>();
+    if (warp == 16) {
+      constexpr uint32_t id_g = tc::idesc_f16(128, 128, tc::kBF16, false, false), id_o = tc::idesc_f16(128, 128, tc::kBF16, false, true),
+                         id_o64 = tc::idesc_f16(128, 64, tc::kBF16, false, true), id_l = tc::idesc_f16(128, 128, tc::kBF16, true, true);
+      auto copy = [&](const CUtensorMap* map, int to, int bar, int c) {
+        if (tc::elect_one()) {
+          tc::mbar_arrive_expect_tx(sh.bar(bar), KB * P::BLOCK);
+#pragma unroll
+          for (int i = 0; i < KB; ++i) tc::tma_load_2d(sbase + to + i * P::BLOCK, map, kh * DK + 64 * i, start + c * kSsmChunk, sh.bar(bar));
+        }
+        __syncwarp();
+      };
+      copy(&q_map, P::Q, P::Q_FULL, 0);
+      copy(&k_map, P::K, P::K_FULL, 0);
+      const uint64_t q_k = tc::desc_sw128(sbase + P::Q, 16, 1024), s_mn = tc::desc_sw128(sbase + P::S16, P::BLOCK, 1024);
+      const uint64_t v_mn = tc::desc_sw128(sbase + P::ROWS, P::BLOCK, 1024);
+      bool was_wide = false;
+      const uint64_t hi_mn = tc::desc_sw128(sbase + P::VHI, P::BLOCK, 1024), lo_mn = tc::desc_sw128(sbase + P::VLO, P::BLOCK, 1024);
+      for (int c = 0; c < chunks && ok; ++c) {
+        const uint32_t ph = c & 1;
+        const int kt = P::K + ph * 2 * P::BLOCK;
+        const uint64_t k_k = tc::desc_sw128(sbase + kt, 16, 1024), k_mn = tc::desc_sw128(sbase + kt, P::BLOCK, 1024);
+        sh.wait(P::Q_FULL, ph, ok);
+        sh.wait(P::K_FULL + ph, (c >> 1) & 1, ok);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+#pragma unroll 2
+          for (int i = 0; i < DK / 16; ++i) {
+            const uint32_t off = ((i >> 2) * P::BLOCK + (i & 3) * 32) >> 4;
+            tc::mma_f16(tmem + P::COL_G, q_k + off, k_k + off, id_g, i > 0);
+          }
+          tc::mma_commit(sh.bar(P::G_FULL));
+        }
+        __syncwarp();
+        if (c + 1 < chunks) {
+          if (c > 0) sh.wait(P::L_FULL, ph ^ 1, ok);  // the products of the chunk before have read the other K
+          if (!ok) break;
+          copy(&k_map, P::K + (ph ^ 1) * 2 * P::BLOCK, P::K_FULL + (ph ^ 1), c + 1);
+        }
+        sh.wait(P::S_READY, ph, ok);
+        sh.wait(P::V_READY, ph, ok);
+        if (!ok) break;
+        // the chunk's buffer of O, and where the decay is wide the other for O1 (free, and started: V_READY says so)
+        const bool wide = ssm_wide(small.total[ph]);
+        const uint32_t o = tmem + P::COL_O + ph * 128, o1 = wide ? tmem + P::COL_O + (ph ^ 1) * 128 : o;
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+#pragma unroll 2
+          for (int i = 0; i < DK / 16; ++i) {
+            const uint32_t off = ((i >> 2) * P::BLOCK + (i & 3) * 32) >> 4;
+            tc::mma_f16(o, q_k + off, s_mn + ((i * 2048) >> 4), id_o, !wide || i > 0);
+          }
+          tc::mma_commit(sh.bar(P::Q_FREE));
+        }
+        __syncwarp();
+        sh.wait(P::A_READY, ph, ok);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+          if (!wide) {
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) tc::mma_f16_ts(o, tmem + P::COL_G + 8 * i + (i & 4) * 8, hi_mn + ((i * 2048) >> 4), id_o, 1);
+          } else {
+            for (int u = 0; u < 2; ++u)
+#pragma unroll 2
+              for (int i = 0; i < 8; ++i)
+                tc::mma_f16_ts(o1 + 64 * u, tmem + P::COL_L + 64 * u + 8 * i, v_mn + ((u * P::BLOCK + i * 2048) >> 4), id_o64, 1);
+          }
+        }
+        __syncwarp();
+        if (c + 1 < chunks) {
+          sh.wait(P::Q_FREE, ph, ok);
+          if (!ok) break;
+          copy(&q_map, P::Q, P::Q_FULL, c + 1);
+        }
+        if (tc::elect_one()) {
+#pragma unroll 2
+          for (int i = 0; i < 8; ++i) tc::mma_f16(tmem + P::COL_L, k_mn + ((i * 2048) >> 4), hi_mn + ((i * 2048) >> 4), id_l, i > 0);
+#pragma unroll 2
+          for (int i = 0; i < 8; ++i) tc::mma_f16(tmem + P::COL_L, k_mn + ((i * 2048) >> 4), lo_mn + ((i * 2048) >> 4), id_l, 1);
+          tc::mma_commit(sh.bar(P::L_FULL));
+        }
+        __syncwarp();
+      }
+    } else if (warp < 19) {
+      // ---- gates, a warp a unit, four tokens a lane -----------------------------------------------
+      const int x = warp - 17;
+      const int is_real = 2 * (pair % per_key) + x < units, unit = 2 * (pair % per_key) + (is_real ? x : 0), h = kh * heads + unit / SLICES;
+      const float a = p.a[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+      const __nv_bfloat16* v = p.v + static_cast<int64_t>(start) * p.v_stride + h * DV + unit % SLICES * 64;
+      float z[4];
+      auto fetch = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = c * kSsmChunk + 4 * lane + i;
+          z[i] = 0.f;
+          if (opaque(is_real) && r < tokens) {
+            const int64_t at = (start + r) * p.dt_stride + h;
+            z[i] = p.dt_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.dt)[at]) : static_cast<const float*>(p.dt)[at];
+          }
+        }
+      };
+      fetch(0);
+      for (int c = 0; c < chunks; ++c) {
+        const uint32_t ph = c & 1;
+        float d[4], suf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float y = z[i] + bias;
+          d[i] = !(opaque(is_real) && c * kSsmChunk + 4 * lane + i < tokens) ? 0.f : opaque(p.softplus) ? fmaxf(y, 0.f) + log1pf(__expf(-fabsf(y))) : y;
+        }
+        if (c + 1 < chunks) fetch(c + 1);
+        // v of the chunk after the next, whose loads then find it in L2
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = (c + 2) * kSsmChunk + 4 * lane + i;
+          if (r < tokens) asm volatile("prefetch.global.L2 [%0];" ::"l"(v + r * p.v_stride));
+        }
+        suf[3] = 0.f;
+#pragma unroll
+        for (int i = 3; i > 0; --i) suf[i - 1] = fmaf(d[i], a, suf[i]);
+        float incl = fmaf(d[0], a, suf[0]);  // from this lane's first token to the chunk's last
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float y = __shfl_down_sync(0xffffffffu, incl, o);
+          if (lane + o < 32) incl += y;
+        }
+        float behind = __shfl_down_sync(0xffffffffu, incl, 1);
+        if (lane == 31) behind = 0.f;
+        if (c > 0) {  // the chunk's before are used
+          sh.wait(P::GATES_READ, ph ^ 1, ok);
+          sh.wait(P::A_READY, ph ^ 1, ok);
+        }
+        *reinterpret_cast<float4*>(&small.d[x][4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
+        *reinterpret_cast<float4*>(&small.suf[x][4 * lane]) = make_float4(suf[0] + behind, suf[1] + behind, suf[2] + behind, suf[3] + behind);
+        if (lane == 0) small.total[ph][x] = incl;
+        sh.arrive(P::GATES);
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (small.abort) {  // products and copies in flight land before the memory is given up
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  if (warp == 16) tc::tmem_dealloc(tmem, P::TMEM_COLS);
+}
+
+}  // namespace gdn
