@@ -128,7 +128,7 @@ def load():
             lib.gdn_causal_conv_backward.argtypes = [vp] * 10 + [i] * 6 + [i64] * 3 + [vp, vp, sz, vp]
             lib.gdn_causal_conv_backward.restype = i
             ssm = vp  # the options, by address
-            lib.gdn_ssm_scan_workspace_bytes.argtypes = [i] * 6
+            lib.gdn_ssm_scan_workspace_bytes.argtypes = [i] * 7
             lib.gdn_ssm_scan_workspace_bytes.restype = sz
             lib.gdn_ssm_scan.argtypes = [vp] * 9 + [i] * 6 + [ssm, vp, vp, sz, vp]
             lib.gdn_ssm_scan.restype = i
@@ -771,8 +771,8 @@ def _ssm_args(q, k, v, dt, a, out, rows, nk, nv, dk, dv, dt_bias, skip, state_is
     return head, op, _SSM(qs, ks, vs, ts, os_, 1 if state_is_table else 0, 1 if dt.dtype is bf16 else 0, 1 if softplus else 0)
 
 
-def ssm_scan_workspace_bytes(B, T, nv, varlen, dk=128, dv=128) -> int:
-    return int(load().gdn_ssm_scan_workspace_bytes(B, T, nv, dk, dv, 1 if varlen else 0))
+def ssm_scan_workspace_bytes(B, T, nk, nv, varlen, dk=128, dv=128) -> int:
+    return int(load().gdn_ssm_scan_workspace_bytes(B, T, nk, nv, dk, dv, 1 if varlen else 0))
 
 
 def ssm_scan(q, k, v, dt, a, state, out, *, nk: int, nv: int, dk: int = 128, dv: int = 128, dt_bias=None,

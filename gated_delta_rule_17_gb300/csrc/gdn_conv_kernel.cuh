@@ -18,7 +18,7 @@ namespace gdn {
 
 constexpr int kConvThreads = 128;
 constexpr int kConvCtasPerSm = 4;
-constexpr int kConvUnroll = 8;  // rows loaded ahead of their arithmetic
+constexpr int kConvUnroll = 4;  // rows loaded ahead of their arithmetic
 
 struct ConvParams {
   const void* x;
@@ -50,15 +50,22 @@ __device__ __forceinline__ T* conv_state(void* state, int table, int s, int64_t 
   return table ? static_cast<T* const*>(state)[s] : static_cast<T*>(state) + s * size;
 }
 
-// The weights of a thread's channels, tap by tap, in pairs.
+// The weights of a thread's 2 P channels, tap by tap, in pairs (c0 is a multiple of 4: their W x 2 P values are whole words).
 template <int W, int P>
 __device__ __forceinline__ void conv_weights(const ConvParams& p, int c0, Pair (&w)[W][P], Pair (&b)[P]) {
+  float f[2 * P * W], g[2 * P];
+#pragma unroll
+  for (int i = 0; i < 2 * P * W; i += 4) load4(p.weight + static_cast<int64_t>(c0) * W + i, *reinterpret_cast<float(*)[4]>(f + i));
+#pragma unroll
+  for (int i = 0; i < 2 * P; ++i) g[i] = 0.f;
+  if (p.bias)
+#pragma unroll
+    for (int i = 0; i < 2 * P; i += 4) load4(p.bias + c0 + i, *reinterpret_cast<float(*)[4]>(g + i));
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int c = c0 + 2 * i;
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = pair_of(p.weight[static_cast<int64_t>(c) * W + j], p.weight[static_cast<int64_t>(c + 1) * W + j]);
-    b[i] = p.bias ? pair_of(p.bias[c], p.bias[c + 1]) : pair_of(0.f, 0.f);
+    for (int j = 0; j < W; ++j) w[j][i] = pair_of(f[2 * i * W + j], f[(2 * i + 1) * W + j]);
+    b[i] = pair_of(g[2 * i], g[2 * i + 1]);
   }
 }
 
@@ -82,7 +89,7 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtasPerSm) gdn_conv_kernel(
     if (end <= row || !rows_held(start, end, p.batch.rows) || start > row) continue;
     T* state = conv_state<T>(p.state, p.state_is_table, s, static_cast<int64_t>(W - 1) * p.D);
     if (state) state += c0;
-    uint4 raw[U], last[W - 1];  // the inputs, and those before them
+    uint4 last[W - 1];  // the inputs before
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
       const int t = row - (W - 1) + i;
@@ -92,40 +99,54 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtasPerSm) gdn_conv_kernel(
     }
     const int to = min(end, stop);
     Pair before[W - 1][P];
+    // one row: `word` in, out to `at`
+    auto step = [&](const uint4 word, T* at) {
+      Pair now[P];
+      unpack16<T>(word, now);
+      float y[N];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        Pair acc = fma2(now[i], w[W - 1][i], b[i]);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) acc = fma2(before[j][i], w[j][i], acc);
+        parts_of(acc, y[2 * i], y[2 * i + 1]);
+      }
+      if (p.silu) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = silu(y[i]);
+      }
+      *reinterpret_cast<uint4*>(at) = pack16<T>(y);
+#pragma unroll
+      for (int j = 0; j + 1 < W - 1; ++j)
+#pragma unroll
+        for (int i = 0; i < P; ++i) before[j][i] = before[j + 1][i];
+#pragma unroll
+      for (int i = 0; i < P; ++i) before[W - 2][i] = now[i];
+    };
+    uint4 raw[U];
+    const bool whole = row + U <= to;
+    const T* from = x + row * p.x_stride;
+    if (whole)
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u] = *reinterpret_cast<const uint4*>(from + u * p.x_stride);
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) unpack16<T>(last[i], before[i]);
-    for (; row < to; row += U) {
+    if (whole) {
+      T* at = out + row * p.out_stride;
+      for (; row + U <= to; row += U) {  // each row's word makes room for the one U rows on
+        const bool more = row + 2 * U <= to;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (row + u < to) raw[u] = *reinterpret_cast<const uint4*>(x + (row + u) * p.x_stride);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (row + u < to) {
-          Pair now[P];
-          unpack16<T>(raw[u], now);
-          float y[N];
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            Pair acc = fma2(now[i], w[W - 1][i], b[i]);
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) acc = fma2(before[j][i], w[j][i], acc);
-            parts_of(acc, y[2 * i], y[2 * i + 1]);
-          }
-          if (p.silu) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) y[i] = silu(y[i]);
-          }
-          *reinterpret_cast<uint4*>(out + (row + u) * p.out_stride) = pack16<T>(y);
-#pragma unroll
-          for (int j = 0; j + 1 < W - 1; ++j)
-#pragma unroll
-            for (int i = 0; i < P; ++i) before[j][i] = before[j + 1][i];
-#pragma unroll
-          for (int i = 0; i < P; ++i) before[W - 2][i] = now[i];
+        for (int u = 0; u < U; ++u) {
+          const uint4 word = raw[u];
+          if (more) raw[u] = *reinterpret_cast<const uint4*>(from + (U + u) * p.x_stride);
+          step(word, at + u * p.out_stride);
         }
+        from += U * p.x_stride;
+        at += U * p.out_stride;
       }
     }
-    row = to;
+#pragma unroll 1
+    for (; row < to; ++row) step(*reinterpret_cast<const uint4*>(x + row * p.x_stride), out + row * p.out_stride);
     if (p.state_here && state) {
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) {
@@ -193,7 +214,7 @@ __device__ __forceinline__ void conv_dy(const Pair (&w)[W][2], const Pair (&b)[2
 // A thread owns four channels and a strip of rows; it walks W - 1 rows past the strip's end, whose dy
 // the last gradients need, and keeps the weight gradients of its own rows.
 template <typename T, int W>
-__global__ void __launch_bounds__(kConvThreads) gdn_conv_bwd_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4) gdn_conv_bwd_kernel(const ConvParams p) {
   using Word = typename Four<T>::Word;
   constexpr int U = kConvBwdUnroll;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
@@ -231,18 +252,21 @@ __global__ void __launch_bounds__(kConvThreads) gdn_conv_bwd_kernel(const ConvPa
       before[i][1] = pair_of(f[2], f[3]);
       past[i][0] = past[i][1] = zero;
     }
-    // the gradient of row t - (W - 1), once dy[t] is there
-    auto put = [&](int t, const Pair (&dy)[2]) {
-      const int at = t - (W - 1);
-      if (at < first || at >= own) return;
-      float f[4];
+    // the gradient of the row W - 1 before that of dy: dy[at + (W - 1) - j] takes w[j]
+    auto gradient = [&](const Pair (&dy)[2], float (&f)[4]) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        Pair acc = mul2(dy[i], w[0][i]);  // dy[at + (W - 1) - j] takes w[j]
+        Pair acc = mul2(dy[i], w[0][i]);
 #pragma unroll
         for (int j = 1; j < W; ++j) acc = fma2(past[W - 1 - j][i], w[j][i], acc);
         parts_of(acc, f[2 * i], f[2 * i + 1]);
       }
+    };
+    auto put = [&](int t, const Pair (&dy)[2]) {
+      const int at = t - (W - 1);
+      if (at < first || at >= own) return;
+      float f[4];
+      gradient(dy, f);
       if (dlast && at >= end - (W - 1)) {
         float e[4];
         load4(dlast + static_cast<int64_t>(at - (end - (W - 1))) * p.D, e);
@@ -259,42 +283,69 @@ __global__ void __launch_bounds__(kConvThreads) gdn_conv_bwd_kernel(const ConvPa
         past[W - 2][i] = dy[i];
       }
     };
-    for (; row < to; row += U) {
+    // one row: its words in; `own_row` whether it is of the strip itself, `at` where the gradient of the row W - 1 before goes
+    auto step = [&](const Word& xw, const Word& gw, bool own_row, auto&& give) {
+      float f[4], g[4];
+      unpack4<T>(xw, f);
+      unpack4<T>(gw, g);
+      const Pair now[2] = {pair_of(f[0], f[1]), pair_of(f[2], f[3])};
+      Pair dy[2];
+      conv_dy<W>(w, b, before, now, g, p.silu, dy);
+      if (own_row) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) dw[j][i] = fma2(dy[i], before[j][i], dw[j][i]);
+          dw[W - 1][i] = fma2(dy[i], now[i], dw[W - 1][i]);
+          db[i] = add2(db[i], dy[i]);
+        }
+      }
+      give(dy);
+      push(dy);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int j = 0; j + 1 < W - 1; ++j) before[j][i] = before[j + 1][i];
+        before[W - 2][i] = now[i];
+      }
+    };
+    auto one = [&](int t) {
+      step(*reinterpret_cast<const Word*>(x + t * p.x_stride), *reinterpret_cast<const Word*>(dout + t * p.dout_stride), t < own,
+           [&](const Pair (&dy)[2]) { put(t, dy); });
+    };
+#pragma unroll 1
+    for (; row < min(to, first + W - 1); ++row) one(row);
+    if (row + U <= own) {  // whole steps inside the strip: no ends to look for
       Word xr[U], gr[U];
+      const T *fx = x + row * p.x_stride, *fg = dout + row * p.dout_stride;
+      T* at = dx + (row - (W - 1)) * p.dx_stride;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (row + u < to) {
-          xr[u] = *reinterpret_cast<const Word*>(x + (row + u) * p.x_stride);
-          gr[u] = *reinterpret_cast<const Word*>(dout + (row + u) * p.dout_stride);
-        }
+      for (int u = 0; u < U; ++u) {
+        xr[u] = *reinterpret_cast<const Word*>(fx + u * p.x_stride);
+        gr[u] = *reinterpret_cast<const Word*>(fg + u * p.dout_stride);
+      }
+      for (; row + U <= own; row += U) {
+        const bool more = row + 2 * U <= own;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (row + u < to) {
-          float f[4], g[4];
-          unpack4<T>(xr[u], f);
-          unpack4<T>(gr[u], g);
-          const Pair now[2] = {pair_of(f[0], f[1]), pair_of(f[2], f[3])};
-          Pair dy[2];
-          conv_dy<W>(w, b, before, now, g, p.silu, dy);
-          if (row + u < own) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-              for (int j = 0; j < W - 1; ++j) dw[j][i] = fma2(dy[i], before[j][i], dw[j][i]);
-              dw[W - 1][i] = fma2(dy[i], now[i], dw[W - 1][i]);
-              db[i] = add2(db[i], dy[i]);
-            }
+        for (int u = 0; u < U; ++u) {
+          const Word xw = xr[u], gw = gr[u];
+          if (more) {
+            xr[u] = *reinterpret_cast<const Word*>(fx + (U + u) * p.x_stride);
+            gr[u] = *reinterpret_cast<const Word*>(fg + (U + u) * p.dout_stride);
           }
-          put(row + u, dy);
-          push(dy);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int j = 0; j + 1 < W - 1; ++j) before[j][i] = before[j + 1][i];
-            before[W - 2][i] = now[i];
-          }
+          step(xw, gw, true, [&](const Pair (&dy)[2]) {
+            float f[4];
+            gradient(dy, f);
+            store4(at + u * p.dx_stride, f);
+          });
         }
+        fx += U * p.x_stride;
+        fg += U * p.dout_stride;
+        at += U * p.dx_stride;
+      }
     }
+#pragma unroll 1
+    for (; row < to; ++row) one(row);
     if (to == end) {  // nothing comes after the sequence's end
       const Pair none[2] = {zero, zero};
 #pragma unroll

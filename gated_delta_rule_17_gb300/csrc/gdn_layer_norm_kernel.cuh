@@ -11,7 +11,9 @@
 //     dx = du (or du s(z), and dz = du x s'(z))
 //
 // Bound by HBM: 4 to 10 bytes a value in 16-bit types. A group is read once and stays in the registers
-// of L lanes of a warp, or of a CTA; the variance is that of the differences from the mean, as they are there.
+// of L lanes of a warp, or of a CTA; the variance is that of the differences from the mean, as they are there. What then
+// counts are the loads under way: a lane takes several groups at once, and the backward's CTAs, which have to stay to
+// keep the columns' sums, copy the rows to come into a ring in shared memory.
 #pragma once
 #include "gdn_row_common.cuh"
 
@@ -31,6 +33,8 @@ struct LayerNormParams {
   int groups, dim;
   int rms, gate_first;
   float eps;
+  int stages;  // backward of wide groups: rows of the ring
+  unsigned* status;
 };
 
 // Sum over the L lanes (a power of two up to 32) or, for larger L, over the CTA of L threads that hold a
@@ -51,9 +55,15 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float* buf, int& turn) 
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      v[k] = 0.f;
+      float f[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < WARPS; ++i) v[k] += at[k * 32 + i];
+      for (int i = 0; i < WARPS; i += 4) {
+        float g[4];
+        load4(at + k * 32 + i, g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] += g[e];
+      }
+      v[k] = (f[0] + f[1]) + (f[2] + f[3]);
     }
   }
 }
@@ -108,223 +118,307 @@ __device__ __forceinline__ void weights8(const float* w, int c, float other, flo
 template <int L>
 constexpr int norm_threads = L > 128 ? L : 128;
 
-// Mean and 1 / deviation of the group's values u (zeros past its end, where `held` is false).
+// Groups that a lane takes at once.
 template <int L, int NV>
-__device__ __forceinline__ void norm_stats(const LayerNormParams& p, const float (&u)[NV][8], const bool (&held)[NV], float* buf, int& turn,
-                                           float& mean, float& r) {
-  const float inv = 1.f / static_cast<float>(p.dim);
-  mean = 0.f;
-  if (!p.rms) {
-    float s[1] = {0.f};
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += u[v][i];
-    group_sum<L>(s, buf, turn);
-    mean = s[0] * inv;
-  }
-  float q[1] = {0.f};
-#pragma unroll
-  for (int v = 0; v < NV; ++v)
-    if (held[v])
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[0] = fmaf(u[v][i] - mean, u[v][i] - mean, q[0]);
-  group_sum<L>(q, buf, turn);
-  r = rsqrtf(q[0] * inv + p.eps);
-}
+constexpr int norm_rows = L <= 32 && NV == 1 ? 4 : 1;
 
-// L lanes hold a group, NV words of eight values each.
+// L lanes hold a group, NV words of eight values each; R groups at once, all loads first.
 template <typename T, int L, int NV, bool kGate>
 __global__ void __launch_bounds__(norm_threads<L>) gdn_layer_norm_kernel(const LayerNormParams p) {
-  constexpr int SLOTS = norm_threads<L> / L;
-  __shared__ float buf[128];
+  constexpr int SLOTS = norm_threads<L> / L, R = norm_rows<L, NV>;
+  __shared__ __align__(16) float buf[128];
   int turn = 0;
   const int lane = threadIdx.x % L;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * SLOTS + threadIdx.x / L;
-  const bool real = item < p.items;
-  const int64_t row = real ? item / p.groups : 0;
-  const int64_t at = real ? (item - row * p.groups) * p.dim : 0;
-  Eight<T> xw[NV], zw[NV];
-  bool held[NV];
+  const uint32_t first = blockIdx.x * (SLOTS * R) + threadIdx.x / L, groups = static_cast<uint32_t>(p.groups), items = static_cast<uint32_t>(p.items);
+  Eight<T> xw[R][NV], zw[kGate ? R : 1][NV];
+  uint32_t row[R], at[R];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * L + lane) * 8;
-    held[v] = real && c < p.dim;
-    xw[v].zero();
-    zw[v].zero();
-    if (held[v]) {
-      xw[v].load(static_cast<const T*>(p.x) + row * p.x_stride + at + c);
-      if (kGate) zw[v].load(static_cast<const T*>(p.gate) + row * p.gate_stride + at + c);
+  for (int k = 0; k < R; ++k) {
+    const uint32_t item = first + k * SLOTS;
+    row[k] = item / groups;
+    at[k] = (item - row[k] * groups) * p.dim;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * L + lane) * 8;
+      xw[k][v].zero();
+      if (kGate) zw[k][v].zero();
+      if (item < items && c < p.dim) {
+        xw[k][v].load(static_cast<const T*>(p.x) + row[k] * p.x_stride + at[k] + c);
+        if (kGate) zw[k][v].load(static_cast<const T*>(p.gate) + row[k] * p.gate_stride + at[k] + c);
+      }
     }
   }
-  float u[NV][8];
+  const float inv = 1.f / static_cast<float>(p.dim);
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    xw[v].floats(u[v]);
-    if (kGate && p.gate_first) {
-      float z[8];
-      zw[v].floats(z);
+  for (int k = 0; k < R; ++k) {
+    float u[NV][8], mean = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[v][i] *= silu(z[i]);
+    for (int v = 0; v < NV; ++v) {
+      xw[k][v].floats(u[v]);
+      if (kGate && p.gate_first) {
+        float z[8];
+        zw[k][v].floats(z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[v][i] *= silu(z[i]);
+      }
     }
-  }
-  float mean, r;
-  norm_stats<L, NV>(p, u, held, buf, turn, mean, r);
+    if (!p.rms) {
+      float s[1] = {0.f};
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * L + lane) * 8;
-    if (!held[v]) continue;
-    float w[8], b[8];
-    weights8(p.weight, c, 1.f, w);
-    weights8(p.bias, c, 0.f, b);
+      for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[v][i] = fmaf((u[v][i] - mean) * r, w[i], b[i]);
-    if (kGate && !p.gate_first) {
-      float z[8];
-      zw[v].floats(z);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[v][i] *= silu(z[i]);
+        for (int i = 0; i < 8; ++i) s[0] += u[v][i];
+      group_sum<L>(s, buf, turn);
+      mean = s[0] * inv;
     }
-    store8(static_cast<T*>(p.out) + row * p.out_stride + at + c, u[v]);
+    float q[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if ((v * L + lane) * 8 < p.dim)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[0] = fmaf(u[v][i] - mean, u[v][i] - mean, q[0]);
+    group_sum<L>(q, buf, turn);
+    const float r = rsqrtf(q[0] * inv + p.eps);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * L + lane) * 8;
+      if (first + k * SLOTS >= items || c >= p.dim) continue;
+      float w[8], b[8];
+      weights8(p.weight, c, 1.f, w);
+      weights8(p.bias, c, 0.f, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[v][i] = fmaf((u[v][i] - mean) * r, w[i], b[i]);
+      if (kGate && !p.gate_first) {
+        float z[8];
+        zw[k][v].floats(z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[v][i] *= silu(z[i]);
+      }
+      store8(static_cast<T*>(p.out) + row[k] * p.out_stride + at[k] + c, u[v]);
+    }
   }
 }
 
 // ---- backward ------------------------------------------------------------------------
-// A fixed grid: a slot of L lanes walks every (grid x slots)-th group, the next one's words under way, and
-// keeps the sums of its own columns.
-template <typename T, int L, int NV, bool kGate>
-__global__ void __launch_bounds__(norm_threads<L>) gdn_layer_norm_bwd_kernel(const LayerNormParams p) {
-  constexpr int SLOTS = norm_threads<L> / L;
-  __shared__ float buf[128];
-  __shared__ float s_sum[SLOTS > 1 ? SLOTS * L * NV * 8 : 1];
-  int turn = 0;
-  const int lane = threadIdx.x % L, slot = threadIdx.x / L;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * SLOTS;
-  float dw[NV][8] = {}, db[NV][8] = {};
-  Eight<T> xw[NV], gw[NV], zw[NV];
-  auto fetch = [&](int64_t item) {
-    const bool real = item < p.items;
-    const int64_t row = real ? item / p.groups : 0, at = real ? (item - row * p.groups) * p.dim : 0;
+// One group's gradients, in the L lanes' words; dw and db take up its columns'. `read` runs once every lane has its words
+// (and its group's lanes have met, where the group is a CTA's).
+template <typename T, int L, int NV, bool kGate, typename Read>
+__device__ __forceinline__ void norm_backward(const LayerNormParams& p, const Eight<T> (&xw)[NV], const Eight<T> (&gw)[NV],
+                                              const Eight<T> (&zw)[kGate ? NV : 1], int lane, bool real, int64_t row, int64_t at, float (&dw)[NV][8],
+                                              float (&db)[NV][8], float* buf, int& turn, Read&& read) {
+  const float inv = 1.f / static_cast<float>(p.dim);
+  const bool after = kGate && !p.gate_first;
+  float u[NV][8], g[NV][8];  // g: dL/dy, before the weight
+  float sums[2] = {0.f, 0.f};
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * L + lane) * 8;
-      xw[v].zero();
-      gw[v].zero();
-      zw[v].zero();
-      if (real && c < p.dim) {
-        xw[v].load(static_cast<const T*>(p.x) + row * p.x_stride + at + c);
-        gw[v].load(static_cast<const T*>(p.dout) + row * p.dout_stride + at + c);
-        if (kGate) zw[v].load(static_cast<const T*>(p.gate) + row * p.gate_stride + at + c);
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * L + lane) * 8;
+    float w[8];
+    xw[v].floats(u[v]);
+    gw[v].floats(g[v]);
+    if constexpr (kGate) {
+      float z[8];
+      zw[v].floats(z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float s = silu(z[i]);
+        if (after) g[v][i] *= s;
+        else u[v][i] *= s;
       }
     }
-  };
-  int64_t item = static_cast<int64_t>(blockIdx.x) * SLOTS + slot;
-  fetch(item);
-  // every slot of the CTA takes as many steps, for the shuffles and barriers among them
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * SLOTS; first < p.items; first += step, item += step) {
-    const bool real = item < p.items;
-    const int64_t row = real ? item / p.groups : 0, at = real ? (item - row * p.groups) * p.dim : 0;
-    float u[NV][8], g[NV][8];
-    Eight<T> xc[NV], zc[NV];
-    bool held[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      held[v] = real && (v * L + lane) * 8 < p.dim;
-      xw[v].floats(u[v]);
-      gw[v].floats(g[v]);
-      if constexpr (kGate) {
-        xc[v] = xw[v];
-        zc[v] = zw[v];
-        if (p.gate_first) {
-          float z[8];
-          zc[v].floats(z);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) u[v][i] *= silu(z[i]);
-        }
-      }
-    }
-    fetch(item + step);
-    float mean, r;
-    norm_stats<L, NV>(p, u, held, buf, turn, mean, r);
-    float sums[2] = {0.f, 0.f};
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * L + lane) * 8;
-      if (!held[v]) continue;
-      float w[8], b[8], z[8], dz[8];
+    if (!p.rms && c < p.dim) {
       weights8(p.weight, c, 1.f, w);
-      if (kGate && !p.gate_first) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sums[0] += u[v][i];
+        sums[1] = fmaf(g[v][i], w[i], sums[1]);
+      }
+    }
+  }
+  float mean = 0.f, mt = 0.f;
+  if (!p.rms) {
+    group_sum<L>(sums, buf, turn);
+    mean = sums[0] * inv;
+    mt = sums[1] * inv;
+  }
+  sums[0] = sums[1] = 0.f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * L + lane) * 8;
+    if (c >= p.dim) continue;
+    float w[8];
+    weights8(p.weight, c, 1.f, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u[v][i] -= mean;
+      sums[0] = fmaf(u[v][i], u[v][i], sums[0]);
+      sums[1] = fmaf(g[v][i] * w[i], u[v][i], sums[1]);
+    }
+  }
+  group_sum<L>(sums, buf, turn);
+  read();
+  const float r = rsqrtf(sums[0] * inv + p.eps), mth = sums[1] * inv * r;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * L + lane) * 8;
+    if (!real || c >= p.dim) continue;
+    float w[8], dx[8];
+    weights8(p.weight, c, 1.f, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u[v][i] *= r;  // h
+      dw[v][i] = fmaf(g[v][i], u[v][i], dw[v][i]);
+      db[v][i] += g[v][i];
+      dx[i] = r * (fmaf(g[v][i], w[i], -mt) - u[v][i] * mth);
+    }
+    if constexpr (kGate) {
+      float z[8], o[8], dz[8], b[8];
+      zw[v].floats(z);
+      if (after) {
+        gw[v].floats(o);
         weights8(p.bias, c, 0.f, b);
-        zc[v].floats(z);
+      } else {
+        xw[v].floats(o);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float h = (u[v][i] - mean) * r;
-        if (kGate && !p.gate_first) {
-          const float sg = sigmoid(z[i]), s = z[i] * sg;
-          dz[i] = g[v][i] * fmaf(h, w[i], b[i]) * (sg + s * (1.f - sg));
-          g[v][i] *= s;
-        }
-        dw[v][i] = fmaf(g[v][i], h, dw[v][i]);
-        db[v][i] += g[v][i];
-        u[v][i] = h;
-        g[v][i] *= w[i];
-        sums[0] += g[v][i];
-        sums[1] = fmaf(g[v][i], h, sums[1]);
+        const float sg = sigmoid(z[i]), s = z[i] * sg, slope = fmaf(s, 1.f - sg, sg);
+        dz[i] = o[i] * slope * (after ? fmaf(u[v][i], w[i], b[i]) : dx[i]);
+        if (!after) dx[i] *= s;
       }
-      if (kGate && !p.gate_first) store8(static_cast<T*>(p.dgate) + row * p.dgate_stride + at + c, dz);
+      store8(static_cast<T*>(p.dgate) + row * p.dgate_stride + at + c, dz);
     }
-    group_sum<L>(sums, buf, turn);
-    const float inv = 1.f / static_cast<float>(p.dim), mt = p.rms ? 0.f : sums[0] * inv, mth = sums[1] * inv;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * L + lane) * 8;
-      if (!held[v]) continue;
-      float dx[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) dx[i] = r * (g[v][i] - mt - u[v][i] * mth);
-      if (kGate && p.gate_first) {
-        float x[8], z[8], dz[8];
-        xc[v].floats(x);
-        zc[v].floats(z);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float sg = sigmoid(z[i]), s = z[i] * sg;
-          dz[i] = dx[i] * x[i] * (sg + s * (1.f - sg));
-          dx[i] *= s;
-        }
-        store8(static_cast<T*>(p.dgate) + row * p.dgate_stride + at + c, dz);
-      }
-      store8(static_cast<T*>(p.out) + row * p.out_stride + at + c, dx);
+    store8(static_cast<T*>(p.out) + row * p.out_stride + at + c, dx);
+  }
+}
+
+// Groups of up to 256: a fixed grid; a slot of L lanes walks every (grid x slots)-th group, the next one's words under way.
+constexpr int kNormSmallCtas = 6;  // an SM
+
+template <typename T, int L, bool kGate>
+__global__ void __launch_bounds__(128, kGate ? 4 : kNormSmallCtas) gdn_layer_norm_bwd_kernel(const LayerNormParams p) {
+  constexpr int SLOTS = 128 / L;
+  __shared__ float s_sum[SLOTS * L * 8];
+  int turn = 0;
+  const int lane = threadIdx.x % L, slot = threadIdx.x / L, c = lane * 8;
+  const uint32_t step = gridDim.x * SLOTS, groups = static_cast<uint32_t>(p.groups), items = static_cast<uint32_t>(p.items);
+  float dw[1][8] = {}, db[1][8] = {};
+  Eight<T> xw[1], gw[1], zw[1];
+  uint32_t item = blockIdx.x * SLOTS + slot, row = item / groups, at = (item - row * groups) * p.dim;
+  auto fetch = [&] {
+    xw[0].zero();
+    gw[0].zero();
+    zw[0].zero();
+    if (item < items && c < p.dim) {
+      xw[0].load(static_cast<const T*>(p.x) + row * p.x_stride + at + c);
+      gw[0].load(static_cast<const T*>(p.dout) + row * p.dout_stride + at + c);
+      if (kGate) zw[0].load(static_cast<const T*>(p.gate) + row * p.gate_stride + at + c);
     }
+  };
+  fetch();
+  // every slot of the CTA takes as many steps, for the shuffles among them
+  for (uint32_t first = blockIdx.x * SLOTS; first < items; first += step) {
+    const Eight<T> xc[1] = {xw[0]}, gc[1] = {gw[0]}, zc[1] = {zw[0]};
+    const uint32_t now_row = row, now_at = at;
+    const bool real = item < items;
+    item += step;
+    row = item / groups;
+    at = (item - row * groups) * p.dim;
+    fetch();
+    norm_backward<T, L, 1, kGate>(p, xc, gc, zc, lane, real, now_row, now_at, dw, db, nullptr, turn, [] {});
   }
   if (!p.partials) return;
   // the CTA's sums, slot after slot
   float* out = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * p.dim;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if constexpr (SLOTS > 1) {
-      __syncthreads();
+    __syncthreads();
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+    for (int i = 0; i < 8; ++i) s_sum[slot * L * 8 + c + i] = k ? db[0][i] : dw[0][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.dim; i += 128) {
+      float acc = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s_sum[(slot * NV + v) * L * 8 + lane * 8 + i] = k ? db[v][i] : dw[v][i];
-      __syncthreads();
-      for (int c = threadIdx.x; c < p.dim; c += norm_threads<L>) {
-        float acc = 0.f;
+      for (int j = 0; j < SLOTS; ++j) acc += s_sum[j * L * 8 + i];
+      out[k * p.dim + i] = acc;
+    }
+  }
+}
+
+// Wider groups: a CTA of L threads has a group, and copies those to come into a ring of `stages` rows.
+template <typename T, int L, int NV, bool kGate>
+__global__ void __launch_bounds__(L, L == 128 ? 6 : kGate || NV > 1 || sizeof(T) == 4 ? 1 : 2) gdn_layer_norm_bwd_wide_kernel(const LayerNormParams p) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t s_full[8];
+  __shared__ __align__(16) float buf[128];
+  __shared__ uint32_t s_abort;
+  constexpr int ARRAYS = kGate ? 3 : 2;
+  const int lane = threadIdx.x;
+  const uint32_t groups = static_cast<uint32_t>(p.groups), items = static_cast<uint32_t>(p.items), step = gridDim.x;
+  const uint32_t bytes = p.dim * static_cast<uint32_t>(sizeof(T)), bars = tc::smem_u32(s_full), base = tc::smem_u32(ring);
+  int turn = 0;
+  auto copy = [&](uint32_t item, int stage) {
+    const uint32_t row = item / groups, at = (item - row * groups) * p.dim, to = base + stage * ARRAYS * bytes, bar = bars + 8 * stage;
+    tc::mbar_arrive_expect_tx(bar, ARRAYS * bytes);
+    tc::bulk_load(to, static_cast<const T*>(p.x) + row * p.x_stride + at, bytes, bar);
+    tc::bulk_load(to + bytes, static_cast<const T*>(p.dout) + row * p.dout_stride + at, bytes, bar);
+    if (kGate) tc::bulk_load(to + 2 * bytes, static_cast<const T*>(p.gate) + row * p.gate_stride + at, bytes, bar);
+  };
+  if (lane == 0) {
+    s_abort = 0;
+    for (int i = 0; i < p.stages; ++i) tc::mbar_init(bars + 8 * i, 1);
+    tc::mbar_fence_init();
+    for (int i = 0; i < p.stages; ++i)
+      if (blockIdx.x + static_cast<uint64_t>(i) * step < items) copy(blockIdx.x + i * step, i);
+  }
+  __syncthreads();
+  float dw[NV][8] = {}, db[NV][8] = {};
+  int stage = 0;
+  uint32_t phase = 0;
+  for (uint32_t item = blockIdx.x; item < items; item += step) {
+    const uint32_t row = item / groups, at = (item - row * groups) * p.dim;
+    bool there = tc::mbar_try_wait(bars + 8 * stage, phase);
+    for (int k = 0; k < (1 << 18) && !there && !*static_cast<volatile uint32_t*>(&s_abort); ++k) there = tc::mbar_try_wait_hint(bars + 8 * stage, phase, 10000u);
+    if (!there) {  // walks on with what there is, so that the barriers fill
+      s_abort = 1;
+      atomicOr(p.status, kStatusTimeout);
+    }
+    Eight<T> xw[NV], gw[NV], zw[kGate ? NV : 1];
+    const T* from = reinterpret_cast<const T*>(ring + stage * ARRAYS * bytes);
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i) acc += s_sum[i * NV * L * 8 + c];
-        out[k * p.dim + c] = acc;
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int c = (v * L + lane) * 8;
-        if (c >= p.dim) continue;
-        store4(out + k * p.dim + c, reinterpret_cast<const float(&)[4]>(k ? db[v][0] : dw[v][0]));
-        store4(out + k * p.dim + c + 4, reinterpret_cast<const float(&)[4]>(k ? db[v][4] : dw[v][4]));
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * L + lane) * 8;
+      xw[v].zero();
+      gw[v].zero();
+      if (kGate) zw[v].zero();
+      if (c < p.dim) {
+        xw[v].load(from + c);
+        gw[v].load(from + p.dim + c);
+        if (kGate) zw[v].load(from + 2 * p.dim + c);
       }
     }
+    norm_backward<T, L, NV, kGate>(p, xw, gw, zw, lane, true, row, at, dw, db, buf, turn, [&] {
+      const uint64_t next = item + static_cast<uint64_t>(p.stages) * step;
+      if (lane == 0 && next < items) copy(static_cast<uint32_t>(next), stage);
+    });
+    if (++stage == p.stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  __syncthreads();
+  if (s_abort) {  // copies in flight land before the ring is given up
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  if (!p.partials) return;
+  float* out = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * p.dim;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * L + lane) * 8;
+    if (c >= p.dim) continue;
+    store8(out + c, dw[v]);
+    store8(out + p.dim + c, db[v]);
   }
 }
 

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -25,6 +26,7 @@ int fail(int code, const char* fmt, ...) {
   return gdn_host::refuse(code, text);
 }
 
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 int launched(int launches) {
@@ -145,7 +147,7 @@ int conv_setup(const void* x, const float* weight, const float* bias, int D, int
   if (int rc = check_flag(silu, "silu")) return rc;
   if (int rc = take_stride(x_stride, D, "x", &p->x_stride)) return rc;
   if (!weight) return fail(GDN_ERR_ARG, "a required pointer is NULL");
-  if (!aligned(x, 16) || !aligned(weight, 4) || !aligned(bias, 4)) return fail(GDN_ERR_ARG, "x must be 16-byte aligned, weight and bias 4-byte");
+  if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(bias, 16)) return fail(GDN_ERR_ARG, "x, weight and bias must be 16-byte aligned");
   p->x = x;
   p->weight = weight;
   p->bias = bias;
@@ -169,26 +171,54 @@ void by_dim(int dim, F&& f) {
   else if (dim <= 4096) f(IntC<128>{}, IntC<4>{});
   else f(IntC<256>{}, IntC<4>{});
 }
-// The backward keeps the columns' sums too, so a group takes more lanes.
+// The backward keeps the columns' sums too, so a group takes more lanes: of one warp up to 256 values (f gets the lanes and 0),
+// a CTA beyond (threads, and words a thread).
 template <typename F>
 void by_dim_backward(int dim, F&& f) {
-  if (dim <= 16) f(IntC<2>{}, IntC<1>{});
-  else if (dim <= 64) f(IntC<8>{}, IntC<1>{});
-  else if (dim <= 128) f(IntC<16>{}, IntC<1>{});
-  else if (dim <= 256) f(IntC<32>{}, IntC<1>{});
+  if (dim <= 16) f(IntC<2>{}, IntC<0>{});
+  else if (dim <= 64) f(IntC<8>{}, IntC<0>{});
+  else if (dim <= 128) f(IntC<16>{}, IntC<0>{});
+  else if (dim <= 256) f(IntC<32>{}, IntC<0>{});
   else if (dim <= 1024) f(IntC<128>{}, IntC<1>{});
   else if (dim <= 4096) f(IntC<512>{}, IntC<1>{});
   else f(IntC<512>{}, IntC<2>{});
 }
 
-int norm_bwd_ctas(int64_t items, int dim, int sms) {
-  int ctas = 0;
-  by_dim_backward(dim, [&](auto lanes, auto) {
-    const int slots = gdn::norm_threads<lanes.value> / lanes.value;
-    const int64_t need = (items + slots - 1) / slots, most = static_cast<int64_t>(sms) * (lanes.value > 128 ? 2 : 8);
-    ctas = static_cast<int>(need < most ? need : most);
+// CTAs and ring of the backward. The ring's stages fill what an SM's CTAs share of 200 KB, eight at most.
+struct NormPlan {
+  int ctas, stages, ring;
+};
+NormPlan norm_plan(int64_t items, int dim, int sms, bool gate, int element) {
+  NormPlan p{};
+  by_dim_backward(dim, [&](auto lanes, auto words) {
+    constexpr int L = lanes.value;
+    int per_sm = gate ? 4 : gdn::kNormSmallCtas;
+    int64_t need = (items + 128 / (L < 128 ? L : 128) - 1) / (128 / (L < 128 ? L : 128));
+    if (words.value) {
+      const int stage = (gate ? 3 : 2) * dim * element;
+      per_sm = L == 128 ? 6 : gate || words.value > 1 || element == 4 ? 1 : 2;
+      p.stages = 200 * 1024 / per_sm / stage;
+      if (p.stages > 8) p.stages = 8;
+      p.ring = p.stages * stage;
+      need = items;
+    }
+    const int64_t most = static_cast<int64_t>(sms) * per_sm;
+    p.ctas = static_cast<int>(need < most ? need : most);
   });
-  return ctas;
+  return p;
+}
+
+// Lets a kernel take the ring's shared memory, once a device (the types name the kernel).
+template <typename T, int L, int NV, bool G>
+int allow_shared(const void* kernel) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < 64 && (done.load() >> dev & 1)) return GDN_OK;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  if (dev < 64) done.fetch_or(uint64_t{1} << dev);
+  return GDN_OK;
 }
 
 int layer_norm_setup(const void* x, const void* gate, const float* weight, const float* bias, float eps, int rows, int groups, int dim,
@@ -211,7 +241,7 @@ int layer_norm_setup(const void* x, const void* gate, const float* weight, const
   if (!aligned(x, 16) || !aligned(gate, 16) || !aligned(weight, 16) || !aligned(bias, 16))
     return fail(GDN_ERR_ARG, "x, gate, weight and bias must be 16-byte aligned");
   p->items = static_cast<int64_t>(rows) * groups;
-  if (p->items > INT32_MAX - 65536) return fail(GDN_ERR_UNSUPPORTED, "%d rows of %d groups exceed the item range", rows, groups);
+  if (p->items > INT32_MAX - 65536 || width > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%d rows of %d groups exceed the item range", rows, groups);
   if (rows && !x) return fail(GDN_ERR_ARG, "a required pointer is NULL");
   p->x = x;
   p->gate = gate;
@@ -284,6 +314,49 @@ int ssm_map(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int64
   return GDN_OK;
 }
 
+// CTAs of a sequence: two slices of 64 value columns of one key head each.
+int ssm_pairs(int nk, int nv, int dv) { return nk * ((nv / nk * (dv / 64) + 1) / 2); }
+
+// Segments of the scan: how many chunks each (0: whole sequences), the items (sequences or segments) that there may be, and
+// the workspace for them.
+struct SsmSegments {
+  int segment, items;
+  size_t states, total;
+};
+SsmSegments ssm_segments(int64_t B, int64_t T, bool varlen, int pairs, int nv, int dk, int dv, int sms) {
+  SsmSegments r{0, static_cast<int>(B), 0, 0};
+  const int64_t chunks = (T + gdn::kSsmChunk - 1) / gdn::kSsmChunk;
+  if (!varlen) {
+    // n segments of `per` chunks: the passes of all CTAs, the first of segments 1 to n - 1 at 0.6 of a chunk's time, and what a pass costs
+    // by itself, about three chunks' time
+    auto passes = [&](int64_t ctas) { return static_cast<double>((ctas + sms - 1) / sms); };
+    double best = passes(B * pairs) * static_cast<double>(chunks);
+    for (int n = 2; n <= 32; ++n) {
+      const int64_t per = (chunks + n - 1) / n;
+      if (per < 4) break;
+      const double time = passes(B * pairs * (n - 1)) * (0.6 * static_cast<double>(per) + 3) + passes(B * pairs * n) * static_cast<double>(per) + 3 + 0.1 * n;
+      if (time < 0.9 * best) {
+        best = time;
+        r.segment = static_cast<int>(per);
+      }
+    }
+    if (r.segment) r.items = static_cast<int>(B * ((chunks + r.segment - 1) / r.segment));
+  } else if (B > 0 && B <= 32) {
+    // the lengths are the device's to see; it takes segments where the longest sequence stands out. Of half the chunks that every SM would
+    // have of an even share
+    const int64_t per = (chunks * pairs / sms + 1) / 2, segment = per < 8 ? 8 : per;
+    if (chunks / B > 0 && chunks > 4 * segment) {
+      r.segment = static_cast<int>(segment);
+      r.items = static_cast<int>(B + chunks / segment + 1);
+    }
+  }
+  if (r.segment) {
+    r.states = align256(static_cast<size_t>(r.items + 1) * nv * dk * dv * sizeof(float));
+    r.total = r.states + align256(static_cast<size_t>(r.items) * nv * sizeof(float));
+  }
+  return r;
+}
+
 // Shared memory of the scan's kernels, once a device.
 int ssm_attributes() {
   static std::mutex mu;
@@ -295,8 +368,9 @@ int ssm_attributes() {
   for (int dk : {64, 128})
     for (int dv : {64, 128})
       by_state(dk, dv, [&](auto K, auto V) {
-        if (e == cudaSuccess)
-          e = cudaFuncSetAttribute(gdn::gdn_ssm_scan_kernel<K.value, V.value>, cudaFuncAttributeMaxDynamicSharedMemorySize, gdn::SsmPlan::DYN_SMEM);
+        for (const void* f : {reinterpret_cast<const void*>(gdn::gdn_ssm_scan_kernel<K.value, V.value, true>),
+                              reinterpret_cast<const void*>(gdn::gdn_ssm_scan_kernel<K.value, V.value, false>)})
+          if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, gdn::SsmPlan::DYN_SMEM);
       });
   if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   if (dev < 64) done[dev] = true;
@@ -410,9 +484,9 @@ int gdn_causal_conv_backward(const void* x, const float* weight, const float* bi
   return release(need ? workspace : nullptr, ws, s, launched((rows > 0) + (sum_ctas + end_ctas > 0)));
 }
 
-size_t gdn_ssm_scan_workspace_bytes(int B, int T, int nv, int dk, int dv, int varlen) {
-  (void)B; (void)T; (void)nv; (void)dk; (void)dv; (void)varlen;
-  return 0;
+size_t gdn_ssm_scan_workspace_bytes(int B, int T, int nk, int nv, int dk, int dv, int varlen) {
+  if (B <= 0 || T <= 0 || nk < 1 || nv < 1 || nv % nk || (dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return 0;
+  return ssm_segments(B, T, varlen != 0, ssm_pairs(nk, nv, dv), nv, dk, dv, gdn_host::plan_sms()).total;
 }
 
 int gdn_ssm_scan(const void* q, const void* k, const void* v, const void* dt, const float* a, const float* dt_bias, const float* skip,
@@ -424,24 +498,35 @@ int gdn_ssm_scan(const void* q, const void* k, const void* v, const void* dt, co
   const int rows = B == 0 ? 0 : p.batch.rows;
   if (int rc = ssm_setup(q, k, v, dt, a, dt_bias, skip, state, out, nk, nv, dk, dv, options, rows, &p)) return rc;
   if (rows == 0) return GDN_OK;
-  if (int rc = check_workspace(workspace, workspace_bytes, 0)) return rc;
   int sms = 0;
   if (int rc = gdn_host::device(&sms, &p.status)) return rc;
+  gdn::SsmScanParams sp{};
+  sp.pairs = ssm_pairs(nk, nv, dv);
+  sp.sms = sms;
+  const SsmSegments seg = ssm_segments(B, T, cu_seqlens != nullptr, sp.pairs, nv, dk, dv, sms);
+  if (static_cast<int64_t>(seg.items) * sp.pairs > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%d sequences of %d heads exceed the item range", B, nv);
+  if (seg.total)
+    if (int rc = check_workspace(workspace, workspace_bytes, seg.total)) return rc;
   if (int rc = ssm_attributes()) return rc;
   CUtensorMap q_map, k_map, v_map, out_map;
   if (int rc = ssm_map(&q_map, q, static_cast<int64_t>(nk) * dk, rows, p.q_stride, "q")) return rc;
   if (int rc = ssm_map(&k_map, k, static_cast<int64_t>(nk) * dk, rows, p.k_stride, "k")) return rc;
   if (int rc = ssm_map(&v_map, v, static_cast<int64_t>(nv) * dv, rows, p.v_stride, "v")) return rc;
   if (int rc = ssm_map(&out_map, out, static_cast<int64_t>(nv) * dv, rows, p.out_stride, "out")) return rc;
-  gdn::SsmScanParams sp{};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* given = seg.total ? workspace : nullptr;
+  void* ws = nullptr;
+  if (int rc = acquire(given, seg.total, s, &ws)) return rc;
   sp.s = p;
-  sp.pairs = nk * ((nv / nk * (dv / 64) + 1) / 2);
-  if (static_cast<int64_t>(B) * sp.pairs > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%d sequences of %d heads exceed the item range", B, nv);
+  sp.segment = seg.segment;
+  sp.states = static_cast<float*>(ws);
+  sp.decays = seg.total ? reinterpret_cast<float*>(static_cast<char*>(ws) + seg.states) : nullptr;
+  const int grid = seg.items * sp.pairs;
   by_state(dk, dv, [&](auto K, auto V) {
-    gdn::gdn_ssm_scan_kernel<K.value, V.value>
-        <<<B * sp.pairs, gdn::kSsmThreads, gdn::SsmPlan::DYN_SMEM, static_cast<cudaStream_t>(stream)>>>(q_map, k_map, v_map, out_map, sp);
+    if (seg.segment) gdn::gdn_ssm_scan_kernel<K.value, V.value, false><<<grid, gdn::kSsmThreads, gdn::SsmPlan::DYN_SMEM, s>>>(q_map, k_map, v_map, out_map, sp);
+    gdn::gdn_ssm_scan_kernel<K.value, V.value, true><<<grid, gdn::kSsmThreads, gdn::SsmPlan::DYN_SMEM, s>>>(q_map, k_map, v_map, out_map, sp);
   });
-  return launched(1);
+  return release(given, ws, s, launched(seg.segment ? 2 : 1));
 }
 
 int gdn_ssm_decode(const void* q, const void* k, const void* v, const void* dt, const float* a, const float* dt_bias, const float* skip,
@@ -476,7 +561,7 @@ int gdn_layer_norm(const void* x, const void* gate, const float* weight, const f
   by_type(dtype, [&](auto t) {
     by_dim(dim, [&](auto lanes, auto words) {
       constexpr int L = lanes.value, threads = gdn::norm_threads<L>;
-      const int grid = ceil_div(p.items, threads / L);
+      const int grid = ceil_div(p.items, threads / L * gdn::norm_rows<L, words.value>);
       if (gate) gdn::gdn_layer_norm_kernel<decltype(t), L, words.value, true><<<grid, threads, 0, s>>>(p);
       else gdn::gdn_layer_norm_kernel<decltype(t), L, words.value, false><<<grid, threads, 0, s>>>(p);
     });
@@ -486,7 +571,8 @@ int gdn_layer_norm(const void* x, const void* gate, const float* weight, const f
 
 size_t gdn_layer_norm_backward_workspace_bytes(int rows, int groups, int dim) {
   if (rows <= 0 || groups < 1 || dim < 8 || dim % 8 || dim > kNormMaxDim) return 0;
-  return static_cast<size_t>(norm_bwd_ctas(static_cast<int64_t>(rows) * groups, dim, gdn_host::plan_sms())) * 2 * dim * sizeof(float);
+  // (without a gate there are as many CTAs as with one, or more)
+  return static_cast<size_t>(norm_plan(static_cast<int64_t>(rows) * groups, dim, gdn_host::plan_sms(), false, 2).ctas) * 2 * dim * sizeof(float);
 }
 
 int gdn_layer_norm_backward(const void* x, const void* gate, const float* weight, const float* bias, float eps, const void* dout, void* dx,
@@ -520,16 +606,34 @@ int gdn_layer_norm_backward(const void* x, const void* gate, const float* weight
   void* ws = nullptr;
   if (int rc = acquire(need ? workspace : nullptr, need, s, &ws)) return rc;
   p.partials = static_cast<float*>(ws);
-  const int ctas = norm_bwd_ctas(p.items, dim, sms);
-  by_type(dtype, [&](auto t) {
+  const NormPlan plan = norm_plan(p.items, dim, sms, gate != nullptr, dtype == GDN_F32 ? 4 : 2);
+  p.stages = plan.stages;
+  p.status = status;
+  int rc = GDN_OK;
+  by_type(dtype, [&](auto type) {
+    using T = decltype(type);
     by_dim_backward(dim, [&](auto lanes, auto words) {
-      constexpr int L = lanes.value, threads = gdn::norm_threads<L>;
-      if (gate) gdn::gdn_layer_norm_bwd_kernel<decltype(t), L, words.value, true><<<ctas, threads, 0, s>>>(p);
-      else gdn::gdn_layer_norm_bwd_kernel<decltype(t), L, words.value, false><<<ctas, threads, 0, s>>>(p);
+      constexpr int L = lanes.value, NV = words.value;
+      auto go = [&](auto gated) {
+        constexpr bool G = gated.value;
+        if constexpr (NV == 0) {
+          gdn::gdn_layer_norm_bwd_kernel<T, L, G><<<plan.ctas, 128, 0, s>>>(p);
+        } else {
+          auto kernel = gdn::gdn_layer_norm_bwd_wide_kernel<T, L, NV, G>;
+          rc = allow_shared<T, L, NV, G>(reinterpret_cast<const void*>(kernel));
+          if (rc == GDN_OK) kernel<<<plan.ctas, L, plan.ring, s>>>(p);
+        }
+      };
+      if (gate) go(std::true_type{});
+      else go(std::false_type{});
     });
   });
-  if (sums) launch_early(gdn::gdn_layer_norm_sum_kernel, ceil_div(2 * dim, 32), 1024, s, static_cast<const float*>(p.partials), ctas, dim, dweight, dbias);
-  return release(need ? workspace : nullptr, ws, s, launched(sums ? 2 : 1));
+  if (rc == GDN_OK) {
+    if (sums)
+      launch_early(gdn::gdn_layer_norm_sum_kernel, ceil_div(2 * dim, 32), 1024, s, static_cast<const float*>(p.partials), plan.ctas, dim, dweight, dbias);
+    rc = launched(sums ? 2 : 1);
+  }
+  return release(need ? workspace : nullptr, ws, s, rc);
 }
 
 }  // extern "C"

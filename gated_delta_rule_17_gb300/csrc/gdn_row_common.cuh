@@ -152,9 +152,15 @@ __device__ __forceinline__ void load32(const void* src, uint32_t* r, bool wide) 
   }
 }
 
-// 1 / (1 + e^-y). e^-y past fp32's range gives 0, as does a sum that the division cannot take.
-__device__ __forceinline__ float sigmoid(float y) { return __fdividef(1.f, 1.f + __expf(-y)); }
-__device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
+// 1 / (1 + e^-y), y of it, in two operations of the special function unit: the plain exponential and division cost
+// twice the instructions for results in the subnormal range. Where e^-y passes fp32's range they give 0.
+__device__ __forceinline__ float sigmoid(float y) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+__device__ __forceinline__ float silu(float y) { return y * sigmoid(y); }
 
 // The packed rows of a batch: sequence s owns rows [start(s), end(s)), from cu_seqlens, or T rows each.
 struct Rows {

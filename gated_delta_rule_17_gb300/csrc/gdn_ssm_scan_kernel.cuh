@@ -38,12 +38,18 @@ template <int N>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr float kSsmSpan = 140.f;  // nats that a chunk may decay for its decays to go into its operands
 
+// A CTA's part: a sequence, a segment of it, and the item of the sequence's first segment.
+struct SsmPlace {
+  int seq, seg, segs, first;
+};
+
 // What the roles tell one another beside tiles.
 struct SsmSmall {
   uint64_t bar[16];
   float suf[2][kSsmChunk], d[2][kSsmChunk];  // of each unit's tokens
   float total[2][2];                         // by chunk parity: each unit's decay
   uint32_t tmem, abort;
+  SsmPlace place;
 };
 
 struct SsmPlan {
@@ -58,8 +64,60 @@ struct SsmPlan {
 
 struct SsmScanParams {
   SsmParams s;
-  int pairs;  // CTAs of a sequence
+  int pairs;      // CTAs of a sequence, or of a segment of one
+  int sms;
+  int segment;    // chunks of a segment; 0: whole sequences
+  float* states;  // segments: [item][nv][DK][DV], item i the state that segment i starts from: S_0 of the first, the end of the first from
+                  // S_0, and behind it each segment's end from zero
+  float* decays;  // [item][nv]: the decay over segment i, as a logarithm
 };
+
+// Found by one warp. Sequences go by themselves, the longest first, or (where `segment` is given, and the longest of them would
+// keep most SMs waiting) in segments: then the state at the end of each segment but the last is worked out first, which takes a
+// little over half of a segment's time again.
+__device__ __forceinline__ SsmPlace ssm_place(const SsmScanParams& params, int item) {
+  const Rows& b = params.s.batch;
+  const int lane = threadIdx.x & 31, seg = params.segment;
+  if (!b.cu) {
+    const int n = seg ? ((b.T + kSsmChunk - 1) / kSsmChunk + seg - 1) / seg : 1;
+    return {item / n, item % n, n, item - item % n};
+  }
+  if (b.B > 32) return {item < b.B ? item : -1, 0, 1, item};
+  int chunks = 0;
+  if (lane < b.B) {
+    const int start = b.start(lane), end = b.end(lane);
+    if (rows_held(start, end, b.rows)) chunks = (end - start + kSsmChunk - 1) / kSsmChunk;
+  }
+  const int longest = __reduce_max_sync(0xffffffffu, chunks), total = __reduce_add_sync(0xffffffffu, chunks);
+  const float even = static_cast<float>(total) * params.pairs / params.sms, whole = fmaxf(even, longest);
+  SsmPlace r{-1, 0, 1, item};
+  unsigned found;
+  if (seg && whole > 1.2f * (1.6f * even + 1.6f * seg + 4.f)) {
+    const int n = (chunks + seg - 1) / seg;
+    int before = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
+    before -= n;
+    found = __ballot_sync(0xffffffffu, item >= before && item < before + n);
+    const int src = found ? __ffs(found) - 1 : 0;
+    r.first = __shfl_sync(0xffffffffu, before, src);
+    r.segs = __shfl_sync(0xffffffffu, n, src);
+    r.seg = item - r.first;
+  } else {
+    int rank = 0;
+#pragma unroll 4
+    for (int o = 0; o < 32; ++o) {
+      const int other = __shfl_sync(0xffffffffu, chunks, o);
+      rank += other > chunks || (other == chunks && o < lane);
+    }
+    found = __ballot_sync(0xffffffffu, rank == item);
+  }
+  r.seq = found && __ffs(found) - 1 < b.B ? __ffs(found) - 1 : -1;
+  return r;
+}
 
 constexpr int kSsmWaits = 1 << 18;  // tries of up to 10 us each before a wait gives up
 
@@ -102,7 +160,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Whether either unit's chunk decays by more than kSsmSpan (the same for all roles).
 __device__ __forceinline__ bool ssm_wide(const float (&total)[2]) { return !(fminf(total[0], total[1]) >= -kSsmSpan); }
 
-template <int DK, int DV>
+// kOut false: the states at the ends of the segments, without outputs.
+template <int DK, int DV, bool kOut>
 __global__ void __launch_bounds__(kSsmThreads, 1)
 gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap out_map,
@@ -116,17 +175,26 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const SsmShared sh{tc::smem_u32(small.bar), &small.abort};
 
-  const int pair = static_cast<int>(blockIdx.x % static_cast<unsigned>(params.pairs)), seq = static_cast<int>(blockIdx.x / static_cast<unsigned>(params.pairs));
+  const int pair = static_cast<int>(blockIdx.x % static_cast<unsigned>(params.pairs)), item = static_cast<int>(blockIdx.x / static_cast<unsigned>(params.pairs));
   const int heads = p.nv / p.nk, units = heads * SLICES, per_key = (units + 1) / 2;  // of a key head
   const int kh = pair / per_key;
-  const int start = p.batch.start(seq), end = p.batch.end(seq);
-  if (pair == 0 && threadIdx.x == 0) p.batch.report(seq, p.status);
-  if (!rows_held(start, end, p.batch.rows) || start == end) return;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.batch.B; i += kSsmThreads) p.batch.report(i, p.status);
+  if (warp == 0) {
+    const SsmPlace found = ssm_place(params, item);
+    if (lane == 0) small.place = found;
+  }
+  __syncthreads();
+  const SsmPlace place = small.place;
+  if (place.seq < 0 || (!kOut && place.seg == place.segs - 1)) return;
+  const int seq = place.seq, begin = p.batch.start(seq), end = p.batch.end(seq);
+  if (!rows_held(begin, end, p.batch.rows) || begin == end) return;
   if (sbase & 1023) {  // the swizzled tiles' place; the linker keeps it
     if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
     return;
   }
-  const int tokens = end - start, chunks = (tokens + kSsmChunk - 1) / kSsmChunk;
+  const int start = begin + place.seg * params.segment * kSsmChunk;
+  const int tokens = place.seg < place.segs - 1 ? params.segment * kSsmChunk : end - start, chunks = (tokens + kSsmChunk - 1) / kSsmChunk;
 
   if (threadIdx.x == 0) {
     small.abort = 0;
@@ -154,17 +222,39 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       // ---- a row of S, and of the outputs ------------------------------------------------
       more_registers<kSsmRowRegs>();
       const float skip = p.skip ? p.skip[h] : 0.f;
-      float* S = ssm_state<DK, DV>(p, seq, h) + static_cast<int64_t>(t) * DV + unit % SLICES * 64;
+      const int64_t in_head = static_cast<int64_t>(t) * DV + unit % SLICES * 64;
+      float* S = ssm_state<DK, DV>(p, seq, h) + in_head;
+      auto kept = [&](int i) { return params.states + (static_cast<int64_t>(i) * p.nv + h) * (DK * DV) + in_head; };
+      const bool held = real && t < DK;
       float s[64];
+      auto load = [&](const float* from, float keep) {  // s keep + from
 #pragma unroll
-      for (int i = 0; i < 64; i += 4) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (real && t < DK) v = *reinterpret_cast<const float4*>(S + i);
-        s[i] = v.x;
-        s[i + 1] = v.y;
-        s[i + 2] = v.z;
-        s[i + 3] = v.w;
+        for (int i = 0; i < 64; i += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(from + i);
+          s[i] = fmaf(s[i], keep, v.x);
+          s[i + 1] = fmaf(s[i + 1], keep, v.y);
+          s[i + 2] = fmaf(s[i + 2], keep, v.z);
+          s[i + 3] = fmaf(s[i + 3], keep, v.w);
+        }
+      };
+      auto save = [&](float* to) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+      };
+#pragma unroll
+      for (int i = 0; i < 64; ++i) s[i] = 0.f;
+      if (held) {
+        if constexpr (kOut) {
+          // of a segment: what the segments before it leave, one after the other
+#pragma unroll 1
+          for (int i = place.segs == 1 ? 0 : min(place.seg, 1); i <= place.seg; ++i)
+            load(place.segs == 1 ? S : kept(place.first + i), i > 1 ? __expf(params.decays[static_cast<int64_t>(place.first + i - 1) * p.nv + h]) : 0.f);
+        } else if (place.seg == 0) {
+          load(S, 0.f);
+          save(kept(item));  // the last segment writes its end over S_0
+        }
       }
+      float decay = 0.f;
       uint8_t* s16 = smem + P::S16 + x * P::BLOCK;
       uint8_t* rows = smem + P::ROWS + x * P::BLOCK;
       const Pair by_v = pair_of(skip, skip);
@@ -173,7 +263,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         float r1, r2, keep, grow;
         bool wide;
       };
-      auto factors = [&](int c) {
+      [[maybe_unused]] auto factors = [&](int c) {
         sh.wait(P::GATES, c & 1, ok);
         const float suf = small.suf[x][t], total = small.total[c & 1][x];
         Factors f;
@@ -184,6 +274,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         f.r2 = __expf(total - suf);
         f.keep = __expf(total);
         f.grow = __expf(mid);
+        if (!kOut) decay += total;
         return f;
       };
       Factors now = factors(0);
@@ -191,7 +282,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       bool wide = false;
       for (int c = 0; c <= chunks; ++c) {
         const uint32_t ph = c & 1;
-        if (c < chunks) {  // S for the products, with what it decays by beside V' where they share an accumulator
+        if (kOut && c < chunks) {  // S for the products, with what it decays by beside V' where they share an accumulator
           const float to16 = now.wide ? 1.f : now.grow;  // e^{total - mid}
           const Pair by = pair_of(to16, to16);
 #pragma unroll
@@ -205,7 +296,11 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           tc::fence_before_sync();
           sh.arrive(P::S_READY);
         }
-        if (c > 0) {  // the rows of the chunk before
+        if (!kOut && c < chunks) {  // L has been read
+          tc::fence_before_sync();
+          sh.arrive(P::S_READY);
+        }
+        if (kOut && c > 0) {  // the rows of the chunk before
           const uint32_t from = tmem + lanes + P::COL_O + 64 * x, off = (c & 1) ? 0 : 128;  // its buffer
           sh.wait(P::X_FULL, ph ^ 1, ok);  // (its O is complete: L was, which comes after)
           const Pair by1 = pair_of(f1, f1), by2 = pair_of(f2, f2);
@@ -283,9 +378,12 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           }
         }
       }
-      if (ok && real && t < DK) {
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) *reinterpret_cast<float4*>(S + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+      if (ok && held) {
+        if (kOut && place.seg == place.segs - 1) save(S);
+        if (!kOut) {
+          save(kept(item + 1));
+          if (t == 0 && unit % SLICES == 0) params.decays[static_cast<int64_t>(item) * p.nv + h] = decay;
+        }
       }
     } else {
       // ---- operands --------------------------------------------------------------------------
@@ -318,7 +416,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         }
         sh.wait(P::GATES, ph, ok);
         const bool wide = ssm_wide(small.total[ph]);
-        const float suf = small.suf[x][t], f = small.d[x][t] * __expf(wide ? suf : fmaf(-0.5f, small.total[ph][x], suf));
+        const float suf = small.suf[x][t], d = small.d[x][t], f = d * __expf(wide ? suf : fmaf(-0.5f, small.total[ph][x], suf));
         const float f_hi = __bfloat162float(__float2bfloat16_rn(f));
         const uint32_t both = pack2<__nv_bfloat16>(f_hi, f - f_hi);
         if (c > 0) sh.wait(P::L_FULL, ph ^ 1, ok);  // V is free
@@ -339,7 +437,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           *reinterpret_cast<uint4*>(hi + at) = make_uint4(a4[0], a4[1], a4[2], a4[3]);
           *reinterpret_cast<uint4*>(lo + at) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
         }
-        if (wide && n < kSsmChunk) {  // nor of v, which O then takes itself
+        if (kOut && wide && n < kSsmChunk) {  // nor of v, which O then takes itself
           sh.wait(P::X_FULL, ph, ok);
 #pragma unroll 1
           for (int i = threadIdx.x - 256; i < (kSsmChunk - n) * 16; i += 256)
@@ -347,41 +445,47 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         }
         tc::fence_proxy_async();
         sh.arrive(P::V_READY);
-        sh.wait(P::G_FULL, ph, ok);
-        // A: row t, columns 16 i .. 16 i + 15, of which it sees those up to itself. Half of it in place of this half of G;
-        // where the decay is wide all of the unit's own, in place of its L, once that has been read.
-        if (wide) sh.wait(P::S_READY, ph, ok);
-        tc::fence_after_sync();
-        const int first = wide ? 0 : 4 * x, last = wide ? 8 : first + 4;
-        const uint32_t to = tmem + lanes + (wide ? P::COL_L + 64 * x : P::COL_G + 32 * x);
-        const float own = suf * kLog2e;
-#pragma unroll 1
-        for (int i = first; i < last; ++i) {
-          uint32_t r[16], k16[8];
-          const int seen = t - 16 * i;
-          if (i <= 2 * quarter + 1) {
-            tc::tmem_ld16u(tmem + lanes + P::COL_G + 16 * i, r);
-            tc::tmem_ld_wait16(r);
-            if (wide) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                r[e] = __float_as_uint(__uint_as_float(r[e]) * (small.d[x][16 * i + e] * ssm_exp2(fmaf(small.suf[x][16 * i + e], kLog2e, -own))));
-            }
-            if (i >= 2 * quarter) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = e <= seen ? r[e] : 0u;
-            }
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) k16[e / 2] = pack2<__nv_bfloat16>(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) k16[e] = 0;
+        if constexpr (kOut) {
+          sh.wait(P::G_FULL, ph, ok);
+          // A: row t, columns 16 i .. 16 i + 15, of which it sees those up to itself. Half of it in place of this half of G;
+          // where the decay is wide and the units are two heads all of the unit's own, in place of its L, once that has been read.
+          const bool own_a = wide && SLICES == 1;
+          if (own_a) sh.wait(P::S_READY, ph, ok);
+          if (wide) {  // log2 of d e^{suf} in the place of d
+            small.d[x][t] = fmaf(suf, kLog2e, __log2f(d));
+            tc::named_barrier(5 + x, 128);
           }
-          tc::tmem_st8(to + 8 * i, k16);
+          tc::fence_after_sync();
+          const int first = own_a ? 0 : 4 * x, last = own_a ? 8 : first + 4;
+          const uint32_t to = tmem + lanes + (own_a ? P::COL_L + 64 * x : P::COL_G + 32 * x);
+          const float own = suf * kLog2e;
+#pragma unroll 1
+          for (int i = first; i < last; ++i) {
+            uint32_t r[16], k16[8];
+            const int seen = t - 16 * i;
+            if (i <= 2 * quarter + 1) {
+              tc::tmem_ld16u(tmem + lanes + P::COL_G + 16 * i, r);
+              tc::tmem_ld_wait16(r);
+              if (wide) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * ssm_exp2(small.d[x][16 * i + e] - own));
+              }
+              if (i >= 2 * quarter) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) r[e] = e <= seen ? r[e] : 0u;
+              }
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) k16[e / 2] = pack2<__nv_bfloat16>(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) k16[e] = 0;
+            }
+            tc::tmem_st8(to + 8 * i, k16);
+          }
+          tc::tmem_st_wait();
+          tc::fence_before_sync();
+          sh.arrive(P::A_READY);
         }
-        tc::tmem_st_wait();
-        tc::fence_before_sync();
-        sh.arrive(P::A_READY);
         if (c + 1 < chunks) fetch(c + 1);
       }
     }
@@ -399,7 +503,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         }
         __syncwarp();
       };
-      copy(&q_map, P::Q, P::Q_FULL, 0);
+      if (kOut) copy(&q_map, P::Q, P::Q_FULL, 0);
       copy(&k_map, P::K, P::K_FULL, 0);
       const uint64_t q_k = tc::desc_sw128(sbase + P::Q, 16, 1024), s_mn = tc::desc_sw128(sbase + P::S16, P::BLOCK, 1024);
       const uint64_t v_mn = tc::desc_sw128(sbase + P::ROWS, P::BLOCK, 1024);
@@ -409,11 +513,11 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         const uint32_t ph = c & 1;
         const int kt = P::K + ph * 2 * P::BLOCK;
         const uint64_t k_k = tc::desc_sw128(sbase + kt, 16, 1024), k_mn = tc::desc_sw128(sbase + kt, P::BLOCK, 1024);
-        sh.wait(P::Q_FULL, ph, ok);
+        if (kOut) sh.wait(P::Q_FULL, ph, ok);
         sh.wait(P::K_FULL + ph, (c >> 1) & 1, ok);
         if (!ok) break;
         tc::fence_after_sync();
-        if (tc::elect_one()) {
+        if (kOut && tc::elect_one()) {
 #pragma unroll 2
           for (int i = 0; i < DK / 16; ++i) {
             const uint32_t off = ((i >> 2) * P::BLOCK + (i & 3) * 32) >> 4;
@@ -427,46 +531,60 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           if (!ok) break;
           copy(&k_map, P::K + (ph ^ 1) * 2 * P::BLOCK, P::K_FULL + (ph ^ 1), c + 1);
         }
-        sh.wait(P::S_READY, ph, ok);
-        if (!ok) break;
-        // the chunk's buffer of O, and where the decay is wide the other for O1
-        const bool wide = ssm_wide(small.total[ph]);
-        const uint32_t o = tmem + P::COL_O + ph * 128, o1 = wide ? tmem + P::COL_O + (ph ^ 1) * 128 : o;
-        if (c > 1) sh.wait(P::O_READ + ph, ((c >> 1) - 1) & 1, ok);
-        if (c > 0 && (wide || was_wide)) sh.wait(P::O_READ + (ph ^ 1), ((c - 1) >> 1) & 1, ok);
-        was_wide = wide;
-        if (!ok) break;
-        tc::fence_after_sync();
-        if (tc::elect_one()) {
-#pragma unroll 2
-          for (int i = 0; i < DK / 16; ++i) {
-            const uint32_t off = ((i >> 2) * P::BLOCK + (i & 3) * 32) >> 4;
-            tc::mma_f16(o, q_k + off, s_mn + ((i * 2048) >> 4), id_o, i > 0);
-          }
-          tc::mma_commit(sh.bar(P::Q_FREE));
-        }
-        __syncwarp();
-        sh.wait(P::V_READY, ph, ok);
-        sh.wait(P::A_READY, ph, ok);
-        if (wide) sh.wait(P::X_FULL, ph, ok);
-        if (!ok) break;
-        tc::fence_after_sync();
-        if (tc::elect_one()) {
-          if (!wide) {
-#pragma unroll 2
-            for (int i = 0; i < 8; ++i) tc::mma_f16_ts(o, tmem + P::COL_G + 8 * i + (i & 4) * 8, hi_mn + ((i * 2048) >> 4), id_o, 1);
-          } else {
-            for (int u = 0; u < 2; ++u)
-#pragma unroll 2
-              for (int i = 0; i < 8; ++i)
-                tc::mma_f16_ts(o1 + 64 * u, tmem + P::COL_L + 64 * u + 8 * i, v_mn + ((u * P::BLOCK + i * 2048) >> 4), id_o64, i > 0);
-          }
-        }
-        __syncwarp();
-        if (c + 1 < chunks) {
-          sh.wait(P::Q_FREE, ph, ok);
+        if constexpr (kOut) {
+          sh.wait(P::S_READY, ph, ok);
           if (!ok) break;
-          copy(&q_map, P::Q, P::Q_FULL, c + 1);
+          // the chunk's buffer of O, and where the decay is wide the other for O1
+          const bool wide = ssm_wide(small.total[ph]);
+          const uint32_t o = tmem + P::COL_O + ph * 128, o1 = wide ? tmem + P::COL_O + (ph ^ 1) * 128 : o;
+          if (c > 1) sh.wait(P::O_READ + ph, ((c >> 1) - 1) & 1, ok);
+          if (c > 0 && (wide || was_wide)) sh.wait(P::O_READ + (ph ^ 1), ((c - 1) >> 1) & 1, ok);
+          was_wide = wide;
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+#pragma unroll 2
+            for (int i = 0; i < DK / 16; ++i) {
+              const uint32_t off = ((i >> 2) * P::BLOCK + (i & 3) * 32) >> 4;
+              tc::mma_f16(o, q_k + off, s_mn + ((i * 2048) >> 4), id_o, i > 0);
+            }
+            tc::mma_commit(sh.bar(P::Q_FREE));
+          }
+          __syncwarp();
+          sh.wait(P::V_READY, ph, ok);
+          sh.wait(P::A_READY, ph, ok);
+          if (wide) sh.wait(P::X_FULL, ph, ok);
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            if (!wide || SLICES == 2) {
+              const uint64_t b_mn = wide ? v_mn : hi_mn;
+#pragma unroll 2
+              for (int i = 0; i < 8; ++i) tc::mma_f16_ts(o1, tmem + P::COL_G + 8 * i + (i & 4) * 8, b_mn + ((i * 2048) >> 4), id_o, !wide || i > 0);
+            } else {
+              for (int u = 0; u < 2; ++u)
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i)
+                  tc::mma_f16_ts(o1 + 64 * u, tmem + P::COL_L + 64 * u + 8 * i, v_mn + ((u * P::BLOCK + i * 2048) >> 4), id_o64, i > 0);
+            }
+          }
+          __syncwarp();
+          if (c + 1 < chunks) {
+            sh.wait(P::Q_FREE, ph, ok);
+            if (!ok) break;
+            copy(&q_map, P::Q, P::Q_FULL, c + 1);
+          }
+        } else {
+          sh.wait(P::S_READY, ph, ok);  // L has been read
+          sh.wait(P::V_READY, ph, ok);
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (c + 2 < chunks && tc::elect_one()) {
+            for (int i = 0; i < KB; ++i) tc::tma_prefetch_2d(&k_map, kh * DK + 64 * i, start + (c + 2) * kSsmChunk);
+            for (int x = 0; x < min(2, units - 2 * (pair % per_key)); ++x)
+              tc::tma_prefetch_2d(&v_map, kh * heads * DV + (2 * (pair % per_key) + x) * 64, start + (c + 2) * kSsmChunk);
+          }
+          __syncwarp();
         }
         if (tc::elect_one()) {
 #pragma unroll 2
@@ -517,14 +635,14 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         if (lane == 31) behind = 0.f;
         if (c > 0) {  // the chunk's before are used
           sh.wait(P::GATES_READ, ph ^ 1, ok);
-          sh.wait(P::A_READY, ph ^ 1, ok);
+          sh.wait(kOut ? P::A_READY : P::V_READY, ph ^ 1, ok);
         }
         *reinterpret_cast<float4*>(&small.d[x][4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
         *reinterpret_cast<float4*>(&small.suf[x][4 * lane]) = make_float4(suf[0] + behind, suf[1] + behind, suf[2] + behind, suf[3] + behind);
         if (lane == 0) small.total[ph][x] = incl;
         sh.arrive(P::GATES);
       }
-    } else {
+    } else if (kOut) {
       // ---- the rows of v, once those before have been used; and what comes two chunks on, into L2 -----------
       const int left = min(2, units - 2 * (pair % per_key));
       for (int c = 0; c < chunks; ++c) {

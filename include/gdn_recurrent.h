@@ -88,7 +88,7 @@ typedef struct {
  *   dk, dv   : 64 or 128 each.
  *   workspace: gdn_ssm_scan_workspace_bytes() bytes, 256-byte aligned, or NULL to
  *              allocate it stream-ordered. Calls that overlap need one each. */
-size_t gdn_ssm_scan_workspace_bytes(int B, int T, int nv, int dk, int dv, int varlen);
+size_t gdn_ssm_scan_workspace_bytes(int B, int T, int nk, int nv, int dk, int dv, int varlen);
 int gdn_ssm_scan(const void* q, const void* k, const void* v, const void* dt, const float* a, const float* dt_bias,
                  const float* skip, void* state, void* out, int B, int T, int nk, int nv, int dk, int dv,
                  const gdn_ssm_options_t* options, const int32_t* cu_seqlens, void* workspace, size_t workspace_bytes,

@@ -483,7 +483,7 @@ def test_other_stream_and_graph(gdn):
     lens = [150, 260]
     s, c, n = ssm(lens, 1, 2, 128, 64, seed=21), make_conv(lens, 128, 4, torch.bfloat16, seed=21), make_norm(410, 2, 64, torch.bfloat16, 0, "rms", "after", seed=21)
     b = batch(lens, True)
-    ws = torch.empty(max(gdn.ssm_scan_workspace_bytes(2, 410, 2, True, dv=64), gdn.causal_conv_backward_workspace_bytes(410, 128, 4),
+    ws = torch.empty(max(gdn.ssm_scan_workspace_bytes(2, 410, 1, 2, True, dv=64), gdn.causal_conv_backward_workspace_bytes(410, 128, 4),
                          gdn.layer_norm_backward_workspace_bytes(410, 2, 64), 1), dtype=torch.uint8, device=DEV)
     outs = [torch.empty(410, 128, dtype=torch.bfloat16, device=DEV) for _ in range(5)]
     state, kept, dw, dnw = s["state"].clone(), c["h0"].clone(), torch.empty_like(c["w"]), torch.empty_like(n["weight"])
@@ -552,3 +552,23 @@ def test_layer_of_them(gdn):
         for p, q in ((one[2][u], parts[2][u]), (one[4][u], parts[4][u])):
             assert float((p.double() - q.double()).norm()) <= 2 * bar * float(p.double().norm())
         assert float((one[3][u] - parts[3][u]).norm()) <= 2e-3 * float(one[3][u].norm())
+
+
+@pytest.mark.parametrize("lens,nk,nv,dk,dv,packed", [
+    ([5000], 1, 3, 128, 64, False), ([4100, 4100], 2, 4, 64, 64, False), ([6001], 1, 1, 128, 128, False), ([2500] * 3, 1, 2, 64, 128, False),
+    ([7000, 3, 0, 130], 1, 4, 128, 64, True), ([0, 9000], 1, 2, 64, 64, True), ([600] * 32, 1, 2, 64, 64, True), ([40] * 40 + [900], 1, 2, 64, 64, True),
+])
+def test_scan_in_segments(gdn, lens, nk, nv, dk, dv, packed):
+    """Long sequences on few heads, whose segments run side by side, among short ones; more sequences than one warp looks at."""
+    for steps, rate in ((0.02, 2.0), (0.5, 8.0)):
+        s = ssm(lens, nk, nv, dk, dv, steps=steps, rate=rate, seed=len(lens))
+        want = ssm_want(s, lens)
+        size = gdn.ssm_scan_workspace_bytes(len(lens), sum(lens) if packed else lens[0], nk, nv, packed, dk=dk, dv=dv)
+        got = []
+        for ws in (None, torch.full((max(size, 1),), 255, dtype=torch.uint8, device=DEV)):
+            out, state = torch.empty(sum(lens), nv * dv, dtype=torch.bfloat16, device=DEV), s["state"].clone()
+            gdn.ssm_scan(s["q"], s["k"], s["v"], s["dt"], s["a"], state, out, workspace=ws, **s["args"], **batch(lens, packed))
+            got.append((out, state))
+        gdn.check()
+        assert all(torch.equal(a, b) for a, b in zip(*got))
+        check_scan(*got[0], want, sum(lens))
