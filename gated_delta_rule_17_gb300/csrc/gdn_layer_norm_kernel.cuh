@@ -94,6 +94,27 @@ struct Eight {
     }
   }
 };
+// The same as pairs; and pairs as values.
+template <typename T>
+__device__ __forceinline__ void pairs8(const Eight<T>& e, Pair (&p)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    unpack16<T>(e.w[0], *reinterpret_cast<Pair(*)[2]>(&p[0]));
+    unpack16<T>(e.w[1], *reinterpret_cast<Pair(*)[2]>(&p[2]));
+  } else {
+    unpack16<T>(e.w[0], p);
+  }
+}
+__device__ __forceinline__ void values8(const Pair (&p)[4], float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) parts_of(p[i], f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ Pair both(float x) { return pair_of(x, x); }
+__device__ __forceinline__ float sum_of(Pair p) {
+  float a, b;
+  parts_of(p, a, b);
+  return a + b;
+}
+
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
   if constexpr (sizeof(T) == 4) {
@@ -200,95 +221,123 @@ __global__ void __launch_bounds__(norm_threads<L>) gdn_layer_norm_kernel(const L
 }
 
 // ---- backward ------------------------------------------------------------------------
-// One group's gradients, in the L lanes' words; dw and db take up its columns'. `read` runs once every lane has its words
-// (and its group's lanes have met, where the group is a CTA's).
+// A lane's columns: their weights (and biases, for a gate behind them), and the sums for both.
+template <int NV, bool kGate>
+struct NormColumns {
+  Pair w[NV][4], b[kGate ? NV : 1][4], dw[NV][4], db[NV][4];
+  __device__ __forceinline__ void start(const LayerNormParams& p, int lane, int lanes) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * lanes + lane) * 8;
+      float f[8] = {}, g[8] = {};
+      if (c < p.dim) {
+        weights8(p.weight, c, 1.f, f);
+        weights8(p.bias, c, 0.f, g);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[v][i] = pair_of(f[2 * i], f[2 * i + 1]);
+        if (kGate) b[v][i] = pair_of(g[2 * i], g[2 * i + 1]);
+        dw[v][i] = db[v][i] = 0;
+      }
+    }
+  }
+};
+
+// One group's gradients, in the L lanes' words (zeros past its end); its columns' sums go to `cols`. `read` runs once every
+// lane has its words (and its group's lanes have met, where the group is a CTA's). In pairs of fp32, and with the columns'
+// weights in registers: what bounds it is the issue of instructions (430 a warp and row without either: 264 us for 32768 rows of
+// 4096 in bf16).
 template <typename T, int L, int NV, bool kGate, typename Read>
 __device__ __forceinline__ void norm_backward(const LayerNormParams& p, const Eight<T> (&xw)[NV], const Eight<T> (&gw)[NV],
-                                              const Eight<T> (&zw)[kGate ? NV : 1], int lane, bool real, int64_t row, int64_t at, float (&dw)[NV][8],
-                                              float (&db)[NV][8], float* buf, int& turn, Read&& read) {
+                                              const Eight<T> (&zw)[kGate ? NV : 1], int lane, bool real, int64_t row, int64_t at,
+                                              NormColumns<NV, kGate>& cols, float* buf, int& turn, Read&& read) {
   const float inv = 1.f / static_cast<float>(p.dim);
   const bool after = kGate && !p.gate_first;
-  float u[NV][8], g[NV][8];  // g: dL/dy, before the weight
-  float sums[2] = {0.f, 0.f};
+  Pair u[NV][4], g[NV][4];  // g: dL/dy, before the weight
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int c = (v * L + lane) * 8;
-    float w[8];
-    xw[v].floats(u[v]);
-    gw[v].floats(g[v]);
+    pairs8<T>(xw[v], u[v]);
+    pairs8<T>(gw[v], g[v]);
     if constexpr (kGate) {
       float z[8];
       zw[v].floats(z);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float s = silu(z[i]);
-        if (after) g[v][i] *= s;
-        else u[v][i] *= s;
-      }
-    }
-    if (!p.rms && c < p.dim) {
-      weights8(p.weight, c, 1.f, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sums[0] += u[v][i];
-        sums[1] = fmaf(g[v][i], w[i], sums[1]);
+      for (int i = 0; i < 4; ++i) {
+        const Pair s = pair_of(silu(z[2 * i]), silu(z[2 * i + 1]));
+        if (after) g[v][i] = mul2(g[v][i], s);
+        else u[v][i] = mul2(u[v][i], s);
       }
     }
   }
-  float mean = 0.f, mt = 0.f;
+  float sums[2], mt = 0.f;
   if (!p.rms) {
+    Pair a = 0, t = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a = add2(a, u[v][i]);
+        t = fma2(g[v][i], cols.w[v][i], t);
+      }
+    sums[0] = sum_of(a);
+    sums[1] = sum_of(t);
     group_sum<L>(sums, buf, turn);
-    mean = sums[0] * inv;
     mt = sums[1] * inv;
+    const Pair mean = both(-sums[0] * inv);
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if ((v * L + lane) * 8 < p.dim)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[v][i] = add2(u[v][i], mean);
   }
-  sums[0] = sums[1] = 0.f;
+  Pair q = 0, c = 0;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * L + lane) * 8;
-    if (c >= p.dim) continue;
-    float w[8];
-    weights8(p.weight, c, 1.f, w);
+  for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      u[v][i] -= mean;
-      sums[0] = fmaf(u[v][i], u[v][i], sums[0]);
-      sums[1] = fmaf(g[v][i] * w[i], u[v][i], sums[1]);
+    for (int i = 0; i < 4; ++i) {
+      q = fma2(u[v][i], u[v][i], q);
+      c = fma2(mul2(g[v][i], cols.w[v][i]), u[v][i], c);
     }
-  }
+  sums[0] = sum_of(q);
+  sums[1] = sum_of(c);
   group_sum<L>(sums, buf, turn);
   read();
-  const float r = rsqrtf(sums[0] * inv + p.eps), mth = sums[1] * inv * r;
+  const float r = rsqrtf(sums[0] * inv + p.eps);
+  const Pair r2 = both(r), by_h = both(-sums[1] * inv * r * r), by_1 = both(-mt * r);  // dx = r t - r mt - r mth h, mth = sum t u r / n
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int c = (v * L + lane) * 8;
-    if (!real || c >= p.dim) continue;
-    float w[8], dx[8];
-    weights8(p.weight, c, 1.f, w);
+    const int at_c = (v * L + lane) * 8;
+    if (!real || at_c >= p.dim) continue;
+    Pair d[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      u[v][i] *= r;  // h
-      dw[v][i] = fmaf(g[v][i], u[v][i], dw[v][i]);
-      db[v][i] += g[v][i];
-      dx[i] = r * (fmaf(g[v][i], w[i], -mt) - u[v][i] * mth);
+    for (int i = 0; i < 4; ++i) {
+      u[v][i] = mul2(u[v][i], r2);  // h
+      cols.dw[v][i] = fma2(g[v][i], u[v][i], cols.dw[v][i]);
+      cols.db[v][i] = add2(cols.db[v][i], g[v][i]);
+      d[i] = fma2(u[v][i], by_h, fma2(mul2(g[v][i], cols.w[v][i]), r2, by_1));
     }
+    float dx[8];
+    values8(d, dx);
     if constexpr (kGate) {
-      float z[8], o[8], dz[8], b[8];
+      float z[8], o[8], y[8], dz[8];
       zw[v].floats(z);
       if (after) {
         gw[v].floats(o);
-        weights8(p.bias, c, 0.f, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) parts_of(fma2(u[v][i], cols.w[v][i], cols.b[v][i]), y[2 * i], y[2 * i + 1]);
       } else {
         xw[v].floats(o);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float sg = sigmoid(z[i]), s = z[i] * sg, slope = fmaf(s, 1.f - sg, sg);
-        dz[i] = o[i] * slope * (after ? fmaf(u[v][i], w[i], b[i]) : dx[i]);
+        dz[i] = o[i] * slope * (after ? y[i] : dx[i]);
         if (!after) dx[i] *= s;
       }
-      store8(static_cast<T*>(p.dgate) + row * p.dgate_stride + at + c, dz);
+      store8(static_cast<T*>(p.dgate) + row * p.dgate_stride + at + at_c, dz);
     }
-    store8(static_cast<T*>(p.out) + row * p.out_stride + at + c, dx);
+    store8(static_cast<T*>(p.out) + row * p.out_stride + at + at_c, dx);
   }
 }
 
@@ -302,7 +351,8 @@ __global__ void __launch_bounds__(128, kGate ? 4 : kNormSmallCtas) gdn_layer_nor
   int turn = 0;
   const int lane = threadIdx.x % L, slot = threadIdx.x / L, c = lane * 8;
   const uint32_t step = gridDim.x * SLOTS, groups = static_cast<uint32_t>(p.groups), items = static_cast<uint32_t>(p.items);
-  float dw[1][8] = {}, db[1][8] = {};
+  NormColumns<1, kGate> cols;
+  cols.start(p, lane, L);
   Eight<T> xw[1], gw[1], zw[1];
   uint32_t item = blockIdx.x * SLOTS + slot, row = item / groups, at = (item - row * groups) * p.dim;
   auto fetch = [&] {
@@ -325,7 +375,7 @@ __global__ void __launch_bounds__(128, kGate ? 4 : kNormSmallCtas) gdn_layer_nor
     row = item / groups;
     at = (item - row * groups) * p.dim;
     fetch();
-    norm_backward<T, L, 1, kGate>(p, xc, gc, zc, lane, real, now_row, now_at, dw, db, nullptr, turn, [] {});
+    norm_backward<T, L, 1, kGate>(p, xc, gc, zc, lane, real, now_row, now_at, cols, nullptr, turn, [] {});
   }
   if (!p.partials) return;
   // the CTA's sums, slot after slot
@@ -333,8 +383,10 @@ __global__ void __launch_bounds__(128, kGate ? 4 : kNormSmallCtas) gdn_layer_nor
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     __syncthreads();
+    float f[8];
+    values8(k ? cols.db[0] : cols.dw[0], f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_sum[slot * L * 8 + c + i] = k ? db[0][i] : dw[0][i];
+    for (int i = 0; i < 8; ++i) s_sum[slot * L * 8 + c + i] = f[i];
     __syncthreads();
     for (int i = threadIdx.x; i < p.dim; i += 128) {
       float acc = 0.f;
@@ -346,8 +398,12 @@ __global__ void __launch_bounds__(128, kGate ? 4 : kNormSmallCtas) gdn_layer_nor
 }
 
 // Wider groups: a CTA of L threads has a group, and copies those to come into a ring of `stages` rows.
+// CTAs of an SM.
+template <int L, bool kGate>
+constexpr int norm_wide_ctas = L == 128 ? (kGate ? 4 : 6) : L == 256 ? 2 : 1;
+
 template <typename T, int L, int NV, bool kGate>
-__global__ void __launch_bounds__(L, L == 128 ? 6 : kGate || NV > 1 || sizeof(T) == 4 ? 1 : 2) gdn_layer_norm_bwd_wide_kernel(const LayerNormParams p) {
+__global__ void __launch_bounds__(L, norm_wide_ctas<L, kGate>) gdn_layer_norm_bwd_wide_kernel(const LayerNormParams p) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(8) uint64_t s_full[8];
   __shared__ __align__(16) float buf[128];
@@ -372,7 +428,8 @@ __global__ void __launch_bounds__(L, L == 128 ? 6 : kGate || NV > 1 || sizeof(T)
       if (blockIdx.x + static_cast<uint64_t>(i) * step < items) copy(blockIdx.x + i * step, i);
   }
   __syncthreads();
-  float dw[NV][8] = {}, db[NV][8] = {};
+  NormColumns<NV, kGate> cols;
+  cols.start(p, lane, L);
   int stage = 0;
   uint32_t phase = 0;
   for (uint32_t item = blockIdx.x; item < items; item += step) {
@@ -397,7 +454,7 @@ __global__ void __launch_bounds__(L, L == 128 ? 6 : kGate || NV > 1 || sizeof(T)
         if (kGate) zw[v].load(from + 2 * p.dim + c);
       }
     }
-    norm_backward<T, L, NV, kGate>(p, xw, gw, zw, lane, true, row, at, dw, db, buf, turn, [&] {
+    norm_backward<T, L, NV, kGate>(p, xw, gw, zw, lane, true, row, at, cols, buf, turn, [&] {
       const uint64_t next = item + static_cast<uint64_t>(p.stages) * step;
       if (lane == 0 && next < items) copy(static_cast<uint32_t>(next), stage);
     });
@@ -417,8 +474,11 @@ __global__ void __launch_bounds__(L, L == 128 ? 6 : kGate || NV > 1 || sizeof(T)
   for (int v = 0; v < NV; ++v) {
     const int c = (v * L + lane) * 8;
     if (c >= p.dim) continue;
-    store8(out + c, dw[v]);
-    store8(out + p.dim + c, db[v]);
+    float f[8];
+    values8(cols.dw[v], f);
+    store8(out + c, f);
+    values8(cols.db[v], f);
+    store8(out + p.dim + c, f);
   }
 }
 

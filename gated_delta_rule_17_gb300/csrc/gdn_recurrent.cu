@@ -171,36 +171,38 @@ void by_dim(int dim, F&& f) {
   else if (dim <= 4096) f(IntC<128>{}, IntC<4>{});
   else f(IntC<256>{}, IntC<4>{});
 }
-// The backward keeps the columns' sums too, so a group takes more lanes: of one warp up to 256 values (f gets the lanes and 0),
-// a CTA beyond (threads, and words a thread).
-template <typename F>
+// The backward keeps the columns' weights and sums too, so a group takes more lanes, the more with a gate: of one warp up to 256
+// values (f gets the lanes and 0), a CTA beyond (threads, and words a thread).
+template <bool kGate, typename F>
 void by_dim_backward(int dim, F&& f) {
   if (dim <= 16) f(IntC<2>{}, IntC<0>{});
   else if (dim <= 64) f(IntC<8>{}, IntC<0>{});
   else if (dim <= 128) f(IntC<16>{}, IntC<0>{});
   else if (dim <= 256) f(IntC<32>{}, IntC<0>{});
   else if (dim <= 1024) f(IntC<128>{}, IntC<1>{});
-  else if (dim <= 4096) f(IntC<512>{}, IntC<1>{});
-  else f(IntC<512>{}, IntC<2>{});
+  else if constexpr (kGate) dim <= 4096 ? f(IntC<512>{}, IntC<1>{}) : f(IntC<1024>{}, IntC<1>{});
+  else dim <= 4096 ? f(IntC<256>{}, IntC<2>{}) : f(IntC<512>{}, IntC<2>{});
 }
 
 // CTAs and ring of the backward. The ring's stages fill what an SM's CTAs share of 200 KB, eight at most.
 struct NormPlan {
   int ctas, stages, ring;
 };
-NormPlan norm_plan(int64_t items, int dim, int sms, bool gate, int element) {
+template <bool kGate>
+NormPlan norm_plan(int64_t items, int dim, int sms, int element) {
   NormPlan p{};
-  by_dim_backward(dim, [&](auto lanes, auto words) {
+  by_dim_backward<kGate>(dim, [&](auto lanes, auto words) {
     constexpr int L = lanes.value;
-    int per_sm = gate ? 4 : gdn::kNormSmallCtas;
-    int64_t need = (items + 128 / (L < 128 ? L : 128) - 1) / (128 / (L < 128 ? L : 128));
-    if (words.value) {
-      const int stage = (gate ? 3 : 2) * dim * element;
-      per_sm = L == 128 ? 6 : gate || words.value > 1 || element == 4 ? 1 : 2;
+    int per_sm = kGate ? 4 : gdn::kNormSmallCtas;
+    int64_t need = items;
+    if constexpr (words.value == 0) {
+      need = (items + 128 / L - 1) / (128 / L);
+    } else {
+      const int stage = (kGate ? 3 : 2) * dim * element;
+      per_sm = gdn::norm_wide_ctas<L, kGate>;
       p.stages = 200 * 1024 / per_sm / stage;
       if (p.stages > 8) p.stages = 8;
       p.ring = p.stages * stage;
-      need = items;
     }
     const int64_t most = static_cast<int64_t>(sms) * per_sm;
     p.ctas = static_cast<int>(need < most ? need : most);
@@ -572,7 +574,7 @@ int gdn_layer_norm(const void* x, const void* gate, const float* weight, const f
 size_t gdn_layer_norm_backward_workspace_bytes(int rows, int groups, int dim) {
   if (rows <= 0 || groups < 1 || dim < 8 || dim % 8 || dim > kNormMaxDim) return 0;
   // (without a gate there are as many CTAs as with one, or more)
-  return static_cast<size_t>(norm_plan(static_cast<int64_t>(rows) * groups, dim, gdn_host::plan_sms(), false, 2).ctas) * 2 * dim * sizeof(float);
+  return static_cast<size_t>(norm_plan<false>(static_cast<int64_t>(rows) * groups, dim, gdn_host::plan_sms(), 2).ctas) * 2 * dim * sizeof(float);
 }
 
 int gdn_layer_norm_backward(const void* x, const void* gate, const float* weight, const float* bias, float eps, const void* dout, void* dx,
@@ -606,16 +608,17 @@ int gdn_layer_norm_backward(const void* x, const void* gate, const float* weight
   void* ws = nullptr;
   if (int rc = acquire(need ? workspace : nullptr, need, s, &ws)) return rc;
   p.partials = static_cast<float*>(ws);
-  const NormPlan plan = norm_plan(p.items, dim, sms, gate != nullptr, dtype == GDN_F32 ? 4 : 2);
+  const int element = dtype == GDN_F32 ? 4 : 2;
+  const NormPlan plan = gate ? norm_plan<true>(p.items, dim, sms, element) : norm_plan<false>(p.items, dim, sms, element);
   p.stages = plan.stages;
   p.status = status;
   int rc = GDN_OK;
   by_type(dtype, [&](auto type) {
     using T = decltype(type);
-    by_dim_backward(dim, [&](auto lanes, auto words) {
-      constexpr int L = lanes.value, NV = words.value;
-      auto go = [&](auto gated) {
-        constexpr bool G = gated.value;
+    auto go = [&](auto gated) {
+      constexpr bool G = gated.value;
+      by_dim_backward<G>(dim, [&](auto lanes, auto words) {
+        constexpr int L = lanes.value, NV = words.value;
         if constexpr (NV == 0) {
           gdn::gdn_layer_norm_bwd_kernel<T, L, G><<<plan.ctas, 128, 0, s>>>(p);
         } else {
@@ -623,10 +626,10 @@ int gdn_layer_norm_backward(const void* x, const void* gate, const float* weight
           rc = allow_shared<T, L, NV, G>(reinterpret_cast<const void*>(kernel));
           if (rc == GDN_OK) kernel<<<plan.ctas, L, plan.ring, s>>>(p);
         }
-      };
-      if (gate) go(std::true_type{});
-      else go(std::false_type{});
-    });
+      });
+    };
+    if (gate) go(std::true_type{});
+    else go(std::false_type{});
   });
   if (rc == GDN_OK) {
     if (sums)
