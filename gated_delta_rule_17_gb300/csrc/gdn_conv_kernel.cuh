@@ -18,7 +18,19 @@ namespace gdn {
 
 constexpr int kConvThreads = 128;
 constexpr int kConvCtasPerSm = 4;
-constexpr int kConvUnroll = 4;  // rows loaded ahead of their arithmetic
+// A thread's words of the rows to come lie in a ring in shared memory, kConvAhead steps of kConvStep rows (cp.async): in registers there
+// is no room for as many as HBM's latency asks for (25% occupancy and a step ahead: 69% of the measured rate forward, 70% backward).
+constexpr int kConvStep = 4, kConvAhead = 4;
+
+template <int BYTES>
+__device__ __forceinline__ void conv_fetch(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void conv_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 struct ConvParams {
   const void* x;
@@ -71,7 +83,8 @@ __device__ __forceinline__ void conv_weights(const ConvParams& p, int c0, Pair (
 
 template <typename T, int W>
 __global__ void __launch_bounds__(kConvThreads, kConvCtasPerSm) gdn_conv_kernel(const ConvParams p) {
-  constexpr int N = Word16<T>::N, P = Word16<T>::PAIRS, U = kConvUnroll;
+  constexpr int N = Word16<T>::N, P = Word16<T>::PAIRS, U = kConvStep, A = kConvAhead;
+  __shared__ uint4 ring[A * U][kConvThreads];
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
   for (int64_t s = item; s < p.batch.B; s += static_cast<int64_t>(gridDim.x) * kConvThreads) p.batch.report(static_cast<int>(s), p.status);
   const int words = p.D / N;
@@ -123,30 +136,29 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtasPerSm) gdn_conv_kernel(
 #pragma unroll
       for (int i = 0; i < P; ++i) before[W - 2][i] = now[i];
     };
-    uint4 raw[U];
-    const bool whole = row + U <= to;
-    const T* from = x + row * p.x_stride;
-    if (whole)
-#pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = *reinterpret_cast<const uint4*>(from + u * p.x_stride);
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) unpack16<T>(last[i], before[i]);
-    if (whole) {
-      T* at = out + row * p.out_stride;
-      for (; row + U <= to; row += U) {  // each row's word makes room for the one U rows on
-        const bool more = row + 2 * U <= to;
+    const T* from = x + row * p.x_stride;
+    T* at = out + row * p.out_stride;
+    uint4* mine = &ring[0][threadIdx.x];
+    const uint32_t slots = tc::smem_u32(mine);
+    auto fetch = [&](int k, int left) {  // step k from here, of `left` rows
+      if (left > 0)
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint4 word = raw[u];
-          if (more) raw[u] = *reinterpret_cast<const uint4*>(from + (U + u) * p.x_stride);
-          step(word, at + u * p.out_stride);
-        }
-        from += U * p.x_stride;
-        at += U * p.out_stride;
-      }
+        for (int u = 0; u < U; ++u)
+          if (u < left) conv_fetch<16>(slots + (k % A * U + u) * (kConvThreads * 16), from + (k * U + u) * p.x_stride);
+      tc::cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < A - 1; ++k) fetch(k, to - row - k * U);
+    for (int k = 0; row < to; row += U, ++k) {
+      fetch(k + A - 1, to - row - (A - 1) * U);
+      conv_wait<A - 1>();
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (row + u < to) step(mine[(k % A * U + u) * kConvThreads], at + (k * U + u) * p.out_stride);
     }
-#pragma unroll 1
-    for (; row < to; ++row) step(*reinterpret_cast<const uint4*>(x + row * p.x_stride), out + row * p.out_stride);
+    row = to;
     if (p.state_here && state) {
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) {
@@ -187,8 +199,6 @@ __global__ void __launch_bounds__(kConvThreads) gdn_conv_state_kernel(const Conv
 }
 
 // ---- backward ------------------------------------------------------------------------
-constexpr int kConvBwdUnroll = 4;
-
 // dy of one row of four channels: y from the inputs before[0..W-2] and now.
 template <int W>
 __device__ __forceinline__ void conv_dy(const Pair (&w)[W][2], const Pair (&b)[2], const Pair (&before)[W - 1][2], const Pair (&now)[2],
@@ -216,7 +226,8 @@ __device__ __forceinline__ void conv_dy(const Pair (&w)[W][2], const Pair (&b)[2
 template <typename T, int W>
 __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4) gdn_conv_bwd_kernel(const ConvParams p) {
   using Word = typename Four<T>::Word;
-  constexpr int U = kConvBwdUnroll;
+  constexpr int U = kConvStep, A = sizeof(T) == 4 ? kConvAhead / 2 : kConvAhead;
+  __shared__ Word ring[A * U][2][kConvThreads];
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
   for (int64_t s = item; s < p.batch.B; s += static_cast<int64_t>(gridDim.x) * kConvThreads) p.batch.report(static_cast<int>(s), p.status);
   const int words = p.D / 4;
@@ -309,43 +320,42 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4) gdn_conv
         before[W - 2][i] = now[i];
       }
     };
-    auto one = [&](int t) {
-      step(*reinterpret_cast<const Word*>(x + t * p.x_stride), *reinterpret_cast<const Word*>(dout + t * p.dout_stride), t < own,
-           [&](const Pair (&dy)[2]) { put(t, dy); });
-    };
-#pragma unroll 1
-    for (; row < min(to, first + W - 1); ++row) one(row);
-    if (row + U <= own) {  // whole steps inside the strip: no ends to look for
-      Word xr[U], gr[U];
-      const T *fx = x + row * p.x_stride, *fg = dout + row * p.dout_stride;
-      T* at = dx + (row - (W - 1)) * p.dx_stride;
+    const T *fx = x + row * p.x_stride, *fg = dout + row * p.dout_stride;
+    T* to_dx = dx + (row - (W - 1)) * p.dx_stride;
+    Word* mine = &ring[0][0][threadIdx.x];
+    const uint32_t slots = tc::smem_u32(mine);
+    constexpr int BYTES = sizeof(Word), ROW = 2 * kConvThreads;
+    auto fetch = [&](int k, int left) {  // step k from here, of `left` rows
+      if (left > 0)
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        xr[u] = *reinterpret_cast<const Word*>(fx + u * p.x_stride);
-        gr[u] = *reinterpret_cast<const Word*>(fg + u * p.dout_stride);
-      }
-      for (; row + U <= own; row += U) {
-        const bool more = row + 2 * U <= own;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const Word xw = xr[u], gw = gr[u];
-          if (more) {
-            xr[u] = *reinterpret_cast<const Word*>(fx + (U + u) * p.x_stride);
-            gr[u] = *reinterpret_cast<const Word*>(fg + (U + u) * p.dout_stride);
+        for (int u = 0; u < U; ++u)
+          if (u < left) {
+            conv_fetch<BYTES>(slots + (k % A * U + u) * (ROW * BYTES), fx + (k * U + u) * p.x_stride);
+            conv_fetch<BYTES>(slots + (k % A * U + u) * (ROW * BYTES) + kConvThreads * BYTES, fg + (k * U + u) * p.dout_stride);
           }
-          step(xw, gw, true, [&](const Pair (&dy)[2]) {
+      tc::cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < A - 1; ++k) fetch(k, to - row - k * U);
+    for (int k = 0; row < to; row += U, ++k) {
+      fetch(k + A - 1, to - row - (A - 1) * U);
+      conv_wait<A - 1>();
+      const Word* now = mine + k % A * U * ROW;
+      if (row >= first + W - 1 && row + U <= own) {  // inside the strip: no ends to look for
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          step(now[u * ROW], now[u * ROW + kConvThreads], true, [&](const Pair (&dy)[2]) {
             float f[4];
             gradient(dy, f);
-            store4(at + u * p.dx_stride, f);
+            store4(to_dx + (k * U + u) * p.dx_stride, f);
           });
-        }
-        fx += U * p.x_stride;
-        fg += U * p.dout_stride;
-        at += U * p.dx_stride;
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < U && row + u < to; ++u)
+          step(now[u * ROW], now[u * ROW + kConvThreads], row + u < own, [&](const Pair (&dy)[2]) { put(row + u, dy); });
       }
     }
-#pragma unroll 1
-    for (; row < to; ++row) one(row);
+    row = to;
     if (to == end) {  // nothing comes after the sequence's end
       const Pair none[2] = {zero, zero};
 #pragma unroll
