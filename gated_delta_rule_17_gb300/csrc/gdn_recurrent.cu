@@ -127,17 +127,16 @@ void by_width(int width, F&& f) {
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-// Rows of a forward thread's strip: as few as give every SM 2048 threads, at most 64, where the rows
-// before a strip (read again) no longer count.
-int conv_strip(int64_t rows, int words, int sms) {
-  const int64_t strip = rows * words / (static_cast<int64_t>(sms) * 2048);
-  return static_cast<int>(strip < 1 ? 1 : strip > 64 ? 64 : strip);
+// Rows of a thread's strip: as few as make `waves` passes of all the threads that the SMs hold (512 each), so that the last pass
+// is as full as the others.
+int conv_strips(int64_t rows, int words, int sms, int waves, int least) {
+  const int64_t strips = static_cast<int64_t>(sms) * 512 * waves / words;
+  const int64_t strip = strips > 1 ? (rows + strips - 1) / strips : rows;
+  return static_cast<int>(strip < least ? least : strip);
 }
-// And of a backward thread's, which walks width - 1 rows more and leaves partial sums.
-int conv_bwd_strip(int64_t rows, int words, int sms) {
-  const int64_t strip = rows * words / (static_cast<int64_t>(sms) * 1024);
-  return static_cast<int>(strip < 16 ? 16 : strip);
-}
+int conv_strip(int64_t rows, int words, int sms) { return conv_strips(rows, words, sms, 4, 1); }
+// The backward's walk width - 1 rows more and leave partial sums, so they are longer.
+int conv_bwd_strip(int64_t rows, int words, int sms) { return conv_strips(rows, words, sms, 2, 16); }
 
 int conv_setup(const void* x, const float* weight, const float* bias, int D, int width, int silu, int dtype, int64_t x_stride,
                gdn::ConvParams* p) {
