@@ -18,9 +18,12 @@ namespace gdn {
 
 constexpr int kConvThreads = 128;
 constexpr int kConvCtasPerSm = 4;
-// A thread's words of the rows to come lie in a ring in shared memory, kConvAhead steps of kConvStep rows (cp.async): in registers there
+// A thread's words of the rows to come lie in a ring in shared memory, kConvAhead steps of conv_step rows (cp.async): in registers there
 // is no room for as many as HBM's latency asks for (25% occupancy and a step ahead: 69% of the measured rate forward, 70% backward).
-constexpr int kConvStep = 4, kConvAhead = 4;
+// A step is a multiple of W - 1 rows, after which the window of inputs is in the registers it was in.
+template <int W>
+constexpr int conv_step = W == 4 ? 6 : 4;
+constexpr int kConvAhead = 3;
 
 template <int BYTES>
 __device__ __forceinline__ void conv_fetch(uint32_t dst, const void* src) {
@@ -83,7 +86,7 @@ __device__ __forceinline__ void conv_weights(const ConvParams& p, int c0, Pair (
 
 template <typename T, int W>
 __global__ void __launch_bounds__(kConvThreads, kConvCtasPerSm) gdn_conv_kernel(const ConvParams p) {
-  constexpr int N = Word16<T>::N, P = Word16<T>::PAIRS, U = kConvStep, A = kConvAhead;
+  constexpr int N = Word16<T>::N, P = Word16<T>::PAIRS, U = conv_step<W>, A = kConvAhead;
   __shared__ uint4 ring[A * U][kConvThreads];
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
   for (int64_t s = item; s < p.batch.B; s += static_cast<int64_t>(gridDim.x) * kConvThreads) p.batch.report(static_cast<int>(s), p.status);
@@ -203,22 +206,25 @@ __global__ void __launch_bounds__(kConvThreads) gdn_conv_state_kernel(const Conv
 template <int W>
 __device__ __forceinline__ void conv_dy(const Pair (&w)[W][2], const Pair (&b)[2], const Pair (&before)[W - 1][2], const Pair (&now)[2],
                                         const float (&g)[4], int with_silu, Pair (&dy)[2]) {
-  float d[4];
+  const Pair one = pair_of(1.f, 1.f), minus = pair_of(-1.f, -1.f), to_log2 = pair_of(-1.4426950408889634f, -1.4426950408889634f);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    Pair acc = fma2(now[i], w[W - 1][i], b[i]);
+    dy[i] = pair_of(g[2 * i], g[2 * i + 1]);
+    if (!with_silu) continue;
+    Pair y = fma2(now[i], w[W - 1][i], b[i]);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) acc = fma2(before[j][i], w[j][i], acc);
-    float y[2];
-    parts_of(acc, y[0], y[1]);
+    for (int j = 0; j < W - 1; ++j) y = fma2(before[j][i], w[j][i], y);
+    // s = 1 / (1 + e^-y); silu' = s (1 + y (1 - s))
+    float e[2], s[2];
+    parts_of(mul2(y, to_log2), e[0], e[1]);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float sg = with_silu ? sigmoid(y[e]) : 1.f;
-      d[2 * i + e] = with_silu ? g[2 * i + e] * (sg * fmaf(y[e], 1.f - sg, 1.f)) : g[2 * i + e];
-    }
+    for (int k = 0; k < 2; ++k) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e[k]));
+    parts_of(add2(pair_of(e[0], e[1]), one), s[0], s[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[k]));
+    const Pair sg = pair_of(s[0], s[1]);
+    dy[i] = mul2(dy[i], mul2(sg, fma2(y, fma2(sg, minus, one), one)));
   }
-  dy[0] = pair_of(d[0], d[1]);
-  dy[1] = pair_of(d[2], d[3]);
 }
 
 // A thread owns four channels and a strip of rows; it walks W - 1 rows past the strip's end, whose dy
@@ -226,7 +232,7 @@ __device__ __forceinline__ void conv_dy(const Pair (&w)[W][2], const Pair (&b)[2
 template <typename T, int W>
 __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4) gdn_conv_bwd_kernel(const ConvParams p) {
   using Word = typename Four<T>::Word;
-  constexpr int U = kConvStep, A = sizeof(T) == 4 ? kConvAhead / 2 : kConvAhead;
+  constexpr int U = conv_step<W>, A = sizeof(T) == 4 ? 2 : kConvAhead;
   __shared__ Word ring[A * U][2][kConvThreads];
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
   for (int64_t s = item; s < p.batch.B; s += static_cast<int64_t>(gridDim.x) * kConvThreads) p.batch.report(static_cast<int>(s), p.status);
