@@ -15,13 +15,14 @@
 //
 // The decays need no exponential a pair (i, j): with V = V' (hi) and e^{-suf_i} on the rows of O1, A is
 // the same for both heads, and bf16 has fp32's exponents. That holds while the chunk's decay stays within
-// kSsmSpan; in chunks that decay further each unit has an A of its own, with d_j e^{suf_j - suf_i} pair by pair,
-// and V = v. Operands of 16 bits cost the output what its own rounding does: 2.2e-3 of its size in
+// kSsmSpan. A head whose chunk decays further has an A of its own, with d_j e^{suf_j - suf_i}, and V = v: beside the diagonal as
+// (d_j e^{suf_j - b}) e^{b - suf_i} about the decay b behind every 16 columns, where neither factor passes 1 or d, on it pair by pair; and
+// O2's rows are scaled before O1 comes on top. Operands of 16 bits cost the output what its own rounding does: 2.2e-3 of its size in
 // bf16, 1.7e-3 if it were rounded only once; the state is off by under 1e-5.
 //
 // Roles: warps 0-7, a thread a row of S and of the outputs (warps 0-3 unit 0, 4-7 unit 1), S in registers; warps 8-15 make
 // the operands, V' of their unit and half of A; warp 16 copies Q and K (TMA) and issues the products. Order on the tensor
-// pipe: O2, O1, L of a chunk, then G of the next. So the update of S, the only step that the next chunk's O2 waits
+// pipe: O2, L, O1 of a chunk, then G of the next. So the update of S, the only step that the next chunk's O2 waits
 // for, runs under G, making A under O2, the rows' way out under L.
 #pragma once
 #include "gdn_ssm_common.cuh"
@@ -45,9 +46,10 @@ struct SsmPlace {
 
 // What the roles tell one another beside tiles.
 struct SsmSmall {
-  uint64_t bar[16];
+  uint64_t bar[18];
   float suf[2][kSsmChunk], d[2][kSsmChunk];  // of each unit's tokens
   float total[2][2];                         // by chunk parity: each unit's decay
+  float behind[2][8];                        // in chunks of wide decay: log2 of the decay behind each 16 tokens
   uint32_t tmem, abort;
   SsmPlace place;
 };
@@ -57,9 +59,9 @@ struct SsmPlan {
   static constexpr int Q = 0, K = 2 * BLOCK, VHI = K + 4 * BLOCK, VLO = VHI + 2 * BLOCK, S16 = VLO + 2 * BLOCK, ROWS = S16 + 2 * BLOCK,
                        SMALL = ROWS + 2 * BLOCK, DYN_SMEM = SMALL + static_cast<int>(sizeof(SsmSmall));
   static constexpr uint32_t COL_G = 0, COL_O = 128, COL_L = 384, TMEM_COLS = 512;  // O: a buffer of 128 for even and odd chunks
-  // mbarriers: copies (Q_FULL, K_FULL + buffer, X_FULL), products (G_FULL, Q_FREE, L_FULL) and warps' signals
-  static constexpr int Q_FULL = 0, K_FULL = 1, G_FULL = 3, Q_FREE = 4, L_FULL = 5, X_FULL = 6, GATES = 7, V_READY = 8, A_READY = 9,
-                       S_READY = 10, GATES_READ = 11, ROWS_FREE = 12, O_READ = 13, NBAR = 15;
+  // mbarriers: copies (Q_FULL, K_FULL + buffer, X_FULL), products (G_FULL, Q_FREE, L_FULL, O_FULL + buffer) and warps' signals
+  static constexpr int Q_FULL = 0, K_FULL = 1, G_FULL = 3, Q_FREE = 4, L_FULL = 5, X_FULL = 6, O_FULL = 7, GATES = 9, V_READY = 10, A_READY = 11,
+                       S_READY = 12, GATES_READ = 13, STAGED = 14, O_READ = 15, NBAR = 17;
 };
 
 struct SsmScanParams {
@@ -157,8 +159,8 @@ __device__ __forceinline__ float ssm_exp2(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Whether either unit's chunk decays by more than kSsmSpan (the same for all roles).
-__device__ __forceinline__ bool ssm_wide(const float (&total)[2]) { return !(fminf(total[0], total[1]) >= -kSsmSpan); }
+// Whether a unit's chunk decays by more than kSsmSpan (the same for all roles).
+__device__ __forceinline__ bool ssm_wide(float total) { return !(total >= -kSsmSpan); }
 
 // kOut false: the states at the ends of the segments, without outputs.
 template <int DK, int DV, bool kOut>
@@ -198,7 +200,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
 
   if (threadIdx.x == 0) {
     small.abort = 0;
-    for (int i = 0; i < P::NBAR; ++i) tc::mbar_init(sh.bar(i), i < P::GATES ? 1 : i == P::GATES || i == P::ROWS_FREE ? 2 : 8);
+    for (int i = 0; i < P::NBAR; ++i) tc::mbar_init(sh.bar(i), i < P::GATES ? 1 : i == P::GATES ? 2 : 8);
     tc::mbar_fence_init();
   }
   if (warp == 16) tc::tmem_alloc(tc::smem_u32(&small.tmem), P::TMEM_COLS);
@@ -258,33 +260,30 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       uint8_t* s16 = smem + P::S16 + x * P::BLOCK;
       uint8_t* rows = smem + P::ROWS + x * P::BLOCK;
       const Pair by_v = pair_of(skip, skip);
-      // the factors of chunk c: of its own sums, of the state in them, of the state, and of its products with V'
+      // the factors of chunk c: of the row's sums, of the state before it, and of its products with V'; and of the state in the sums
       struct Factors {
-        float r1, r2, keep, grow;
-        bool wide;
+        float row, keep, grow, to16;
       };
       [[maybe_unused]] auto factors = [&](int c) {
         sh.wait(P::GATES, c & 1, ok);
         const float suf = small.suf[x][t], total = small.total[c & 1][x];
-        Factors f;
-        f.wide = ssm_wide(small.total[c & 1]);
+        const bool wide = ssm_wide(total);
         sh.arrive(P::GATES_READ);
-        const float mid = f.wide ? 0.f : 0.5f * total;
-        f.r1 = f.wide ? 1.f : __expf(mid - suf);
-        f.r2 = __expf(total - suf);
+        const float mid = wide ? 0.f : 0.5f * total;
+        Factors f;
+        f.row = wide ? 1.f : __expf(mid - suf);
         f.keep = __expf(total);
         f.grow = __expf(mid);
+        f.to16 = wide ? 1.f : f.grow;  // e^{total - mid}
         if (!kOut) decay += total;
         return f;
       };
       Factors now = factors(0);
-      float f1 = 0.f, f2 = 0.f;  // of the row's outputs in the chunk before
-      bool wide = false;
+      float scale = 0.f;  // of the row's outputs in the chunk before
       for (int c = 0; c <= chunks; ++c) {
         const uint32_t ph = c & 1;
         if (kOut && c < chunks) {  // S for the products, with what it decays by beside V' where they share an accumulator
-          const float to16 = now.wide ? 1.f : now.grow;  // e^{total - mid}
-          const Pair by = pair_of(to16, to16);
+          const Pair by = pair_of(now.to16, now.to16);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float y[8];
@@ -302,8 +301,10 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         }
         if (kOut && c > 0) {  // the rows of the chunk before
           const uint32_t from = tmem + lanes + P::COL_O + 64 * x, off = (c & 1) ? 0 : 128;  // its buffer
-          sh.wait(P::X_FULL, ph ^ 1, ok);  // (its O is complete: L was, which comes after)
-          const Pair by1 = pair_of(f1, f1), by2 = pair_of(f2, f2);
+          sh.wait(P::X_FULL, ph ^ 1, ok);
+          sh.wait(P::O_FULL + (ph ^ 1), ((c - 1) >> 1) & 1, ok);
+          tc::fence_after_sync();
+          const Pair by = pair_of(scale, scale);
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             uint32_t o[16], w[8];
@@ -312,17 +313,8 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             unpack16<__nv_bfloat16>(*reinterpret_cast<const uint4*>(rows + tc::sw128(t, 32 * i)), *reinterpret_cast<Pair(*)[4]>(&v[0]));
             unpack16<__nv_bfloat16>(*reinterpret_cast<const uint4*>(rows + tc::sw128(t, 32 * i + 16)), *reinterpret_cast<Pair(*)[4]>(&v[4]));
             tc::tmem_ld_wait16(o);
-            if (!wide) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = fma2(pair_of(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), by1, mul2(v[e], by_v));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = fma2(pair_of(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), by2, mul2(v[e], by_v));
-              tc::tmem_ld16u(from + (off ^ 128) + 16 * i, o);
-              tc::tmem_ld_wait16(o);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = add2(pair_of(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), v[e]);
-            }
+            for (int e = 0; e < 8; ++e) v[e] = fma2(pair_of(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), by, mul2(v[e], by_v));
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               float y[2];
@@ -338,16 +330,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           const int at = (c - 1) * kSsmChunk, n = tokens - at;
           if (n >= kSsmChunk) {
             tc::fence_proxy_async();
-            tc::named_barrier(3 + x, 128);
-            if (t == 0) {
-              if (ok && opaque(is_real)) {
-                tc::tma_store_2d(&out_map, col, start + at, tc::smem_u32(rows));
-                tc::tma_store_commit();
-                tc::tma_store_wait_read();
-              }
-              tc::mbar_arrive(sh.bar(P::ROWS_FREE));
-            }
-            __syncwarp();
+            sh.arrive(P::STAGED);
           } else {
             __syncwarp();
 #pragma unroll 1
@@ -359,9 +342,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           }
         }
         if (c < chunks) {
-          f1 = now.r1;
-          f2 = now.r2;
-          wide = now.wide;
+          scale = now.row;
           const Pair by = pair_of(now.keep, now.keep), in = pair_of(now.grow, now.grow);
           if (c + 1 < chunks) now = factors(c + 1);
           sh.wait(P::L_FULL, ph, ok);
@@ -415,11 +396,14 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           }
         }
         sh.wait(P::GATES, ph, ok);
-        const bool wide = ssm_wide(small.total[ph]);
+        const bool wide = ssm_wide(small.total[ph][x]), any = wide || ssm_wide(small.total[ph][x ^ 1]);
         const float suf = small.suf[x][t], d = small.d[x][t], f = d * __expf(wide ? suf : fmaf(-0.5f, small.total[ph][x], suf));
         const float f_hi = __bfloat162float(__float2bfloat16_rn(f));
         const uint32_t both = pack2<__nv_bfloat16>(f_hi, f - f_hi);
-        if (c > 0) sh.wait(P::L_FULL, ph ^ 1, ok);  // V is free
+        if (c > 0) {  // V is free
+          sh.wait(P::L_FULL, ph ^ 1, ok);
+          if (kOut) sh.wait(P::O_FULL + (ph ^ 1), ((c - 1) >> 1) & 1, ok);
+        }
         // V' = v f in pairs of bf16: with f = f_hi + f_lo, hi = v f_hi rounded, lo = (v f_hi - hi, exact) + v f_lo
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -437,7 +421,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           *reinterpret_cast<uint4*>(hi + at) = make_uint4(a4[0], a4[1], a4[2], a4[3]);
           *reinterpret_cast<uint4*>(lo + at) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
         }
-        if (kOut && wide && n < kSsmChunk) {  // nor of v, which O then takes itself
+        if (kOut && any && n < kSsmChunk) {  // nor of v, which O then takes itself
           sh.wait(P::X_FULL, ph, ok);
 #pragma unroll 1
           for (int i = threadIdx.x - 256; i < (kSsmChunk - n) * 16; i += 256)
@@ -447,40 +431,75 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         sh.arrive(P::V_READY);
         if constexpr (kOut) {
           sh.wait(P::G_FULL, ph, ok);
-          // A: row t, columns 16 i .. 16 i + 15, of which it sees those up to itself. Half of it in place of this half of G;
-          // where the decay is wide and the units are two heads all of the unit's own, in place of its L, once that has been read.
-          const bool own_a = wide && SLICES == 1;
-          if (own_a) sh.wait(P::S_READY, ph, ok);
-          if (wide) {  // log2 of d e^{suf} in the place of d
-            small.d[x][t] = fmaf(suf, kLog2e, __log2f(d));
+          // A: row t, columns 32 i .. 32 i + 31, of which it sees those up to itself. Half of it in place of this half of G;
+          // where a decay is wide and the units are two heads, the 32 columns of both units in place of those of G, once both have them.
+          const bool own_a = any && SLICES == 1;
+          const float own = suf * kLog2e;
+          if (wide) {  // d e^{suf - behind} in the place of d, and log2 of d e^{suf} in that of suf, once the rows' warps have it
+            const float last = __shfl_sync(0xffffffffu, suf, lane | 15);
+            sh.wait(P::GATES_READ, ph, ok);
+            small.d[x][t] = d * __expf(suf - last);
+            small.suf[x][t] = own + __log2f(d);
+            if ((lane & 15) == 15) small.behind[x][t >> 4] = own;
             tc::named_barrier(5 + x, 128);
           }
           tc::fence_after_sync();
-          const int first = own_a ? 0 : 4 * x, last = own_a ? 8 : first + 4;
-          const uint32_t to = tmem + lanes + (own_a ? P::COL_L + 64 * x : P::COL_G + 32 * x);
-          const float own = suf * kLog2e;
+          const int first = own_a ? 0 : 2 * x, last = own_a ? 4 : first + 2;
+          const uint32_t to = tmem + lanes + P::COL_G + (own_a ? 16 * x : 32 * x), apart = own_a ? 32 : 16;
 #pragma unroll 1
           for (int i = first; i < last; ++i) {
-            uint32_t r[16], k16[8];
-            const int seen = t - 16 * i;
-            if (i <= 2 * quarter + 1) {
-              tc::tmem_ld16u(tmem + lanes + P::COL_G + 16 * i, r);
-              tc::tmem_ld_wait16(r);
-              if (wide) {
+            uint32_t r[32], k16[16];
+            float f[2] = {1.f, 1.f};
+            if (wide && i < quarter) {
+              f[0] = ssm_exp2(small.behind[x][2 * i] - own);
+              f[1] = ssm_exp2(small.behind[x][2 * i + 1] - own);
+            }
+            if (i <= quarter && __any_sync(0xffffffffu, f[1] > 0.f)) {
+              tc::tmem_ld32(tmem + lanes + P::COL_G + 32 * i, r);
+              tc::tmem_ld_wait32(r);
+              if (wide && i < quarter) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * ssm_exp2(small.d[x][16 * i + e] - own));
+                for (int e = 0; e < 32; e += 4) {
+                  const Pair row = pair_of(f[e / 16], f[e / 16]);
+                  float c4[4], y[4];
+                  load4(&small.d[x][32 * i + e], c4);
+#pragma unroll
+                  for (int k = 0; k < 4; k += 2)
+                    parts_of(mul2(mul2(pair_of(__uint_as_float(r[e + k]), __uint_as_float(r[e + k + 1])), pair_of(c4[k], c4[k + 1])), row), y[k], y[k + 1]);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) r[e + k] = __float_as_uint(y[k]);
+                }
+              } else if (wide) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * ssm_exp2(small.suf[x][32 * i + e] - own));
               }
-              if (i >= 2 * quarter) {
+              if (i == quarter) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = e <= seen ? r[e] : 0u;
+                for (int e = 0; e < 32; ++e) r[e] = e <= lane ? r[e] : 0u;
               }
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) k16[e / 2] = pack2<__nv_bfloat16>(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+              for (int e = 0; e < 32; e += 2) k16[e / 2] = pack2<__nv_bfloat16>(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
             } else {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) k16[e] = 0;
+              for (int e = 0; e < 16; ++e) k16[e] = 0;
             }
-            tc::tmem_st8(to + 8 * i, k16);
+            if (own_a) tc::named_barrier(7 + quarter, 64);
+            tc::tmem_st16u(to + apart * i, k16);
+          }
+          if (wide) {  // O2's rows take the decay before them
+            const float f = __expf(small.total[ph][x] - suf);
+            const uint32_t o = tmem + lanes + P::COL_O + ph * 128 + 64 * x;
+            sh.wait(P::Q_FREE, ph, ok);
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              uint32_t r[16];
+              tc::tmem_ld16u(o + 16 * i, r);
+              tc::tmem_ld_wait16(r);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+              tc::tmem_st16u(o + 16 * i, r);
+            }
           }
           tc::tmem_st_wait();
           tc::fence_before_sync();
@@ -507,7 +526,6 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       copy(&k_map, P::K, P::K_FULL, 0);
       const uint64_t q_k = tc::desc_sw128(sbase + P::Q, 16, 1024), s_mn = tc::desc_sw128(sbase + P::S16, P::BLOCK, 1024);
       const uint64_t v_mn = tc::desc_sw128(sbase + P::ROWS, P::BLOCK, 1024);
-      bool was_wide = false;
       const uint64_t hi_mn = tc::desc_sw128(sbase + P::VHI, P::BLOCK, 1024), lo_mn = tc::desc_sw128(sbase + P::VLO, P::BLOCK, 1024);
       for (int c = 0; c < chunks && ok; ++c) {
         const uint32_t ph = c & 1;
@@ -531,16 +549,22 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           if (!ok) break;
           copy(&k_map, P::K + (ph ^ 1) * 2 * P::BLOCK, P::K_FULL + (ph ^ 1), c + 1);
         }
+        auto state = [&] {  // L
+          if (tc::elect_one()) {
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) tc::mma_f16(tmem + P::COL_L, k_mn + ((i * 2048) >> 4), hi_mn + ((i * 2048) >> 4), id_l, i > 0);
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) tc::mma_f16(tmem + P::COL_L, k_mn + ((i * 2048) >> 4), lo_mn + ((i * 2048) >> 4), id_l, 1);
+            tc::mma_commit(sh.bar(P::L_FULL));
+          }
+          __syncwarp();
+        };
+        sh.wait(P::S_READY, ph, ok);  // and L has been read
         if constexpr (kOut) {
-          sh.wait(P::S_READY, ph, ok);
-          if (!ok) break;
-          // the chunk's buffer of O, and where the decay is wide the other for O1
-          const bool wide = ssm_wide(small.total[ph]);
-          const uint32_t o = tmem + P::COL_O + ph * 128, o1 = wide ? tmem + P::COL_O + (ph ^ 1) * 128 : o;
           if (c > 1) sh.wait(P::O_READ + ph, ((c >> 1) - 1) & 1, ok);
-          if (c > 0 && (wide || was_wide)) sh.wait(P::O_READ + (ph ^ 1), ((c - 1) >> 1) & 1, ok);
-          was_wide = wide;
           if (!ok) break;
+          const bool wide[2] = {ssm_wide(small.total[ph][0]), ssm_wide(small.total[ph][1])}, any = wide[0] || wide[1];
+          const uint32_t o = tmem + P::COL_O + ph * 128;  // the chunk's buffer
           tc::fence_after_sync();
           if (tc::elect_one()) {
 #pragma unroll 2
@@ -552,30 +576,33 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           }
           __syncwarp();
           sh.wait(P::V_READY, ph, ok);
-          sh.wait(P::A_READY, ph, ok);
-          if (wide) sh.wait(P::X_FULL, ph, ok);
           if (!ok) break;
           tc::fence_after_sync();
-          if (tc::elect_one()) {
-            if (!wide || SLICES == 2) {
-              const uint64_t b_mn = wide ? v_mn : hi_mn;
-#pragma unroll 2
-              for (int i = 0; i < 8; ++i) tc::mma_f16_ts(o1, tmem + P::COL_G + 8 * i + (i & 4) * 8, b_mn + ((i * 2048) >> 4), id_o, !wide || i > 0);
-            } else {
-              for (int u = 0; u < 2; ++u)
-#pragma unroll 2
-                for (int i = 0; i < 8; ++i)
-                  tc::mma_f16_ts(o1 + 64 * u, tmem + P::COL_L + 64 * u + 8 * i, v_mn + ((u * P::BLOCK + i * 2048) >> 4), id_o64, i > 0);
-            }
-          }
-          __syncwarp();
+          state();  // L before O1: the next state then waits for neither A nor O1
           if (c + 1 < chunks) {
             sh.wait(P::Q_FREE, ph, ok);
             if (!ok) break;
             copy(&q_map, P::Q, P::Q_FULL, c + 1);
           }
+          sh.wait(P::A_READY, ph, ok);
+          if (any) sh.wait(P::X_FULL, ph, ok);
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            if (!any || SLICES == 2) {
+              const uint64_t b_mn = any ? v_mn : hi_mn;
+#pragma unroll 2
+              for (int i = 0; i < 8; ++i) tc::mma_f16_ts(o, tmem + P::COL_G + 8 * i + (i & 4) * 8, b_mn + ((i * 2048) >> 4), id_o, 1);
+            } else {
+              for (int u = 0; u < 2; ++u)
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i)
+                  tc::mma_f16_ts(o + 64 * u, tmem + P::COL_G + 32 * (i >> 1) + 16 * u + 8 * (i & 1), (wide[u] ? v_mn : hi_mn) + ((u * P::BLOCK + i * 2048) >> 4), id_o64, 1);
+            }
+            tc::mma_commit(sh.bar(P::O_FULL + ph));
+          }
+          __syncwarp();
         } else {
-          sh.wait(P::S_READY, ph, ok);  // L has been read
           sh.wait(P::V_READY, ph, ok);
           if (!ok) break;
           tc::fence_after_sync();
@@ -585,15 +612,8 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
               tc::tma_prefetch_2d(&v_map, kh * heads * DV + (2 * (pair % per_key) + x) * 64, start + (c + 2) * kSsmChunk);
           }
           __syncwarp();
+          state();
         }
-        if (tc::elect_one()) {
-#pragma unroll 2
-          for (int i = 0; i < 8; ++i) tc::mma_f16(tmem + P::COL_L, k_mn + ((i * 2048) >> 4), hi_mn + ((i * 2048) >> 4), id_l, i > 0);
-#pragma unroll 2
-          for (int i = 0; i < 8; ++i) tc::mma_f16(tmem + P::COL_L, k_mn + ((i * 2048) >> 4), lo_mn + ((i * 2048) >> 4), id_l, 1);
-          tc::mma_commit(sh.bar(P::L_FULL));
-        }
-        __syncwarp();
       }
     } else if (warp < 19) {
       // ---- gates, a warp a unit, four tokens a lane -----------------------------------------------
@@ -643,16 +663,21 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         sh.arrive(P::GATES);
       }
     } else if (kOut) {
-      // ---- the rows of v, once those before have been used; and what comes two chunks on, into L2 -----------
-      const int left = min(2, units - 2 * (pair % per_key));
+      // ---- the rows: out what is there of the chunk before, then v in its place; and what comes two chunks on, into L2 ---------
+      const int left = min(2, units - 2 * (pair % per_key)), col = kh * heads * DV + 2 * (pair % per_key) * 64;
       for (int c = 0; c < chunks; ++c) {
-        if (c > 0) sh.wait(P::ROWS_FREE, (c & 1) ^ 1, ok);
+        const int at = start + c * kSsmChunk, ahead = at + 2 * kSsmChunk;
+        if (c > 0) sh.wait(P::STAGED, (c & 1) ^ 1, ok);
         if (!ok) break;
         if (tc::elect_one()) {
+          if (c > 0) {
+            for (int x = 0; x < left; ++x) tc::tma_store_2d(&out_map, col + 64 * x, at - kSsmChunk, sbase + P::ROWS + x * P::BLOCK);
+            tc::tma_store_commit();
+            tc::tma_store_wait_read();
+          }
           tc::mbar_arrive_expect_tx(sh.bar(P::X_FULL), left * P::BLOCK);
-          const int col = kh * heads * DV + 2 * (pair % per_key) * 64, ahead = start + (c + 2) * kSsmChunk;
           for (int x = 0; x < left; ++x) {
-            tc::tma_load_2d(sbase + P::ROWS + x * P::BLOCK, &v_map, col + 64 * x, start + c * kSsmChunk, sh.bar(P::X_FULL));
+            tc::tma_load_2d(sbase + P::ROWS + x * P::BLOCK, &v_map, col + 64 * x, at, sh.bar(P::X_FULL));
             if (c + 2 < chunks) tc::tma_prefetch_2d(&v_map, col + 64 * x, ahead);
           }
           if (c + 2 < chunks)
@@ -663,6 +688,13 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         }
         __syncwarp();
       }
+      if (tokens % kSsmChunk == 0) sh.wait(P::STAGED, (chunks - 1) & 1, ok);
+      if (ok && tokens % kSsmChunk == 0 && tc::elect_one()) {
+        for (int x = 0; x < left; ++x) tc::tma_store_2d(&out_map, col + 64 * x, start + tokens - kSsmChunk, sbase + P::ROWS + x * P::BLOCK);
+        tc::tma_store_commit();
+        tc::tma_store_wait_read();
+      }
+      __syncwarp();
     }
   }
   __syncwarp();
