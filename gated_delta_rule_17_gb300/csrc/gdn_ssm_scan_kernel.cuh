@@ -17,8 +17,8 @@
 // the same for both heads, and bf16 has fp32's exponents. That holds while the chunk's decay stays within
 // kSsmSpan. A head whose chunk decays further has an A of its own, with d_j e^{suf_j - suf_i}, and V = v: beside the diagonal as
 // (d_j e^{suf_j - b}) e^{b - suf_i} about the decay b behind every 16 columns, where neither factor passes 1 or d, on it pair by pair; and
-// O2's rows are scaled before O1 comes on top. Operands of 16 bits cost the output what its own rounding does: 2.2e-3 of its size in
-// bf16, 1.7e-3 if it were rounded only once; the state is off by under 1e-5.
+// O2's rows are scaled before O1 comes on top. Operands of 16 bits cost the output little beside its own rounding: it is off by 1.9e-3 of
+// its size in the mean, 1.7e-3 if it were rounded only once; the state is off by 4e-6.
 //
 // Roles: warps 0-7, a thread a row of S and of the outputs (warps 0-3 unit 0, 4-7 unit 1), S in registers; warps 8-15 make
 // the operands, V' of their unit and half of A; warp 16 copies Q and K (TMA) and issues the products. Order on the tensor
@@ -191,7 +191,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   if (place.seq < 0 || (!kOut && place.seg == place.segs - 1)) return;
   const int seq = place.seq, begin = p.batch.start(seq), end = p.batch.end(seq);
   if (!rows_held(begin, end, p.batch.rows) || begin == end) return;
-  if (sbase & 1023) {  // the swizzled tiles' place; the linker keeps it
+  if (sbase & 1023) {  // the swizzle goes by the address; the alignment that smem is declared with gives it
     if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
     return;
   }
@@ -264,7 +264,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       struct Factors {
         float row, keep, grow, to16;
       };
-      [[maybe_unused]] auto factors = [&](int c) {
+      auto factors = [&](int c) {
         sh.wait(P::GATES, c & 1, ok);
         const float suf = small.suf[x][t], total = small.total[c & 1][x];
         const bool wide = ssm_wide(total);
@@ -326,7 +326,8 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           }
           tc::fence_before_sync();
           sh.arrive(P::O_READ + (ph ^ 1));
-          // out by one copy, the last chunk of a sequence by its rows (a row a thread with plain stores took 4000 cycles a chunk)
+          // out by one copy (by plain stores of eight lanes a row the scan of 4 x 8192 took half as long again), the last chunk of a
+          // sequence by its rows, of which the copy would write those behind it too
           const int at = (c - 1) * kSsmChunk, n = tokens - at;
           if (n >= kSsmChunk) {
             tc::fence_proxy_async();
@@ -642,10 +643,16 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           d[i] = !(opaque(is_real) && c * kSsmChunk + 4 * lane + i < tokens) ? 0.f : opaque(p.softplus) ? fmaxf(y, 0.f) + log1pf(__expf(-fabsf(y))) : y;
         }
         if (c + 1 < chunks) fetch(c + 1);
+        // a token's decay; from e^-200 on it is none in fp32, and as no more than that the sums behind it keep their last bits for the
+        // tokens before it
+        auto gate = [&](int i) {
+          const float g = d[i] * a;
+          return g < -200.f ? -200.f : g;
+        };
         suf[3] = 0.f;
 #pragma unroll
-        for (int i = 3; i > 0; --i) suf[i - 1] = fmaf(d[i], a, suf[i]);
-        float incl = fmaf(d[0], a, suf[0]);  // from this lane's first token to the chunk's last
+        for (int i = 3; i > 0; --i) suf[i - 1] = gate(i) + suf[i];
+        float incl = gate(0) + suf[0];  // from this lane's first token to the chunk's last
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const float y = __shfl_down_sync(0xffffffffu, incl, o);

@@ -572,3 +572,28 @@ def test_scan_in_segments(gdn, lens, nk, nv, dk, dv, packed):
         gdn.check()
         assert all(torch.equal(a, b) for a, b in zip(*got))
         check_scan(*got[0], want, sum(lens))
+
+
+def test_scan_over_decays_of_all_sizes(gdn):
+    """Chunks that decay by little and by much in one sequence, heads of both kinds side by side, and tokens that reset the state:
+    a step so large that its decay is none in fp32 leaves the tokens before it as exact as the others."""
+    lens = [900, 390]
+    for dk, dv, nk, nv in ((128, 64, 1, 4), (64, 64, 2, 6), (128, 128, 1, 2)):
+        s = ssm(lens, nk, nv, dk, dv, seed=17, steps=0.05, rate=8.0)
+        rows = sum(lens)
+        gen = torch.Generator(device=DEV).manual_seed(3)
+        s["dt"][130:256, ::2] += 5.0
+        s["dt"][256:384] += 2.0
+        s["dt"][500:640, 1::2] += 8.0
+        at = torch.randperm(rows, generator=gen, device=DEV)[:12]
+        s["dt"][at] = torch.tensor([30.0, 1e3, 1e5, 1e7, 1e9, 300.0] * 2, device=DEV)[:, None]
+        s["v"][at] = (s["v"][at].float() * 1e-3).to(torch.bfloat16)
+        z = s["dt"].double() + s["bias"].double()
+        s["d"] = torch.logaddexp(z, torch.zeros_like(z))  # softplus without an overflow at any size
+        want = ssm_want(s, lens)
+        out, state = torch.empty(rows, nv * dv, dtype=torch.bfloat16, device=DEV), s["state"].clone()
+        gdn.ssm_scan(s["q"], s["k"], s["v"], s["dt"], s["a"], state, out, **s["args"], **batch(lens, True))
+        gdn.check()
+        o, S, mags, M = want
+        near(out.view(o.shape), o, 2.0 ** -6 * mags + 2.0 ** -8 * o.abs() + 1e-30, "out")
+        near(state, S, 2.0 ** -14 * M + 1e-30, "state")
