@@ -64,6 +64,18 @@ int check_flag(int value, const char* name) {
   return GDN_OK;
 }
 
+// An output in the place of an input takes its rows' stride too.
+struct Same {
+  const char *out_name, *in_name;
+  const void *out, *in;
+  int64_t out_stride, in_stride;
+};
+int check_same(const Same& s) {
+  if (s.out && s.out == s.in && s.out_stride != s.in_stride)
+    return fail(GDN_ERR_ARG, "%s in the place of %s needs its row stride: %lld, not %lld", s.out_name, s.in_name, (long long)s.in_stride, (long long)s.out_stride);
+  return GDN_OK;
+}
+
 int check_batch(int B, int T, const int32_t* cu, gdn::Rows* out) {
   if (B < 0 || T < 0) return fail(GDN_ERR_ARG, "B = %d or T = %d is negative", B, T);
   const int64_t rows = cu ? T : static_cast<int64_t>(B) * T;
@@ -118,6 +130,8 @@ void launch_early(void (*kernel)(A...), int64_t grid, int threads, cudaStream_t 
 
 // ---- convolution ---------------------------------------------------------------------
 
+constexpr int kConvMaxD = 1 << 26;  // (width + 1) D in 32 bits
+
 template <typename F>
 void by_width(int width, F&& f) {
   if (width == 2) f(IntC<2>{});
@@ -140,7 +154,9 @@ int conv_bwd_strip(int64_t rows, int words, int sms) { return conv_strips(rows, 
 
 int conv_setup(const void* x, const float* weight, const float* bias, int D, int width, int silu, int dtype, int64_t x_stride,
                gdn::ConvParams* p) {
-  if (D < 1 || D % 8) return fail(GDN_ERR_UNSUPPORTED, "D = %d is not a positive multiple of 8", D);
+  if (D < 8 || D % 8 || D > kConvMaxD) return fail(GDN_ERR_UNSUPPORTED, "D = %d is not a multiple of 8 in 8..%d", D, kConvMaxD);
+  if (static_cast<int64_t>(p->batch.B) * D > static_cast<int64_t>(INT32_MAX) * 128)  // CTAs of a thread for four channels of a state
+    return fail(GDN_ERR_UNSUPPORTED, "%d sequences of %d channels exceed the item range", p->batch.B, D);
   if (width < 2 || width > 4) return fail(GDN_ERR_UNSUPPORTED, "width = %d is not 2, 3 or 4", width);
   if (int rc = check_type(dtype)) return rc;
   if (int rc = check_flag(silu, "silu")) return rc;
@@ -270,6 +286,7 @@ int ssm_setup(const void* q, const void* k, const void* v, const void* dt, const
   if (nv % nk) return fail(GDN_ERR_UNSUPPORTED, "nv = %d is not a multiple of nk = %d", nv, nk);
   if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return fail(GDN_ERR_UNSUPPORTED, "dk = %d or dv = %d is neither 64 nor 128", dk, dv);
   const int64_t wk = static_cast<int64_t>(nk) * dk, wv = static_cast<int64_t>(nv) * dv;
+  if (wv > INT32_MAX || wk > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%d heads of %d values exceed a row's range", nv, dv);
   if (int rc = take_stride(o ? o->q : 0, wk, "q", &p->q_stride)) return rc;
   if (int rc = take_stride(o ? o->k : 0, wk, "k", &p->k_stride)) return rc;
   if (int rc = take_stride(o ? o->v : 0, wv, "v", &p->v_stride)) return rc;
@@ -412,7 +429,6 @@ int gdn_causal_conv(const void* x, const float* weight, const float* bias, void*
   }
   p.strips = ceil_div(rows, p.strip);
   const int64_t threads = static_cast<int64_t>(p.strips) * words;
-  if (threads > static_cast<int64_t>(INT32_MAX) * 64) return fail(GDN_ERR_UNSUPPORTED, "%d rows of %d channels exceed the item range", rows, D);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool after = state && !p.state_here;
   by_type(dtype, [&](auto t) {
@@ -427,7 +443,7 @@ int gdn_causal_conv(const void* x, const float* weight, const float* bias, void*
 }
 
 size_t gdn_causal_conv_backward_workspace_bytes(int rows, int D, int width) {
-  if (rows <= 0 || D < 1 || D % 8 || width < 2 || width > 4) return 0;
+  if (rows <= 0 || D < 8 || D % 8 || D > kConvMaxD || width < 2 || width > 4) return 0;
   const int strip = conv_bwd_strip(rows, D / 4, gdn_host::plan_sms());
   return static_cast<size_t>(ceil_div(rows, strip)) * (width + 1) * D * sizeof(float);
 }
@@ -451,13 +467,14 @@ int gdn_causal_conv_backward(const void* x, const float* weight, const float* bi
   const size_t need = sums ? gdn_causal_conv_backward_workspace_bytes(rows, D, width) : 0;
   if (need)
     if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
-  int sms = 0;
-  if (int rc = gdn_host::device(&sms, &p.status)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (rows == 0) {  // sums over no rows
     if (int rc = zero(dweight, static_cast<int64_t>(D) * width, s)) return rc;
     if (int rc = zero(dbias, D, s)) return rc;
+    if (B == 0 || !dh0) return GDN_OK;
   }
+  int sms = 0;
+  if (int rc = gdn_host::device(&sms, &p.status)) return rc;
   p.state = const_cast<void*>(h0);
   p.dout = dout;
   p.dx = dx;
@@ -499,6 +516,7 @@ int gdn_ssm_scan(const void* q, const void* k, const void* v, const void* dt, co
   const int rows = B == 0 ? 0 : p.batch.rows;
   if (int rc = ssm_setup(q, k, v, dt, a, dt_bias, skip, state, out, nk, nv, dk, dv, options, rows, &p)) return rc;
   if (rows == 0) return GDN_OK;
+  if (out == v || out == q || out == k) return fail(GDN_ERR_ARG, "out must not be q, k or v: rows are read by several CTAs");
   int sms = 0;
   if (int rc = gdn_host::device(&sms, &p.status)) return rc;
   gdn::SsmScanParams sp{};
@@ -554,6 +572,8 @@ int gdn_layer_norm(const void* x, const void* gate, const float* weight, const f
   if (rows == 0) return GDN_OK;
   if (!out) return fail(GDN_ERR_ARG, "a required pointer is NULL");
   if (!aligned(out, 16)) return fail(GDN_ERR_ARG, "out must be 16-byte aligned");
+  for (const auto& a : {Same{"out", "x", out, x, p.out_stride, p.x_stride}, Same{"out", "gate", out, gate, p.out_stride, p.gate_stride}})
+    if (int rc = check_same(a)) return rc;
   int sms = 0;
   unsigned* status = nullptr;
   if (int rc = gdn_host::device(&sms, &status)) return rc;
@@ -593,14 +613,19 @@ int gdn_layer_norm_backward(const void* x, const void* gate, const float* weight
   const size_t need = sums ? gdn_layer_norm_backward_workspace_bytes(rows, groups, dim) : 0;
   if (need)
     if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
-  int sms = 0;
-  unsigned* status = nullptr;
-  if (int rc = gdn_host::device(&sms, &status)) return rc;
+  for (const auto& a : {Same{"dx", "x", dx, x, p.out_stride, p.x_stride}, Same{"dx", "dout", dx, dout, p.out_stride, p.dout_stride},
+                        Same{"dx", "gate", dx, gate, p.out_stride, p.gate_stride}, Same{"dgate", "gate", dgate, gate, p.dgate_stride, p.gate_stride},
+                        Same{"dgate", "x", dgate, x, p.dgate_stride, p.x_stride}, Same{"dgate", "dout", dgate, dout, p.dgate_stride, p.dout_stride}})
+    if (int rc = check_same(a)) return rc;
+  if (dx && dx == dgate) return fail(GDN_ERR_ARG, "dx and dgate must not be the same");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (rows == 0) {  // sums over no rows
     if (int rc = zero(dweight, dim, s)) return rc;
     return zero(dbias, dim, s);
   }
+  int sms = 0;
+  unsigned* status = nullptr;
+  if (int rc = gdn_host::device(&sms, &status)) return rc;
   p.dout = dout;
   p.out = dx;
   p.dgate = dgate;

@@ -139,19 +139,6 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* r, bool wide)
   }
 }
 
-// 32 bytes from global memory, likewise.
-__device__ __forceinline__ void load32(const void* src, uint32_t* r, bool wide) {
-  if (wide) {
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "l"(__cvta_generic_to_global(src)));
-  } else {
-    const uint4 a = reinterpret_cast<const uint4*>(src)[0], b = reinterpret_cast<const uint4*>(src)[1];
-    r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
-    r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
-  }
-}
-
 // 1 / (1 + e^-y), y of it, in two operations of the special function unit: the plain exponential and division cost
 // twice the instructions for results in the subnormal range. Where e^-y passes fp32's range they give 0.
 __device__ __forceinline__ float sigmoid(float y) {

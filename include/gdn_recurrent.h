@@ -42,7 +42,7 @@ extern "C" {
  *             inputs together); with state_is_table = 1 a device array of B device
  *             pointers, each to a 16-byte aligned [width-1][D]. NULL: zeros, and
  *             nothing is kept.
- * D is a multiple of 8. One launch (two where a sequence that has a state may be
+ * A table's pointers differ from one another. D is a multiple of 8 up to 2^26. One launch (two where a sequence that has a state may be
  * longer than a thread's strip of rows). */
 int gdn_causal_conv(const void* x, const float* weight, const float* bias, void* state, void* out, int B, int T,
                     int D, int width, int silu, int dtype, int state_is_table, int64_t x_stride, int64_t out_stride,
@@ -84,10 +84,18 @@ typedef struct {
  *   q, k     : bf16 [rows][nk][dk];  v, out : bf16 [rows][nv][dv]; out overlaps no input
  *   a        : fp32 [nv], <= 0;  dt_bias, skip : fp32 [nv] or NULL (zeros). Steps are >= 0.
  *   state    : fp32 [B][nv][dk][dv] (or a table of B pointers to [nv][dk][dv], each
- *              16-byte aligned), read as S_0 and overwritten with the last S.
+ *              16-byte aligned, no two the same), read as S_0 and overwritten with
+ *              the last S.
  *   dk, dv   : 64 or 128 each.
+ * Chunks of 128 tokens on the tensor cores: products take bf16 operands and sum in
+ * fp32; the state is fp32, its updates keep 16 bits of each term. Steps, decays and
+ * their sums are fp32. q, k and v of a sequence's own tokens must be finite (a value
+ * that is not reaches the whole chunk's outputs); what lies behind a sequence need not.
+ * The same inputs give the same bits.
  *   workspace: gdn_ssm_scan_workspace_bytes() bytes, 256-byte aligned, or NULL to
- *              allocate it stream-ordered. Calls that overlap need one each. */
+ *              allocate it stream-ordered. Calls that overlap need one each. It may be 0:
+ *              segments of long sequences take it, where there are few heads for the SMs.
+ * One launch, or two with segments. */
 size_t gdn_ssm_scan_workspace_bytes(int B, int T, int nk, int nv, int dk, int dv, int varlen);
 int gdn_ssm_scan(const void* q, const void* k, const void* v, const void* dt, const float* a, const float* dt_bias,
                  const float* skip, void* state, void* out, int B, int T, int nk, int nv, int dk, int dv,
@@ -119,7 +127,7 @@ int gdn_layer_norm(const void* x, const void* gate, const float* weight, const f
 
 /* Backward of gdn_layer_norm. x, gate, weight, bias and the rest as given to it.
  *   dx, dgate      : dL/dx, dL/dgate, `dtype` elements; dgate wherever there is a gate.
- *                    dx may be x or dout itself, dgate may be gate (with their strides).
+ *                    Each may be x, dout or gate itself (with its stride), not both the same.
  *   dweight, dbias : fp32 [dim], overwritten with the sums over rows and groups, in a
  *                    fixed order; NULL where not wanted.
  *   workspace      : gdn_layer_norm_backward_workspace_bytes() bytes, 256-byte aligned,
