@@ -326,40 +326,51 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4) gdn_conv
         before[W - 2][i] = now[i];
       }
     };
-    const T *fx = x + row * p.x_stride, *fg = dout + row * p.dout_stride;
+    const T *fx = x + row * p.x_stride, *fg = dout + row * p.dout_stride;  // of the row that is fetched next
     T* to_dx = dx + (row - (W - 1)) * p.dx_stride;
     Word* mine = &ring[0][0][threadIdx.x];
-    const uint32_t slots = tc::smem_u32(mine);
     constexpr int BYTES = sizeof(Word), ROW = 2 * kConvThreads;
-    auto fetch = [&](int k, int left) {  // step k from here, of `left` rows
-      if (left > 0)
+    const uint32_t slots = tc::smem_u32(mine), after = slots + A * U * ROW * BYTES;
+    uint32_t slot = slots;
+    auto fetch = [&](int left) {  // a step, of `left` rows
+      auto one = [&](int u) {
+        conv_fetch<BYTES>(slot + u * (ROW * BYTES), fx);
+        conv_fetch<BYTES>(slot + u * (ROW * BYTES) + kConvThreads * BYTES, fg);
+        fx += p.x_stride;
+        fg += p.dout_stride;
+      };
+      if (left >= U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) one(u);
+      } else {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (u < left) {
-            conv_fetch<BYTES>(slots + (k % A * U + u) * (ROW * BYTES), fx + (k * U + u) * p.x_stride);
-            conv_fetch<BYTES>(slots + (k % A * U + u) * (ROW * BYTES) + kConvThreads * BYTES, fg + (k * U + u) * p.dout_stride);
-          }
+          if (u < left) one(u);
+      }
+      slot = slot + U * ROW * BYTES == after ? slots : slot + U * ROW * BYTES;
       tc::cp_async_commit();
     };
 #pragma unroll
-    for (int k = 0; k < A - 1; ++k) fetch(k, to - row - k * U);
-    for (int k = 0; row < to; row += U, ++k) {
-      fetch(k + A - 1, to - row - (A - 1) * U);
+    for (int k = 0; k < A - 1; ++k) fetch(to - row - k * U);
+    for (const Word* now = mine; row < to; row += U) {
+      fetch(to - row - (A - 1) * U);
       conv_wait<A - 1>();
-      const Word* now = mine + k % A * U * ROW;
       if (row >= first + W - 1 && row + U <= own) {  // inside the strip: no ends to look for
 #pragma unroll
         for (int u = 0; u < U; ++u)
           step(now[u * ROW], now[u * ROW + kConvThreads], true, [&](const Pair (&dy)[2]) {
             float f[4];
             gradient(dy, f);
-            store4(to_dx + (k * U + u) * p.dx_stride, f);
+            store4(to_dx, f);
+            to_dx += p.dx_stride;
           });
       } else {
 #pragma unroll 1
         for (int u = 0; u < U && row + u < to; ++u)
           step(now[u * ROW], now[u * ROW + kConvThreads], row + u < own, [&](const Pair (&dy)[2]) { put(row + u, dy); });
+        to_dx += U * p.dx_stride;
       }
+      now = now + U * ROW == mine + A * U * ROW ? mine : now + U * ROW;
     }
     row = to;
     if (to == end) {  // nothing comes after the sequence's end
