@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtasPerSm) gdn_conv_kernel(
   constexpr int N = Word16<T>::N, P = Word16<T>::PAIRS, U = conv_step<W>, A = kConvAhead;
   __shared__ uint4 ring[A * U][kConvThreads];
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
+  tc::grid_dependency_wait();
   for (int64_t s = item; s < p.batch.B; s += static_cast<int64_t>(gridDim.x) * kConvThreads) p.batch.report(static_cast<int>(s), p.status);
   const int words = p.D / N;
   const int strip = static_cast<int>(item / words);
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4) gdn_conv
   constexpr int U = conv_step<W>, A = sizeof(T) == 4 ? 2 : kConvAhead;
   __shared__ Word ring[A * U][2][kConvThreads];
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
+  tc::grid_dependency_wait();
   for (int64_t s = item; s < p.batch.B; s += static_cast<int64_t>(gridDim.x) * kConvThreads) p.batch.report(static_cast<int>(s), p.status);
   const int words = p.D / 4;
   const int strip = static_cast<int>(item / words);

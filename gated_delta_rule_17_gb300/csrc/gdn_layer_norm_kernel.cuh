@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(norm_threads<L>) gdn_layer_norm_kernel(const L
   int turn = 0;
   const int lane = threadIdx.x % L;
   const uint32_t first = blockIdx.x * (SLOTS * R) + threadIdx.x / L, groups = static_cast<uint32_t>(p.groups), items = static_cast<uint32_t>(p.items);
+  tc::grid_dependency_wait();
   Eight<T> xw[R][NV], zw[kGate ? R : 1][NV];
   uint32_t row[R], at[R];
 #pragma unroll
@@ -351,6 +352,7 @@ __global__ void __launch_bounds__(128, kGate ? 4 : kNormSmallCtas) gdn_layer_nor
   int turn = 0;
   const int lane = threadIdx.x % L, slot = threadIdx.x / L, c = lane * 8;
   const uint32_t step = gridDim.x * SLOTS, groups = static_cast<uint32_t>(p.groups), items = static_cast<uint32_t>(p.items);
+  tc::grid_dependency_wait();
   NormColumns<1, kGate> cols;
   cols.start(p, lane, L);
   Eight<T> xw[1], gw[1], zw[1];
@@ -413,6 +415,7 @@ __global__ void __launch_bounds__(L, norm_wide_ctas<L, kGate>) gdn_layer_norm_bw
   const uint32_t groups = static_cast<uint32_t>(p.groups), items = static_cast<uint32_t>(p.items), step = gridDim.x;
   const uint32_t bytes = p.dim * static_cast<uint32_t>(sizeof(T)), bars = tc::smem_u32(s_full), base = tc::smem_u32(ring);
   int turn = 0;
+  tc::grid_dependency_wait();
   auto copy = [&](uint32_t item, int stage) {
     const uint32_t row = item / groups, at = (item - row * groups) * p.dim, to = base + stage * ARRAYS * bytes, bar = bars + 8 * stage;
     tc::mbar_arrive_expect_tx(bar, ARRAYS * bytes);

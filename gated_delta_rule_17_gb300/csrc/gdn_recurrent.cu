@@ -115,10 +115,11 @@ int zero(float* p, int64_t n, cudaStream_t s) {
 // A launch that may start while the kernel before it in the stream ends; these kernels wait for that
 // one (tc::grid_dependency_wait) before they read or write global memory.
 template <typename... A, typename... B>
-void launch_early(void (*kernel)(A...), int64_t grid, int threads, cudaStream_t s, const B&... args) {
+void launch_early(void (*kernel)(A...), int64_t grid, int threads, int shared, cudaStream_t s, const B&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(shared);
   cfg.stream = s;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -433,10 +434,10 @@ int gdn_causal_conv(const void* x, const float* weight, const float* bias, void*
   const bool after = state && !p.state_here;
   by_type(dtype, [&](auto t) {
     by_width(width, [&](auto w) {
-      gdn::gdn_conv_kernel<decltype(t), w.value><<<ceil_div(threads, gdn::kConvThreads), gdn::kConvThreads, 0, s>>>(p);
+      launch_early(gdn::gdn_conv_kernel<decltype(t), w.value>, ceil_div(threads, gdn::kConvThreads), gdn::kConvThreads, 0, s, p);
       if (after)
         launch_early(gdn::gdn_conv_state_kernel<decltype(t), w.value>, ceil_div(static_cast<int64_t>(B) * words, gdn::kConvThreads),
-                     gdn::kConvThreads, s, p);
+                     gdn::kConvThreads, 0, s, p);
     });
   });
   return launched(after ? 2 : 1);
@@ -493,10 +494,10 @@ int gdn_causal_conv_backward(const void* x, const float* weight, const float* bi
   by_type(dtype, [&](auto t) {
     by_width(width, [&](auto w) {
       if (rows)
-        gdn::gdn_conv_bwd_kernel<decltype(t), w.value>
-            <<<ceil_div(static_cast<int64_t>(p.strips) * words, gdn::kConvThreads), gdn::kConvThreads, 0, s>>>(p);
+        launch_early(gdn::gdn_conv_bwd_kernel<decltype(t), w.value>, ceil_div(static_cast<int64_t>(p.strips) * words, gdn::kConvThreads),
+                     gdn::kConvThreads, 0, s, p);
       if (sum_ctas + end_ctas)
-        launch_early(gdn::gdn_conv_bwd_ends_kernel<decltype(t), w.value>, sum_ctas + end_ctas, gdn::kConvSumThreads, s, p, sum_ctas);
+        launch_early(gdn::gdn_conv_bwd_ends_kernel<decltype(t), w.value>, sum_ctas + end_ctas, gdn::kConvSumThreads, 0, s, p, sum_ctas);
     });
   });
   return release(need ? workspace : nullptr, ws, s, launched((rows > 0) + (sum_ctas + end_ctas > 0)));
@@ -542,8 +543,9 @@ int gdn_ssm_scan(const void* q, const void* k, const void* v, const void* dt, co
   sp.decays = seg.total ? reinterpret_cast<float*>(static_cast<char*>(ws) + seg.states) : nullptr;
   const int grid = seg.items * sp.pairs;
   by_state(dk, dv, [&](auto K, auto V) {
-    if (seg.segment) gdn::gdn_ssm_scan_kernel<K.value, V.value, false><<<grid, gdn::kSsmThreads, gdn::SsmPlan::DYN_SMEM, s>>>(q_map, k_map, v_map, out_map, sp);
-    gdn::gdn_ssm_scan_kernel<K.value, V.value, true><<<grid, gdn::kSsmThreads, gdn::SsmPlan::DYN_SMEM, s>>>(q_map, k_map, v_map, out_map, sp);
+    auto go = [&](auto kernel) { launch_early(kernel, grid, gdn::kSsmThreads, gdn::SsmPlan::DYN_SMEM, s, q_map, k_map, v_map, out_map, sp); };
+    if (seg.segment) go(gdn::gdn_ssm_scan_kernel<K.value, V.value, false>);
+    go(gdn::gdn_ssm_scan_kernel<K.value, V.value, true>);
   });
   return release(given, ws, s, launched(seg.segment ? 2 : 1));
 }
@@ -559,7 +561,7 @@ int gdn_ssm_decode(const void* q, const void* k, const void* v, const void* dt, 
   int sms = 0;
   if (int rc = gdn_host::device(&sms, &p.status)) return rc;
   by_state(dk, dv, [&](auto K, auto V) {
-    gdn::gdn_ssm_decode_kernel<K.value, V.value><<<B * nv, gdn::ssm_threads<K.value, V.value>, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    launch_early(gdn::gdn_ssm_decode_kernel<K.value, V.value>, B * nv, gdn::ssm_threads<K.value, V.value>, 0, static_cast<cudaStream_t>(stream), p);
   });
   return launched(1);
 }
@@ -583,8 +585,8 @@ int gdn_layer_norm(const void* x, const void* gate, const float* weight, const f
     by_dim(dim, [&](auto lanes, auto words) {
       constexpr int L = lanes.value, threads = gdn::norm_threads<L>;
       const int grid = ceil_div(p.items, threads / L * gdn::norm_rows<L, words.value>);
-      if (gate) gdn::gdn_layer_norm_kernel<decltype(t), L, words.value, true><<<grid, threads, 0, s>>>(p);
-      else gdn::gdn_layer_norm_kernel<decltype(t), L, words.value, false><<<grid, threads, 0, s>>>(p);
+      if (gate) launch_early(gdn::gdn_layer_norm_kernel<decltype(t), L, words.value, true>, grid, threads, 0, s, p);
+      else launch_early(gdn::gdn_layer_norm_kernel<decltype(t), L, words.value, false>, grid, threads, 0, s, p);
     });
   });
   return launched(1);
@@ -644,11 +646,11 @@ int gdn_layer_norm_backward(const void* x, const void* gate, const float* weight
       by_dim_backward<G>(dim, [&](auto lanes, auto words) {
         constexpr int L = lanes.value, NV = words.value;
         if constexpr (NV == 0) {
-          gdn::gdn_layer_norm_bwd_kernel<T, L, G><<<plan.ctas, 128, 0, s>>>(p);
+          launch_early(gdn::gdn_layer_norm_bwd_kernel<T, L, G>, plan.ctas, 128, 0, s, p);
         } else {
           auto kernel = gdn::gdn_layer_norm_bwd_wide_kernel<T, L, NV, G>;
           rc = allow_shared<T, L, NV, G>(reinterpret_cast<const void*>(kernel));
-          if (rc == GDN_OK) kernel<<<plan.ctas, L, plan.ring, s>>>(p);
+          if (rc == GDN_OK) launch_early(kernel, plan.ctas, L, plan.ring, s, p);
         }
       });
     };
@@ -657,7 +659,7 @@ int gdn_layer_norm_backward(const void* x, const void* gate, const float* weight
   });
   if (rc == GDN_OK) {
     if (sums)
-      launch_early(gdn::gdn_layer_norm_sum_kernel, ceil_div(2 * dim, 32), 1024, s, static_cast<const float*>(p.partials), plan.ctas, dim, dweight, dbias);
+      launch_early(gdn::gdn_layer_norm_sum_kernel, ceil_div(2 * dim, 32), 1024, 0, s, static_cast<const float*>(p.partials), plan.ctas, dim, dweight, dbias);
     rc = launched(sums ? 2 : 1);
   }
   return release(need ? workspace : nullptr, ws, s, rc);

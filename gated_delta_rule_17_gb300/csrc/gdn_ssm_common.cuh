@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(ssm_threads<DK, DV>) gdn_ssm_decode_kernel(con
   const int tid = threadIdx.x, col = 4 * (tid % LANES), r0 = tid / LANES;
   const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.nv)), b = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.nv));
   const int kh = h / (p.nv / p.nk);
+  tc::grid_dependency_wait();
   float* S = ssm_state<DK, DV>(p, b, h) + col;
   float4 s[16];
 #pragma unroll

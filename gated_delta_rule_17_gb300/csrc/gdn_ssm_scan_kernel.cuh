@@ -180,6 +180,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   const int pair = static_cast<int>(blockIdx.x % static_cast<unsigned>(params.pairs)), item = static_cast<int>(blockIdx.x / static_cast<unsigned>(params.pairs));
   const int heads = p.nv / p.nk, units = heads * SLICES, per_key = (units + 1) / 2;  // of a key head
   const int kh = pair / per_key;
+  tc::grid_dependency_wait();
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.batch.B; i += kSsmThreads) p.batch.report(i, p.status);
   if (warp == 0) {

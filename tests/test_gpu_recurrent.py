@@ -597,3 +597,74 @@ def test_scan_over_decays_of_all_sizes(gdn):
         o, S, mags, M = want
         near(out.view(o.shape), o, 2.0 ** -6 * mags + 2.0 ** -8 * o.abs() + 1e-30, "out")
         near(state, S, 2.0 ** -14 * M + 1e-30, "state")
+
+
+def calls_of_each(gdn, seed, given):
+    """A call of every operator, with workspaces of its own (`given`) or the stream's; outputs are the call's. A dense scan in segments
+    among them."""
+    lens = [150, 0, 260]
+    s, c = ssm(lens, 1, 2, 128, 64, seed=seed), make_conv(lens, 128, 4, torch.bfloat16, seed=seed)
+    n, m = make_norm(410, 2, 64, torch.bfloat16, 0, "rms", "after", seed=seed), make_norm(300, 1, 1000, torch.float16, 8, "layer", None, seed=seed)
+    long = ssm([4000], 1, 2, 64, 64, seed=seed)
+    b, one = batch(lens, True), batch([4000], False)
+    space = lambda size: torch.empty(max(size, 1), dtype=torch.uint8, device=DEV) if given else None
+    sizes = [gdn.causal_conv_backward_workspace_bytes(410, 128, 4), gdn.ssm_scan_workspace_bytes(3, 410, 1, 2, True, dv=64),
+             gdn.ssm_scan_workspace_bytes(1, 4000, 1, 2, False, dk=64, dv=64), gdn.layer_norm_backward_workspace_bytes(410, 2, 64),
+             gdn.layer_norm_backward_workspace_bytes(300, 1, 1000)]
+    assert sizes[2] > 0  # it goes in segments
+    ws = [space(x) for x in sizes]
+    bf = lambda *shape: torch.empty(*shape, dtype=torch.bfloat16, device=DEV)
+    o = [bf(410, 128) for _ in range(5)] + [bf(4000, 128), torch.empty(300, 1000, dtype=torch.float16, device=DEV), bf(410, 128)]
+    states = [s["state"].clone(), long["state"].clone(), s["state"].clone(), c["h0"].clone()]
+    sums = [torch.empty_like(t) for t in (c["w"], c["b"], n["weight"], m["weight"], m["weight"])] + [torch.empty_like(c["h0"])]
+
+    def run():
+        for t, f in zip(states, (s["state"], long["state"], s["state"], c["h0"])):
+            t.copy_(f)
+        gdn.causal_conv_backward(c["x"], c["w"], c["dout"], o[1], sums[0], sums[1], bias=c["b"], h0=c["h0"], dh0=sums[5], workspace=ws[0], **b)
+        gdn.causal_conv(c["x"], c["w"], o[0], bias=c["b"], state=states[3], **b)
+        gdn.ssm_scan(s["q"], s["k"], s["v"], s["dt"], s["a"], states[0], o[2], workspace=ws[1], **s["args"], **b)
+        gdn.ssm_scan(long["q"], long["k"], long["v"], long["dt"], long["a"], states[1], o[5], workspace=ws[2], **long["args"], **one)
+        gdn.ssm_decode(s["q"][:3], s["k"][:3], s["v"][:3], s["dt"][:3], s["a"], states[2], o[3][:3], **s["args"])
+        gdn.layer_norm_backward(n["x"], n["dout"], o[4], sums[2], weight=n["weight"], gate=n["gate"], dgate=o[7], workspace=ws[3], **n["form"])
+        gdn.layer_norm(n["x"], o[3], weight=n["weight"], gate=n["gate"], **n["form"])
+        gdn.layer_norm_backward(m["x"], m["dout"], o[6], sums[3], sums[4], weight=m["weight"], workspace=ws[4], **m["form"])
+
+    return run, lambda: [t.clone() for t in o + states + sums]
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_calls_that_overlap(gdn, given):
+    """Two runs of every operator at once, on two streams, as calls and as graphs, each against its own run alone."""
+    runs = [calls_of_each(gdn, seed, given) for seed in (41, 42)]
+    want = []
+    for run, got in runs:
+        run()
+        torch.cuda.synchronize()
+        want.append(got())
+    sides = [torch.cuda.Stream() for _ in runs]
+
+    def check():
+        torch.cuda.synchronize()
+        for w, (_, got) in zip(want, runs):
+            assert all(torch.equal(x, y) for x, y in zip(w, got()))
+
+    for _ in range(3):
+        for side, (run, _) in zip(sides, runs):
+            with torch.cuda.stream(side):
+                run()
+    check()
+    graphs = []
+    for side, (run, _) in zip(sides, runs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            run()
+    for _ in range(3):
+        for side, graph in zip(sides, graphs):
+            with torch.cuda.stream(side):
+                graph.replay()
+    check()
+    for run, _ in runs:  # and calls beside a graph
+        run()
+    check()
+    gdn.check()
