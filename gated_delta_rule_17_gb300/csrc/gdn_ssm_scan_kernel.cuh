@@ -61,7 +61,7 @@ struct SsmPlan {
   static constexpr uint32_t COL_G = 0, COL_O = 128, COL_L = 384, TMEM_COLS = 512;  // O: a buffer of 128 for even and odd chunks
   // mbarriers: copies (Q_FULL, K_FULL + buffer, X_FULL), products (G_FULL, Q_FREE, L_FULL, O_FULL + buffer) and warps' signals
   static constexpr int Q_FULL = 0, K_FULL = 1, G_FULL = 3, Q_FREE = 4, L_FULL = 5, X_FULL = 6, O_FULL = 7, GATES = 9, V_READY = 10, A_READY = 11,
-                       S_READY = 12, GATES_READ = 13, STAGED = 14, O_READ = 15, NBAR = 17;
+                       S_READY = 12, GATES_READ = 13, STAGED = 14, O_READ = 15, STEPS_READ = 17, NBAR = 18;
 };
 
 struct SsmScanParams {
@@ -372,20 +372,22 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       // ---- operands --------------------------------------------------------------------------
       fewer_registers<kSsmOperandRegs>();
       const int r0 = t & 96, quarter = warp & 3;  // the warp's tokens: r0 + 4 i + lane / 8, eight lanes a row
-      const __nv_bfloat16* v = p.v + static_cast<int64_t>(start) * p.v_stride + col + 8 * (lane & 7);
+      const __nv_bfloat16* v = p.v + static_cast<int64_t>(start + r0 + (lane >> 3)) * p.v_stride + col + 8 * (lane & 7);
       uint8_t* hi = smem + P::VHI + x * P::BLOCK;
       uint8_t* lo = smem + P::VLO + x * P::BLOCK;
       uint4 word[8];  // a chunk's v, ahead
       auto fetch = [&](int c) {
-        const bool held = opaque(is_real);
+        const int left = opaque(is_real) ? tokens - c * kSsmChunk - r0 - (lane >> 3) : 0;
+        const __nv_bfloat16* at = v + static_cast<int64_t>(c * kSsmChunk) * p.v_stride;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int r = c * kSsmChunk + r0 + 4 * i + (lane >> 3);
           word[i] = make_uint4(0, 0, 0, 0);
-          if (held && r < tokens) word[i] = *reinterpret_cast<const uint4*>(v + r * p.v_stride);
+          if (left > 4 * i) word[i] = *reinterpret_cast<const uint4*>(at);
+          at += 4 * p.v_stride;
         }
       };
       fetch(0);
+      bool own_v = false;  // whether O1 of the chunk before took v itself for this unit
       for (int c = 0; c < chunks; ++c) {
         const uint32_t ph = c & 1;
         const int n = min(kSsmChunk, tokens - c * kSsmChunk);
@@ -404,8 +406,9 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         const uint32_t both = pack2<__nv_bfloat16>(f_hi, f - f_hi);
         if (c > 0) {  // V is free
           sh.wait(P::L_FULL, ph ^ 1, ok);
-          if (kOut) sh.wait(P::O_FULL + (ph ^ 1), ((c - 1) >> 1) & 1, ok);
+          if (kOut && !own_v) sh.wait(P::O_FULL + (ph ^ 1), ((c - 1) >> 1) & 1, ok);
         }
+        own_v = wide;
         // V' = v f in pairs of bf16: with f = f_hi + f_lo, hi = v f_hi rounded, lo = (v f_hi - hi, exact) + v f_lo
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -431,6 +434,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         }
         tc::fence_proxy_async();
         sh.arrive(P::V_READY);
+        if (!kOut) sh.arrive(P::STEPS_READ);
         if constexpr (kOut) {
           sh.wait(P::G_FULL, ph, ok);
           // A: row t, columns 32 i .. 32 i + 31, of which it sees those up to itself. Half of it in place of this half of G;
@@ -488,6 +492,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             if (own_a) tc::named_barrier(7 + quarter, 64);
             tc::tmem_st16u(to + apart * i, k16);
           }
+          sh.arrive(P::STEPS_READ);
           if (wide) {  // O2's rows take the decay before them
             const float f = __expf(small.total[ph][x] - suf);
             const uint32_t o = tmem + lanes + P::COL_O + ph * 128 + 64 * x;
@@ -663,7 +668,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         if (lane == 31) behind = 0.f;
         if (c > 0) {  // the chunk's before are used
           sh.wait(P::GATES_READ, ph ^ 1, ok);
-          sh.wait(kOut ? P::A_READY : P::V_READY, ph ^ 1, ok);
+          sh.wait(P::STEPS_READ, ph ^ 1, ok);
         }
         *reinterpret_cast<float4*>(&small.d[x][4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
         *reinterpret_cast<float4*>(&small.suf[x][4 * lane]) = make_float4(suf[0] + behind, suf[1] + behind, suf[2] + behind, suf[3] + behind);
