@@ -373,8 +373,9 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       fewer_registers<kSsmOperandRegs>();
       const int r0 = t & 96, quarter = warp & 3;  // the warp's tokens: r0 + 4 i + lane / 8, eight lanes a row
       const __nv_bfloat16* v = p.v + static_cast<int64_t>(start + r0 + (lane >> 3)) * p.v_stride + col + 8 * (lane & 7);
-      uint8_t* hi = smem + P::VHI + x * P::BLOCK;
-      uint8_t* lo = smem + P::VLO + x * P::BLOCK;
+      uint8_t* hi[2];  // a lane's place in V' for even and odd i
+#pragma unroll
+      for (int i = 0; i < 2; ++i) hi[i] = smem + P::VHI + x * P::BLOCK + tc::sw128(r0 + 4 * i + (lane >> 3), 16 * (lane & 7));
       uint4 word[8];  // a chunk's v, ahead
       auto fetch = [&](int c) {
         const int left = opaque(is_real) ? tokens - c * kSsmChunk - r0 - (lane >> 3) : 0;
@@ -422,9 +423,9 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             a4[k] = as_u32(high);
             b4[k] = as_u32(__hfma2(e, fl, __hfma2(e, fh, __hneg2(high))));
           }
-          const uint32_t at = tc::sw128(r0 + 4 * i + (lane >> 3), 16 * (lane & 7));
-          *reinterpret_cast<uint4*>(hi + at) = make_uint4(a4[0], a4[1], a4[2], a4[3]);
-          *reinterpret_cast<uint4*>(lo + at) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
+          uint8_t* at = hi[i & 1] + i / 2 * 1024;
+          *reinterpret_cast<uint4*>(at) = make_uint4(a4[0], a4[1], a4[2], a4[3]);
+          *reinterpret_cast<uint4*>(at + (P::VLO - P::VHI)) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
         }
         if (kOut && any && n < kSsmChunk) {  // nor of v, which O then takes itself
           sh.wait(P::X_FULL, ph, ok);
