@@ -668,3 +668,58 @@ def test_calls_that_overlap(gdn, given):
         run()
     check()
     gdn.check()
+
+
+def test_offsets_past_32_bits(gdn):
+    """Rows that lie 2^29 elements apart, so that the last ones' offsets pass 32 bits, against the same rows packed."""
+    rows, far = 5, 1 << 29
+    s, c = ssm([2, 3], 1, 2, 128, 64, seed=51), make_conv([2, 3], 128, 4, torch.bfloat16, seed=51)
+    n = make_norm(rows, 2, 64, torch.bfloat16, 0, "rms", "after", seed=51)
+    b = batch([2, 3], True)
+    space = torch.empty(rows * far, dtype=torch.bfloat16, device=DEV)
+    used = [0]
+
+    def apart(t):  # the same rows, far from one another
+        v = space.as_strided((rows, t.shape[1]), (far, 1), used[0])
+        used[0] += 256
+        return v.copy_(t)
+
+    outs = []
+    for wide_apart in (False, True):
+        put = apart if wide_apart else lambda t: t.clone()
+        bf = lambda w=128: put(torch.zeros(rows, w, dtype=torch.bfloat16, device=DEV))
+        o = [bf() for _ in range(7)]
+        states = [c["h0"].clone(), s["state"].clone(), s["state"][:1].expand(rows, -1, -1, -1).contiguous()]
+        sums = [torch.empty_like(c["w"]), torch.empty_like(n["weight"])]
+        x, dout, q, k, v, z, g = (put(t) for t in (c["x"], c["dout"], s["q"], s["k"], s["v"], n["gate"], n["x"]))
+        gdn.causal_conv(x, c["w"], o[0], bias=c["b"], state=states[0], **b)
+        gdn.causal_conv_backward(x, c["w"], dout, o[1], sums[0], bias=c["b"], h0=c["h0"], **b)
+        gdn.ssm_scan(q, k, v, s["dt"], s["a"], states[1], o[2], **s["args"], **b)
+        gdn.ssm_decode(q, k, v, s["dt"], s["a"], states[2], o[3], **s["args"])
+        gdn.layer_norm(g, o[4], weight=n["weight"], gate=z, **n["form"])
+        gdn.layer_norm_backward(g, dout, o[5], sums[1], weight=n["weight"], gate=z, dgate=o[6], **n["form"])
+        gdn.check()
+        outs.append([t.clone() for t in o + states + sums])
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+
+
+def test_states_past_32_bits(gdn):
+    """A step of so many heads that the last states' offsets pass 32 bits, against those sequences alone."""
+    B, nv = 1100, 128
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    state = torch.empty(B, nv, 128, 128, device=DEV)
+    state[-2:] = rand(gen, 2, nv, 128, 128)
+    state[:-2] = 0
+    bf = torch.bfloat16
+    q, k, v = rand(gen, B, 128, dtype=bf), rand(gen, B, 128, dtype=bf), rand(gen, B, nv * 128, dtype=bf)
+    dt, a = rand(gen, B, nv), -torch.rand(nv, generator=gen, device=DEV)
+    assert state.numel() > 2 ** 31
+    few, out, one = state[-2:].clone(), torch.empty_like(v), torch.empty_like(v[-2:])
+    gdn.ssm_decode(q, k, v, dt, a, state, out, nk=1, nv=nv)
+    gdn.ssm_decode(q[-2:], k[-2:], v[-2:], dt[-2:], a, few, one, nk=1, nv=nv)
+    gdn.check()
+    assert torch.equal(state[-2:], few) and torch.equal(out[-2:], one)
+    d = torch.nn.functional.softplus(dt[0].double())
+    # the first sequence from nothing: k (d v)^T, d off by 4 steps of fp32, the products by one each
+    want = k[0].double()[None, :, None] * (d[:, None] * v[0].double().view(nv, 128))[:, None, :]
+    near(state[0], want, 2.0 ** -20 * want.abs() + 1e-30, "state")
