@@ -31,6 +31,7 @@
 // and copies for as much again; the rest is the roles' hand-offs. Copies of v and x by rows instead of by TMA, rows out by plain stores, one buffer of K,
 // and O begun from skip v each took 8% to half as long again. A segment's first pass takes 0.6 of the second's time.
 #pragma once
+#include <type_traits>
 #include "gdn_ssm_common.cuh"
 
 namespace gdn {
@@ -383,17 +384,27 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
 #pragma unroll
       for (int i = 0; i < 2; ++i) hi[i] = smem + P::VHI + x * P::BLOCK + tc::sw128(r0 + 4 * i + (lane >> 3), 16 * (lane & 7));
       uint4 word[8];  // a chunk's v, ahead
-      auto fetch = [&](int c) {
-        const int left = opaque(is_real) ? tokens - c * kSsmChunk - r0 - (lane >> 3) : 0;
-        const __nv_bfloat16* at = v + static_cast<int64_t>(c * kSsmChunk) * p.v_stride;
+      // Half of the next chunk's words come while A is made, where there are registers for no more, but not beside wide decays, whose A
+      // reads shared memory behind these loads: ragged prompts 362 -> 337 us, 448 -> 405 with wide decays (461 where those fetch early too)
+      auto fetch = [&](int c, auto first, auto last, bool now) {  // words first .. last - 1
+        constexpr int from = decltype(first)::value, to = decltype(last)::value;
+        const int left = opaque(is_real) && now ? tokens - c * kSsmChunk - r0 - (lane >> 3) : 0;
+        const __nv_bfloat16* at = v + static_cast<int64_t>(c * kSsmChunk + 4 * from) * p.v_stride;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          word[i] = make_uint4(0, 0, 0, 0);
+        for (int i = from; i < to; ++i) {
           if (left > 4 * i) word[i] = *reinterpret_cast<const uint4*>(at);
           at += 4 * p.v_stride;
         }
       };
-      fetch(0);
+      auto clear = [&] {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) word[i] = make_uint4(0, 0, 0, 0);
+      };
+      clear();
+      using None = std::integral_constant<int, 0>;
+      using Half = std::integral_constant<int, 4>;
+      using All = std::integral_constant<int, 8>;
+      fetch(0, None{}, All{}, true);
       bool own_v = false;  // whether O1 of the chunk before took v itself for this unit
       for (int c = 0; c < chunks; ++c) {
         const uint32_t ph = c & 1;
@@ -441,6 +452,8 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         }
         tc::fence_proxy_async();
         sh.arrive(P::V_READY);
+        clear();
+        fetch(c + 1, None{}, Half{}, c + 1 < chunks && !any);
         if (!kOut) sh.arrive(P::STEPS_READ);
         if constexpr (kOut) {
           sh.wait(P::G_FULL, ph, ok);
@@ -519,7 +532,10 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           tc::fence_before_sync();
           sh.arrive(P::A_READY);
         }
-        if (c + 1 < chunks) fetch(c + 1);
+        if (c + 1 < chunks) {
+          fetch(c + 1, None{}, Half{}, any);
+          fetch(c + 1, Half{}, All{}, true);
+        }
       }
     }
   } else {
