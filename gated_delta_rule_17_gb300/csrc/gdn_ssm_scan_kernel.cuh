@@ -27,7 +27,7 @@
 //
 // 4 x 8192 tokens of 32 heads of 128 x 128 on 16: 186 us, 198 to 209 with a few heads whose chunks decay by more than kSsmSpan; HBM alone
 // would take 122, the products 35. There is a CTA for 128 of the 152 SMs, and a chunk takes it 2.9 us. The tensor pipe is
-// busy for 29% of it, the issue slots for 42%, loads and stores keep shared memory for 37% and the products' operands (288 KB a chunk)
+// busy for 29% of it, the issue slots for 43%, loads and stores keep shared memory for 39% and the products' operands (288 KB a chunk)
 // and copies for as much again; the rest is the roles' hand-offs. Copies of v and x by rows instead of by TMA, rows out by plain stores, one buffer of K,
 // and O begun from skip v each took 8% to half as long again. A segment's first pass takes 0.6 of the second's time.
 #pragma once
