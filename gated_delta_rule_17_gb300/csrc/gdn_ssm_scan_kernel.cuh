@@ -53,7 +53,7 @@ struct SsmPlace {
 
 // What the roles tell one another beside tiles.
 struct SsmSmall {
-  uint64_t bar[18];
+  uint64_t bar[20];
   float suf[2][kSsmChunk], d[2][kSsmChunk];  // of each unit's tokens
   float total[2][2];                         // by chunk parity: each unit's decay
   float behind[2][8];                        // in chunks of wide decay: log2 of the decay behind each 16 tokens
@@ -66,9 +66,12 @@ struct SsmPlan {
   static constexpr int Q = 0, K = 2 * BLOCK, VHI = K + 4 * BLOCK, VLO = VHI + 2 * BLOCK, S16 = VLO + 2 * BLOCK, ROWS = S16 + 2 * BLOCK,
                        SMALL = ROWS + 2 * BLOCK, DYN_SMEM = SMALL + static_cast<int>(sizeof(SsmSmall));
   static constexpr uint32_t COL_G = 0, COL_O = 128, COL_L = 384, TMEM_COLS = 512;  // O: a buffer of 128 for even and odd chunks
-  // mbarriers: copies (Q_FULL, K_FULL + buffer, X_FULL), products (G_FULL, Q_FREE, L_FULL, O_FULL + buffer) and warps' signals
-  static constexpr int Q_FULL = 0, K_FULL = 1, G_FULL = 3, Q_FREE = 4, L_FULL = 5, X_FULL = 6, O_FULL = 7, GATES = 9, V_READY = 10, A_READY = 11,
-                       S_READY = 12, GATES_READ = 13, STAGED = 14, O_READ = 15, STEPS_READ = 17, NBAR = 18;
+  // mbarriers: copies (Q_FULL, K_FULL + buffer, X_FULL + chunk parity, X_LANDED), products (G_FULL, Q_FREE, L_FULL, O_FULL + buffer) and
+  // warps' signals. A wait by parity takes the phase before for its own unless that one is known to be over, and waits for ever where the
+  // phase behind its own may be over too; so each role either waits for every phase of a barrier, or the comment at its wait says what
+  // it knows them by.
+  static constexpr int Q_FULL = 0, K_FULL = 1, G_FULL = 3, Q_FREE = 4, L_FULL = 5, X_FULL = 6, X_LANDED = 8, O_FULL = 9, GATES = 11, V_READY = 12,
+                       A_READY = 13, S_READY = 14, GATES_READ = 15, STAGED = 16, O_READ = 17, STEPS_READ = 19, NBAR = 20;
 };
 
 struct SsmScanParams {
@@ -309,7 +312,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         }
         if (kOut && c > 0) {  // the rows of the chunk before
           const uint32_t from = tmem + lanes + P::COL_O + 64 * x, off = (c & 1) ? 0 : 128;  // its buffer
-          sh.wait(P::X_FULL, ph ^ 1, ok);
+          sh.wait(P::X_FULL + (ph ^ 1), ((c - 1) >> 1) & 1, ok);
           sh.wait(P::O_FULL + (ph ^ 1), ((c - 1) >> 1) & 1, ok);
           tc::fence_after_sync();
           const Pair by = pair_of(scale, scale);
@@ -410,7 +413,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         const uint32_t ph = c & 1;
         const int n = min(kSsmChunk, tokens - c * kSsmChunk);
         if (n < kSsmChunk) {  // rows of K behind the sequence are someone else's, or nobody's: as zeros they are no NaN
-          sh.wait(P::K_FULL + ph, (c >> 1) & 1, ok);
+          sh.wait(P::K_FULL + ph, (c >> 1) & 1, ok);  // (the phase before: L_FULL of chunk c - 2, which has read that K)
 #pragma unroll 1
           for (int i = threadIdx.x - 256; i < (kSsmChunk - n) * 8 * KB; i += 256) {
             const int r = n + i / (8 * KB), w = i % (8 * KB);
@@ -424,6 +427,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         const uint32_t both = pack2<__nv_bfloat16>(f_hi, f - f_hi);
         if (c > 0) {  // V is free
           sh.wait(P::L_FULL, ph ^ 1, ok);
+          // (the phase before: L of chunk c - 1 was issued behind O_READ of chunk c - 3)
           if (kOut && !own_v) sh.wait(P::O_FULL + (ph ^ 1), ((c - 1) >> 1) & 1, ok);
         }
         own_v = wide;
@@ -444,12 +448,6 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           *reinterpret_cast<uint4*>(at) = make_uint4(a4[0], a4[1], a4[2], a4[3]);
           *reinterpret_cast<uint4*>(at + (P::VLO - P::VHI)) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
         }
-        if (kOut && any && n < kSsmChunk) {  // nor of v, which O then takes itself
-          sh.wait(P::X_FULL, ph, ok);
-#pragma unroll 1
-          for (int i = threadIdx.x - 256; i < (kSsmChunk - n) * 16; i += 256)
-            *reinterpret_cast<uint4*>(smem + P::ROWS + (i & 8) / 8 * P::BLOCK + (n + i / 16) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
         tc::fence_proxy_async();
         sh.arrive(P::V_READY);
         clear();
@@ -463,7 +461,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           const float own = suf * kLog2e;
           if (wide) {  // d e^{suf - behind} in the place of d, and log2 of d e^{suf} in that of suf, once the rows' warps have it
             const float last = __shfl_sync(0xffffffffu, suf, lane | 15);
-            sh.wait(P::GATES_READ, ph, ok);
+            sh.wait(P::GATES_READ, ph, ok);  // (the phase before: GATES of this chunk came behind it)
             small.d[x][t] = d * __expf(suf - last);
             small.suf[x][t] = own + __log2f(d);
             if ((lane & 15) == 15) small.behind[x][t >> 4] = own;
@@ -516,7 +514,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           if (wide) {  // O2's rows take the decay before them
             const float f = __expf(small.total[ph][x] - suf);
             const uint32_t o = tmem + lanes + P::COL_O + ph * 128 + 64 * x;
-            sh.wait(P::Q_FREE, ph, ok);
+            sh.wait(P::Q_FREE, ph, ok);  // (the phase before: G of this chunk was issued behind it)
             tc::fence_after_sync();
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
@@ -615,7 +613,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             copy(&q_map, P::Q, P::Q_FULL, c + 1);
           }
           sh.wait(P::A_READY, ph, ok);
-          if (any) sh.wait(P::X_FULL, ph, ok);
+          if (any) sh.wait(P::X_FULL + ph, (c >> 1) & 1, ok);  // (the phase before: O_READ of chunk c - 2, whose rows had v)
           if (!ok) break;
           tc::fence_after_sync();
           if (tc::elect_one()) {
@@ -702,7 +700,8 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       // ---- the rows: out what is there of the chunk before, then v in its place; and what comes two chunks on, into L2 ---------
       const int left = min(2, units - 2 * (pair % per_key)), col = kh * heads * DV + 2 * (pair % per_key) * 64;
       for (int c = 0; c < chunks; ++c) {
-        const int at = start + c * kSsmChunk, ahead = at + 2 * kSsmChunk;
+        const int at = start + c * kSsmChunk, ahead = at + 2 * kSsmChunk, n = tokens - c * kSsmChunk;
+        const int full = n < kSsmChunk ? P::X_LANDED : P::X_FULL + (c & 1);
         if (c > 0) sh.wait(P::STAGED, (c & 1) ^ 1, ok);
         if (!ok) break;
         if (tc::elect_one()) {
@@ -711,9 +710,9 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             tc::tma_store_commit();
             tc::tma_store_wait_read();
           }
-          tc::mbar_arrive_expect_tx(sh.bar(P::X_FULL), left * P::BLOCK);
+          tc::mbar_arrive_expect_tx(sh.bar(full), left * P::BLOCK);
           for (int x = 0; x < left; ++x) {
-            tc::tma_load_2d(sbase + P::ROWS + x * P::BLOCK, &v_map, col + 64 * x, at, sh.bar(P::X_FULL));
+            tc::tma_load_2d(sbase + P::ROWS + x * P::BLOCK, &v_map, col + 64 * x, at, sh.bar(full));
             if (c + 2 < chunks) tc::tma_prefetch_2d(&v_map, col + 64 * x, ahead);
           }
           if (c + 2 < chunks)
@@ -723,6 +722,17 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             }
         }
         __syncwarp();
+        if (n < kSsmChunk) {  // where O1 takes v itself, rows behind the sequence are zeros before anyone has them, so that they are no NaN
+          sh.wait(P::X_LANDED, 0, ok);
+          sh.wait(P::GATES, c & 1, ok);  // (the phase before: STAGED of chunk c - 1, whose rows have the factors of c; none comes after)
+          if (!ok) break;
+          if (ssm_wide(small.total[c & 1][0]) || ssm_wide(small.total[c & 1][1]))
+#pragma unroll 4
+            for (int i = lane; i < (kSsmChunk - n) * 8 * left; i += 32)
+              *reinterpret_cast<uint4*>(smem + P::ROWS + (i & 8) / 8 * (left - 1) * P::BLOCK + (n + i / (8 * left)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          tc::fence_proxy_async();
+          sh.arrive(P::X_FULL + (c & 1));
+        }
       }
       if (tokens % kSsmChunk == 0) sh.wait(P::STAGED, (chunks - 1) & 1, ok);
       if (ok && tokens % kSsmChunk == 0 && tc::elect_one()) {
