@@ -31,6 +31,7 @@
 // and copies for as much again; the rest is the roles' hand-offs. Copies of v and x by rows instead of by TMA, rows out by plain stores, one buffer of K,
 // and O begun from skip v each took 8% to half as long again. A segment's first pass takes 0.6 of the second's time.
 #pragma once
+#include <cstddef>
 #include <type_traits>
 #include "gdn_ssm_common.cuh"
 
@@ -53,13 +54,15 @@ struct SsmPlace {
 
 // What the roles tell one another beside tiles.
 struct SsmSmall {
-  uint64_t bar[20];
-  float suf[2][kSsmChunk], d[2][kSsmChunk];  // of each unit's tokens
+  uint64_t bar[22];
+  alignas(16) float suf[2][kSsmChunk], d[2][kSsmChunk];  // of each unit's tokens
   float total[2][2];                         // by chunk parity: each unit's decay
   float behind[2][8];                        // in chunks of wide decay: log2 of the decay behind each 16 tokens
   uint32_t tmem, abort;
   SsmPlace place;
 };
+
+static_assert(offsetof(SsmSmall, suf) % 16 == 0 && offsetof(SsmSmall, d) % 16 == 0, "four tokens' are read and written at once");
 
 struct SsmPlan {
   static constexpr int BLOCK = 128 * 128;  // 128 rows of 64 16-bit values
@@ -71,7 +74,9 @@ struct SsmPlan {
   // phase behind its own may be over too; so each role either waits for every phase of a barrier, or the comment at its wait says what
   // it knows them by.
   static constexpr int Q_FULL = 0, K_FULL = 1, G_FULL = 3, Q_FREE = 4, L_FULL = 5, X_FULL = 6, X_LANDED = 8, O_FULL = 9, GATES = 11, V_READY = 12,
-                       A_READY = 13, S_READY = 14, GATES_READ = 15, STAGED = 16, O_READ = 17, STEPS_READ = 19, NBAR = 20;
+                       A_READY = 13, S_READY = 14, GATES_READ = 15, STAGED = 16, O_READ = 17, STEPS_READ = 19, STEPS_SET = 20, NBAR = 22;
+  static_assert(sizeof(SsmSmall::bar) == NBAR * 8 && SMALL % 16 == 0 && DYN_SMEM <= 227 * 1024, "");
+  static __device__ __forceinline__ int arrivals(int i) { return i < GATES ? 1 : i == GATES ? 2 : i >= STEPS_SET ? 4 : 8; }
 };
 
 struct SsmScanParams {
@@ -137,9 +142,9 @@ struct SsmShared {
   uint32_t bars;
   volatile uint32_t* abort;
   __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
-  // Bounded wait by a whole warp, with one answer. A warp that gave up waits no more but walks on, so that
-  // the barriers among warps still fill. (Counted, not timed: the clock and a call cost every wait code, of which
-  // the roles share the instruction caches.)
+  // Bounded wait by a whole warp, with one answer. A warp that gave up waits no more but walks on, and may then take another way than
+  // its neighbours. So a barrier without a limit is one that a warp comes to as often whichever way it takes. (Counted, not timed: the
+  // clock and a call cost every wait code, of which the roles share the instruction caches.)
   __device__ __forceinline__ void wait(int i, uint32_t parity, bool& ok) const {
     if (!ok) return;
     bool there = tc::mbar_try_wait(bar(i), parity);
@@ -211,7 +216,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
 
   if (threadIdx.x == 0) {
     small.abort = 0;
-    for (int i = 0; i < P::NBAR; ++i) tc::mbar_init(sh.bar(i), i < P::GATES ? 1 : i == P::GATES ? 2 : 8);
+    for (int i = 0; i < P::NBAR; ++i) tc::mbar_init(sh.bar(i), P::arrivals(i));
     tc::mbar_fence_init();
   }
   if (warp == 16) tc::tmem_alloc(tc::smem_u32(&small.tmem), P::TMEM_COLS);
@@ -408,6 +413,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       using Half = std::integral_constant<int, 4>;
       using All = std::integral_constant<int, 8>;
       fetch(0, None{}, All{}, true);
+      uint32_t set = 0;    // phase of STEPS_SET
       bool own_v = false;  // whether O1 of the chunk before took v itself for this unit
       for (int c = 0; c < chunks; ++c) {
         const uint32_t ph = c & 1;
@@ -457,6 +463,8 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           sh.wait(P::G_FULL, ph, ok);
           // A: row t, columns 32 i .. 32 i + 31, of which it sees those up to itself. Half of it in place of this half of G;
           // where a decay is wide and the units are two heads, the 32 columns of both units in place of those of G, once both have them.
+          // For that the two warps of these rows meet at a barrier once a block, in every chunk. (With waits of the bounded kind in its
+          // place the ragged prompts take 465 us for 410, as the two no longer run through the code together.)
           const bool own_a = any && SLICES == 1;
           const float own = suf * kLog2e;
           if (wide) {  // d e^{suf - behind} in the place of d, and log2 of d e^{suf} in that of suf, once the rows' warps have it
@@ -465,23 +473,23 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             small.d[x][t] = d * __expf(suf - last);
             small.suf[x][t] = own + __log2f(d);
             if ((lane & 15) == 15) small.behind[x][t >> 4] = own;
-            tc::named_barrier(5 + x, 128);
+            sh.arrive(P::STEPS_SET + x);
+            sh.wait(P::STEPS_SET + x, set, ok);
+            set ^= 1;
           }
           tc::fence_after_sync();
-          const int first = own_a ? 0 : 2 * x, last = own_a ? 4 : first + 2;
-          const uint32_t to = tmem + lanes + P::COL_G + (own_a ? 16 * x : 32 * x), apart = own_a ? 32 : 16;
-#pragma unroll 1
-          for (int i = first; i < last; ++i) {
-            uint32_t r[32], k16[16];
+          // block i of 32 columns, `spread` with a wide decay's factors
+          auto block = [&](int i, bool spread, uint32_t (&k16)[16]) {
+            uint32_t r[32];
             float f[2] = {1.f, 1.f};
-            if (wide && i < quarter) {
+            if (spread && i < quarter) {
               f[0] = ssm_exp2(small.behind[x][2 * i] - own);
               f[1] = ssm_exp2(small.behind[x][2 * i + 1] - own);
             }
             if (i <= quarter && __any_sync(0xffffffffu, f[1] > 0.f)) {
               tc::tmem_ld32(tmem + lanes + P::COL_G + 32 * i, r);
               tc::tmem_ld_wait32(r);
-              if (wide && i < quarter) {
+              if (spread && i < quarter) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
                   const Pair row = pair_of(f[e / 16], f[e / 16]);
@@ -493,7 +501,7 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
 #pragma unroll
                   for (int k = 0; k < 4; ++k) r[e + k] = __float_as_uint(y[k]);
                 }
-              } else if (wide) {
+              } else if (spread) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * ssm_exp2(small.suf[x][32 * i + e] - own));
               }
@@ -507,8 +515,25 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
 #pragma unroll
               for (int e = 0; e < 16; ++e) k16[e] = 0;
             }
-            if (own_a) tc::named_barrier(7 + quarter, 64);
-            tc::tmem_st16u(to + apart * i, k16);
+          };
+          if (own_a) {
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              uint32_t k16[16];
+              block(i, wide, k16);
+              if (i <= quarter) tc::named_barrier(7 + quarter, 64);
+              tc::tmem_st16u(tmem + lanes + P::COL_G + 32 * i + 16 * x, k16);
+            }
+          } else {
+            if (SLICES == 1)
+#pragma unroll 1
+              for (int i = 0; i <= quarter; ++i) tc::named_barrier(7 + quarter, 64);
+#pragma unroll 1
+            for (int i = 2 * x; i < 2 * x + 2; ++i) {
+              uint32_t k16[16];
+              block(i, SLICES == 2 && wide, k16);
+              tc::tmem_st16u(tmem + lanes + P::COL_G + 32 * x + 16 * i, k16);
+            }
           }
           sh.arrive(P::STEPS_READ);
           if (wide) {  // O2's rows take the decay before them
