@@ -783,7 +783,8 @@ def ssm_scan(q, k, v, dt, a, state, out, *, nk: int, nv: int, dk: int = 128, dv:
 
     q, k: bf16 [rows, nk*dk] (C and B in state space terms); v, out: bf16 [rows, nv*dv]; dt: fp32 or bf16 [rows, nv];
     ``a`` (<= 0), ``dt_bias``, ``skip``: fp32 [nv], the last two or None. ``softplus=False`` takes dt + dt_bias as it is.
-    ``state``, batches, ``state_is_table`` and ``workspace`` (``ssm_scan_workspace_bytes``) as for ``prefill``. dk and dv are 64 or 128."""
+    ``state``, batches, ``state_is_table`` and ``workspace`` (``ssm_scan_workspace_bytes``) as for ``prefill``. dk and dv are 64 or 128.
+    The values are finite, and sums of |q.k| d |v| and |k| d |v| over 128 tokens below 6e16."""
     torch = _torch or _setup()
     if _cards > 1:
         _one_card(q=q, k=k, v=v, dt=dt, a=a, state=state, out=out, dt_bias=dt_bias, skip=skip, cu_seqlens=cu_seqlens, workspace=workspace)

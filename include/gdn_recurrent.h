@@ -91,6 +91,10 @@ typedef struct {
  * fp32; the state is fp32, its updates keep 16 bits of each term. Steps, decays and
  * their sums are fp32. q, k and v of a sequence's own tokens must be finite (a value
  * that is not reaches the whole chunk's outputs); what lies behind a sequence need not.
+ * Chunks may be summed up to 5e21 times above or below their size: the sums over 128
+ * tokens of |q.k| d |v| and of |k| d |v| stay below 6e16, beyond which outputs and state
+ * may be infinite; of d |v| and state elements below 6e-17 outputs may take less than
+ * 8 bits, or nothing.
  * The same inputs give the same bits.
  *   workspace: gdn_ssm_scan_workspace_bytes() bytes, 256-byte aligned, or NULL to
  *              allocate it stream-ordered. Calls that overlap need one each. It may be 0:

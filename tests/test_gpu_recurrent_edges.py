@@ -40,3 +40,47 @@ def test_scan_partial_chunks_of_wide_decay(gdn, dk, dv, nk, nv):
             gdn.ssm_scan(one["q"], one["k"], one["v"], one["dt"], s["a"], S, o, **s["args"], **batch([b - a], True))
             gdn.check()
             assert torch.equal(o[:b - a], out[a:b]) and torch.equal(S[0], state[i]) and (o[b - a:] == 7).all()
+
+
+@pytest.mark.parametrize("size", [2.0 ** -20, 1e-3, 1.0, 1e2, 1e3])
+@pytest.mark.parametrize("dk,dv", [(128, 64), (128, 128), (64, 64)])
+def test_scan_of_large_and_small_values(gdn, dk, dv, size):
+    """Heads whose chunks decay by 60 to 141 nats, with q, k and v of any size that the header names: finite, and within the bounds of
+    values about one."""
+    nats = [60.0, 79.0, 81.0, 99.0, 101.0, 120.0, 139.0, 141.0]
+    nv, T = len(nats), 300
+    s = ssm([T], 1, nv, dk, dv, seed=71, softplus=False)
+    s["args"]["dt_bias"] = None
+    for n in ("q", "k", "v"):
+        s[n] = (s[n].float() * size).to(torch.bfloat16)
+    s["state"] *= size * size
+    s["dt"] = torch.ones(T, nv, device=DEV)
+    s["a"] = -torch.tensor(nats, device=DEV) / 128
+    s["d"] = s["dt"].double()
+    o, S, mags, M = ssm_want(s, [T])
+    out, state = torch.empty(T, nv * dv, dtype=torch.bfloat16, device=DEV), s["state"].clone()
+    gdn.ssm_scan(s["q"], s["k"], s["v"], s["dt"], s["a"], state, out, B=1, T=T, **s["args"])
+    gdn.check()
+    got = out.view(o.shape).double()
+    assert torch.isfinite(got).all() and torch.isfinite(state).all()
+    # the bounds of check_scan, per head: bf16 operands 2^-6 of the terms, the output 2^-8, the state 2^-14 of its terms
+    near(got, o, 2.0 ** -6 * mags + 2.0 ** -8 * o.abs(), "out")
+    near(state, S, 2.0 ** -14 * M, "state")
+    off, term = ((got - o) ** 2).sum((0, 2)).sqrt(), (mags ** 2).sum((0, 2)).sqrt()
+    assert (off <= 5e-3 * term).all(), (off / term).tolist()
+    off, term = ((state.double() - S) ** 2).sum((0, 2, 3)).sqrt(), (M ** 2).sum((0, 2, 3)).sqrt()
+    assert (off <= 1e-5 * term).all(), (off / term).tolist()
+
+
+def test_scan_of_equal_large_values(gdn):
+    """All values alike, the largest sums: 100 in every place of q, k and v, steps of 1, chunks of 139.5 nats."""
+    T = 256
+    full = lambda w: torch.full((T, w), 100.0, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    dt, a, state = torch.ones(T, 1, device=DEV), torch.full((1,), -1.09, device=DEV), torch.zeros(1, 1, 128, 64, device=DEV)
+    out = torch.empty(T, 64, dtype=torch.bfloat16, device=DEV)
+    gdn.ssm_scan(full(128), full(128), full(64), dt, a, state, out, nk=1, nv=1, dv=64, softplus=False, B=1, T=T)
+    gdn.check()
+    t = torch.arange(T, device=DEV, dtype=torch.float64)
+    sums = (1 - torch.exp(a.double() * (t + 1))) / (1 - torch.exp(a.double()))
+    near(out, (128e6 * sums)[:, None].expand(-1, 64), (2.0 ** -6 * 128e6 * sums)[:, None], "out")
+    near(state, (1e4 * sums[-1]).expand_as(state), 2.0 ** -14 * 1e4 * sums[-1], "state")
