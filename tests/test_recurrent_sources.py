@@ -23,3 +23,16 @@ def test_the_roles_of_the_scan_meet_alike_on_every_way():
     assert re.match(r"\s*if \(SLICES == 1\)\s*#pragma unroll 1\s*for \(int i = 0; i <= quarter; \+\+i\) tc::named_barrier", other)
     operands = roles[roles.index("fewer_registers<kSsmOperandRegs>"):roles.index("fewer_registers<kSsmIssueRegs>")]
     assert not re.search(r"\bbreak\b|\breturn\b|\bcontinue\b", operands)  # every chunk, to the end
+
+
+def test_every_kernel_source_is_built():
+    """CUDA sources lie with the library's, and each is one of its units or included by another."""
+    root = os.path.dirname(os.path.dirname(CSRC))
+    tracked = [os.path.join(d, f) for d, dirs, files in os.walk(root) for f in files if f.endswith((".cu", ".cuh"))
+               if not os.path.relpath(d, root).startswith((".", "_work", "gpurun_out", "baseline", "build"))] + [
+        os.path.join(root, f) for f in os.listdir(root) if f.endswith((".cu", ".cuh"))]
+    assert {os.path.dirname(f) for f in tracked} == {CSRC}, sorted(tracked)
+    included = set(re.findall(r'#include "([^"]+)"', "".join(open(f).read() for f in tracked)))
+    for f in tracked:
+        assert f.endswith(".cu") or os.path.basename(f) in included, f
+    assert not [i for i in included if os.path.isabs(i)]
