@@ -36,3 +36,10 @@ def test_every_kernel_source_is_built():
     for f in tracked:
         assert f.endswith(".cu") or os.path.basename(f) in included, f
     assert not [i for i in included if os.path.isabs(i)]
+
+
+def test_every_helper_is_called():
+    text = "".join(source(f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh")))
+    names = set(re.findall(r"__device__ __(?:force|no)inline__ [\w:]+ (\w+)\(", text))
+    assert len(names) > 100
+    assert not [n for n in names if len(re.findall(rf"\b{n}\b", text)) < 2]
