@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtasPerSm) gdn_conv_kernel(
   conv_weights<W, P>(p, c0, w, b);
   for (int s = p.batch.find(row); row < stop && s < p.batch.B; ++s) {
     const int start = p.batch.start(s), end = p.batch.end(s);
-    if (end <= row || !rows_held(start, end, p.batch.rows) || start > row) continue;
+    if (end <= row || start >= stop || !rows_held(start, end, p.batch.rows)) continue;
+    row = max(row, start);  // behind rows of refused sequences
     T* state = conv_state<T>(p.state, p.state_is_table, s, static_cast<int64_t>(W - 1) * p.D);
     if (state) state += c0;
     uint4 last[W - 1];  // the inputs before
@@ -258,7 +259,8 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4) gdn_conv
   for (int j = 0; j < W; ++j) dw[j][0] = dw[j][1] = zero;
   for (int s = p.batch.find(row); row < stop && s < p.batch.B; ++s) {
     const int start = p.batch.start(s), end = p.batch.end(s);
-    if (end <= row || !rows_held(start, end, p.batch.rows) || start > row) continue;
+    if (end <= row || start >= stop || !rows_held(start, end, p.batch.rows)) continue;
+    row = max(row, start);  // behind rows of refused sequences
     const int64_t size = static_cast<int64_t>(W - 1) * p.D;
     const T* state = conv_state<const T>(p.state, 0, s, size);
     const T* dlast = p.dlast ? static_cast<const T*>(p.dlast) + s * size + c0 : nullptr;

@@ -84,3 +84,78 @@ def test_scan_of_equal_large_values(gdn):
     sums = (1 - torch.exp(a.double() * (t + 1))) / (1 - torch.exp(a.double()))
     near(out, (128e6 * sums)[:, None].expand(-1, 64), (2.0 ** -6 * 128e6 * sums)[:, None], "out")
     near(state, (1e4 * sums[-1]).expand_as(state), 2.0 ** -14 * 1e4 * sums[-1], "state")
+
+
+BAD = [[0, 50, 40, 90], [5, 40, 60, 90], [0, 200, 60, 90], [-4, 40, 60, 90], [0, 40, 60, 200], [0, 2 ** 31 - 1, 60, 90], [0, 95, 33, 90]]
+
+
+@pytest.mark.parametrize("cu", BAD)
+def test_sequences_with_bad_offsets_write_nothing(gdn, cu):
+    """Beside the report: rows that only refused sequences would own keep what they held, as do the rows around the buffers and the states of
+    those sequences; the rows of a sequence whose offsets are its own come out as in a batch of their own."""
+    rows, D, pad = 90, 64, 4
+    off = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    held = [i for i in range(3) if 0 <= cu[i] <= cu[i + 1] <= rows]
+    owners = [[i for i in held if cu[i] <= r < cu[i + 1]] for r in range(rows)]
+    free = torch.tensor([not o for o in owners], device=DEV)
+    s, c = ssm([30] * 3, 1, 2, 128, 64, seed=81), make_conv([30] * 3, D, 4, torch.bfloat16, seed=81)
+
+    def framed(width):
+        t = torch.full((rows + 2 * pad, width), 7.0, dtype=torch.bfloat16, device=DEV)
+        return t, t[pad:-pad]
+
+    def reported():
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.check()
+        assert e.value.code == gdn.GDN_ERR_DEVICE_STATUS
+
+    def untouched(frame, part):
+        assert (frame[:pad] == 7).all() and (frame[-pad:] == 7).all() and (part[free] == 7).all()
+
+    def alone(i):  # a sequence's rows, and which of them no other sequence writes too
+        a, b = cu[i], cu[i + 1]
+        return slice(a, b), torch.tensor([owners[r] == [i] for r in range(a, b)], dtype=torch.bool, device=DEV)
+
+    frame, out = framed(128)
+    state = s["state"].clone()
+    gdn.ssm_scan(s["q"], s["k"], s["v"], s["dt"], s["a"], state, out, cu_seqlens=off, **s["args"])
+    reported()
+    untouched(frame, out)
+    for i in range(3):
+        if i not in held:
+            assert torch.equal(state[i], s["state"][i])
+        elif cu[i] < cu[i + 1]:
+            r, own = alone(i)
+            one, S = torch.empty_like(out[r]), s["state"][i:i + 1].clone()
+            gdn.ssm_scan(s["q"][r], s["k"][r], s["v"][r], s["dt"][r], s["a"], S, one, B=1, T=one.shape[0], **s["args"])
+            assert torch.equal(one[own], out[r][own]) and torch.equal(S[0], state[i])
+
+    frame, out = framed(D)
+    state = c["h0"].clone()
+    gdn.causal_conv(c["x"], c["w"], out, bias=c["b"], state=state, cu_seqlens=off)
+    reported()
+    untouched(frame, out)
+    for i in range(3):
+        if i not in held:
+            assert torch.equal(state[i], c["h0"][i])
+        elif cu[i] < cu[i + 1]:
+            r, own = alone(i)
+            one, S = torch.empty_like(out[r]), c["h0"][i:i + 1].clone()
+            gdn.causal_conv(c["x"][r], c["w"], one, bias=c["b"], state=S, B=1, T=one.shape[0])
+            assert torch.equal(one[own], out[r][own]) and torch.equal(S[0], state[i])
+
+    frame, dx = framed(D)
+    dh0 = torch.full_like(c["h0"], 7)
+    dw = torch.empty_like(c["w"])
+    gdn.causal_conv_backward(c["x"], c["w"], c["dout"], dx, dw, bias=c["b"], h0=c["h0"], dST=c["dST"], dh0=dh0, cu_seqlens=off)
+    reported()
+    untouched(frame, dx)
+    for i in range(3):
+        if i not in held:
+            assert (dh0[i] == 7).all()
+        elif cu[i] < cu[i + 1]:
+            r, own = alone(i)
+            one, S = torch.empty_like(dx[r]), torch.empty_like(dh0[i:i + 1])
+            gdn.causal_conv_backward(c["x"][r], c["w"], c["dout"][r], one, bias=c["b"], h0=c["h0"][i:i + 1], dST=c["dST"][i:i + 1], dh0=S, B=1, T=one.shape[0])
+            assert torch.equal(one[own], dx[r][own]) and torch.equal(S[0], dh0[i])
+    gdn.check()
