@@ -159,3 +159,31 @@ def test_sequences_with_bad_offsets_write_nothing(gdn, cu):
             gdn.causal_conv_backward(c["x"][r], c["w"], c["dout"][r], one, bias=c["b"], h0=c["h0"][i:i + 1], dST=c["dST"][i:i + 1], dh0=S, B=1, T=one.shape[0])
             assert torch.equal(one[own], dx[r][own]) and torch.equal(S[0], dh0[i])
     gdn.check()
+
+
+@pytest.mark.parametrize("gate,first,kind", [(False, False, "layer"), (True, False, "rms"), (True, True, "layer")])
+@pytest.mark.parametrize("dim,dtype", [(256, torch.bfloat16), (1000, torch.bfloat16), (1024, torch.float32), (4096, torch.float16), (8192, torch.bfloat16), (8192, torch.float32)])
+def test_wide_norms_in_place(gdn, dim, dtype, gate, first, kind):
+    """Rows that the backward has under way while it writes others: several a CTA, outputs in the place of each input that they may take."""
+    c = make_norm(2000, 1, dim, dtype, 0, kind, "before" if first else "after" if gate else None, seed=91)
+    f = c["form"]
+    want = torch.empty_like(c["x"])
+    gdn.layer_norm(c["x"], want, weight=c["weight"], bias=c["bias"], gate=c["gate"], **f)
+    places = ["x", "gate"] if gate else ["x"]
+    for place in places:
+        t = {n: c[n].clone() for n in places}
+        gdn.layer_norm(t["x"], t[place], weight=c["weight"], bias=c["bias"], gate=t.get("gate"), **f)
+        assert torch.equal(t[place], want), place
+    new = lambda t: torch.empty_like(t)  # noqa: E731
+    dx, dz, dw, db = new(c["x"]), new(c["x"]) if gate else None, new(c["weight"]), new(c["bias"])
+    gdn.layer_norm_backward(c["x"], c["dout"], dx, dw, db, weight=c["weight"], bias=c["bias"], gate=c["gate"], dgate=dz, **f)
+    inputs = ["x", "dout"] + (["gate"] if gate else [])
+    for a in inputs:
+        for b in inputs if gate else [None]:
+            if a == b:
+                continue
+            t = {n: c[n].clone() for n in inputs}
+            w, d = new(dw), new(db)
+            gdn.layer_norm_backward(t["x"], t["dout"], t[a], w, d, weight=c["weight"], bias=c["bias"], gate=t.get("gate"), dgate=t[b] if gate else None, **f)
+            assert torch.equal(t[a], dx) and torch.equal(w, dw) and torch.equal(d, db) and (not gate or torch.equal(t[b], dz)), (a, b)
+    gdn.check()
