@@ -801,7 +801,7 @@ def ssm_scan(q, k, v, dt, a, state, out, *, nk: int, nv: int, dk: int = 128, dv:
 def ssm_decode(q, k, v, dt, a, state, out, *, nk: int, nv: int, dk: int = 128, dv: int = 128, dt_bias=None,
                softplus: bool = True, skip=None, state_is_table: bool = False, stream=None) -> None:
     """One token of ``ssm_scan`` for every row (sequence) b: ``state[b]`` (or the b-th address of a table) is advanced by
-    it and its output written to ``out[b]`` (``gdn_ssm_decode``)."""
+    it and its output written to ``out[b]``, which may be v's row itself (``gdn_ssm_decode``)."""
     torch = _torch or _setup()
     if _cards > 1:
         _one_card(q=q, k=k, v=v, dt=dt, a=a, state=state, out=out, dt_bias=dt_bias, skip=skip)

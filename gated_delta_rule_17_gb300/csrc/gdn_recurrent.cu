@@ -558,6 +558,8 @@ int gdn_ssm_decode(const void* q, const void* k, const void* v, const void* dt, 
   if (int rc = ssm_setup(q, k, v, dt, a, dt_bias, skip, state, out, nk, nv, dk, dv, options, B, &p)) return rc;
   if (static_cast<int64_t>(B) * nv > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%d sequences of %d heads exceed the item range", B, nv);
   if (B == 0) return GDN_OK;
+  if (out == q || out == k) return fail(GDN_ERR_ARG, "out must not be q or k: a row's are read by several CTAs");
+  if (int rc = check_same({"out", "v", out, v, p.out_stride, p.v_stride})) return rc;
   int sms = 0;
   if (int rc = gdn_host::device(&sms, &p.status)) return rc;
   by_state(dk, dv, [&](auto K, auto V) {

@@ -107,7 +107,7 @@ int gdn_ssm_scan(const void* q, const void* k, const void* v, const void* dt, co
                  void* stream);
 
 /* One token of every sequence: row b of q, k, v, dt and out belongs to sequence b.
- * One launch. */
+ * out may be v itself (with its stride), and overlaps no other input. One launch. */
 int gdn_ssm_decode(const void* q, const void* k, const void* v, const void* dt, const float* a, const float* dt_bias,
                    const float* skip, void* state, void* out, int B, int nk, int nv, int dk, int dv,
                    const gdn_ssm_options_t* options, void* stream);

@@ -187,3 +187,13 @@ def test_wide_norms_in_place(gdn, dim, dtype, gate, first, kind):
             gdn.layer_norm_backward(t["x"], t["dout"], t[a], w, d, weight=c["weight"], bias=c["bias"], gate=t.get("gate"), dgate=t[b] if gate else None, **f)
             assert torch.equal(t[a], dx) and torch.equal(w, dw) and torch.equal(d, db) and (not gate or torch.equal(t[b], dz)), (a, b)
     gdn.check()
+
+
+@pytest.mark.parametrize("B,nk,nv,dk,dv,pad", [(3, 1, 24, 128, 64, 8), (17, 4, 4, 128, 128, 0), (300, 2, 6, 64, 64, 16)])
+def test_step_in_the_place_of_v(gdn, B, nk, nv, dk, dv, pad):
+    s = ssm([1] * B, nk, nv, dk, dv, pad, steps=0.5, seed=95)
+    out, states = torch.empty(B, nv * dv, dtype=torch.bfloat16, device=DEV), [s["state"].clone() for _ in range(2)]
+    gdn.ssm_decode(s["q"], s["k"], s["v"], s["dt"], s["a"], states[0], out, **s["args"])
+    gdn.ssm_decode(s["q"], s["k"], s["v"], s["dt"], s["a"], states[1], s["v"], **s["args"])
+    gdn.check()
+    assert torch.equal(out, s["v"]) and torch.equal(*states)

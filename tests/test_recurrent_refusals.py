@@ -277,3 +277,11 @@ def test_rows_over_one_another(gdn):
     refused(gdn, lambda: gdn.layer_norm(t(6, 128), t(6, 128), dim=48, stream=0), "groups of 48")
     refused(gdn, lambda: gdn.layer_norm(t(6, 128), t(6, 128), dim=0, stream=0), "dim")
     refused(gdn, lambda: gdn.layer_norm(t(128), t(128), dim=64, stream=0), "rows")
+
+
+def test_step_refuses_what_other_heads_read_as_output(gdn):
+    for name in ("q", "k"):
+        rc, msg = step(gdn, **{name: 2 * P})
+        assert rc == gdn.GDN_ERR_ARG and "must not be q or k" in msg, msg
+    rc, msg = step(gdn, v=2 * P, o=opt(4, 512))
+    assert rc == gdn.GDN_ERR_ARG and "in the place of v" in msg, msg
