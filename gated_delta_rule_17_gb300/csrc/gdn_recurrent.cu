@@ -409,7 +409,7 @@ int gdn_causal_conv(const void* x, const float* weight, const float* bias, void*
   if (int rc = conv_setup(x, weight, bias, D, width, silu, dtype, x_stride, &p)) return rc;
   if (int rc = take_stride(out_stride, D, "out", &p.out_stride)) return rc;
   if (int rc = check_flag(state_is_table, "state_is_table")) return rc;
-  if (state_is_table && !state) return fail(GDN_ERR_ARG, "a state table without its pointer");
+  if (B && state_is_table && !state) return fail(GDN_ERR_ARG, "a state table without its pointer");
   if (B == 0 || p.batch.rows == 0) return GDN_OK;
   if (!x || !out) return fail(GDN_ERR_ARG, "a required pointer is NULL");
   if (x == out) return fail(GDN_ERR_ARG, "out must not be x: a row's inputs are read by several threads");

@@ -285,3 +285,14 @@ def test_step_refuses_what_other_heads_read_as_output(gdn):
         assert rc == gdn.GDN_ERR_ARG and "must not be q or k" in msg, msg
     rc, msg = step(gdn, v=2 * P, o=opt(4, 512))
     assert rc == gdn.GDN_ERR_ARG and "in the place of v" in msg, msg
+
+
+def test_tables_of_no_sequences(gdn):
+    """An empty tensor's address is 0, also that of an empty table: a batch of no sequences has nothing to refuse."""
+    assert conv(gdn, B=0, x=None, out=None, state=None, table=1)[0] == gdn.GDN_OK
+    rows = t(0, 64)
+    for kw in (dict(B=0, T=3), dict(cu_seqlens=t(1, dtype="int32"))):
+        gdn.causal_conv(rows, f32(64, 4), t(0, 64), state=t(0, dtype="int64"), state_is_table=True, stream=0, **kw)
+    step = dict(q=t(0, 128), k=t(0, 128), v=t(0, 128), dt=f32(0, 2), a=f32(2), state=t(0, dtype="int64"), out=t(0, 128), state_is_table=True, stream=0, **SIZES)
+    gdn.ssm_decode(**step)
+    gdn.ssm_scan(**step, B=0, T=3)
