@@ -197,3 +197,29 @@ def test_step_in_the_place_of_v(gdn, B, nk, nv, dk, dv, pad):
     gdn.ssm_decode(s["q"], s["k"], s["v"], s["dt"], s["a"], states[1], s["v"], **s["args"])
     gdn.check()
     assert torch.equal(out, s["v"]) and torch.equal(*states)
+
+
+@pytest.mark.parametrize("dk,dv,nk,nv", [(128, 64, 1, 4), (128, 128, 1, 2), (64, 64, 1, 3)])
+def test_scan_of_tokens_without_a_step(gdn, dk, dv, nk, nv):
+    """Steps of exactly zero (dt of -infinity under softplus, as masked tokens have it): such a token leaves the state alone, in chunks of
+    either kind, at their ends, and for whole chunks and sequences."""
+    lens = [300, 128, 40, 129]
+    s = ssm(lens, nk, nv, dk, dv, seed=97, steps=0.05, rate=8.0)
+    low, rows = float("-inf"), sum(lens)
+    s["a"][0] = -16.0
+    s["dt"][:300, 0] += 2.0  # a head whose chunks decay by much
+    for r in (slice(0, 3), slice(17, 20), slice(96, 160), slice(255, 257), slice(290, 300), slice(300, 428), slice(430, 468), slice(469, 470), slice(596, 597)):
+        s["dt"][r] = low
+    s["dt"][130:140, 1:] = low
+    s["d"] = torch.nn.functional.softplus(s["dt"].double() + s["bias"].double(), threshold=1e4)
+    assert (s["d"][300:428] == 0).all()
+    o, S, mags, M = ssm_want(s, lens)
+    out, state = torch.empty(rows, nv * dv, dtype=torch.bfloat16, device=DEV), s["state"].clone()
+    gdn.ssm_scan(s["q"], s["k"], s["v"], s["dt"], s["a"], state, out, **s["args"], **batch(lens, True))
+    gdn.check()
+    check_scan(out, state, (o, S, mags, M), rows)
+    near(state[1], s["state"][1].double(), 2.0 ** -22 * s["state"][1].double().abs(), "a sequence without steps")  # e^0 S, one rounding at most
+    one = s["state"].clone()
+    gdn.ssm_decode(s["q"][:4], s["k"][:4], s["v"][:4], torch.full_like(s["dt"][:4], low), s["a"], one, out[:4], **s["args"])
+    gdn.check()
+    assert torch.equal(one, s["state"])
