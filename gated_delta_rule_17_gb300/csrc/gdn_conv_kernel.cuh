@@ -232,7 +232,7 @@ __device__ __forceinline__ void conv_dy(const Pair (&w)[W][2], const Pair (&b)[2
 
 // A thread owns four channels and a strip of rows; it walks W - 1 rows past the strip's end, whose dy
 // the last gradients need, and keeps the weight gradients of its own rows. (Eight channels would need twice its 128 registers.)
-// 32768 rows of 8192 in bf16: 284 us, 5.68 TB/s, 84% of the measured copy rate. It issues in 55% of the slots, its fp32 pipe is at
+// 32768 rows of 8192 in bf16: 282 us, 5.71 TB/s, 84% of the measured copy rate. It issues in 55% of the slots, its fp32 pipe is at
 // half, with 14 warps an SM: what is left is the arithmetic. Addresses by products of row and stride cost another 14 us.
 template <typename T, int W>
 __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4) gdn_conv_bwd_kernel(const ConvParams p) {

@@ -25,9 +25,9 @@
 // pipe: O2, L, O1 of a chunk, then G of the next. So the update of S, the only step that the next chunk's O2 waits
 // for, runs under G, making A under O2, the rows' way out under L.
 //
-// 4 x 8192 tokens of 32 heads of 128 x 128 on 16: 186 us, 198 to 209 with a few heads whose chunks decay by more than kSsmSpan; HBM alone
-// would take 122, the products 35. There is a CTA for 128 of the 152 SMs, and a chunk takes it 2.9 us. The tensor pipe is
-// busy for 29% of it, the issue slots for 43%, loads and stores keep shared memory for 39% and the products' operands (288 KB a chunk)
+// 4 x 8192 tokens of 32 heads of 128 x 128 on 16: 188 us, 206 to 216 with a few heads whose chunks decay by more than kSsmSpan; HBM alone
+// would take 122, the products at their least 35. There is a CTA for 128 of the 152 SMs, and a chunk takes it 2.9 us. The tensor pipe is
+// busy for 29% of it, the issue slots for 43%, loads and stores keep shared memory for 40% and the products' operands (288 KB a chunk)
 // and copies for as much again; the rest is the roles' hand-offs. Copies of v and x by rows instead of by TMA, rows out by plain stores, one buffer of K,
 // and O begun from skip v each took 8% to half as long again. A segment's first pass takes 0.6 of the second's time.
 #pragma once
@@ -93,9 +93,10 @@ struct SsmScanParams {
   float* decays;  // [item][nv]: the decay over segment i, as a logarithm
 };
 
-// Found by one warp. Sequences go by themselves, the longest first, or (where `segment` is given, and the longest of them would
+// Found by one warp. Sequences go by themselves, packed ones the longest first, or (where `segment` is given, and the longest of them would
 // keep most SMs waiting) in segments: then the state at the end of each segment but the last is worked out first, which takes a
-// little over half of a segment's time again.
+// little over half of a segment's time again. The warp has a lane for a sequence, so that packed batches of more than 32 go in their given
+// order and whole: a prompt of 32768 among 31 of 100, 8 heads of 128 x 64 on 2: 142 us, among 32 of them 675.
 __device__ __forceinline__ SsmPlace ssm_place(const SsmScanParams& params, int item) {
   const Rows& b = params.s.batch;
   const int lane = threadIdx.x & 31, seg = params.segment;
@@ -397,7 +398,8 @@ gdn_ssm_scan_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       for (int i = 0; i < 2; ++i) hi[i] = smem + P::VHI + x * P::BLOCK + tc::sw128(r0 + 4 * i + (lane >> 3), 16 * (lane & 7));
       uint4 word[8];  // a chunk's v, ahead
       // Half of the next chunk's words come while A is made, where there are registers for no more, but not beside wide decays, whose A
-      // reads shared memory behind these loads: ragged prompts 362 -> 337 us, 448 -> 405 with wide decays (461 where those fetch early too)
+      // reads shared memory behind these loads: without it ragged prompts took 362 us for 337, and 448 for 405 with wide decays (461 where
+      // those fetch early too)
       auto fetch = [&](int c, auto first, auto last, bool now) {  // words first .. last - 1
         constexpr int from = decltype(first)::value, to = decltype(last)::value;
         const int left = opaque(is_real) && now ? tokens - c * kSsmChunk - r0 - (lane >> 3) : 0;

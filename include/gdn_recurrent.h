@@ -95,7 +95,9 @@ typedef struct {
  * tokens of |q.k| d |v| and of |k| d |v| stay below 6e16, beyond which outputs and state
  * may be infinite; of d |v| and state elements below 6e-17 outputs may take less than
  * 8 bits, or nothing.
- * The same inputs give the same bits.
+ * The same inputs give the same bits. Packed batches of more than 32 sequences run in
+ * their given order, without segments: long ones go first in them, or into a call of
+ * their own.
  *   workspace: gdn_ssm_scan_workspace_bytes() bytes, 256-byte aligned, or NULL to
  *              allocate it stream-ordered. Calls that overlap need one each. It may be 0:
  *              segments of long sequences take it, where there are few heads for the SMs.
